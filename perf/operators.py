@@ -141,11 +141,13 @@ def _randn(gen, *shape, dtype=torch.bfloat16):
 def _summaries(k):
     """Codes and scales of every 64-row block of k [..., rows, d] (rows a
     multiple of 64): the block's mean key in fp32 (from an exact sum),
-    scale = max |mean| / 127, code = mean * (127 / max |mean|) rounded to even."""
+    scale = max |mean| / 127, code = mean * (127 / max |mean|) rounded to even.
+    (Tensors on both sides: torch multiplies by a rounded reciprocal where one
+    side of a quotient is a plain number.)"""
     m = k.unflatten(-2, (-1, BLOCK)).double().mean(-2).float()
     top = m.abs().amax(-1, keepdim=True)
-    inv = torch.where(top > 0, 127.0 / top, torch.zeros_like(top))
-    return torch.round(m * inv).to(torch.int8), (top / 127.0).squeeze(-1)
+    inv = torch.where(top > 0, torch.full_like(top, 127.0) / top, torch.zeros_like(top))
+    return torch.round(m * inv).to(torch.int8), (top / torch.full_like(top, 127.0)).squeeze(-1)
 
 
 def prepare(case, seed):
@@ -273,7 +275,7 @@ def _choose(q, codes, scales, blocks, top):
     """Indices of the `top` best blocks [n, hkv, tok, top], ascending, -1 where
     there are fewer; q [n, hkv, g, tok, d], blocks [n] complete blocks."""
     amax = q.abs().amax((2, 4), keepdim=True)
-    inv = torch.where(amax > 0, 127.0 / amax, torch.zeros_like(amax))
+    inv = torch.where(amax > 0, torch.full_like(amax, 127.0) / amax, torch.zeros_like(amax))
     qi = torch.round(q * inv)
     # sums of 128 products of 8-bit numbers stay below 2^24: exact in fp32
     dots = qi.flatten(2, 3) @ codes.float().transpose(-1, -2)
@@ -413,7 +415,7 @@ def exact(case, seed):
             # product in fp32
             m = (x.sum(2) / BLOCK).float()
             big = m.abs().max(-1).values
-            code = torch.round(m * (127.0 / big)[..., None])
+            code = torch.round(m * (127 / big.double()).float()[..., None])
             scl[i, :, lo:hi] = big.double() / 127
             out[i, :, lo:hi] = code.double() * scl[i, :, lo:hi, None]
         return out, scl
@@ -445,7 +447,7 @@ def exact(case, seed):
                 if nb:
                     # whole-number scores of the 8-bit query against the codes
                     big = q.float().abs().max()
-                    qi = torch.round(q.float() * (127.0 / big)).double()
+                    qi = torch.round(q.float() * (127 / big.double()).float()).double()
                     sc = (qi @ s["codes"][i, h, :nb].double().T).max(0).values.float() * s["scales"][i, h, :nb]
                     best = sorted(range(nb), key=lambda b, v=sc.tolist(): (-v[b], b))[:case["top"]]
                     keep[:nb * BLOCK].view(nb, BLOCK)[torch.tensor(best, device=DEV)] = True
