@@ -377,6 +377,154 @@ int statekv_attend_scores_static(const void* q_rot, const void* pool_k,
                                  int32_t dtype, void* o, float* scores,
                                  uint32_t* status, void* cuda_stream);
 
+/* ------------------------------------------- text operators, handle-free */
+
+/*
+ * Operators of text decoding over a cache of keys and values (a handle's
+ * detailed state D, or any other cache), for callers that hold their own
+ * tensors.  No counterpart in the page except for the rotation (关键设计 3);
+ * the handle's statekv_decode_tree, statekv_accept and statekv_decode_sparse
+ * run the same kernels over D.
+ *
+ * Tensors are views [batch][heads][tokens][head_dim] of DEVICE memory on the
+ * current device: the last dimension contiguous, the other strides free (in
+ * elements), every row on a 16-byte boundary.  The batch is sequences x
+ * layers: batch entry n belongs to sequence n / layers, and lengths, trees,
+ * paths and destination rows have one entry per sequence.  Query head j uses
+ * KV head j / (q_heads / kv_heads).  Outputs must not overlap inputs unless
+ * said otherwise.
+ *
+ * `lengths` (int32, device) gives each sequence's rows in the cache; where it
+ * is NULL every sequence has `length` rows.  A length, count, row or node out
+ * of range is known only on the device: the kernel clamps or skips it, and
+ * records STATEKV_E_DEVICE in the status word.  `status` is a device
+ * uint32[4] (4-byte aligned, required), zeroed once by the caller and kept
+ * over any number of calls: the first failure stays in it (status[0] a
+ * STATEKV_E_* code, as for statekv_check_device_status) until the caller
+ * clears it.
+ *
+ * Calls allocate nothing, keep nothing between calls and may be captured into
+ * CUDA graphs.  Calls that overlap on the GPU need workspaces of their own;
+ * they may share a status word.
+ */
+typedef struct statekv_view {
+    void*   data;
+    int64_t batch_stride, head_stride, token_stride;   /* in elements */
+} statekv_view;
+
+#define STATEKV_BLOCK 64            /* cache rows per summarised block */
+
+/*
+ * RMS norm of every head of Q and K, rotation at the tokens' virtual
+ * positions, and the store of Q, K and V, in one pass:
+ *   y = x * w / sqrt(mean(x^2) + eps), rotated by the angles p * omega[k]
+ * (element k with element k + head_dim/2), in fp32, rounded once.
+ *   q -> q_out rows t; k -> k_out and v -> v_out rows out_rows[sequence] + t
+ *   (row t where out_rows is NULL), of out_capacity rows.
+ * q_weight, k_weight [head_dim] in weight_dtype, or NULL: no norm of that
+ * tensor.  omega: float64 [head_dim/2], radians per position.  positions:
+ * int32 [batch / position_layers][position_stride >= tokens], or
+ * position_stride 0 for one row shared by all; NULL: position0 + t.  v.data
+ * and v_out.data may both be NULL.  Each output may be its own input (the
+ * same view).  A sequence whose rows do not fit in k_out is recorded, and its
+ * K and V are not stored.
+ * dtype: STATEKV_BF16 or STATEKV_F32; head_dim 64 or 128.
+ */
+typedef struct statekv_norm_rope_args {
+    statekv_view q, k, v, q_out, k_out, v_out;
+    const void* q_weight;
+    const void* k_weight;
+    const double* omega;
+    const int32_t* positions;
+    const int32_t* out_rows;
+    uint32_t* status;
+    int64_t position0;
+    int32_t position_stride, position_layers;
+    int32_t batch, layers, q_heads, kv_heads, tokens, head_dim;
+    int32_t out_capacity;
+    int32_t dtype, weight_dtype;
+    float eps;
+} statekv_norm_rope_args;
+int statekv_norm_rope(const statekv_norm_rope_args* args, void* cuda_stream);
+
+/*
+ * Attention of a tree of `tokens` (1..64) drafted tokens over the cache:
+ *   o = softmax(q [cache_K[:length]; K_new]^T * scale, masked) [cache_V; V_new]
+ * Every cache row is visible; drafted token j is visible to drafted token i
+ * iff bit j of tree[i] is set (the node's ancestors and itself; any mask is
+ * allowed).  q and k_new are already rotated.  A key that is masked, and
+ * cache rows from `length` on, contribute nothing whatever they hold
+ * (infinities and NaN included); a row that sees no key at all gets zeros.
+ * tree: uint64 [sequences][tree_stride >= tokens], or tree_stride 0 for one
+ * tree shared by all; bits from `tokens` on are ignored.
+ * bf16, head_dim 64 or 128, q_heads / kv_heads <= 64, cache_rows >= 0 rows
+ * per head in the cache views.  workspace: device memory of
+ * statekv_tree_attention_workspace() bytes, 16-byte aligned, contents
+ * irrelevant; that function depends on the current device and returns -1 for
+ * sizes that the call would refuse.  The results do not depend on the
+ * workspace or on the other calls, but sums are grouped by the whole batch:
+ * they agree between batchings up to rounding.
+ */
+typedef struct statekv_tree_args {
+    statekv_view q, out, k_new, v_new, k_cache, v_cache;
+    const uint64_t* tree;
+    const int32_t* lengths;
+    uint32_t* status;
+    void* workspace;
+    int64_t workspace_bytes;
+    double scale;
+    int32_t tree_stride, length;
+    int32_t batch, layers, q_heads, kv_heads, tokens, head_dim, cache_rows;
+} statekv_tree_args;
+int64_t statekv_tree_attention_workspace(int32_t batch, int32_t q_heads, int32_t kv_heads,
+                                         int32_t tokens, int32_t head_dim);
+int statekv_tree_attention(const statekv_tree_args* args, void* cuda_stream);
+
+/*
+ * The accepted drafted tokens join the cache: for i < counts[sequence],
+ *   cache row length + i = new row path[sequence][i],
+ * K and V of every layer and head; other rows stay as they are.  path: int32
+ * [sequences][path_stride >= path_len] (path_stride 0: shared), each entry in
+ * [0, tokens), in any order.  counts (int32, each 0..path_len) NULL: path_len
+ * for all.  new_lengths, if not NULL, receives length + count (memory of its
+ * own, not the `lengths` or `counts` array).  A sequence whose rows do not
+ * fit appends nothing; an entry out of range is skipped.  Any head_dim of
+ * whole 16-byte units up to 512; dtype STATEKV_BF16 or STATEKV_F32.
+ */
+typedef struct statekv_append_args {
+    statekv_view k_new, v_new, k_cache, v_cache;
+    const int32_t* path;
+    const int32_t* counts;
+    const int32_t* lengths;
+    int32_t* new_lengths;
+    uint32_t* status;
+    int32_t path_stride, path_len, length;
+    int32_t batch, layers, kv_heads, tokens, head_dim, cache_rows, dtype;
+} statekv_append_args;
+int statekv_append_accepted(const statekv_append_args* args, void* cuda_stream);
+
+/*
+ * Summaries of the complete blocks of STATEKV_BLOCK cache rows, block b =
+ * rows [64 b, 64 b + 64): the mean key (fp32, from a sum exact to fp32) as
+ * 8-bit codes of one scale,
+ *   scale = max |mean| / 127,  code = round_to_even(mean * (127 / max |mean|)).
+ * Brings up to date the blocks that the last `appended` rows completed, [
+ * (length - appended) / 64, length / 64 ); the others are left as they are.
+ * codes: int8 [batch][kv_heads][blocks][head_dim] (8-byte aligned), scales:
+ * float [batch][kv_heads][blocks], blocks >= cache_rows / 64 (else
+ * E_CAPACITY).  Keys must be finite.  bf16, head_dim 64 or 128.
+ */
+typedef struct statekv_summary_args {
+    statekv_view k_cache;
+    int8_t* codes;
+    float* scales;
+    const int32_t* lengths;
+    uint32_t* status;
+    int32_t length, appended, blocks;
+    int32_t batch, layers, kv_heads, head_dim, cache_rows;
+} statekv_summary_args;
+int statekv_block_summaries(const statekv_summary_args* args, void* cuda_stream);
+
 #ifdef __cplusplus
 }
 #endif

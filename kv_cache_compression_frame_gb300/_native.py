@@ -40,7 +40,11 @@ EXPORTS = (
     "statekv_set_compressed", "statekv_profile_enable", "statekv_profile_read",
     "statekv_profile_kernels",
     "statekv_attend_scores_static", "statekv_decode", "statekv_text_tokens",
+    "statekv_norm_rope", "statekv_tree_attention", "statekv_tree_attention_workspace",
+    "statekv_append_accepted", "statekv_block_summaries",
 )
+
+BLOCK = 64          # STATEKV_BLOCK
 
 
 class Config(C.Structure):
@@ -54,6 +58,36 @@ class Config(C.Structure):
         ("rope_orig_ctx", C.c_int64), ("position_offset", C.c_int64),
         ("select_policy", C.c_int32),
     ]
+
+
+class View(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("batch_stride", C.c_int64),
+                ("head_stride", C.c_int64), ("token_stride", C.c_int64)]
+
+
+def _struct(name: str, *groups) -> type:
+    """A ctypes mirror of one of the header's argument structures."""
+    fields = [(f, t) for t, names in groups for f in names.split()]
+    return type(name, (C.Structure,), {"_fields_": fields})
+
+
+NormRopeArgs = _struct(
+    "NormRopeArgs", (View, "q k v q_out k_out v_out"),
+    (C.c_void_p, "q_weight k_weight omega positions out_rows status"), (C.c_int64, "position0"),
+    (C.c_int32, "position_stride position_layers batch layers q_heads kv_heads tokens head_dim "
+                "out_capacity dtype weight_dtype"), (C.c_float, "eps"))
+TreeArgs = _struct(
+    "TreeArgs", (View, "q out k_new v_new k_cache v_cache"),
+    (C.c_void_p, "tree lengths status workspace"), (C.c_int64, "workspace_bytes"),
+    (C.c_double, "scale"),
+    (C.c_int32, "tree_stride length batch layers q_heads kv_heads tokens head_dim cache_rows"))
+AppendArgs = _struct(
+    "AppendArgs", (View, "k_new v_new k_cache v_cache"),
+    (C.c_void_p, "path counts lengths new_lengths status"),
+    (C.c_int32, "path_stride path_len length batch layers kv_heads tokens head_dim cache_rows dtype"))
+SummaryArgs = _struct(
+    "SummaryArgs", (View, "k_cache"), (C.c_void_p, "codes scales lengths status"),
+    (C.c_int32, "length appended blocks batch layers kv_heads head_dim cache_rows"))
 
 
 class StateKVError(RuntimeError):
@@ -108,6 +142,11 @@ def load() -> C.CDLL:
                                                    C.c_int32, C.c_double, C.c_int32,
                                                    _P, _P, _P, _P]),
     }
+    for name, args in (("statekv_norm_rope", NormRopeArgs), ("statekv_tree_attention", TreeArgs),
+                       ("statekv_append_accepted", AppendArgs),
+                       ("statekv_block_summaries", SummaryArgs)):
+        sig[name] = (C.c_int, [C.POINTER(args), _P])
+    sig["statekv_tree_attention_workspace"] = (C.c_int64, [C.c_int32] * 5)
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
         fn.restype = res

@@ -979,6 +979,23 @@ bool encode_view(CUtensorMap* m, const void* base, int d, int64_t rows, int64_t 
            CUDA_SUCCESS;
 }
 
+bool encode_view4(CUtensorMap* m, const statekv_view& v, int d, int64_t rows, int64_t heads,
+                  int64_t batch) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    // the stride of a dimension of one entry is never used, but has to be valid
+    auto stride = [&](int64_t s, int64_t n) { return (cuuint64_t)(n > 1 ? s * 2 : d * 2); };
+    cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)rows, (cuuint64_t)heads, (cuuint64_t)batch};
+    cuuint64_t strides[3] = {stride(v.token_stride, rows), stride(v.head_stride, heads),
+                             stride(v.batch_stride, batch)};
+    cuuint32_t box[4] = {64, 128, 1, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, v.data, dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+           CUDA_SUCCESS;
+}
+
 bool make_tc_maps(TcMaps* m, const void* pool_k, const void* pool_v, int d, int64_t slots,
                   int64_t units) {
     return encode_view(&m->k, pool_k, d, slots, units, 128) &&

@@ -1,0 +1,197 @@
+// Rows of a cache of keys and values: the accepted path of a drafted tree
+// joins the cache, and complete 64-row blocks get the summaries that
+// sparse_attention.cu selects them by.
+#include "views.cuh"
+#include "sm100_ptx.cuh"
+
+namespace statekv {
+namespace {
+
+// ------------------------------------------------------------ accepted rows
+//   cache[len + i] = new[path[i]], i < count
+// One CTA per (batch entry, KV head); every 16 bytes are read and written
+// once, and all of a thread's loads are independent.  Bound by the launch: 13
+// rows of 512 units are 7 MB in and out.
+constexpr int kAppendThreads = 256;
+
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ statekv_append_args a) {
+    const int n = blockIdx.x / a.kv_heads, h = blockIdx.x - n * a.kv_heads;
+    const int seq = n / a.layers;
+    const int len = cache_length(a.lengths, a.length, seq, a.cache_rows, a.status);
+    int count = a.counts ? a.counts[seq] : a.path_len;
+    if (count < 0 || count > a.path_len || count > a.cache_rows - len) {
+        record_error(a.status, (uint32_t)STATEKV_E_DEVICE, kSiteLength, (uint32_t)count);
+        count = 0;                                           // nothing of this sequence is appended
+    }
+    const int row_units = a.head_dim * (a.dtype == STATEKV_BF16 ? 2 : 4) / 16;
+    const int es = a.dtype == STATEKV_BF16 ? 2 : 4;
+    const int32_t* path = a.path + (int64_t)seq * a.path_stride;
+    for (int i = threadIdx.x; i < 2 * count * row_units; i += kAppendThreads) {
+        const int r = i / row_units, x = i - r * row_units;
+        const bool is_v = r >= count;
+        const int step = is_v ? r - count : r;
+        const int node = path[step];
+        if (node < 0 || node >= a.tokens) {
+            record_error(a.status, (uint32_t)STATEKV_E_DEVICE, kSiteNode, (uint32_t)node);
+            continue;
+        }
+        const statekv_view& s = is_v ? a.v_new : a.k_new;
+        const statekv_view& d = is_v ? a.v_cache : a.k_cache;
+        const char* src = static_cast<const char*>(s.data) +
+                          (n * s.batch_stride + h * s.head_stride + node * s.token_stride) * es;
+        char* dst = static_cast<char*>(d.data) +
+                    (n * d.batch_stride + h * d.head_stride + (int64_t)(len + step) * d.token_stride) * es;
+        reinterpret_cast<uint4*>(dst)[x] = reinterpret_cast<const uint4*>(src)[x];
+    }
+    if (a.new_lengths && h == 0 && n == seq * a.layers && threadIdx.x == 0) a.new_lengths[seq] = len + count;
+}
+
+// ---------------------------------------------------------- block summaries
+// For each complete block of 64 rows:
+//   mean  = fp32(sum of the rows) / 64
+//   scale = max |mean| / 127,  code = round_even(mean * (127 / max |mean|))
+// The codes have to come out the same however the rows are summed (a block's
+// rank among the scores hangs on them), so the sum is exact to well below
+// half an fp32 ulp: two-term accumulation, s + b = fl(s + b) + e with e
+// recovered by Knuth's two-sum, in packed fp32 pairs.  Bound by HBM (each key
+// is read once): one warp per block, 16 bytes per lane and load, the block's
+// loads of a lane all independent.
+constexpr int kSumThreads = 128;
+
+__device__ __forceinline__ float2 neg2(float2 a) { return make_float2(-a.x, -a.y); }
+
+// hi + lo += b
+__device__ __forceinline__ void two_add(float2& hi, float2& lo, float2 b) {
+    const float2 s = ptx::add2(hi, b);
+    const float2 bb = ptx::add2(s, neg2(hi));
+    const float2 ea = ptx::add2(hi, neg2(ptx::add2(s, neg2(bb))));
+    const float2 eb = ptx::add2(b, neg2(bb));
+    lo = ptx::add2(lo, ptx::add2(ea, eb));
+    hi = s;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kSumThreads) summary_kernel(const __grid_constant__ statekv_summary_args a,
+                                                              int window) {
+    constexpr int LPR = D / 8;                               // lanes per row
+    constexpr int RPI = 32 / LPR;                            // rows per load
+    const int lane = threadIdx.x & 31;
+    const int64_t item = (int64_t)blockIdx.x * (kSumThreads / 32) + (threadIdx.x >> 5);
+    const int64_t unit = item / window;
+    if (unit >= (int64_t)a.batch * a.kv_heads) return;
+    const int n = (int)(unit / a.kv_heads), h = (int)(unit - (int64_t)n * a.kv_heads);
+    const int len = cache_length(a.lengths, a.length, n / a.layers, a.cache_rows, a.status);
+    const int first = a.appended < len ? (len - a.appended) / STATEKV_BLOCK : 0;
+    const int b = first + (int)(item - unit * window);
+    if (b >= len / STATEKV_BLOCK) return;
+    const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(a.k_cache.data) + n * a.k_cache.batch_stride +
+                             h * a.k_cache.head_stride +
+                             ((int64_t)b * STATEKV_BLOCK + lane / LPR) * a.k_cache.token_stride +
+                             (lane % LPR) * 8;
+    float2 hi[4], lo[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) hi[j] = lo[j] = make_float2(0.f, 0.f);
+#pragma unroll 8
+    for (int r = 0; r < STATEKV_BLOCK / RPI; ++r) {
+        const uint4 u = *reinterpret_cast<const uint4*>(k + (int64_t)r * RPI * a.k_cache.token_stride);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            two_add(hi[j], lo[j], make_float2(__uint_as_float(w[j] << 16),
+                                              __uint_as_float(w[j] & 0xffff0000u)));
+    }
+#pragma unroll
+    for (int off = LPR; off < 32; off <<= 1)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 oh = make_float2(__shfl_xor_sync(0xffffffffu, hi[j].x, off),
+                                          __shfl_xor_sync(0xffffffffu, hi[j].y, off));
+            const float2 ol = make_float2(__shfl_xor_sync(0xffffffffu, lo[j].x, off),
+                                          __shfl_xor_sync(0xffffffffu, lo[j].y, off));
+            // symmetric in the two lanes, so that both hold the same bits
+            float2 e = make_float2(0.f, 0.f);
+            two_add(hi[j], e, oh);
+            lo[j] = ptx::add2(ptx::add2(lo[j], ol), e);
+        }
+    float m[8], top = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        m[2 * j] = (hi[j].x + lo[j].x) * (1.f / STATEKV_BLOCK);
+        m[2 * j + 1] = (hi[j].y + lo[j].y) * (1.f / STATEKV_BLOCK);
+        top = fmaxf(top, fmaxf(fabsf(m[2 * j]), fabsf(m[2 * j + 1])));
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    const float inv = top > 0.f ? 127.f / top : 0.f;
+    const int64_t out = unit * a.blocks + b;
+    if (lane < LPR) {
+        uint32_t w[2] = {0u, 0u};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int code = (int)fminf(fmaxf(rintf(m[j] * inv), -127.f), 127.f);
+            w[j >> 2] |= (uint32_t)(code & 0xff) << (8 * (j & 3));
+        }
+        *reinterpret_cast<uint2*>(a.codes + out * D + lane * 8) = make_uint2(w[0], w[1]);
+    }
+    if (lane == 0) a.scales[out] = top / 127.f;
+}
+
+}  // namespace
+
+cudaError_t launch_append(const statekv_append_args& a, cudaStream_t st) {
+    append_kernel<<<(unsigned)(a.batch * a.kv_heads), kAppendThreads, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_summary(const statekv_summary_args& a, cudaStream_t st) {
+    // blocks that the appended rows can have completed
+    const int window = a.appended / STATEKV_BLOCK + 1 < a.blocks ? a.appended / STATEKV_BLOCK + 1 : a.blocks;
+    const int64_t items = (int64_t)a.batch * a.kv_heads * window;
+    const int64_t grid = (items + kSumThreads / 32 - 1) / (kSumThreads / 32);
+    if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    if (a.head_dim == 128) summary_kernel<128><<<(unsigned)grid, kSumThreads, 0, st>>>(a, window);
+    else summary_kernel<64><<<(unsigned)grid, kSumThreads, 0, st>>>(a, window);
+    return cudaGetLastError();
+}
+
+}  // namespace statekv
+
+extern "C" int statekv_append_accepted(const statekv_append_args* args, void* cuda_stream) {
+    using namespace statekv;
+    if (!args) return STATEKV_E_INVALID_ARG;
+    const statekv_append_args& a = *args;
+    if (a.dtype != STATEKV_BF16 && a.dtype != STATEKV_F32) return STATEKV_E_INVALID_ARG;
+    const int es = a.dtype == STATEKV_BF16 ? 2 : 4;
+    if (a.batch < 0 || a.layers < 1 || a.batch % a.layers != 0 || a.kv_heads < 1 || a.tokens < 0 ||
+        a.path_len < 0 || a.path_stride < 0 || a.cache_rows < 0 || a.length < 0)
+        return STATEKV_E_INVALID_ARG;
+    if (a.head_dim < 8 || a.head_dim > 512 || a.head_dim * es % 16 != 0) return STATEKV_E_UNSUPPORTED;
+    if ((int64_t)a.batch * a.kv_heads > 0x7fffffffll) return STATEKV_E_UNSUPPORTED;
+    if (!a.status || reinterpret_cast<uintptr_t>(a.status) % 4) return STATEKV_E_INVALID_ARG;
+    if (a.batch == 0) return STATEKV_OK;
+    if (a.path_len > 0 && (!a.path || !view_ok(a.k_new, es) || !view_ok(a.v_new, es))) return STATEKV_E_INVALID_ARG;
+    if (a.cache_rows > 0 && (!view_ok(a.k_cache, es) || !view_ok(a.v_cache, es))) return STATEKV_E_INVALID_ARG;
+    // the sequence's length is read by every head's CTA while one writes the new one
+    if (a.new_lengths && (a.new_lengths == a.lengths || a.new_lengths == a.counts)) return STATEKV_E_INVALID_ARG;
+    if (!a.lengths && !a.counts && (int64_t)a.length + a.path_len > a.cache_rows) return STATEKV_E_CAPACITY;
+    if (launch_append(a, reinterpret_cast<cudaStream_t>(cuda_stream)) != cudaSuccess) return view_cuda_fail();
+    return STATEKV_OK;
+}
+
+extern "C" int statekv_block_summaries(const statekv_summary_args* args, void* cuda_stream) {
+    using namespace statekv;
+    if (!args) return STATEKV_E_INVALID_ARG;
+    const statekv_summary_args& a = *args;
+    if (a.batch < 0 || a.layers < 1 || a.batch % a.layers != 0 || a.kv_heads < 1 || a.blocks < 0 ||
+        a.cache_rows < 0 || a.length < 0 || a.appended < 0)
+        return STATEKV_E_INVALID_ARG;
+    if (a.head_dim != 64 && a.head_dim != 128) return STATEKV_E_UNSUPPORTED;
+    if (!a.status || reinterpret_cast<uintptr_t>(a.status) % 4) return STATEKV_E_INVALID_ARG;
+    if (a.blocks < a.cache_rows / STATEKV_BLOCK) return STATEKV_E_CAPACITY;
+    if (a.batch == 0 || a.cache_rows < STATEKV_BLOCK) return STATEKV_OK;
+    if (!view_ok(a.k_cache, 2) || !a.codes || reinterpret_cast<uintptr_t>(a.codes) % 8 || !a.scales ||
+        reinterpret_cast<uintptr_t>(a.scales) % 4)
+        return STATEKV_E_INVALID_ARG;
+    if (launch_summary(a, reinterpret_cast<cudaStream_t>(cuda_stream)) != cudaSuccess) return view_cuda_fail();
+    return STATEKV_OK;
+}

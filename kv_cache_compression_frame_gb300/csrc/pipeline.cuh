@@ -70,5 +70,10 @@ struct Sync {
 // swizzle row) x box_rows rows; rows past `rows` read as zero.
 bool encode_view(CUtensorMap* m, const void* base, int d, int64_t rows, int64_t units,
                  int box_rows);
+// The same for a strided view [batch][heads][rows][d] (bf16, every stride a
+// multiple of 16 bytes): coordinates (column, row, head, batch), boxes of 64
+// columns x 128 rows.
+bool encode_view4(CUtensorMap* m, const statekv_view& v, int d, int64_t rows, int64_t heads,
+                  int64_t batch);
 
 }  // namespace statekv

@@ -19,6 +19,7 @@ enum ErrSite : uint32_t {
     kSiteQFull = 1, kSiteKvFull, kSiteKvEmpty, kSiteSFull, kSiteSEmpty,
     kSitePFull, kSitePEmpty, kSiteOFull, kSiteDrain, kSiteTmemAddr, kSiteCol,
     kSiteSelect = 32,
+    kSiteLength = 40, kSiteNode,
 };
 
 // ------------------------------------------------------------- launchers
@@ -120,6 +121,12 @@ bool make_decode_maps(DecodeMaps* m, const void* q_rot, int R, int npad, const v
                       const void* det_v, int64_t det_pitch, int64_t units);
 cudaError_t launch_decode(const DecodeArgs& a, const DecodeMaps& m, cudaStream_t st);
 cudaError_t launch_select(const SelectArgs& a, cudaStream_t st);
+
+// Text operators on strided views; the arguments are checked by the entry
+// points of the same files.
+cudaError_t launch_norm_rope(const statekv_norm_rope_args& a, cudaStream_t st);
+cudaError_t launch_append(const statekv_append_args& a, cudaStream_t st);
+cudaError_t launch_summary(const statekv_summary_args& a, cudaStream_t st);
 
 // Query-row tile heights of the two attention paths (the column-sum buffer
 // holds one row of partial sums per tile).

@@ -1,0 +1,877 @@
+// Attention of a tree of drafted tokens over a cache of keys and values
+// (tcgen05, TMA): the verification step of speculative decoding.
+//
+//   o = softmax(scale * q [K_cache[:len]; K_new]^T, masked) [V_cache; V_new]
+//
+// Every drafted token sees the whole cache and, among the drafted ones, the
+// nodes its mask names.  Per (batch entry, KV head) the R = G * tokens query
+// rows share one pass over the cache, so the bound is HBM up to R ~ 256 (at
+// 128 rows a 128-key tile is 64 KB of K and V, 2700 cycles of one SM's share
+// of HBM, against ~1100 of tensor work and 1024 of exponentials).
+//
+// Work: a unit is one (batch entry, KV head, block of query rows); its key
+// tiles are the cache's 128-row tiles and then one tile of drafted keys.  All
+// units' tiles, end to end, are cut into equal contiguous shares, one per CTA
+// (one CTA per SM), so ragged lengths balance by themselves and a CTA starts
+// a new unit only a few times.  The piece of a unit in one CTA's share is a
+// segment; with units in order, segment number = CTA + unit.  A segment that
+// is the whole unit writes the output itself, the others leave (m, l, O) in
+// the workspace and tree_combine_kernel merges them in CTA order (the same
+// bits on every run).
+//
+// Inside a CTA two slots of four softmax warps each take turns: with at most
+// 128 query rows a slot takes every second key tile of the one row tile
+// (SPLIT_ROWS = false), otherwise each slot has its own 128-row tile and all
+// key tiles.  A slot is one S buffer, one O accumulator and one running
+// maximum and sum per row.  Thread = query row (TMEM lane): no reduction
+// across threads.  A "job" is one S = Q K^T, softmax, O += P V of a slot; the
+// issuer runs S two jobs ahead of P V, so one slot's exponentials overlap the
+// other's products.
+// P (bf16 pairs) overwrites its own S buffer: the products of one thread run
+// in issue order, and S of a slot's next job is issued after P V of its last.
+// That order also makes S(next) complete imply P V(last) complete, so a warp
+// that raises its reference may rescale O right away.
+//
+// Precision: S, m, l and O in fp32; P is rounded to bf16 for the product (as
+// the values V are), l sums the unrounded P.  A row's reference is raised
+// only when a tile's maximum passes it by 2^8: P stays below 2^8 and keeps
+// bf16's relative precision.
+//
+// Masked places may hold anything: scores are selected, not added to; V rows
+// past the cache's end are zeroed in shared memory, and non-finite values of
+// drafted V rows too (0 * NaN would reach rows that mask them) and put back
+// at the end for the rows that see them.
+#include <algorithm>
+
+#include "pipeline.cuh"
+#include "views.cuh"
+
+namespace statekv {
+namespace {
+
+constexpr int kTile = 128;                   // keys per tile, query rows per row tile
+constexpr float kSlack = 8.f;                // raise the reference past 2^8
+constexpr int kMinTiles = 2;                 // key tiles per CTA, at least, before more CTAs join
+constexpr int kTreeThreads = 320;
+
+struct TreeKernelArgs {
+    statekv_tree_args a;
+    float* part_o;                           // [segments][d/4][rows][4]
+    float2* part_ml;                         // [segments][rows] (reference, sum)
+    float scale_log2;
+    int32_t G, R, rb, rows;                  // rows: most rows of a unit
+    int32_t grid;                            // CTAs of the main kernel
+};
+
+// The schedule, from the sequences' lengths: where unit u's tiles start.
+struct Plan {
+    int64_t total;                           // tiles of all units
+    int ctas;                                // CTAs that get a share
+    __device__ int64_t start(int c) const { return total * c / ctas; }
+    // the CTA whose share holds tile w
+    __device__ int cta_of(int64_t w) const { return (int)(((w + 1) * ctas - 1) / total); }
+};
+
+__device__ __forceinline__ int seq_tiles(const TreeKernelArgs& k, int s) {
+    return (cache_length(k.a.lengths, k.a.length, s, k.a.cache_rows, k.a.status) + kTile - 1) / kTile + 1;
+}
+
+// Tiles before sequence s and of all sequences, in units of one (layer, head,
+// row block); a whole warp, the same result in every lane.
+__device__ __forceinline__ void sum_tiles(const TreeKernelArgs& k, int s, int64_t& before, int64_t& all) {
+    const int seqs = k.a.batch / k.a.layers;
+    if (!k.a.lengths) {
+        const int t = seq_tiles(k, 0);
+        before = (int64_t)t * s;
+        all = (int64_t)t * seqs;
+        return;
+    }
+    before = all = 0;
+    for (int i = threadIdx.x & 31; i < seqs; i += 32) {
+        const int t = seq_tiles(k, i);
+        all += t;
+        if (i < s) before += t;
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        before += __shfl_xor_sync(0xffffffffu, before, off);
+        all += __shfl_xor_sync(0xffffffffu, all, off);
+    }
+}
+
+__device__ __forceinline__ Plan make_plan(const TreeKernelArgs& k, int64_t seq_sum) {
+    Plan p;
+    p.total = seq_sum * k.a.layers * k.a.kv_heads * k.rb;
+    const int64_t most = (p.total + kMinTiles - 1) / kMinTiles;
+    p.ctas = most < k.grid ? (int)most : k.grid;
+    return p;
+}
+
+// A position in the run of all tiles: sequence s and its cache length, unit u
+// and tile t of the unit.
+struct Cursor {
+    int s, len, nt;
+    int64_t u;
+    int t;
+    __device__ void enter(const TreeKernelArgs& k) {
+        len = cache_length(k.a.lengths, k.a.length, s, k.a.cache_rows, k.a.status);
+        nt = (len + kTile - 1) / kTile + 1;
+    }
+    __device__ void next_unit(const TreeKernelArgs& k) {
+        ++u;
+        t = 0;
+        const int64_t per_seq = (int64_t)k.a.layers * k.a.kv_heads * k.rb;
+        if (u == (s + 1) * per_seq && s + 1 < k.a.batch / k.a.layers) {
+            ++s;
+            enter(k);
+        }
+    }
+};
+
+// The cursor at tile w (a whole warp, the same result in every lane).
+__device__ __forceinline__ Cursor find(const TreeKernelArgs& k, int64_t w) {
+    const int64_t per_seq = (int64_t)k.a.layers * k.a.kv_heads * k.rb;
+    const int seqs = k.a.batch / k.a.layers;
+    Cursor c;
+    c.s = 0;
+    if (!k.a.lengths) {
+        c.enter(k);
+        c.s = (int)(w / (c.nt * per_seq));
+        w -= c.s * (c.nt * per_seq);
+    } else {
+        const int lane = threadIdx.x & 31;
+        int64_t base = 0;
+        for (int s0 = 0; s0 < seqs; s0 += 32) {
+            const int64_t mine = s0 + lane < seqs ? seq_tiles(k, s0 + lane) * per_seq : 0;
+            int64_t upto = mine;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int64_t x = __shfl_up_sync(0xffffffffu, upto, off);
+                if (lane >= off) upto += x;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, base + upto > w);
+            if (hit) {
+                const int l = __ffs((int)hit) - 1;
+                c.s = s0 + l;
+                base += __shfl_sync(0xffffffffu, upto - mine, l);
+                break;
+            }
+            base += __shfl_sync(0xffffffffu, upto, 31);
+        }
+        w -= base;
+        c.enter(k);
+    }
+    const int64_t local = w / c.nt;
+    c.u = c.s * per_seq + local;
+    c.t = (int)(w - local * c.nt);
+    return c;
+}
+
+template <int D, bool SPLIT_ROWS>
+struct TreeLayout {
+    static constexpr int KCH = D / 64;
+    static constexpr int CHUNK = 128 * 128;              // [128 rows][64 bf16], 128B-swizzled
+    static constexpr int TILE = KCH * CHUNK;
+    static constexpr int RT = SPLIT_ROWS ? 2 : 1;        // row tiles
+    // as many stages as fit beside Q
+    static constexpr int KS = D == 64 ? 6 : 3;
+    static constexpr int VS = D == 64 ? 5 : (SPLIT_ROWS ? 2 : 3);
+    static constexpr int LEAD = SPLIT_ROWS ? 1 : 2;      // key tiles that S runs ahead of P V
+    static constexpr int OFF_K = 0;
+    static constexpr int OFF_V = OFF_K + KS * TILE;
+    static constexpr int OFF_Q = OFF_V + VS * TILE;      // [RT] row tiles
+    static constexpr int OFF_BAR = OFF_Q + RT * TILE;
+    static constexpr int B_K_FULL = 0;
+    static constexpr int B_K_EMPTY = B_K_FULL + KS;
+    static constexpr int B_V_FULL = B_K_EMPTY + KS;
+    static constexpr int B_V_EMPTY = B_V_FULL + VS;
+    static constexpr int B_Q_FULL = B_V_EMPTY + VS;      // Q of the segment stored (8 warps)
+    static constexpr int B_S_FULL = B_Q_FULL + 1;        // [2 slots]
+    static constexpr int B_P_FULL = B_S_FULL + 2;        // [2 slots] (4 warps)
+    static constexpr int B_O_FULL = B_P_FULL + 2;        // the segment's products are done
+    static constexpr int B_SYNC = B_O_FULL + 1;          // the 8 softmax warps
+    static constexpr int B_DRAIN = B_SYNC + 1;
+    static constexpr int NBAR = B_DRAIN + 1;
+    static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;  // TMEM address, abort flag, odd nodes [2]
+    static constexpr int SMEM = OFF_MISC + 24 + 1024;
+    static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
+    static_assert(NBAR * 8 % 8 == 0 && OFF_MISC % 8 == 0, "the node mask is 8-byte aligned");
+    static constexpr uint32_t TMEM_COLS = 512, TM_S = 0, TM_O = 256;
+};
+
+// bf16 pairs of a 32-bit word: a mask of the halves that are infinite or NaN
+__device__ __forceinline__ uint32_t odd_halves(uint32_t w) {
+    return ((w & 0x7f80u) == 0x7f80u ? 0xffffu : 0u) | ((w & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u);
+}
+
+template <int D, bool SPLIT_ROWS>
+__global__ void __launch_bounds__(kTreeThreads, 1)
+tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+            const __grid_constant__ CUtensorMap tm_kn, const __grid_constant__ CUtensorMap tm_vn,
+            const __grid_constant__ TreeKernelArgs k) {
+    using L = TreeLayout<D, SPLIT_ROWS>;
+    const statekv_tree_args& a = k.a;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_u32 = ptx::smem_u32(smem_raw);
+    const uint32_t sbase = (raw_u32 + 1023u) & ~1023u;
+    uint8_t* base = smem_raw + (sbase - raw_u32);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    // every warp finds the CTA's share by itself
+    int64_t none, seq_sum;
+    sum_tiles(k, 0, none, seq_sum);
+    const Plan plan = make_plan(k, seq_sum);
+    const int c = (int)blockIdx.x;
+    if (c >= plan.ctas) return;
+    const int64_t w0 = plan.start(c), w1 = plan.start(c + 1);
+    const Cursor first = find(k, w0);
+
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + L::OFF_MISC);
+    volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(base + L::OFF_MISC + 4);
+    unsigned long long* odd_nodes = reinterpret_cast<unsigned long long*>(base + L::OFF_MISC + 8);
+    Sync sy{sbase + (uint32_t)L::OFF_BAR, abort_flag, a.status};
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < L::KS; ++s) {
+            ptx::mbar_init(sy.bar(L::B_K_FULL + s), 1);
+            ptx::mbar_init(sy.bar(L::B_K_EMPTY + s), 1);
+        }
+        for (int s = 0; s < L::VS; ++s) {
+            ptx::mbar_init(sy.bar(L::B_V_FULL + s), 1);
+            ptx::mbar_init(sy.bar(L::B_V_EMPTY + s), 1);
+        }
+        ptx::mbar_init(sy.bar(L::B_Q_FULL), 8);
+        for (int s = 0; s < 2; ++s) {
+            ptx::mbar_init(sy.bar(L::B_S_FULL + s), 1);
+            ptx::mbar_init(sy.bar(L::B_P_FULL + s), 4);
+        }
+        ptx::mbar_init(sy.bar(L::B_O_FULL), 1);
+        ptx::mbar_init(sy.bar(L::B_SYNC), 8);
+        ptx::mbar_init(sy.bar(L::B_DRAIN), 1);
+        *abort_flag = 0u;
+        odd_nodes[0] = odd_nodes[1] = 0ull;
+        ptx::fence_barrier_init();
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(ptx::smem_u32(tmem_slot), L::TMEM_COLS);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    // the merge may be launched now; it waits for this grid to end
+    ptx::dep_trigger();
+    const uint32_t sK = sbase + L::OFF_K, sV = sbase + L::OFF_V, sQ = sbase + L::OFF_Q;
+
+    if (warp == 0) {
+        // ------------------------------------------------------ TMA producer
+        if (lane == 0) {
+            ptx::tma_prefetch_desc(&tm_k);
+            ptx::tma_prefetch_desc(&tm_v);
+            Cursor ck = first, cv = first;
+            const int n_tiles = (int)(w1 - w0);
+            int kt = 0, vt = 0;
+            bool ok = true;
+            auto load = [&](bool is_v) -> bool {
+                Cursor& cu = is_v ? cv : ck;
+                int& cnt = is_v ? vt : kt;
+                const int ns = is_v ? L::VS : L::KS;
+                const int s = cnt % ns, j = cnt / ns;
+                if (!sy.wait((is_v ? L::B_V_EMPTY : L::B_K_EMPTY) + s, (uint32_t)(j & 1) ^ 1u, kSiteKvEmpty))
+                    return false;
+                const uint32_t fb = sy.bar((is_v ? L::B_V_FULL : L::B_K_FULL) + s);
+                ptx::mbar_arrive_expect_tx(fb, L::TILE);
+                const uint32_t dst = (is_v ? sV : sK) + s * L::TILE;
+                const bool drafted = cu.t == cu.nt - 1;
+                const CUtensorMap* map = drafted ? (is_v ? &tm_vn : &tm_kn) : (is_v ? &tm_v : &tm_k);
+                const int64_t nh = cu.u / k.rb;
+                const int n = (int)(nh / a.kv_heads), h = (int)(nh - (int64_t)n * a.kv_heads);
+#pragma unroll
+                for (int kc = 0; kc < L::KCH; ++kc)
+                    ptx::tma_load_4d(dst + kc * L::CHUNK, map, fb, kc * 64, drafted ? 0 : cu.t * kTile, h, n);
+                ++cnt;
+                if (++cu.t == cu.nt) cu.next_unit(k);
+                return true;
+            };
+            for (int t = 0; ok && t < n_tiles && t < L::LEAD; ++t) ok = load(false);
+            for (int t = 0; ok && t < n_tiles; ++t) {
+                ok = load(true);
+                if (ok && t + L::LEAD < n_tiles) ok = load(false);
+            }
+            // never leave a copy in flight into this CTA's shared memory
+            for (int s = 0; s < L::KS && s < kt; ++s)
+                sy.drain(L::B_K_FULL + s, (uint32_t)(((kt - 1 - s) / L::KS) & 1));
+            for (int s = 0; s < L::VS && s < vt; ++s)
+                sy.drain(L::B_V_FULL + s, (uint32_t)(((vt - 1 - s) / L::VS) & 1));
+        }
+    } else if (warp == 1) {
+        // -------------------------------------------------------- MMA issuer
+        constexpr uint32_t idesc_s = ptx::idesc_bf16_f32(128, 128, false, false);
+        constexpr uint32_t idesc_o = ptx::idesc_bf16_f32(128, D, false, true);
+        const uint32_t kmaj_hi = (uint32_t)(ptx::sdesc_sw128(0, 16, 1024) >> 32);
+        const uint32_t v_hi = (uint32_t)(ptx::sdesc_sw128(0, L::CHUNK, 1024) >> 32);
+        const uint32_t kb0 = (uint32_t)ptx::sdesc_sw128(sK, 16, 1024);
+        const uint32_t qb0 = (uint32_t)ptx::sdesc_sw128(sQ, 16, 1024);
+        const uint32_t vb0 = (uint32_t)ptx::sdesc_sw128(sV, L::CHUNK, 1024);
+        Cursor cu = first;
+        int g0 = 0, seg = 0;                             // tiles before this segment, segments done
+        uint32_t p_par[2] = {0, 0};
+        bool ok = true;
+        auto issue_s = [&](int j) -> bool {
+            const int slot = j & 1, g = g0 + (SPLIT_ROWS ? j >> 1 : j), s = g % L::KS;
+            if (!sy.wait(L::B_K_FULL + s, (uint32_t)((g / L::KS) & 1), kSiteKvFull)) return false;
+            ptx::tc_fence_after();
+            if (ptx::elect_one()) {
+                const uint32_t kb = kb0 + (uint32_t)s * (L::TILE >> 4);
+                const uint32_t qb = qb0 + (SPLIT_ROWS ? (uint32_t)slot * (L::TILE >> 4) : 0u);
+#pragma unroll
+                for (int kc = 0; kc < L::KCH; ++kc)
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                        ptx::umma_ss_lh(tmem + L::TM_S + 128u * slot, qb + kc * (L::CHUNK >> 4) + 2 * ks, kmaj_hi,
+                                        kb + kc * (L::CHUNK >> 4) + 2 * ks, kmaj_hi, idesc_s,
+                                        (kc | ks) ? 1u : 0u);
+                ptx::umma_commit(sy.bar(L::B_S_FULL + slot));
+                if (!SPLIT_ROWS || slot == 1) ptx::umma_commit(sy.bar(L::B_K_EMPTY + s));
+            }
+            __syncwarp();
+            return true;
+        };
+        auto issue_pv = [&](int j) -> bool {
+            const int slot = j & 1, g = g0 + (SPLIT_ROWS ? j >> 1 : j), s = g % L::VS;
+            if (!sy.wait(L::B_V_FULL + s, (uint32_t)((g / L::VS) & 1), kSiteKvFull)) return false;
+            if (!sy.wait(L::B_P_FULL + slot, p_par[slot], kSitePFull)) return false;
+            p_par[slot] ^= 1u;
+            ptx::tc_fence_after();
+            if (ptx::elect_one()) {
+                const uint32_t vb = vb0 + (uint32_t)s * (L::TILE >> 4);
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)           // 16 keys per step
+                    ptx::umma_ts_lh(tmem + L::TM_O + 128u * slot, tmem + L::TM_S + 128u * slot + 8u * ks,
+                                    vb + 128u * ks, v_hi, idesc_o, (j > 1 || ks > 0) ? 1u : 0u);
+                if (!SPLIT_ROWS || slot == 1) ptx::umma_commit(sy.bar(L::B_V_EMPTY + s));
+            }
+            __syncwarp();
+            return true;
+        };
+        for (int64_t w = w0; ok && w < w1; ++seg) {
+            const int tiles = (int)min((int64_t)(cu.nt - cu.t), w1 - w);
+            const int jobs = SPLIT_ROWS ? 2 * tiles : tiles;
+            if (!(ok = sy.wait(L::B_Q_FULL, (uint32_t)(seg & 1), kSiteQFull))) break;
+            ptx::tc_fence_after();
+            ok = issue_s(0);
+            if (ok && jobs > 1) ok = issue_s(1);
+            for (int j = 0; ok && j < jobs; ++j) {
+                ok = issue_pv(j);
+                if (ok && j + 2 < jobs) ok = issue_s(j + 2);
+            }
+            if (!ok) break;
+            if (ptx::elect_one()) ptx::umma_commit(sy.bar(L::B_O_FULL));
+            __syncwarp();
+            w += tiles;
+            g0 += tiles;
+            cu.next_unit(k);
+        }
+        if (ptx::elect_one()) ptx::umma_commit(sy.bar(L::B_DRAIN));
+        __syncwarp();
+        sy.drain(L::B_DRAIN, 0);
+    } else {
+        // ------------------------------------------------ softmax / epilogue
+        const int slot = (warp - 2) >> 2, q4 = warp & 3;
+        const int st = (int)threadIdx.x - 64 - 128 * slot;       // thread of the slot
+        const int lrow = q4 * 32 + lane;                         // row of the row tile = TMEM lane
+        const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
+        const uint32_t t_s = tmem + L::TM_S + 128u * slot + lane_base;
+        const uint32_t t_o = tmem + L::TM_O + 128u * slot + lane_base;
+        const float sc = k.scale_log2;
+        Cursor cu = first;
+        int g0 = 0, seg = 0;
+        uint32_t s_par = 0, sync_par = 0;
+        bool ok = true;
+        // barrier of the softmax warps (a bounded mbarrier wait: a warp that
+        // gave up cannot leave the others blocked)
+        auto sync_sm = [&]() -> bool {
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(sy.bar(L::B_SYNC));
+            const bool r = sy.wait(L::B_SYNC, sync_par, kSiteCol);
+            sync_par ^= 1u;
+            return r;
+        };
+        for (int64_t w = w0; ok && w < w1; ++seg) {
+            const int tiles = (int)min((int64_t)(cu.nt - cu.t), w1 - w);
+            const int64_t nh = cu.u / k.rb;
+            const int rblk = (int)(cu.u - nh * k.rb);
+            const int n = (int)(nh / a.kv_heads), h = (int)(nh - (int64_t)n * a.kv_heads);
+            const int row_base = rblk * L::RT * kTile;
+            const int rows = min(L::RT * kTile, k.R - row_base);  // rows of this unit
+            // ---- Q: rows r = g * tokens + j, zeros past the last
+            {
+                constexpr int UPR = D / 8;                       // 16-byte units per row
+                const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q.data) + n * a.q.batch_stride;
+                for (int i = (int)threadIdx.x - 64; i < L::RT * kTile * UPR; i += 256) {
+                    const int r = i / UPR, x = i - r * UPR;
+                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                    if (r < rows) {
+                        const int g = (row_base + r) / a.tokens, j = row_base + r - g * a.tokens;
+                        v = *reinterpret_cast<const uint4*>(q + (int64_t)(h * k.G + g) * a.q.head_stride +
+                                                            j * a.q.token_stride + 8 * x);
+                    }
+                    *reinterpret_cast<uint4*>(base + L::OFF_Q + (r / kTile) * L::TILE + (x >> 3) * L::CHUNK +
+                                              (r % kTile) * 128 + (((x & 7) ^ (r & 7)) << 4)) = v;
+                }
+                ptx::fence_proxy_async_smem();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(sy.bar(L::B_Q_FULL));
+            }
+            // this thread's row of the unit (both slots' threads have the
+            // same row where they share the row tile)
+            const int r = (SPLIT_ROWS ? slot * kTile : 0) + lrow;
+            const bool live = r < rows;
+            const int node = live ? (row_base + r) % a.tokens : 0;
+            uint64_t sees = 0;
+            if (live) sees = a.tree[(int64_t)cu.s * a.tree_stride + node];
+            if (a.tokens < 64) sees &= (1ull << a.tokens) - 1ull;
+            const bool idle = (SPLIT_ROWS ? slot * kTile : 0) + q4 * 32 >= rows;   // no row in this warp
+
+            float m = -INFINITY, l = 0.f;                        // reference (log2 units) and sum
+            const int jobs = SPLIT_ROWS ? tiles : (tiles - slot + 1) / 2;   // of this slot
+            for (int i = 0; ok && i < jobs; ++i) {
+                const int dt = SPLIT_ROWS ? i : 2 * i + slot;    // tile of the segment
+                const int t = cu.t + dt;
+                const bool drafted = t == cu.nt - 1;
+                const int valid = drafted ? a.tokens : min(kTile, cu.len - t * kTile);
+                if (drafted || valid < kTile) {
+                    // V rows whose products with P = 0 must be 0
+                    const int g = g0 + dt, vs = g % L::VS;
+                    if (!(ok = sy.wait(L::B_V_FULL + vs, (uint32_t)((g / L::VS) & 1), kSiteKvFull))) break;
+                    uint8_t* vt = base + L::OFF_V + vs * L::TILE;
+                    constexpr int UPR = D / 8;
+                    if (drafted) {
+                        // (rows past the drafted ones were filled with zeros)
+                        for (int x = st; x < valid * UPR; x += 128) {
+                            const int vr = x / UPR, e = x - vr * UPR;
+                            uint4* p = reinterpret_cast<uint4*>(vt + (e >> 3) * L::CHUNK + vr * 128 +
+                                                                (((e & 7) ^ (vr & 7)) << 4));
+                            uint4 v = *p;
+                            const uint32_t o0 = odd_halves(v.x), o1 = odd_halves(v.y), o2 = odd_halves(v.z),
+                                           o3 = odd_halves(v.w);
+                            if (o0 | o1 | o2 | o3) {
+                                atomicOr(odd_nodes + (seg & 1), 1ull << vr);
+                                __threadfence_block();
+                                *p = make_uint4(v.x & ~o0, v.y & ~o1, v.z & ~o2, v.w & ~o3);
+                            }
+                        }
+                    } else {
+                        for (int x = valid * UPR + st; x < kTile * UPR; x += 128) {
+                            const int vr = x / UPR, e = x - vr * UPR;
+                            *reinterpret_cast<uint4*>(vt + (e >> 3) * L::CHUNK + vr * 128 +
+                                                      (((e & 7) ^ (vr & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                    }
+                    ptx::fence_proxy_async_smem();
+                }
+                if (!(ok = sy.wait(L::B_S_FULL + slot, s_par, kSiteSFull))) break;
+                s_par ^= 1u;
+                __syncwarp();
+                ptx::tc_fence_after();
+                if (!idle) {
+                    // 64 scores at a time stay in registers: the upper half
+                    // is read again after the lower half became P (which
+                    // overwrites columns of the lower half only)
+                    uint32_t x[64];
+                    auto load = [&](int hh) {
+                        ptx::tmem_ld_32x32b_x64(t_s + 64 * hh, x);
+                        ptx::tmem_ld_wait();
+                        if (drafted) {
+                            // node e of the tree is key e; no key past 63
+#pragma unroll
+                            for (int e = 0; e < 64; ++e)
+                                if (hh == 1 || !((sees >> e) & 1ull)) x[e] = 0xff800000u;
+                        } else if (valid < kTile) {
+#pragma unroll
+                            for (int e = 0; e < 64; ++e)
+                                if (64 * hh + e >= valid) x[e] = 0xff800000u;
+                        }
+                    };
+                    float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                    for (int hh = 1; hh >= 0; --hh) {
+                        load(hh);
+#pragma unroll
+                        for (int e = 0; e < 64; e += 4)
+#pragma unroll
+                            for (int b = 0; b < 2; ++b)
+                                mx[b] = ptx::max3(mx[b], __uint_as_float(x[e + 2 * b]),
+                                                  __uint_as_float(x[e + 2 * b + 1]));
+                    }
+                    const float top = fmaxf(mx[0], mx[1]) * sc;
+                    const bool raise = top > m + kSlack;
+                    if (__any_sync(0xffffffffu, raise)) {
+                        const float f = raise ? ptx::ex2_approx(m - top) : 1.f;
+                        if (raise) m = top;
+                        l *= f;
+                        __syncwarp();
+                        // S full: every product into O so far is done
+                        if (i > 0) {
+#pragma unroll
+                            for (int cc = 0; cc < D; cc += 32) {
+                                uint32_t o[32];
+                                ptx::tmem_ld_32x32b_x32(t_o + cc, o);
+                                ptx::tmem_ld_wait();
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                ptx::tmem_st_32x32b_x32(t_o + cc, o);
+                            }
+                            ptx::tmem_st_wait();
+                        }
+                    }
+                    const float nm = m == -INFINITY ? 0.f : -m;
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh) {
+                        if (hh == 1) load(1);
+                        uint32_t p[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const float2 z = ptx::fma2(make_float2(__uint_as_float(x[2 * e]),
+                                                                   __uint_as_float(x[2 * e + 1])),
+                                                       make_float2(sc, sc), make_float2(nm, nm));
+                            const float2 y = make_float2(ptx::ex2_approx(z.x), ptx::ex2_approx(z.y));
+                            sum[e & 1] = ptx::add2(sum[e & 1], y);
+                            p[e] = ptx::pack_bf16x2(y.x, y.y);
+                        }
+                        ptx::tmem_st_32x32b_x32(t_s + 32 * hh, p);
+                    }
+                    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                    ptx::tmem_st_wait();
+                }
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(sy.bar(L::B_P_FULL + slot));
+            }
+            if (!ok) break;
+            // ---- end of the segment
+            if (!(ok = sy.wait(L::B_O_FULL, (uint32_t)(seg & 1), kSiteOFull))) break;
+            ptx::tc_fence_after();
+            // the slots that share a row tile tell each other (m, l) through
+            // Q's memory, which no product reads any more
+            float2* ml = reinterpret_cast<float2*>(base + L::OFF_Q);
+            if (!SPLIT_ROWS) ml[slot * kTile + lrow] = make_float2(m, l);
+            if (!(ok = sync_sm())) break;
+            // the next segment's mask (every read of it was before the last
+            // segment's second sync, every write comes after the next one)
+            if (threadIdx.x == 64) odd_nodes[(seg + 1) & 1] = 0ull;
+            const bool whole = cu.t == 0 && tiles == cu.nt;
+            constexpr int COLS = SPLIT_ROWS ? D : D / 2;         // columns this thread merges
+            const int c0 = SPLIT_ROWS ? 0 : slot * COLS;
+            float f0 = 1.f, f1 = 0.f;
+            bool use1 = false;
+            uint32_t t_o0 = t_o;
+            if (!SPLIT_ROWS) {
+                const float2 x0 = ml[lrow], x1 = ml[kTile + lrow];
+                use1 = tiles > 1;                                // slot 1 had a tile
+                m = fmaxf(x0.x, use1 ? x1.x : -INFINITY);
+                f0 = x0.x == -INFINITY ? 0.f : ptx::ex2_approx(x0.x - m);
+                f1 = !use1 || x1.x == -INFINITY ? 0.f : ptx::ex2_approx(x1.x - m);
+                l = x0.y * f0 + (use1 ? x1.y * f1 : 0.f);
+                t_o0 = tmem + L::TM_O + lane_base + c0;
+            }
+            const uint64_t odd = live ? *reinterpret_cast<volatile unsigned long long*>(odd_nodes + (seg & 1)) & sees : 0ull;
+            const int64_t sgm = (int64_t)c + cu.u;               // segment number
+            const float inv = whole ? (l > 0.f || l != l ? 1.f / l : 0.f) : 1.f;
+            if (!idle) {
+#pragma unroll 1
+                for (int cc = 0; cc < COLS; cc += 32) {
+                    uint32_t o0[32], o1[32];
+                    __syncwarp();
+                    ptx::tmem_ld_32x32b_x32(t_o0 + cc, o0);
+                    if (use1) ptx::tmem_ld_32x32b_x32(t_o0 + 128 + cc, o1);
+                    ptx::tmem_ld_wait();
+                    float v[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        v[e] = __uint_as_float(o0[e]) * f0;
+                        if (use1) v[e] = fmaf(__uint_as_float(o1[e]), f1, v[e]);
+                    }
+                    if (odd != 0ull) {
+                        // infinities and NaN of the drafted rows that this row sees
+                        for (uint64_t b = odd; b; b &= b - 1) {
+                            const __nv_bfloat16* vr = static_cast<const __nv_bfloat16*>(a.v_new.data) +
+                                                      n * a.v_new.batch_stride + h * a.v_new.head_stride +
+                                                      (int64_t)(__ffsll((long long)b) - 1) * a.v_new.token_stride;
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                const float y = __bfloat162float(vr[c0 + cc + e]);
+                                if (!(fabsf(y) < INFINITY)) v[e] += y;
+                            }
+                        }
+                    }
+                    if (live && whole) {
+                        const int gg = (row_base + r) / a.tokens;
+                        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out.data) + n * a.out.batch_stride +
+                                             (int64_t)(h * k.G + gg) * a.out.head_stride +
+                                             (int64_t)node * a.out.token_stride + c0 + cc;
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8)
+                            *reinterpret_cast<uint4*>(out + e) =
+                                make_uint4(ptx::pack_bf16x2(v[e] * inv, v[e + 1] * inv),
+                                           ptx::pack_bf16x2(v[e + 2] * inv, v[e + 3] * inv),
+                                           ptx::pack_bf16x2(v[e + 4] * inv, v[e + 5] * inv),
+                                           ptx::pack_bf16x2(v[e + 6] * inv, v[e + 7] * inv));
+                    } else if (live) {
+                        float4* po = reinterpret_cast<float4*>(k.part_o) +
+                                     (sgm * (D / 4) + (c0 + cc) / 4) * k.rows + r;
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            po[(int64_t)(e / 4) * k.rows] = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                    }
+                }
+                if (live && !whole && c0 == 0) k.part_ml[sgm * k.rows + r] = make_float2(m, l);
+            }
+            ptx::tc_fence_before();
+            // O and Q's memory are read: the next segment may write them
+            if (!(ok = sync_sm())) break;
+            w += tiles;
+            g0 += tiles;
+            cu.next_unit(k);
+        }
+    }
+    __syncthreads();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, L::TMEM_COLS);
+    }
+}
+
+// Merges the segments of a unit that several CTAs shared, in CTA order:
+//   O = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i
+// Thread = 4 columns of a row, consecutive threads consecutive rows (how the
+// partials lie).  kWays threads share one such output, each taking every
+// kWays-th segment: with one layer at 128 k rows a unit has up to 76.
+constexpr int kWays = 8;
+constexpr int kMergeOut = 32;                // outputs per CTA
+
+template <int D>
+__global__ void __launch_bounds__(kWays * kMergeOut) tree_combine_kernel(const __grid_constant__ TreeKernelArgs k) {
+    const statekv_tree_args& a = k.a;
+    const int per_unit = (k.rows * (D / 4) + kMergeOut - 1) / kMergeOut;
+    const int64_t u = blockIdx.x / per_unit;
+    const int part = (int)(blockIdx.x - u * per_unit);
+    const int64_t per_seq = (int64_t)a.layers * a.kv_heads * k.rb;
+    const int s = (int)(u / per_seq);
+    int64_t before, all;
+    sum_tiles(k, s, before, all);
+    const Plan plan = make_plan(k, all);
+    const int nt = seq_tiles(k, s);
+    const int64_t w = before * per_seq + (u - s * per_seq) * nt;
+    const int ca = plan.cta_of(w), cb = plan.cta_of(w + nt - 1);
+    if (ca == cb) return;                    // written by the one CTA
+    const int rblk = (int)(u % k.rb);
+    const int row_tile = k.R > kTile ? 2 * kTile : kTile;
+    const int rows = min(row_tile, k.R - rblk * row_tile);
+    const int out = part * kMergeOut + (threadIdx.x % kMergeOut), way = threadIdx.x / kMergeOut;
+    const int c4 = out / rows, r = out - c4 * rows;
+    const bool live = c4 < D / 4;
+    __shared__ float s_m[kWays][kMergeOut], s_l[kWays][kMergeOut];
+    __shared__ float4 s_o[kWays][kMergeOut];
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    ptx::dep_wait();                         // the segments are written
+    if (live) {
+        const float2* ml = k.part_ml + (ca + u) * k.rows + r;
+        const float4* po = reinterpret_cast<const float4*>(k.part_o) + ((ca + u) * (D / 4) + c4) * k.rows + r;
+        const int n = cb - ca + 1;
+        constexpr int B = 4;
+        for (int i0 = way; i0 < n; i0 += B * kWays) {
+            float2 x[B];
+            float4 y[B];
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                const int i = i0 + b * kWays;
+                x[b] = make_float2(-INFINITY, 0.f);
+                y[b] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i < n) {
+                    x[b] = ml[(int64_t)i * k.rows];
+                    y[b] = po[(int64_t)i * (D / 4) * k.rows];
+                }
+            }
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                const float mn = fmaxf(m, x[b].x);
+                const float f = m == -INFINITY ? 0.f : ptx::ex2_approx(m - mn);
+                const float g = x[b].x == -INFINITY ? 0.f : ptx::ex2_approx(x[b].x - mn);
+                l = l * f + x[b].y * g;
+                o.x = o.x * f + y[b].x * g;
+                o.y = o.y * f + y[b].y * g;
+                o.z = o.z * f + y[b].z * g;
+                o.w = o.w * f + y[b].w * g;
+                m = mn;
+            }
+        }
+    }
+    s_m[way][threadIdx.x % kMergeOut] = m;
+    s_l[way][threadIdx.x % kMergeOut] = l;
+    s_o[way][threadIdx.x % kMergeOut] = o;
+    __syncthreads();
+    if (way != 0 || !live) return;
+    const int x = threadIdx.x;
+    float mm = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kWays; ++i) mm = fmaxf(mm, s_m[i][x]);
+    float ls = 0.f;
+    o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < kWays; ++i) {
+        const float g = s_m[i][x] == -INFINITY ? 0.f : ptx::ex2_approx(s_m[i][x] - mm);
+        ls += s_l[i][x] * g;
+        o.x += s_o[i][x].x * g;
+        o.y += s_o[i][x].y * g;
+        o.z += s_o[i][x].z * g;
+        o.w += s_o[i][x].w * g;
+    }
+    const float inv = ls > 0.f || ls != ls ? 1.f / ls : 0.f;
+    const int64_t nh = u / k.rb;
+    const int n = (int)(nh / a.kv_heads), h = (int)(nh - (int64_t)n * a.kv_heads);
+    const int row = rblk * row_tile + r, gg = row / a.tokens, j = row - gg * a.tokens;
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out.data) + n * a.out.batch_stride +
+                         (int64_t)(h * k.G + gg) * a.out.head_stride + (int64_t)j * a.out.token_stride + c4 * 4;
+    *reinterpret_cast<uint2*>(dst) = make_uint2(ptx::pack_bf16x2(o.x * inv, o.y * inv),
+                                                ptx::pack_bf16x2(o.z * inv, o.w * inv));
+}
+
+struct TreeMaps {
+    CUtensorMap k, v, kn, vn;
+};
+
+template <int D, bool SPLIT_ROWS>
+cudaError_t launch_main(const TreeKernelArgs& k, const TreeMaps& m, cudaStream_t st) {
+    using L = TreeLayout<D, SPLIT_ROWS>;
+    cudaError_t e = cudaFuncSetAttribute(tree_kernel<D, SPLIT_ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         L::SMEM);
+    if (e != cudaSuccess) return e;
+    tree_kernel<D, SPLIT_ROWS><<<(unsigned)k.grid, kTreeThreads, L::SMEM, st>>>(m.k, m.v, m.kn, m.vn, k);
+    return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_combine(const TreeKernelArgs& k, int64_t units, cudaStream_t st) {
+    const int64_t per_unit = (k.rows * (D / 4) + kMergeOut - 1) / kMergeOut;
+    if (units * per_unit > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(units * per_unit));
+    cfg.blockDim = dim3(kWays * kMergeOut);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, tree_combine_kernel<D>, k);
+}
+
+// Sizes that follow from the arguments; false where they are refused.
+struct TreeSizes {
+    int G, R, rb, rows;
+    int64_t units;
+};
+int tree_sizes(int batch, int q_heads, int kv_heads, int tokens, int head_dim, TreeSizes* z) {
+    if (batch < 0 || kv_heads < 1 || q_heads < kv_heads || q_heads % kv_heads != 0 || tokens < 1)
+        return STATEKV_E_INVALID_ARG;
+    if (tokens > 64 || (head_dim != 64 && head_dim != 128) || q_heads / kv_heads > 64) return STATEKV_E_UNSUPPORTED;
+    z->G = q_heads / kv_heads;
+    z->R = z->G * tokens;
+    const int row_tile = z->R > kTile ? 2 * kTile : kTile;
+    z->rb = (z->R + row_tile - 1) / row_tile;
+    z->rows = std::min(z->R, row_tile);
+    z->units = (int64_t)batch * kv_heads * z->rb;
+    return z->units > 0x7fffffff / 1024 ? STATEKV_E_UNSUPPORTED : STATEKV_OK;
+}
+
+bool device_sms(int* sms) {
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess &&
+           cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess;
+}
+
+int64_t workspace_for(const TreeSizes& z, int sms, int d) {
+    // one segment per CTA and per unit; O, then (m, l)
+    return ((int64_t)sms + z.units) * z.rows * (d * 4 + 8);
+}
+
+// A dimension of several entries that share their memory has no TMA view.
+bool spread(const statekv_view& v, int64_t batch, int64_t heads, int64_t rows) {
+    return (batch < 2 || v.batch_stride > 0) && (heads < 2 || v.head_stride > 0) && (rows < 2 || v.token_stride > 0);
+}
+
+}  // namespace
+}  // namespace statekv
+
+extern "C" int64_t statekv_tree_attention_workspace(int32_t batch, int32_t q_heads, int32_t kv_heads,
+                                                    int32_t tokens, int32_t head_dim) {
+    using namespace statekv;
+    TreeSizes z;
+    if (tree_sizes(batch, q_heads, kv_heads, tokens, head_dim, &z) != STATEKV_OK) return -1;
+    int sms = 0;
+    if (!device_sms(&sms)) {
+        cudaGetLastError();
+        return -1;
+    }
+    return workspace_for(z, sms, head_dim);
+}
+
+extern "C" int statekv_tree_attention(const statekv_tree_args* args, void* cuda_stream) {
+    using namespace statekv;
+    if (!args) return STATEKV_E_INVALID_ARG;
+    const statekv_tree_args& a = *args;
+    if (a.layers < 1 || a.batch < 0 || a.batch % a.layers != 0 || a.cache_rows < 0 || a.length < 0 ||
+        a.tree_stride < 0 || !(a.scale > 0.0) || !(a.scale < 1e30))
+        return STATEKV_E_INVALID_ARG;
+    TreeSizes z;
+    int r = tree_sizes(a.batch, a.q_heads, a.kv_heads, a.tokens, a.head_dim, &z);
+    if (r != STATEKV_OK) return r;
+    if (!a.status || reinterpret_cast<uintptr_t>(a.status) % 4) return STATEKV_E_INVALID_ARG;
+    if (!a.lengths && a.length > a.cache_rows) return STATEKV_E_CAPACITY;
+    if (a.batch == 0) return STATEKV_OK;
+    if (!a.tree || reinterpret_cast<uintptr_t>(a.tree) % 8 || !view_ok(a.q, 2) || !view_ok(a.out, 2) ||
+        !view_ok(a.k_new, 2) || !view_ok(a.v_new, 2))
+        return STATEKV_E_INVALID_ARG;
+    // an empty cache needs no memory: its maps are never read
+    const bool cached = a.cache_rows > 0;
+    if (cached && (!view_ok(a.k_cache, 2) || !view_ok(a.v_cache, 2))) return STATEKV_E_INVALID_ARG;
+    if (!spread(a.k_new, a.batch, a.kv_heads, a.tokens) || !spread(a.v_new, a.batch, a.kv_heads, a.tokens) ||
+        (cached && (!spread(a.k_cache, a.batch, a.kv_heads, a.cache_rows) ||
+                    !spread(a.v_cache, a.batch, a.kv_heads, a.cache_rows))))
+        return STATEKV_E_INVALID_ARG;
+    int sms = 0;
+    if (!device_sms(&sms)) return view_cuda_fail();
+    if (!aligned16(a.workspace) || a.workspace_bytes < workspace_for(z, sms, a.head_dim))
+        return STATEKV_E_INVALID_ARG;
+    TreeMaps m;
+    if (!encode_view4(&m.kn, a.k_new, a.head_dim, a.tokens, a.kv_heads, a.batch) ||
+        !encode_view4(&m.vn, a.v_new, a.head_dim, a.tokens, a.kv_heads, a.batch))
+        return STATEKV_E_UNSUPPORTED;
+    m.k = m.kn;
+    m.v = m.vn;
+    if (cached && (!encode_view4(&m.k, a.k_cache, a.head_dim, a.cache_rows, a.kv_heads, a.batch) ||
+                   !encode_view4(&m.v, a.v_cache, a.head_dim, a.cache_rows, a.kv_heads, a.batch)))
+        return STATEKV_E_UNSUPPORTED;
+    TreeKernelArgs k{};
+    k.a = a;
+    k.G = z.G; k.R = z.R; k.rb = z.rb; k.rows = z.rows;
+    k.scale_log2 = (float)(a.scale * 1.4426950408889634074);
+    // no more CTAs than the longest cache could use
+    const int64_t most = z.units * (((int64_t)(a.lengths ? a.cache_rows : a.length) + kTile - 1) / kTile + 1);
+    k.grid = (int)std::min<int64_t>(sms, (most + kMinTiles - 1) / kMinTiles);
+    const int64_t segments = (int64_t)sms + z.units;
+    k.part_o = static_cast<float*>(a.workspace);
+    k.part_ml = reinterpret_cast<float2*>(k.part_o + segments * z.rows * a.head_dim);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(cuda_stream);
+    const bool two = z.R > kTile;
+    cudaError_t e = a.head_dim == 128 ? (two ? launch_main<128, true>(k, m, st) : launch_main<128, false>(k, m, st))
+                                      : (two ? launch_main<64, true>(k, m, st) : launch_main<64, false>(k, m, st));
+    // one CTA holds whole units only
+    if (e == cudaSuccess && k.grid > 1)
+        e = a.head_dim == 128 ? launch_combine<128>(k, z.units, st) : launch_combine<64>(k, z.units, st);
+    return e == cudaSuccess ? STATEKV_OK : view_cuda_fail();
+}

@@ -1,0 +1,44 @@
+// Pieces shared by the handle-free text operators (norm_rope.cu,
+// cache_rows.cu, tree_attention.cu, sparse_attention.cu): checks of strided
+// views and the lookup of a sequence's cache length.
+#pragma once
+
+#include "statekv_internal.cuh"
+
+namespace statekv {
+
+// A failed CUDA call: clear the runtime's last-error state (a refused launch,
+// for instance, would otherwise be reported again by the next call that
+// checks it, in this library or the caller's code) and report E_CUDA.
+inline int view_cuda_fail() {
+    cudaGetLastError();
+    return STATEKV_E_CUDA;
+}
+
+inline bool aligned16(const void* p) { return p && reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+// Every row of the view starts on a 16-byte boundary (what 16-byte loads and
+// TMA need), and no stride is negative.
+inline bool view_ok(const statekv_view& v, int esize) {
+    if (!aligned16(v.data)) return false;
+    for (int64_t s : {v.batch_stride, v.head_stride, v.token_stride})
+        if (s < 0 || (s * esize) % 16 != 0) return false;
+    return true;
+}
+
+#ifdef __CUDACC__
+// Rows of sequence s, from the array or the common value.  A negative length
+// or one past `most` is recorded and clamped, so that every access that
+// follows from it stays in bounds.
+__device__ __forceinline__ int cache_length(const int32_t* lengths, int32_t length, int s, int most,
+                                            uint32_t* err) {
+    int n = lengths ? lengths[s] : length;
+    if (n < 0 || n > most) {
+        record_error(err, (uint32_t)STATEKV_E_DEVICE, kSiteLength, (uint32_t)n);
+        n = n < 0 ? 0 : most;
+    }
+    return n;
+}
+#endif
+
+}  // namespace statekv

@@ -1,0 +1,647 @@
+"""The text operators against their definitions in 64 bits: per-head norm with
+rotation, attention of drafted trees, the accepted path's append, block
+summaries, and a chain of them.
+
+Tolerances, all derived beforehand.
+ * Stored values: half a step of the storage type, 2^-8 |x| (bf16) or 2^-24
+   |x| (fp32).
+ * norm_rope adds the fp32 arithmetic: a result is a sum of two products of
+   norm factor (rsqrtf, two ulp), weight and cosine (two ulp, angle rounded to
+   2^-24 half turns): below 2^-20 of the pair's magnitude |y_k| + |y_k+h|.
+ * Attention with P rounded to bf16: each term p v is off by at most 2^-8 of
+   itself, so the output by 2^-8 A with A = sum p |v| / sum p.  Scores are sums
+   of 128 exact products in fp32, each step at worst 2^-23 of sum |q k| scale
+   (about 7 here): 1.1e-4 on the exponent, twice that on a quotient: 2^-12 A.
+"""
+
+import math
+
+import pytest
+import torch
+
+import kv_cache_compression_frame_gb300 as kv
+from kv_cache_compression_frame_gb300 import _native as N
+
+gpu = pytest.mark.gpu
+DEV = "cuda"
+BF16 = torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from kv_cache_compression_frame_gb300 import build_lib
+    build_lib.build()
+
+
+def gen(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return g
+
+
+def randn(g, *shape, dtype=BF16):
+    return torch.randn(shape, generator=g, device=DEV).to(dtype)
+
+
+def within(got, ref, tol, what=""):
+    got = got.double()
+    bad = ~((got - ref).abs() <= tol)
+    bad &= ~(got.isnan() & ref.isnan()) & ~((got == ref) & ref.isinf())
+    assert not bad.any(), (f"{what}: {int(bad.sum())} of {bad.numel()} values off, worst "
+                           f"{float((got - ref).abs()[bad].max()):.3g}")
+
+
+# ---------------------------------------------------------------- norm_rope
+def ref_norm_rope(x, pos, omega, w, eps):
+    """x [n][H][t][d], pos [n][t]: the result and each pair's magnitude."""
+    x = x.double()
+    h = x.shape[-1] // 2
+    if w is not None:
+        x = x / (x.pow(2).mean(-1, keepdim=True) + eps).sqrt() * w.double()
+    a, b = x[..., :h], x[..., h:]
+    ang = pos.double()[:, None, :, None] * omega
+    c, s = ang.cos(), ang.sin()
+    return torch.cat([a * c - b * s, b * c + a * s], -1), (a.abs() + b.abs()).repeat(1, 1, 1, 2)
+
+
+def half_step(dtype):
+    return torch.finfo(dtype).eps / 2
+
+
+def omega_of(d, theta=1e6):
+    return theta ** (-2.0 * torch.arange(d // 2, dtype=torch.float64, device=DEV) / d)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, torch.float32])
+@pytest.mark.parametrize("n,hq,hkv,t,d", [(1, 16, 8, 1, 128), (1, 14, 2, 3, 64), (3, 5, 1, 33, 128),
+                                          (4, 12, 2, 256, 128), (2, 1, 1, 7, 64)])
+def test_norm_rope_projection_layout(dtype, n, hq, hkv, t, d):
+    """Heads of q, k and v side by side, tokens outermost; far positions."""
+    g = gen(n * 100 + t)
+    qkv = 3 * randn(g, n, t, hq + 2 * hkv, d, dtype=dtype)
+    q, k, v = (x.transpose(1, 2) for x in qkv.split([hq, hkv, hkv], 2))
+    qw, kw = (1 + randn(g, d, dtype=dtype) / 4 for _ in range(2))
+    pos = torch.randint(0, 1 << 20, (n, t), generator=g, device=DEV).to(torch.int32)
+    omega = omega_of(d)
+    qo, ko, vo = kv.qk_norm_rope(q, k, pos, omega, qw, kw, v=v, eps=1e-5)
+    for got, x, w in ((qo, q, qw), (ko, k, kw)):
+        ref, mag = ref_norm_rope(x, pos, omega, w, 1e-5)
+        within(got, ref, half_step(dtype) * ref.abs() + 2.0 ** -20 * mag)
+    assert torch.equal(vo, v)
+    kv.check_status()
+
+
+@gpu
+def test_norm_rope_positions_weights_and_zero_rows():
+    g = gen(5)
+    q, k = randn(g, 2, 4, 9, 64), randn(g, 2, 2, 9, 64)
+    q[0, 1, 3] = 0                                   # a zero row stays zero
+    w = 1 + randn(g, 64, dtype=torch.float32) / 4    # fp32 weights with bf16 tensors
+    omega = omega_of(64)
+    for first in (0, -3, 131072, (1 << 31) - 20):
+        pos = first + torch.arange(9, device=DEV)
+        got = {"int": kv.qk_norm_rope(q, k, first, omega, w, None)}
+        got["row"] = kv.qk_norm_rope(q, k, pos.to(torch.int32), omega, w, None)
+        got["rows"] = kv.qk_norm_rope(q, k, pos.to(torch.int32).expand(2, 9).contiguous(), omega, w, None)
+        for qo, ko in got.values():
+            # fp64 p * omega itself is off by 2^-53 p
+            far = 2.0 ** -52 * (abs(first) + 9)
+            ref, mag = ref_norm_rope(q, pos.expand(2, 9), omega, w, 1e-6)
+            within(qo, ref, 2.0 ** -8 * ref.abs() + (2.0 ** -20 + far) * mag, f"q at {first}")
+            ref, mag = ref_norm_rope(k, pos.expand(2, 9), omega, None, 0)   # no norm: rotation alone
+            within(ko, ref, 2.0 ** -8 * ref.abs() + (2.0 ** -20 + far) * mag, f"k at {first}")
+            assert torch.equal(qo[0, 1, 3], torch.zeros_like(qo[0, 1, 3]))
+
+
+@gpu
+def test_norm_rope_into_a_cache_and_in_place():
+    """K and V land at each sequence's rows; every other row stays as it was."""
+    g = gen(6)
+    seqs, layers, t, d = 3, 2, 5, 128
+    n = seqs * layers
+    q, k, v = randn(g, n, 4, t, d), randn(g, n, 2, t, d), randn(g, n, 2, t, d)
+    kc, vc = randn(g, n, 2, 40, d), randn(g, n, 2, 40, d)
+    kc0, vc0 = kc.clone(), vc.clone()
+    rows = torch.tensor([0, 35, 17], dtype=torch.int32, device=DEV)
+    pos = (rows[:, None] + torch.arange(t, device=DEV)).to(torch.int32)
+    w = 1 + randn(g, d) / 4
+    q0 = q.clone()
+    ref, mag = ref_norm_rope(k, pos.repeat_interleave(layers, 0), omega_of(d), w, 1e-6)
+    out = kv.qk_norm_rope(q, k, pos, omega_of(d), w, w, v=v, q_out=q, k_out=kc, v_out=vc, out_rows=rows)
+    assert out[0] is q and out[1] is kc
+    for i in range(n):
+        r = int(rows[i // layers])
+        within(kc[i, :, r:r + t], ref[i], 2.0 ** -8 * ref[i].abs() + 2.0 ** -20 * mag[i])
+        assert torch.equal(vc[i, :, r:r + t], v[i])
+        kc[i, :, r:r + t], vc[i, :, r:r + t] = kc0[i, :, r:r + t], vc0[i, :, r:r + t]
+    assert torch.equal(kc, kc0) and torch.equal(vc, vc0)
+    ref, mag = ref_norm_rope(q0, pos.repeat_interleave(layers, 0), omega_of(d), w, 1e-6)
+    within(q, ref, 2.0 ** -8 * ref.abs() + 2.0 ** -20 * mag)
+    kv.check_status()
+    # rows that do not fit: recorded, and nothing of that sequence is stored
+    kv.qk_norm_rope(q, k, pos, omega_of(d), w, w, v=v, k_out=kc, v_out=vc,
+                    out_rows=torch.tensor([36, -1, 40], dtype=torch.int32, device=DEV))
+    with pytest.raises(kv.StateKVError) as e:
+        kv.check_status()
+    assert e.value.status == N.E_DEVICE
+    assert torch.equal(kc, kc0) and torch.equal(vc, vc0)
+    kv.check_status()                                # cleared
+
+
+# --------------------------------------------------------------------- tree
+def seen(tree, tok):
+    """int64 masks [..., tok] -> bool [..., tok, tok]"""
+    return ((tree[..., None] >> torch.arange(tok, device=tree.device)) & 1).bool()
+
+
+def ref_attend(q, k, v, mask, scale):
+    """One unit: q [r][d], k, v [m][d], mask [r][m] -> output and A.  A key that
+    is masked contributes nothing whatever it holds."""
+    x = (q.double() @ k.double().T) * scale
+    x = torch.where(mask, x, -math.inf)
+    top = x.amax(-1, keepdim=True)
+    p = torch.where(mask, torch.exp(x - torch.where(top == -math.inf, 0.0, top)), 0.0)
+    den = p.sum(-1, keepdim=True)
+    den = torch.where(mask.any(-1, keepdim=True), den, 1.0)
+    v = v.double()
+    if not bool(v.isfinite().all()):
+        o = torch.zeros(q.shape, dtype=torch.float64, device=q.device)
+        for r in range(q.shape[0]):
+            o[r] = (p[r, mask[r], None] * v[mask[r]]).sum(0) / den[r]
+        return o, o.nan_to_num(0, 0, 0).abs() + 8
+    return p @ v / den, p @ v.abs() / den
+
+
+def check_tree(q, kn, vn, tree, kc, vc, lengths, scale, got, what=""):
+    n, hq, tok, d = q.shape
+    hkv = kc.shape[1]
+    G = hq // hkv
+    for i in range(n):
+        rows = lengths if isinstance(lengths, int) else int(lengths[i * len(lengths) // n])
+        mask = seen(tree if tree.dim() == 1 else tree[i * tree.shape[0] // n], tok)
+        mask = torch.cat([torch.ones(tok, rows, dtype=torch.bool, device=DEV), mask], 1).repeat(G, 1)
+        for h in range(hkv):
+            ref, a = ref_attend(q[i, h * G:(h + 1) * G].reshape(-1, d), torch.cat([kc[i, h, :rows], kn[i, h]]),
+                                torch.cat([vc[i, h, :rows], vn[i, h]]), mask, scale)
+            within(got[i, h * G:(h + 1) * G].reshape(-1, d), ref,
+                   2.0 ** -8 * ref.abs() + (2.0 ** -8 + 2.0 ** -12) * a, f"{what} entry {i} head {h}")
+
+
+def random_tree(tok, seqs, seed):
+    import random
+    r = random.Random(seed)
+    return kv.tree_masks([[-1] + [r.randrange(max(0, i - 4), i) for i in range(1, tok)] for _ in range(seqs)],
+                         DEV)[0]
+
+
+def tree_inputs(seed, n, hq, hkv, tok, d, cap):
+    g = gen(seed)
+    return (randn(g, n, hq, tok, d), randn(g, n, hkv, tok, d), randn(g, n, hkv, tok, d),
+            randn(g, n, hkv, cap, d), randn(g, n, hkv, cap, d))
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hkv,tok,rows", [
+    (1, 1, 1, 0), (1, 1, 1, 1), (4, 2, 3, 127), (4, 2, 5, 128), (14, 2, 7, 129), (14, 2, 7, 300),
+    (12, 2, 16, 2000),           # 96 rows
+    (2, 1, 64, 700),             # 128 rows: the last size of one row tile
+    (3, 1, 43, 513),             # 129 rows: two tiles, one live row in the second
+    (12, 2, 42, 5000),           # 252 rows
+    (4, 1, 64, 256),             # 256 rows
+    (8, 1, 33, 400),             # 264 rows: two row blocks
+    (16, 1, 64, 1000),           # 1024 rows: four
+])
+def test_tree_sizes(d, hq, hkv, tok, rows):
+    x = tree_inputs(rows * 7 + tok, 2, hq, hkv, tok, d, rows + 3)
+    tree = random_tree(tok, 2, rows)
+    scale = 1 / math.sqrt(d)
+    got = kv.tree_attention(*x[:3], tree, *x[3:], rows, scale=scale)
+    check_tree(*x[:3], tree, *x[3:], rows, scale, got)
+    kv.check_status()
+
+
+@gpu
+@pytest.mark.parametrize("layers", [1, 3])
+def test_tree_ragged_lengths(layers):
+    lens = [0, 1, 900, 128, 4097, 64, 255]
+    n = len(lens) * layers
+    x = tree_inputs(3, n, 4, 2, 9, 128, 4100)
+    tree = random_tree(9, len(lens), 1)
+    lengths = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    got = kv.tree_attention(*x[:3], tree, *x[3:], lengths, scale=0.09)
+    check_tree(*x[:3], tree, *x[3:], lengths, 0.09, got)
+    kv.check_status()
+    again = kv.tree_attention(*x[:3], tree, *x[3:], lengths, scale=0.09)
+    assert torch.equal(got, again)
+
+
+@gpu
+def test_tree_many_sequences():
+    """More sequences than a warp's lanes, more units than SMs."""
+    n = 70
+    lengths = torch.randint(0, 600, (n,), generator=gen(1), device=DEV).to(torch.int32)
+    x = tree_inputs(4, n, 6, 3, 4, 64, 600)
+    tree = random_tree(4, n, 1)
+    got = kv.tree_attention(*x[:3], tree, *x[3:], lengths, scale=0.125)
+    check_tree(*x[:3], tree, *x[3:], lengths, 0.125, got)
+
+
+@gpu
+@pytest.mark.parametrize("tok,hq", [(6, 4), (40, 8)])
+def test_tree_masked_places_may_hold_anything(tok, hq):
+    """Stale rows past the length, masked nodes and rows that see nothing."""
+    rows = 200
+    q, kn, vn, kc, vc = tree_inputs(8, 2, hq, 2, tok, 128, rows + 60)
+    for c in (kc, vc):
+        c[:, :, rows:] = float("nan")
+        c[0, :, rows + 1] = float("inf")
+    tree = random_tree(tok, 2, 3)
+    tree[:, 4] = 0                                    # sees no node, only the cache
+    # node 2 is seen by itself alone; its key and value are not numbers
+    tree &= ~(1 << 2)
+    tree[:, 2] |= 1 << 2
+    kn[:, :, 2] = float("nan")
+    vn[:, 0, 2, 5] = float("inf")
+    vn[:, 1, 2] = float("nan")
+    # a value of a node that others see too
+    vn[1, 0, 1, 7] = -float("inf")
+    tree[:, 3] |= 1 << 1
+    got = kv.tree_attention(q, kn, vn, tree, kc, vc, rows, scale=0.1)
+    G = hq // 2
+    out = got.view(2, 2, G, tok, 128)
+    assert out[:, :, :, 2].isnan().all()
+    mask = seen(tree, tok)
+    for i in range(2):
+        for j in range(tok):
+            if j == 2:
+                continue
+            o = out[i, :, :, j].clone()
+            if i == 1 and mask[1, j, 1]:
+                assert (o[0, :, 7] == -math.inf).all()
+                o[0, :, 7] = 0
+            assert o.isfinite().all(), (i, j)
+    # the finite rows against the definition
+    keep = [j for j in range(tok) if j != 2]
+    vn2 = vn.nan_to_num(0, 0, 0)
+    vn2[1, 0, 1, 7] = 0
+    kn2 = kn.nan_to_num(0)
+    # rows that see node 2 are left out, so its key and value do not matter
+    ref = torch.zeros_like(out).double()
+    a = torch.zeros_like(ref)
+    for i in range(2):
+        for h in range(2):
+            m = torch.cat([torch.ones(tok, rows, dtype=torch.bool, device=DEV), mask[i]], 1).repeat(G, 1)
+            r, aa = ref_attend(q[i, h * G:(h + 1) * G].reshape(-1, 128), torch.cat([kc[i, h, :rows], kn2[i, h]]),
+                               torch.cat([vc[i, h, :rows], vn2[i, h]]), m, 0.1)
+            ref[i, h], a[i, h] = r.view(G, tok, 128), aa.view(G, tok, 128)
+    o = out.clone()
+    o[1, 0, ..., 7] = ref[1, 0, ..., 7].to(BF16)
+    within(o[:, :, :, keep], ref[:, :, :, keep], (2.0 ** -8 * ref.abs() + (2.0 ** -8 + 2.0 ** -12) * a)[:, :, :, keep])
+    # nothing at all to see: zeros
+    tree = torch.zeros(tok, dtype=torch.int64, device=DEV)
+    got = kv.tree_attention(q, kn, vn, tree, kc, vc, 0, scale=0.1)
+    assert torch.equal(got, torch.zeros_like(got))
+    kv.check_status()
+
+
+@gpu
+def test_tree_large_scores_and_order():
+    """Rising maxima (the reference is raised many times) and a huge common part."""
+    tok, rows, d = 5, 1500, 64
+    q, kn, vn, kc, vc = tree_inputs(9, 1, 4, 2, tok, d, rows)
+    ramp = torch.linspace(0.1, 12, rows, device=DEV)[None, None, :, None]
+    for order in (1, -1):
+        k = (kc.float() * (ramp if order == 1 else ramp.flip(2))).to(BF16)
+        tree = random_tree(tok, 1, 2)
+        got = kv.tree_attention(q, kn, vn, tree, k, vc, rows, scale=0.2)
+        # scores reach 12 * 7 * 1.6 of the derivation's 7: 2^-12 grows with them
+        for h in range(2):
+            m = torch.cat([torch.ones(tok, rows, dtype=torch.bool, device=DEV), seen(tree[0], tok)], 1).repeat(2, 1)
+            ref, a = ref_attend(q[0, 2 * h:2 * h + 2].reshape(-1, d), torch.cat([k[0, h], kn[0, h]]),
+                                torch.cat([vc[0, h], vn[0, h]]), m, 0.2)
+            within(got[0, 2 * h:2 * h + 2].reshape(-1, d), ref,
+                   2.0 ** -8 * ref.abs() + (2.0 ** -8 + 20 * 2.0 ** -12) * a, f"order {order}")
+
+
+@gpu
+def test_tree_views_workspace_stream_and_shared_tree():
+    """Token-major caches and queries, one tree for all, own workspace, another stream."""
+    g = gen(11)
+    n, hq, hkv, tok, d, rows = 2, 6, 3, 8, 128, 333
+    q = randn(g, n, tok, hq + 2 * hkv, d).transpose(1, 2)
+    q, kn, vn = q.split([hq, hkv, hkv], 1)
+    pool = randn(g, n, rows, 2, hkv, d)
+    kc, vc = pool[:, :, 0].transpose(1, 2), pool[:, :, 1].transpose(1, 2)
+    tree = random_tree(tok, 1, 5)[0]
+    ws = torch.full((kv.tree_attention_workspace(n, hq, hkv, tok, d),), 255, dtype=torch.uint8, device=DEV)
+    out = torch.zeros(n, tok, hq, d, dtype=BF16, device=DEV).transpose(1, 2)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = kv.tree_attention(q, kn, vn, tree, kc, vc, rows - 2, scale=0.1, out=out, workspace=ws, stream=s)
+    s.synchronize()
+    assert got is out
+    check_tree(q, kn, vn, tree, kc, vc, rows - 2, 0.1, got)
+    assert torch.equal(got, kv.tree_attention(q.contiguous(), kn.contiguous(), vn.contiguous(), tree,
+                                              kc.contiguous(), vc.contiguous(), rows - 2, scale=0.1))
+
+
+@gpu
+def test_tree_lengths_out_of_range_are_recorded():
+    x = tree_inputs(12, 2, 2, 1, 3, 64, 50)
+    tree = random_tree(3, 1, 1)[0]
+    lengths = torch.tensor([51, -1], dtype=torch.int32, device=DEV)
+    kv.check_status()
+    got = kv.tree_attention(*x[:3], tree, *x[3:], lengths, scale=0.1)
+    with pytest.raises(kv.StateKVError) as e:
+        kv.check_status()
+    assert e.value.status == N.E_DEVICE
+    # clamped
+    check_tree(*x[:3], tree, *x[3:], torch.tensor([50, 0]), 0.1, got)
+
+
+# ------------------------------------------------------------------- append
+@gpu
+@pytest.mark.parametrize("dtype,d", [(BF16, 128), (BF16, 64), (torch.float32, 64)])
+@pytest.mark.parametrize("layers", [1, 2])
+def test_append_accepted(dtype, d, layers):
+    g = gen(21)
+    seqs, hkv, tok, cap = 4, 3, 11, 60
+    n = seqs * layers
+    kn, vn = randn(g, n, tok, 2, hkv, d, dtype=dtype).unbind(2)   # token-major drafts
+    kn, vn = kn.transpose(1, 2), vn.transpose(1, 2)
+    kc, vc = randn(g, n, hkv, cap, d, dtype=dtype), randn(g, n, hkv, cap, d, dtype=dtype)
+    k0, v0 = kc.clone(), vc.clone()
+    path = torch.tensor([[0, 2, 5, 10], [0, 1, 2, 3], [0, 9, 10, 10], [10, 0, 3, 3]], dtype=torch.int32, device=DEV)
+    counts = torch.tensor([4, 1, 0, 3], dtype=torch.int32, device=DEV)
+    lengths = torch.tensor([0, 59, 60, 7], dtype=torch.int32, device=DEV)
+    new = kv.append_accepted(kn, vn, path, counts, kc, vc, lengths)
+    assert new.tolist() == [4, 60, 60, 10]
+    for i in range(n):
+        s = i // layers
+        for j in range(int(counts[s])):
+            k0[i, :, int(lengths[s]) + j] = kn[i, :, int(path[s, j])]
+            v0[i, :, int(lengths[s]) + j] = vn[i, :, int(path[s, j])]
+    assert torch.equal(kc, k0) and torch.equal(vc, v0)
+    kv.check_status()
+    # one path for all, common length
+    assert kv.append_accepted(kn, vn, path[0].contiguous(), None, kc, vc, 20) == 24
+    for j in range(4):
+        k0[:, :, 20 + j], v0[:, :, 20 + j] = kn[:, :, int(path[0, j])], vn[:, :, int(path[0, j])]
+    assert torch.equal(kc, k0) and torch.equal(vc, v0)
+    # what does not fit or does not exist is recorded and left out
+    new = kv.append_accepted(kn, vn, path, torch.tensor([4, 2, 1, 5], dtype=torch.int32, device=DEV), kc, vc,
+                             torch.tensor([57, 59, 60, 7], dtype=torch.int32, device=DEV))
+    assert new.tolist() == [57, 59, 60, 7]
+    with pytest.raises(kv.StateKVError):
+        kv.check_status()
+    bad = torch.tensor([-1, tok, 4], dtype=torch.int32, device=DEV)
+    kv.append_accepted(kn, vn, bad, None, kc, vc, 30)
+    with pytest.raises(kv.StateKVError):
+        kv.check_status()
+    k0[:, :, 32], v0[:, :, 32] = kn[:, :, 4], vn[:, :, 4]
+    assert torch.equal(kc, k0) and torch.equal(vc, v0)
+
+
+# ---------------------------------------------------------------- summaries
+def ref_summaries(k):
+    """[..., blocks * 64, d] -> int8 codes and scales, as the header defines them."""
+    m = (k.unflatten(-2, (-1, 64)).double().sum(-2)).float() / 64
+    top = m.abs().amax(-1)
+    # quotients in fp64, rounded: the correctly rounded fp32 quotient (torch
+    # multiplies by a rounded reciprocal where one side is a plain number)
+    inv = torch.where(top > 0, (127 / top.double()).float(), torch.zeros_like(top))
+    return torch.round(m * inv[..., None]).to(torch.int8), (top.double() / 127).float()
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("token_major", [False, True])
+def test_block_summaries(d, token_major):
+    g = gen(31)
+    seqs, layers, hkv, cap = 3, 2, 2, 700
+    n = seqs * layers
+    k = randn(g, n, cap, hkv, d).transpose(1, 2)
+    # values of very different sizes, cancelling sums, a zero block
+    k[0, :, :64] *= torch.logspace(-20, 10, 64, device=DEV)[:, None]
+    k[1, 0, 64:96] = -k[1, 0, 96:128]
+    k[2, :, 64:128] = 0
+    k[3, 1, :64] *= 1e30
+    if not token_major:
+        k = k.contiguous()
+    blocks = cap // 64 + 1
+    codes = torch.full((n, hkv, blocks, d), 77, dtype=torch.int8, device=DEV)
+    scales = torch.full((n, hkv, blocks), 7.0, device=DEV)
+    c, s = ref_summaries(k[:, :, :cap // 64 * 64])
+    lens = [700, 63, 129]
+    lengths = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    kv.block_summaries(k, codes, scales, lengths)
+    for i in range(n):
+        b = lens[i // layers] // 64
+        assert torch.equal(codes[i, :, :b], c[i, :, :b]) and torch.equal(scales[i, :, :b], s[i, :, :b])
+        assert (codes[i, :, b:] == 77).all() and (scales[i, :, b:] == 7).all()
+    # later: 60 more rows of the second sequence, the last ones alone
+    codes.fill_(77)
+    kv.block_summaries(k, codes, scales, torch.tensor([700, 128, 129], dtype=torch.int32, device=DEV), appended=65)
+    for i in range(n):
+        fresh = {0: range(9, 10), 1: range(0, 2), 2: range(1, 2)}[i // layers]
+        for b in range(blocks):
+            want = c[i, :, b] if b in fresh else torch.full_like(c[i, :, 0], 77)
+            assert torch.equal(codes[i, :, b], want), (i, b)
+    kv.block_summaries(k, codes, scales, 640, appended=0)
+    kv.check_status()
+
+
+# ------------------------------------------------------------------- chains
+@gpu
+def test_speculative_step_as_used_and_captured():
+    """Norm and rotate the drafted tokens, attend as a tree, append the accepted
+    path, summarise: eager against the definitions, then captured and replayed."""
+    g = gen(41)
+    seqs, layers, hq, hkv, d, cap = 2, 2, 6, 2, 128, 600
+    n = seqs * layers
+    parents = [[-1, 0, 0, 1, 1, 2, 5], [-1, 0, 1, 2, 3, 4, 5]]
+    tree, depth = kv.tree_masks(parents, DEV)
+    tok = tree.shape[1]
+    kc, vc = randn(g, n, hkv, cap, d), randn(g, n, hkv, cap, d)
+    lengths = torch.tensor([500, 317], dtype=torch.int32, device=DEV)
+    w = 1 + randn(g, d) / 4
+    omega = omega_of(d)
+    path = torch.tensor([[0, 2, 5, 6], [0, 1, 2, 3]], dtype=torch.int32, device=DEV)
+    counts = torch.tensor([4, 2], dtype=torch.int32, device=DEV)
+    codes = torch.zeros((n, hkv, cap // 64, d), dtype=torch.int8, device=DEV)
+    scales = torch.zeros((n, hkv, cap // 64), device=DEV)
+    x = randn(g, n, tok, hq + 2 * hkv, d)
+
+    def step():
+        q, k, v = x.transpose(1, 2).split([hq, hkv, hkv], 1)
+        pos = lengths[:, None] + depth
+        qr, kr, vr = kv.qk_norm_rope(q, k, pos, omega, w, w, v=v)
+        o = kv.tree_attention(qr, kr, vr, tree, kc, vc, lengths, scale=0.09)
+        new = kv.append_accepted(kr, vr, path, counts, kc, vc, lengths)
+        kv.block_summaries(kc, codes, scales, new, appended=4)
+        return qr, kr, vr, o, new
+
+    kv.block_summaries(kc, codes, scales, lengths)
+    for round_ in range(2):
+        k0, v0 = kc.clone(), vc.clone()
+        qr, kr, vr, o, new = step()
+        check_tree(qr, kr, vr, tree, k0, v0, lengths, 0.09, o, f"round {round_}")
+        assert (new - lengths).tolist() == [4, 2]
+        for i in range(n):
+            at, cnt = int(lengths[i // layers]), int(counts[i // layers])
+            sel = path[i // layers, :cnt].long()
+            assert torch.equal(kc[i, :, at:at + cnt], kr[i][:, sel])
+            c, s = ref_summaries(kc[i, :, :int(new[i // layers]) // 64 * 64])
+            assert torch.equal(codes[i, :, :c.shape[1]], c)
+        lengths.copy_(new)
+    kv.check_status()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+        lengths_next = out[4]
+    for round_ in range(3):
+        x.copy_(randn(g, *x.shape))
+        k0, v0 = kc.clone(), vc.clone()
+        graph.replay()
+        got = [t.clone() for t in out]
+        kc.copy_(k0), vc.copy_(v0)
+        want = step()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        lengths.copy_(lengths_next)
+    kv.check_status()
+
+
+@gpu
+def test_two_captured_graphs_at_once():
+    """Two graphs on two streams: each has a workspace of its own."""
+    xs = [tree_inputs(50 + i, 1, 12, 2, 8, 128, 9000) for i in range(2)]
+    tree = random_tree(8, 1, 1)
+    want = [kv.tree_attention(*x[:3], tree, *x[3:], 9000, scale=0.09) for x in xs]
+    graphs, outs, streams = [], [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for x in xs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(kv.tree_attention(*x[:3], tree, *x[3:], 9000, scale=0.09))
+        graphs.append(g)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(outs, want):
+        assert torch.equal(a, b)
+    kv.check_status()
+
+
+# ----------------------------------------------------------------- refusals
+def test_tree_masks_on_the_host():
+    m, d = kv.tree_masks([-1, 0, 0, 1])
+    assert m.tolist() == [[1, 3, 5, 11]] and d.tolist() == [[0, 1, 1, 2]]
+    m, _ = kv.tree_masks([[-1] + list(range(63))] * 2)
+    assert m.shape == (2, 64) and m[1, 63] == -1
+    for bad in ([], [0], [-1, 1], [-1, -2], [-1] * 65, [[-1], [-1, 0]]):
+        with pytest.raises(ValueError):
+            kv.tree_masks(bad)
+
+
+def view(p=16, b=1024, h=512, t=128):
+    return N.View(p, b, h, t)
+
+
+def tree_args(**kw):
+    a = dict(q=view(), out=view(), k_new=view(), v_new=view(), k_cache=view(), v_cache=view(), tree=16, status=16,
+             workspace=16, workspace_bytes=1 << 40, scale=0.1, tree_stride=0, length=2, batch=2, layers=1, q_heads=4,
+             kv_heads=2, tokens=3, head_dim=128, cache_rows=4)
+    a.update(kw)
+    return N.TreeArgs(**a)
+
+
+@pytest.mark.parametrize("bad,want", [
+    (dict(tokens=0), N.E_INVALID_ARG), (dict(tokens=65), N.E_UNSUPPORTED), (dict(head_dim=96), N.E_UNSUPPORTED),
+    (dict(q_heads=3), N.E_INVALID_ARG), (dict(kv_heads=0), N.E_INVALID_ARG), (dict(layers=3), N.E_INVALID_ARG),
+    (dict(layers=0), N.E_INVALID_ARG), (dict(batch=-1), N.E_INVALID_ARG), (dict(scale=0.0), N.E_INVALID_ARG),
+    (dict(scale=math.nan), N.E_INVALID_ARG), (dict(scale=math.inf), N.E_INVALID_ARG),
+    (dict(length=5), N.E_CAPACITY), (dict(length=-1), N.E_INVALID_ARG), (dict(status=None), N.E_INVALID_ARG),
+    (dict(status=18), N.E_INVALID_ARG), (dict(tree=None), N.E_INVALID_ARG), (dict(tree=20), N.E_INVALID_ARG),
+    (dict(q=view(8)), N.E_INVALID_ARG), (dict(q=view(t=4)), N.E_INVALID_ARG), (dict(out=view(h=-512)), N.E_INVALID_ARG),
+    (dict(k_cache=view(None)), N.E_INVALID_ARG), (dict(k_cache=view(t=0)), N.E_INVALID_ARG),
+    (dict(k_new=view(h=0)), N.E_INVALID_ARG), (dict(batch=0), N.OK),
+])
+def test_tree_refusals_before_device_work(bad, want):
+    assert N.load().statekv_tree_attention(tree_args(**bad), None) == want
+
+
+@pytest.mark.parametrize("bad,want", [
+    (dict(dtype=5), N.E_INVALID_ARG), (dict(weight_dtype=5), N.E_INVALID_ARG), (dict(head_dim=96), N.E_UNSUPPORTED),
+    (dict(omega=None), N.E_INVALID_ARG), (dict(omega=20), N.E_INVALID_ARG), (dict(status=None), N.E_INVALID_ARG),
+    (dict(q=view(8)), N.E_INVALID_ARG), (dict(k_out=view(b=4)), N.E_INVALID_ARG), (dict(v_out=view(None)), N.E_INVALID_ARG),
+    (dict(layers=0), N.E_INVALID_ARG), (dict(position_layers=0), N.E_INVALID_ARG), (dict(batch=3, layers=2), N.E_INVALID_ARG),
+    (dict(out_capacity=2), N.E_CAPACITY), (dict(eps=-1.0), N.E_INVALID_ARG), (dict(eps=math.nan), N.E_INVALID_ARG),
+    (dict(tokens=-1), N.E_INVALID_ARG), (dict(q_heads=70000), N.E_UNSUPPORTED), (dict(tokens=0, out_capacity=0), N.OK),
+    (dict(batch=0), N.OK),
+])
+def test_norm_rope_refusals_before_device_work(bad, want):
+    a = dict(q=view(), k=view(), v=view(), q_out=view(), k_out=view(), v_out=view(), omega=16, status=16,
+             position_layers=1, batch=2, layers=1, q_heads=4, kv_heads=2, tokens=3, head_dim=128, out_capacity=3,
+             dtype=0, weight_dtype=0, eps=1e-6)
+    a.update(bad)
+    assert N.load().statekv_norm_rope(N.NormRopeArgs(**a), None) == want
+
+
+@pytest.mark.parametrize("bad,want", [
+    (dict(dtype=5), N.E_INVALID_ARG), (dict(head_dim=4), N.E_UNSUPPORTED), (dict(head_dim=100), N.E_UNSUPPORTED),
+    (dict(path=None), N.E_INVALID_ARG), (dict(k_new=view(8)), N.E_INVALID_ARG), (dict(v_cache=view(None)), N.E_INVALID_ARG),
+    (dict(length=3), N.E_CAPACITY), (dict(new_lengths=64, lengths=64), N.E_INVALID_ARG),
+    (dict(new_lengths=64, counts=64), N.E_INVALID_ARG), (dict(status=None), N.E_INVALID_ARG),
+    (dict(layers=0), N.E_INVALID_ARG), (dict(path_len=-1), N.E_INVALID_ARG), (dict(batch=0), N.OK),
+])
+def test_append_refusals_before_device_work(bad, want):
+    a = dict(k_new=view(), v_new=view(), k_cache=view(), v_cache=view(), path=16, status=16, path_len=2, length=2,
+             batch=2, layers=1, kv_heads=2, tokens=3, head_dim=128, cache_rows=4, dtype=0)
+    a.update(bad)
+    assert N.load().statekv_append_accepted(N.AppendArgs(**a), None) == want
+
+
+@pytest.mark.parametrize("bad,want", [
+    (dict(head_dim=96), N.E_UNSUPPORTED), (dict(blocks=1), N.E_CAPACITY), (dict(codes=20), N.E_INVALID_ARG),
+    (dict(scales=None), N.E_INVALID_ARG), (dict(k_cache=view(8)), N.E_INVALID_ARG), (dict(appended=-1), N.E_INVALID_ARG),
+    (dict(status=None), N.E_INVALID_ARG), (dict(batch=0), N.OK), (dict(cache_rows=63, blocks=0), N.OK),
+])
+def test_summary_refusals_before_device_work(bad, want):
+    a = dict(k_cache=view(), codes=16, scales=16, status=16, length=128, appended=64, blocks=2, batch=2, layers=1,
+             kv_heads=2, head_dim=128, cache_rows=128)
+    a.update(bad)
+    assert N.load().statekv_block_summaries(N.SummaryArgs(**a), None) == want
+
+
+def test_null_arguments():
+    lib = N.load()
+    for f in ("norm_rope", "tree_attention", "append_accepted", "block_summaries"):
+        assert getattr(lib, "statekv_" + f)(None, None) == N.E_INVALID_ARG
+    assert lib.statekv_tree_attention_workspace(1, 4, 2, 65, 128) == -1
+    assert lib.statekv_tree_attention_workspace(1, 3, 2, 4, 128) == -1
+
+
+@gpu
+def test_python_checks_name_the_argument():
+    q, kn, vn, kc, vc = tree_inputs(1, 2, 4, 2, 3, 64, 10)
+    tree = random_tree(3, 1, 1)
+    call = lambda **kw: kv.tree_attention(**{**dict(q=q, k_new=kn, v_new=vn, tree=tree, k_cache=kc, v_cache=vc,  # noqa: E731
+                                                    lengths=4, scale=0.1), **kw})
+    for name, bad in (("k_new", kn[:1]), ("k_new", kn.float()), ("v_cache", vc.transpose(2, 3)), ("tree", tree.int()),
+                      ("tree", tree[:, :2].contiguous()), ("q", q[0]), ("q", q.cpu()),
+                      ("lengths", torch.tensor([1, 2, 3], dtype=torch.int32, device=DEV)),
+                      ("lengths", torch.tensor([1, 2], device=DEV)), ("q", q.clone().requires_grad_())):
+        with pytest.raises(ValueError, match=name):
+            call(**{name: bad})
+    with torch.no_grad():
+        call(q=q.clone().requires_grad_())
+    with pytest.raises(kv.StateKVError):
+        call(lengths=11)
+    with pytest.raises(kv.StateKVError):
+        call(workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+    with pytest.raises(kv.StateKVError):
+        call(k_cache=kc[:, :1].expand(2, 2, 10, 64))
