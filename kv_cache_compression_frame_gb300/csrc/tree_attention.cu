@@ -441,8 +441,15 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                 const int t = cu.t + dt;
                 const bool drafted = t == cu.nt - 1;
                 const int valid = drafted ? a.tokens : min(kTile, cu.len - t * kTile);
+                if (!(ok = sy.wait(L::B_S_FULL + slot, s_par, kSiteSFull))) break;
+                s_par ^= 1u;
+                __syncwarp();
+                ptx::tc_fence_after();
                 if (drafted || valid < kTile) {
-                    // V rows whose products with P = 0 must be 0
+                    // V rows whose products with P = 0 must be 0.  (After S
+                    // full, which implies that the slot's last P V is done
+                    // and with it the load before this one in V's stage: a
+                    // wait for a phase before the last one ended would pass.)
                     const int g = g0 + dt, vs = g % L::VS;
                     if (!(ok = sy.wait(L::B_V_FULL + vs, (uint32_t)((g / L::VS) & 1), kSiteKvFull))) break;
                     uint8_t* vt = base + L::OFF_V + vs * L::TILE;
@@ -471,10 +478,6 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                     }
                     ptx::fence_proxy_async_smem();
                 }
-                if (!(ok = sy.wait(L::B_S_FULL + slot, s_par, kSiteSFull))) break;
-                s_par ^= 1u;
-                __syncwarp();
-                ptx::tc_fence_after();
                 if (!idle) {
                     // 64 scores at a time stay in registers: the upper half
                     // is read again after the lower half became P (which

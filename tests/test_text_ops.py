@@ -238,6 +238,20 @@ def test_tree_ragged_lengths(layers):
 
 
 @gpu
+@pytest.mark.parametrize("hq,tok", [(16, 32), (16, 43), (32, 64)])    # 64, 86 and 256 rows
+def test_tree_long_ragged_caches(hq, tok):
+    """A CTA's share holds the end of one long unit and the start of the next."""
+    n = 16
+    lengths = torch.randint(3000, 20000, (n,), generator=gen(2), device=DEV).to(torch.int32)
+    x = tree_inputs(5, n, hq, 8, tok, 128, 20000)
+    tree = random_tree(tok, n, 1)
+    got = [kv.tree_attention(*x[:3], tree, *x[3:], lengths, scale=0.09) for _ in range(10)]
+    check_tree(*x[:3], tree, *x[3:], lengths, 0.09, got[0])
+    for o in got[1:]:
+        assert torch.equal(o, got[0])
+
+
+@gpu
 def test_tree_many_sequences():
     """More sequences than a warp's lanes, more units than SMs."""
     n = 70
