@@ -525,6 +525,39 @@ typedef struct statekv_summary_args {
 } statekv_summary_args;
 int statekv_block_summaries(const statekv_summary_args* args, void* cuda_stream);
 
+/*
+ * Block-sparse attention of the last `tokens` rows of each sequence over the
+ * cache they are already part of (token j is row length - tokens + j).  With
+ * first = length - tokens, each token and KV head
+ *   1. scores the complete blocks of rows [0, first): the head group's query
+ *      rows are rounded to 8 bits with one scale, qi = round_to_even(q * (127 /
+ *      max |q|)), and score_b = float(max over the group of qi . code_b) *
+ *      scale_b.  The products are whole numbers, so the scores, and the choice,
+ *      do not depend on the order of summation;
+ *   2. keeps the `top` best (1..1024), ties to the lower block;
+ *   3. attends over those blocks' rows, the rows since the last complete block
+ *      and, causally, the new rows.
+ * With top >= first / 64 this is full attention.  selected, if not NULL:
+ * int32 [batch][kv_heads][tokens][top], the chosen blocks in ascending order,
+ * -1 from the last one on.  codes and scales as statekv_block_summaries
+ * writes them, up to date for every complete block before `first`, codes
+ * 16-byte aligned.  bf16, head_dim 64 or 128, q_heads / kv_heads <= 16,
+ * at most 32768 blocks, tokens <= length (a shorter sequence gives zeros for the
+ * tokens before its first row).  No workspace.
+ */
+typedef struct statekv_sparse_args {
+    statekv_view q, out, k_cache, v_cache;
+    const int8_t* codes;
+    const float* scales;
+    const int32_t* lengths;
+    int32_t* selected;
+    uint32_t* status;
+    double scale;
+    int32_t length, top, blocks;
+    int32_t batch, layers, q_heads, kv_heads, tokens, head_dim, cache_rows;
+} statekv_sparse_args;
+int statekv_sparse_attention(const statekv_sparse_args* args, void* cuda_stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -42,6 +42,7 @@ EXPORTS = (
     "statekv_attend_scores_static", "statekv_decode", "statekv_text_tokens",
     "statekv_norm_rope", "statekv_tree_attention", "statekv_tree_attention_workspace",
     "statekv_append_accepted", "statekv_block_summaries",
+    "statekv_sparse_attention",
 )
 
 BLOCK = 64          # STATEKV_BLOCK
@@ -88,6 +89,11 @@ AppendArgs = _struct(
 SummaryArgs = _struct(
     "SummaryArgs", (View, "k_cache"), (C.c_void_p, "codes scales lengths status"),
     (C.c_int32, "length appended blocks batch layers kv_heads head_dim cache_rows"))
+
+SparseArgs = _struct(
+    "SparseArgs", (View, "q out k_cache v_cache"), (C.c_void_p, "codes scales lengths selected status"),
+    (C.c_double, "scale"),
+    (C.c_int32, "length top blocks batch layers q_heads kv_heads tokens head_dim cache_rows"))
 
 
 class StateKVError(RuntimeError):
@@ -144,7 +150,8 @@ def load() -> C.CDLL:
     }
     for name, args in (("statekv_norm_rope", NormRopeArgs), ("statekv_tree_attention", TreeArgs),
                        ("statekv_append_accepted", AppendArgs),
-                       ("statekv_block_summaries", SummaryArgs)):
+                       ("statekv_block_summaries", SummaryArgs),
+                       ("statekv_sparse_attention", SparseArgs)):
         sig[name] = (C.c_int, [C.POINTER(args), _P])
     sig["statekv_tree_attention_workspace"] = (C.c_int64, [C.c_int32] * 5)
     for name, (res, args) in sig.items():

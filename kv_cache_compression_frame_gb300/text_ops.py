@@ -336,3 +336,36 @@ def _summary_ptrs(codes, scales, n: int, hkv: int, d: int, dev) -> tuple[int, in
         raise ValueError(f"codes and scales: want ({n}, {hkv}, blocks, {d}) and ({n}, {hkv}, blocks), got "
                          f"{tuple(codes.shape)} and {tuple(scales.shape)}")
     return pc, ps, blocks
+
+
+def sparse_attention(q, k_cache, v_cache, codes, scales, lengths, top: int, *, scale: float, out=None,
+                     selected=None, stream=None):
+    """Attention of the last tokens of each sequence, q [n][Hq][tokens][d] at
+    cache rows lengths - tokens + j, over the `top` blocks of k_cache and
+    v_cache [n][Hkv][rows][d] that codes and scales (block_summaries) score
+    best for each token and KV head, and the rows since the last complete
+    block.  bf16.  Returns (out like q, selected int32 [n][Hkv][tokens][top]:
+    the chosen blocks in ascending order, then -1)."""
+    n, hq, tok, d = _shape4(q, "q")
+    hkv, rows = _shape4(k_cache, "k_cache")[1:3]
+    dev, top = q.device, int(top)
+    a = N.SparseArgs()
+    a.q = _view(q, "q", (n, hq, tok, d), _BF16, dev)
+    a.k_cache = _view(k_cache, "k_cache", (n, hkv, rows, d), _BF16, dev)
+    a.v_cache = _view(v_cache, "v_cache", (n, hkv, rows, d), _BF16, dev)
+    a.codes, a.scales, a.blocks = _summary_ptrs(codes, scales, n, hkv, d, dev)
+    a.lengths, a.length, layers = _lengths(lengths, n, dev)
+    with _On(dev, stream) as st:
+        a.status = _status_ptr(dev.index)
+        if out is None:
+            out = torch.empty((n, hq, tok, d), dtype=_BF16, device=dev)
+        a.out = _view(out, "out", (n, hq, tok, d), _BF16, dev)
+        if selected is None:
+            selected = torch.empty((n, hkv, tok, max(0, top)), dtype=_I32, device=dev)
+        elif selected.shape != (n, hkv, tok, top):
+            raise ValueError(f"selected: want {(n, hkv, tok, top)}, got {tuple(selected.shape)}")
+        a.selected = _vector(selected, "selected", _I32, dev, 4)
+        a.scale, a.top, a.layers = scale, top, layers or 1
+        a.batch, a.q_heads, a.kv_heads, a.tokens, a.head_dim, a.cache_rows = n, hq, hkv, tok, d, rows
+        N.check(N.load().statekv_sparse_attention(C.byref(a), st), "statekv_sparse_attention")
+    return out, selected

@@ -467,6 +467,130 @@ def test_block_summaries(d, token_major):
     kv.check_status()
 
 
+# ------------------------------------------------------------------- sparse
+def ref_choice(q, codes, scales, nb, top):
+    """q [g][d] of one token and KV head -> the chosen blocks, ascending."""
+    big = q.float().abs().max()
+    qi = torch.round(q.float() * (127 / big.double()).float()) if big > 0 else torch.zeros_like(q.float())
+    s = (qi.double() @ codes[:nb].double().T).amax(0).float() * scales[:nb]
+    return sorted(sorted(range(nb), key=lambda b, v=s.tolist(): (-v[b], b))[:top])
+
+
+def check_sparse(q, kc, vc, codes, scales, lengths, top, scale, got, selected):
+    n, hq, tok, d = q.shape
+    hkv = kc.shape[1]
+    G = hq // hkv
+    for i in range(n):
+        rows = lengths if isinstance(lengths, int) else int(lengths[i * len(lengths) // n])
+        nb = max(0, rows - tok) // 64
+        for h in range(hkv):
+            for t in range(tok):
+                at = rows - tok + t
+                if at < 0:
+                    assert (got[i, h * G:(h + 1) * G, t] == 0).all() and (selected[i, h, t] == -1).all()
+                    continue
+                qs = q[i, h * G:(h + 1) * G, t]
+                keep = ref_choice(qs, codes[i, h], scales[i, h], nb, top)
+                assert selected[i, h, t].tolist() == keep + [-1] * (top - len(keep)), (i, h, t)
+                idx = torch.cat([64 * torch.tensor(keep, dtype=torch.int64)[:, None].expand(-1, 64).reshape(-1)
+                                 + torch.arange(64).repeat(len(keep)), torch.arange(64 * nb, at + 1)]).to(DEV)
+                ref, a = ref_attend(qs, kc[i, h, idx], vc[i, h, idx],
+                                    torch.ones(G, len(idx), dtype=torch.bool, device=DEV), scale)
+                within(got[i, h * G:(h + 1) * G, t], ref, 2.0 ** -8 * ref.abs() + (2.0 ** -8 + 2.0 ** -12) * a,
+                       f"entry {i} head {h} token {t}")
+
+
+def sparse_inputs(seed, n, hq, hkv, tok, d, cap):
+    g = gen(seed)
+    kc, vc = randn(g, n, hkv, cap, d), randn(g, n, hkv, cap, d)
+    kc[:, :, :cap // 64 * 64].view(n, hkv, -1, 64, d).add_(randn(g, n, hkv, cap // 64, 1, d) / 2)
+    codes, scales = ref_summaries(kc[:, :, :cap // 64 * 64])
+    return randn(g, n, hq, tok, d), kc, vc, codes, scales
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n,hq,hkv,tok,rows,top", [
+    (1, 1, 1, 1, 1, 1), (1, 2, 1, 1, 64, 1), (1, 2, 1, 1, 65, 1), (1, 4, 2, 3, 190, 2), (1, 12, 2, 1, 4100, 5),
+    (2, 16, 8, 2, 2000, 31),      # cluster of 4
+    (3, 16, 8, 5, 1000, 7),       # 120 items: no cluster
+    (1, 32, 2, 1, 9001, 64),      # 16 query heads per KV head
+    (1, 14, 2, 70, 700, 4),       # more tokens than a block has rows
+    (1, 6, 2, 1, 40000, 1),       # 624 blocks, one kept
+])
+def test_sparse_sizes(d, n, hq, hkv, tok, rows, top):
+    x = sparse_inputs(rows + tok, n, hq, hkv, tok, d, rows + 5)
+    got, sel = kv.sparse_attention(*x, rows, top, scale=0.1)
+    check_sparse(*x, rows, top, 0.1, got, sel)
+    kv.check_status()
+
+
+@gpu
+@pytest.mark.parametrize("layers", [1, 2])
+def test_sparse_ragged(layers):
+    lens = [3, 0, 1, 700, 64, 129, 650, 2]
+    n = len(lens) * layers
+    x = sparse_inputs(7, n, 6, 2, 3, 128, 705)
+    # what a sequence has not reached yet may hold anything
+    for i in range(n):
+        for c in x[1:3]:
+            c[i, :, lens[i // layers]:] = float("nan")
+    lengths = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    got, sel = kv.sparse_attention(*x, lengths, 4, scale=0.1)
+    check_sparse(*x, lengths, 4, 0.1, got, sel)
+    kv.check_status()
+
+
+@gpu
+def test_sparse_ties_and_full_attention():
+    """Equal scores keep the lower blocks; enough blocks make it full attention."""
+    x = list(sparse_inputs(8, 1, 4, 2, 2, 64, 64 * 40 + 10))
+    x[3][:, :, 5:] = x[3][:, :, 5:6]
+    x[4][:, :, 5:] = x[4][:, :, 5:6]
+    for top in (1, 7, 30):
+        got, sel = kv.sparse_attention(*x, 64 * 40 + 10, top, scale=0.1)
+        check_sparse(*x, 64 * 40 + 10, top, 0.1, got, sel)
+    zero = [torch.zeros_like(x[0])] + x[1:]              # no query: every score is 0
+    got, sel = kv.sparse_attention(*zero, 64 * 40 + 10, 9, scale=0.1)
+    assert (sel == torch.arange(9, device=DEV)).all()
+    check_sparse(*zero, 64 * 40 + 10, 9, 0.1, got, sel)
+    q, kc, vc, rows = x[0], x[1], x[2], 64 * 40 + 10
+    got, sel = kv.sparse_attention(*x, rows, 1024, scale=0.1)
+    assert (sel[..., :40] == torch.arange(40, device=DEV)).all() and (sel[..., 40:] == -1).all()
+    tree = kv.tree_masks([-1, 0], DEV)[0]
+    full = kv.tree_attention(q, kc[:, :, rows - 2:rows].contiguous(), vc[:, :, rows - 2:rows].contiguous(), tree,
+                             kc, vc, rows - 2, scale=0.1)
+    # two results, each within its tolerance of the same value (|v| < 8)
+    assert (got.double() - full.double()).abs().max() < 2 * (2 * 2.0 ** -8 + 2.0 ** -12) * 8
+
+
+@gpu
+def test_sparse_many_blocks_views_and_stream():
+    """The largest number of blocks, token-major cache, another stream, captured."""
+    g = gen(61)
+    rows = 32768 * 64 + 40
+    pool = torch.randn(1, rows, 2, 1, 64, generator=g, device=DEV, dtype=BF16)
+    kc, vc = pool[:, :, 0].transpose(1, 2), pool[:, :, 1].transpose(1, 2)
+    codes = torch.empty((1, 1, 32768, 64), dtype=torch.int8, device=DEV)
+    scales = torch.empty((1, 1, 32768), device=DEV)
+    kv.block_summaries(kc, codes, scales, rows)
+    c, s = ref_summaries(kc[:, :, :32768 * 64])
+    assert torch.equal(codes, c) and torch.equal(scales, s)
+    q = randn(g, 1, 2, 4, 64).transpose(1, 2).contiguous().transpose(1, 2).view(1, 2, 4, 64)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    got, sel = kv.sparse_attention(q, kc, vc, codes, scales, rows, 100, scale=0.1, stream=st)
+    st.synchronize()
+    check_sparse(q, kc, vc, codes, scales, rows, 100, 0.1, got, sel)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        again = kv.sparse_attention(q, kc, vc, codes, scales, rows, 100, scale=0.1)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(again[0], got) and torch.equal(again[1], sel)
+    kv.check_status()
+
+
 # ------------------------------------------------------------------- chains
 @gpu
 def test_speculative_step_as_used_and_captured():
@@ -631,9 +755,26 @@ def test_summary_refusals_before_device_work(bad, want):
     assert N.load().statekv_block_summaries(N.SummaryArgs(**a), None) == want
 
 
+@pytest.mark.parametrize("bad,want", [
+    (dict(head_dim=96), N.E_UNSUPPORTED), (dict(q_heads=34), N.E_UNSUPPORTED), (dict(q_heads=3), N.E_INVALID_ARG),
+    (dict(top=0), N.E_INVALID_ARG), (dict(top=1025), N.E_UNSUPPORTED), (dict(blocks=1), N.E_CAPACITY),
+    (dict(length=257), N.E_CAPACITY), (dict(codes=24), N.E_INVALID_ARG), (dict(scales=None), N.E_INVALID_ARG),
+    (dict(selected=18), N.E_INVALID_ARG), (dict(status=None), N.E_INVALID_ARG), (dict(scale=-1.0), N.E_INVALID_ARG),
+    (dict(q=view(8)), N.E_INVALID_ARG), (dict(k_cache=view(None)), N.E_INVALID_ARG), (dict(out=view(t=4)), N.E_INVALID_ARG),
+    (dict(cache_rows=64 * 32769, blocks=40000), N.E_UNSUPPORTED), (dict(batch=1 << 28), N.E_UNSUPPORTED),
+    (dict(layers=3), N.E_INVALID_ARG), (dict(batch=0), N.OK), (dict(tokens=0), N.OK),
+])
+def test_sparse_refusals_before_device_work(bad, want):
+    a = dict(q=view(), out=view(), k_cache=view(), v_cache=view(), codes=16, scales=16, selected=16, status=16,
+             scale=0.1, length=256, top=2, blocks=4, batch=2, layers=1, q_heads=4, kv_heads=2, tokens=3, head_dim=128,
+             cache_rows=256)
+    a.update(bad)
+    assert N.load().statekv_sparse_attention(N.SparseArgs(**a), None) == want
+
+
 def test_null_arguments():
     lib = N.load()
-    for f in ("norm_rope", "tree_attention", "append_accepted", "block_summaries"):
+    for f in ("norm_rope", "tree_attention", "append_accepted", "block_summaries", "sparse_attention"):
         assert getattr(lib, "statekv_" + f)(None, None) == N.E_INVALID_ARG
     assert lib.statekv_tree_attention_workspace(1, 4, 2, 65, 128) == -1
     assert lib.statekv_tree_attention_workspace(1, 3, 2, 4, 128) == -1
