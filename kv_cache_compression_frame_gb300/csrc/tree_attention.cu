@@ -51,8 +51,13 @@ namespace {
 
 constexpr int kTile = 128;                   // keys per tile, query rows per row tile
 constexpr float kSlack = 8.f;                // raise the reference past 2^8
-constexpr int kMinTiles = 2;                 // key tiles per CTA, at least, before more CTAs join
-constexpr int kTreeThreads = 320;
+constexpr int kUnitCost = 2;                 // a unit's start and end in key tiles' time
+constexpr int kMinShare = 4;                 // least share (in tiles' time) before more CTAs join
+constexpr int kTreeThreads = 384;
+// registers a thread after the split: 128 threads of the first warpgroup and
+// 256 softmax threads, together the 168 x 384 of the launch
+constexpr int kRegsIssue = 56, kRegsSoftmax = 224;
+static_assert(kRegsIssue + 2 * kRegsSoftmax <= 3 * 168, "registers of the launch");
 
 struct TreeKernelArgs {
     statekv_tree_args a;
@@ -63,7 +68,9 @@ struct TreeKernelArgs {
     int32_t grid;                            // CTAs of the main kernel
 };
 
-// The schedule, from the sequences' lengths: where unit u's tiles start.
+// The schedule, from the sequences' lengths.  A unit of nt key tiles counts as
+// kUnitCost + nt tiles (it starts with kUnitCost of no content): without that
+// a CTA whose share held many short units took 1.5 times as long as the rest.
 struct Plan {
     int64_t total;                           // tiles of all units
     int ctas;                                // CTAs that get a share
@@ -72,23 +79,28 @@ struct Plan {
     __device__ int cta_of(int64_t w) const { return (int)(((w + 1) * ctas - 1) / total); }
 };
 
-__device__ __forceinline__ int seq_tiles(const TreeKernelArgs& k, int s) {
-    return (cache_length(k.a.lengths, k.a.length, s, k.a.cache_rows, k.a.status) + kTile - 1) / kTile + 1;
+__device__ __forceinline__ int seq_length(const TreeKernelArgs& k, int s) {
+    return cache_length(k.a.lengths, k.a.length, s, k.a.cache_rows, k.a.status);
+}
+// Key tiles of a unit: the cache's and the drafted one.
+__device__ __forceinline__ int unit_tiles(int len) { return (len + kTile - 1) / kTile + 1; }
+__device__ __forceinline__ int unit_cost(const TreeKernelArgs& k, int s) {
+    return unit_tiles(seq_length(k, s)) + kUnitCost;
 }
 
-// Tiles before sequence s and of all sequences, in units of one (layer, head,
-// row block); a whole warp, the same result in every lane.
-__device__ __forceinline__ void sum_tiles(const TreeKernelArgs& k, int s, int64_t& before, int64_t& all) {
+// Cost of one unit of every sequence before s, and of all sequences; a whole
+// warp, the same result in every lane.
+__device__ __forceinline__ void sum_costs(const TreeKernelArgs& k, int s, int64_t& before, int64_t& all) {
     const int seqs = k.a.batch / k.a.layers;
     if (!k.a.lengths) {
-        const int t = seq_tiles(k, 0);
+        const int t = unit_cost(k, 0);
         before = (int64_t)t * s;
         all = (int64_t)t * seqs;
         return;
     }
     before = all = 0;
     for (int i = threadIdx.x & 31; i < seqs; i += 32) {
-        const int t = seq_tiles(k, i);
+        const int t = unit_cost(k, i);
         all += t;
         if (i < s) before += t;
     }
@@ -99,50 +111,62 @@ __device__ __forceinline__ void sum_tiles(const TreeKernelArgs& k, int s, int64_
     }
 }
 
-__device__ __forceinline__ Plan make_plan(const TreeKernelArgs& k, int64_t seq_sum) {
+__device__ __forceinline__ Plan make_plan(const TreeKernelArgs& k, int64_t costs) {
     Plan p;
-    p.total = seq_sum * k.a.layers * k.a.kv_heads * k.rb;
-    const int64_t most = (p.total + kMinTiles - 1) / kMinTiles;
+    p.total = costs * k.a.layers * k.a.kv_heads * k.rb;
+    const int64_t most = (p.total + kMinShare - 1) / kMinShare;
     p.ctas = most < k.grid ? (int)most : k.grid;
     return p;
 }
 
-// A position in the run of all tiles: sequence s and its cache length, unit u
-// and tile t of the unit.
-struct Cursor {
-    int s, len, nt;
-    int64_t u;
-    int t;
-    __device__ void enter(const TreeKernelArgs& k) {
-        len = cache_length(k.a.lengths, k.a.length, s, k.a.cache_rows, k.a.status);
-        nt = (len + kTile - 1) / kTile + 1;
-    }
-    __device__ void next_unit(const TreeKernelArgs& k) {
-        ++u;
-        t = 0;
-        const int64_t per_seq = (int64_t)k.a.layers * k.a.kv_heads * k.rb;
-        if (u == (s + 1) * per_seq && s + 1 < k.a.batch / k.a.layers) {
-            ++s;
-            enter(k);
+// Walks a share segment by segment.
+struct Walk {
+    int next_s, next_len, v;                 // the next segment's sequence, its length, place in the unit
+    int next_u;
+    int64_t left;                            // of the share
+    // the current segment: sequence, cache rows, key tiles of the unit, unit,
+    // first key tile and number of them
+    int s, len, nt, u, t, tiles;
+    __device__ bool next(const TreeKernelArgs& k) {
+        const int per_seq = k.a.layers * k.a.kv_heads * k.rb;
+        while (left > 0) {
+            s = next_s;
+            len = next_len;
+            nt = unit_tiles(len);
+            u = next_u;
+            const int take = (int)min((int64_t)(nt + kUnitCost - v), left);
+            t = max(v - kUnitCost, 0);
+            tiles = max(v + take - kUnitCost, 0) - t;
+            left -= take;
+            v += take;
+            if (v == nt + kUnitCost) {
+                v = 0;
+                ++next_u;
+                if (next_u == (s + 1) * per_seq && s + 1 < k.a.batch / k.a.layers) next_len = seq_length(k, ++next_s);
+            }
+            if (tiles > 0) return true;
         }
+        return false;
     }
 };
 
-// The cursor at tile w (a whole warp, the same result in every lane).
-__device__ __forceinline__ Cursor find(const TreeKernelArgs& k, int64_t w) {
+// The walk of the share [w, w1) (a whole warp, the same result in every lane).
+__device__ __forceinline__ Walk find(const TreeKernelArgs& k, int64_t w, int64_t w1) {
     const int64_t per_seq = (int64_t)k.a.layers * k.a.kv_heads * k.rb;
     const int seqs = k.a.batch / k.a.layers;
-    Cursor c;
-    c.s = 0;
+    Walk c{};
+    c.left = w1 - w;
+    int cost;
     if (!k.a.lengths) {
-        c.enter(k);
-        c.s = (int)(w / (c.nt * per_seq));
-        w -= c.s * (c.nt * per_seq);
+        c.next_len = seq_length(k, 0);
+        cost = unit_tiles(c.next_len) + kUnitCost;
+        c.next_s = (int)(w / (cost * per_seq));
+        w -= c.next_s * (cost * per_seq);
     } else {
         const int lane = threadIdx.x & 31;
         int64_t base = 0;
         for (int s0 = 0; s0 < seqs; s0 += 32) {
-            const int64_t mine = s0 + lane < seqs ? seq_tiles(k, s0 + lane) * per_seq : 0;
+            const int64_t mine = s0 + lane < seqs ? unit_cost(k, s0 + lane) * per_seq : 0;
             int64_t upto = mine;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
@@ -152,18 +176,19 @@ __device__ __forceinline__ Cursor find(const TreeKernelArgs& k, int64_t w) {
             const unsigned hit = __ballot_sync(0xffffffffu, base + upto > w);
             if (hit) {
                 const int l = __ffs((int)hit) - 1;
-                c.s = s0 + l;
+                c.next_s = s0 + l;
                 base += __shfl_sync(0xffffffffu, upto - mine, l);
                 break;
             }
             base += __shfl_sync(0xffffffffu, upto, 31);
         }
         w -= base;
-        c.enter(k);
+        c.next_len = seq_length(k, c.next_s);
+        cost = unit_tiles(c.next_len) + kUnitCost;
     }
-    const int64_t local = w / c.nt;
-    c.u = c.s * per_seq + local;
-    c.t = (int)(w - local * c.nt);
+    const int64_t local = w / cost;
+    c.next_u = (int)(c.next_s * per_seq + local);
+    c.v = (int)(w - local * cost);
     return c;
 }
 
@@ -187,8 +212,8 @@ struct TreeLayout {
     static constexpr int B_V_EMPTY = B_V_FULL + VS;
     static constexpr int B_Q_FULL = B_V_EMPTY + VS;      // Q of the segment stored (8 warps)
     static constexpr int B_S_FULL = B_Q_FULL + 1;        // [2 slots]
-    static constexpr int B_P_FULL = B_S_FULL + 2;        // [2 slots] (4 warps)
-    static constexpr int B_O_FULL = B_P_FULL + 2;        // the segment's products are done
+    static constexpr int B_P_FULL = B_S_FULL + 2;        // [2 slots][2 halves of 64 keys] (4 warps)
+    static constexpr int B_O_FULL = B_P_FULL + 4;        // the segment's products are done
     static constexpr int B_SYNC = B_O_FULL + 1;          // the 8 softmax warps
     static constexpr int B_DRAIN = B_SYNC + 1;
     static constexpr int NBAR = B_DRAIN + 1;
@@ -218,13 +243,12 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     // every warp finds the CTA's share by itself
-    int64_t none, seq_sum;
-    sum_tiles(k, 0, none, seq_sum);
-    const Plan plan = make_plan(k, seq_sum);
+    int64_t none, costs;
+    sum_costs(k, 0, none, costs);
+    const Plan plan = make_plan(k, costs);
     const int c = (int)blockIdx.x;
     if (c >= plan.ctas) return;
-    const int64_t w0 = plan.start(c), w1 = plan.start(c + 1);
-    const Cursor first = find(k, w0);
+    const Walk first = find(k, plan.start(c), plan.start(c + 1));
 
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + L::OFF_MISC);
     volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(base + L::OFF_MISC + 4);
@@ -242,7 +266,8 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         ptx::mbar_init(sy.bar(L::B_Q_FULL), 8);
         for (int s = 0; s < 2; ++s) {
             ptx::mbar_init(sy.bar(L::B_S_FULL + s), 1);
-            ptx::mbar_init(sy.bar(L::B_P_FULL + s), 4);
+            ptx::mbar_init(sy.bar(L::B_P_FULL + 2 * s), 4);
+            ptx::mbar_init(sy.bar(L::B_P_FULL + 2 * s + 1), 4);
         }
         ptx::mbar_init(sy.bar(L::B_O_FULL), 1);
         ptx::mbar_init(sy.bar(L::B_SYNC), 8);
@@ -263,40 +288,45 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     ptx::dep_trigger();
     const uint32_t sK = sbase + L::OFF_K, sV = sbase + L::OFF_V, sQ = sbase + L::OFF_Q;
 
+    if (warp < 4) {
+        ptx::regs_dec<kRegsIssue>();
     if (warp == 0) {
         // ------------------------------------------------------ TMA producer
         if (lane == 0) {
             ptx::tma_prefetch_desc(&tm_k);
             ptx::tma_prefetch_desc(&tm_v);
-            Cursor ck = first, cv = first;
-            const int n_tiles = (int)(w1 - w0);
+            Walk wk = first, wv = first;
+            wk.tiles = wv.tiles = 0;
             int kt = 0, vt = 0;
-            bool ok = true;
-            auto load = [&](bool is_v) -> bool {
-                Cursor& cu = is_v ? cv : ck;
+            // the next key tile of the share; 1 loaded, 0 none left, -1 gave up
+            auto load = [&](bool is_v) -> int {
+                Walk& x = is_v ? wv : wk;
+                if (x.tiles == 0 && !x.next(k)) return 0;
                 int& cnt = is_v ? vt : kt;
                 const int ns = is_v ? L::VS : L::KS;
                 const int s = cnt % ns, j = cnt / ns;
                 if (!sy.wait((is_v ? L::B_V_EMPTY : L::B_K_EMPTY) + s, (uint32_t)(j & 1) ^ 1u, kSiteKvEmpty))
-                    return false;
+                    return -1;
                 const uint32_t fb = sy.bar((is_v ? L::B_V_FULL : L::B_K_FULL) + s);
                 ptx::mbar_arrive_expect_tx(fb, L::TILE);
                 const uint32_t dst = (is_v ? sV : sK) + s * L::TILE;
-                const bool drafted = cu.t == cu.nt - 1;
+                const bool drafted = x.t == x.nt - 1;
                 const CUtensorMap* map = drafted ? (is_v ? &tm_vn : &tm_kn) : (is_v ? &tm_v : &tm_k);
-                const int64_t nh = cu.u / k.rb;
-                const int n = (int)(nh / a.kv_heads), h = (int)(nh - (int64_t)n * a.kv_heads);
+                const int nh = x.u / k.rb, n = nh / a.kv_heads, h = nh - n * a.kv_heads;
 #pragma unroll
                 for (int kc = 0; kc < L::KCH; ++kc)
-                    ptx::tma_load_4d(dst + kc * L::CHUNK, map, fb, kc * 64, drafted ? 0 : cu.t * kTile, h, n);
+                    ptx::tma_load_4d(dst + kc * L::CHUNK, map, fb, kc * 64, drafted ? 0 : x.t * kTile, h, n);
                 ++cnt;
-                if (++cu.t == cu.nt) cu.next_unit(k);
-                return true;
+                ++x.t;
+                --x.tiles;
+                return 1;
             };
-            for (int t = 0; ok && t < n_tiles && t < L::LEAD; ++t) ok = load(false);
-            for (int t = 0; ok && t < n_tiles; ++t) {
-                ok = load(true);
-                if (ok && t + L::LEAD < n_tiles) ok = load(false);
+            int got = 1;
+            for (int t = 0; got == 1 && t < L::LEAD; ++t) got = load(false);
+            while (got >= 0) {
+                const int r = load(true);
+                if (r <= 0) break;
+                got = load(false);
             }
             // never leave a copy in flight into this CTA's shared memory
             for (int s = 0; s < L::KS && s < kt; ++s)
@@ -313,7 +343,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         const uint32_t kb0 = (uint32_t)ptx::sdesc_sw128(sK, 16, 1024);
         const uint32_t qb0 = (uint32_t)ptx::sdesc_sw128(sQ, 16, 1024);
         const uint32_t vb0 = (uint32_t)ptx::sdesc_sw128(sV, L::CHUNK, 1024);
-        Cursor cu = first;
+        Walk x = first;
         int g0 = 0, seg = 0;                             // tiles before this segment, segments done
         uint32_t p_par[2] = {0, 0};
         bool ok = true;
@@ -340,23 +370,26 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         auto issue_pv = [&](int j) -> bool {
             const int slot = j & 1, g = g0 + (SPLIT_ROWS ? j >> 1 : j), s = g % L::VS;
             if (!sy.wait(L::B_V_FULL + s, (uint32_t)((g / L::VS) & 1), kSiteKvFull)) return false;
-            if (!sy.wait(L::B_P_FULL + slot, p_par[slot], kSitePFull)) return false;
-            p_par[slot] ^= 1u;
-            ptx::tc_fence_after();
-            if (ptx::elect_one()) {
-                const uint32_t vb = vb0 + (uint32_t)s * (L::TILE >> 4);
+            // the first 64 keys' products run while the other 64 are exponentiated
 #pragma unroll
-                for (int ks = 0; ks < 8; ++ks)           // 16 keys per step
-                    ptx::umma_ts_lh(tmem + L::TM_O + 128u * slot, tmem + L::TM_S + 128u * slot + 8u * ks,
-                                    vb + 128u * ks, v_hi, idesc_o, (j > 1 || ks > 0) ? 1u : 0u);
-                if (!SPLIT_ROWS || slot == 1) ptx::umma_commit(sy.bar(L::B_V_EMPTY + s));
+            for (int hf = 0; hf < 2; ++hf) {
+                if (!sy.wait(L::B_P_FULL + 2 * slot + hf, p_par[slot], kSitePFull)) return false;
+                ptx::tc_fence_after();
+                if (ptx::elect_one()) {
+                    const uint32_t vb = vb0 + (uint32_t)s * (L::TILE >> 4);
+#pragma unroll
+                    for (int ks = 4 * hf; ks < 4 * hf + 4; ++ks)     // 16 keys per step
+                        ptx::umma_ts_lh(tmem + L::TM_O + 128u * slot, tmem + L::TM_S + 128u * slot + 8u * ks,
+                                        vb + 128u * ks, v_hi, idesc_o, (j > 1 || ks > 0) ? 1u : 0u);
+                    if (hf == 1 && (!SPLIT_ROWS || slot == 1)) ptx::umma_commit(sy.bar(L::B_V_EMPTY + s));
+                }
+                __syncwarp();
             }
-            __syncwarp();
+            p_par[slot] ^= 1u;
             return true;
         };
-        for (int64_t w = w0; ok && w < w1; ++seg) {
-            const int tiles = (int)min((int64_t)(cu.nt - cu.t), w1 - w);
-            const int jobs = SPLIT_ROWS ? 2 * tiles : tiles;
+        for (; ok && x.next(k); ++seg) {
+            const int jobs = SPLIT_ROWS ? 2 * x.tiles : x.tiles;
             if (!(ok = sy.wait(L::B_Q_FULL, (uint32_t)(seg & 1), kSiteQFull))) break;
             ptx::tc_fence_after();
             ok = issue_s(0);
@@ -368,23 +401,23 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             if (!ok) break;
             if (ptx::elect_one()) ptx::umma_commit(sy.bar(L::B_O_FULL));
             __syncwarp();
-            w += tiles;
-            g0 += tiles;
-            cu.next_unit(k);
+            g0 += x.tiles;
         }
         if (ptx::elect_one()) ptx::umma_commit(sy.bar(L::B_DRAIN));
         __syncwarp();
         sy.drain(L::B_DRAIN, 0);
+    }
     } else {
         // ------------------------------------------------ softmax / epilogue
-        const int slot = (warp - 2) >> 2, q4 = warp & 3;
-        const int st = (int)threadIdx.x - 64 - 128 * slot;       // thread of the slot
+        ptx::regs_inc<kRegsSoftmax>();
+        const int tid = (int)threadIdx.x - 128;
+        const int slot = tid >> 7, q4 = warp & 3;
+        const int st = tid & 127;                                // thread of the slot
         const int lrow = q4 * 32 + lane;                         // row of the row tile = TMEM lane
         const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
         const uint32_t t_s = tmem + L::TM_S + 128u * slot + lane_base;
         const uint32_t t_o = tmem + L::TM_O + 128u * slot + lane_base;
         const float sc = k.scale_log2;
-        Cursor cu = first;
         int g0 = 0, seg = 0;
         uint32_t s_par = 0, sync_par = 0;
         bool ok = true;
@@ -397,33 +430,49 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             sync_par ^= 1u;
             return r;
         };
-        for (int64_t w = w0; ok && w < w1; ++seg) {
-            const int tiles = (int)min((int64_t)(cu.nt - cu.t), w1 - w);
-            const int64_t nh = cu.u / k.rb;
-            const int rblk = (int)(cu.u - nh * k.rb);
-            const int n = (int)(nh / a.kv_heads), h = (int)(nh - (int64_t)n * a.kv_heads);
-            const int row_base = rblk * L::RT * kTile;
-            const int rows = min(L::RT * kTile, k.R - row_base);  // rows of this unit
-            // ---- Q: rows r = g * tokens + j, zeros past the last
-            {
-                constexpr int UPR = D / 8;                       // 16-byte units per row
-                const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q.data) + n * a.q.batch_stride;
-                for (int i = (int)threadIdx.x - 64; i < L::RT * kTile * UPR; i += 256) {
-                    const int r = i / UPR, x = i - r * UPR;
-                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                    if (r < rows) {
-                        const int g = (row_base + r) / a.tokens, j = row_base + r - g * a.tokens;
-                        v = *reinterpret_cast<const uint4*>(q + (int64_t)(h * k.G + g) * a.q.head_stride +
-                                                            j * a.q.token_stride + 8 * x);
-                    }
-                    *reinterpret_cast<uint4*>(base + L::OFF_Q + (r / kTile) * L::TILE + (x >> 3) * L::CHUNK +
-                                              (r % kTile) * 128 + (((x & 7) ^ (r & 7)) << 4)) = v;
+        // Q of a unit: rows r = g * tokens + j, zeros past the last; loaded
+        // into registers ahead of the previous unit's end, stored after it
+        constexpr int UPR = D / 8;                               // 16-byte units per row
+        constexpr int QN = L::RT * kTile * UPR / 256;            // of them per thread
+        uint4 qv[QN];
+        auto load_q = [&](int u) {
+            const int nh = u / k.rb, n = nh / a.kv_heads, h = nh - n * a.kv_heads;
+            const int row_base = (u - nh * k.rb) * L::RT * kTile;
+            const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q.data) + n * a.q.batch_stride;
+#pragma unroll
+            for (int i = 0; i < QN; ++i) {
+                const int r = row_base + (i * 256 + tid) / UPR, e = tid % UPR;
+                qv[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (r < k.R) {
+                    const int g = r / a.tokens, j = r - g * a.tokens;
+                    qv[i] = *reinterpret_cast<const uint4*>(q + (int64_t)(h * k.G + g) * a.q.head_stride +
+                                                            j * a.q.token_stride + 8 * e);
                 }
-                ptx::fence_proxy_async_smem();
-                ptx::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(sy.bar(L::B_Q_FULL));
             }
+        };
+        auto store_q = [&]() {
+#pragma unroll
+            for (int i = 0; i < QN; ++i) {
+                const int r = (i * 256 + tid) / UPR, e = tid % UPR;
+                *reinterpret_cast<uint4*>(base + L::OFF_Q + (r / kTile) * L::TILE + (e >> 3) * L::CHUNK +
+                                          (r % kTile) * 128 + (((e & 7) ^ (r & 7)) << 4)) = qv[i];
+            }
+            ptx::fence_proxy_async_smem();
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(sy.bar(L::B_Q_FULL));
+        };
+        Walk nx = first;                                         // one segment ahead
+        bool more = nx.next(k);
+        if (more) load_q(nx.u);
+        for (; ok && more; ++seg) {
+            const Walk cu = nx;
+            const int tiles = cu.tiles;
+            const int nh = cu.u / k.rb, rblk = cu.u - nh * k.rb;
+            const int n = nh / a.kv_heads, h = nh - n * a.kv_heads;
+            const int row_base = rblk * L::RT * kTile;
+            const int rows = min(L::RT * kTile, k.R - row_base); // rows of this unit
+            store_q();
             // this thread's row of the unit (both slots' threads have the
             // same row where they share the row tile)
             const int r = (SPLIT_ROWS ? slot * kTile : 0) + lrow;
@@ -479,35 +528,30 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                     ptx::fence_proxy_async_smem();
                 }
                 if (!idle) {
-                    // 64 scores at a time stay in registers: the upper half
-                    // is read again after the lower half became P (which
-                    // overwrites columns of the lower half only)
-                    uint32_t x[64];
-                    auto load = [&](int hh) {
-                        ptx::tmem_ld_32x32b_x64(t_s + 64 * hh, x);
-                        ptx::tmem_ld_wait();
-                        if (drafted) {
-                            // node e of the tree is key e; no key past 63
+                    uint32_t x[2][64];
+                    ptx::tmem_ld_32x32b_x64(t_s, x[0]);
+                    ptx::tmem_ld_32x32b_x64(t_s + 64, x[1]);
+                    ptx::tmem_ld_wait();
+                    if (drafted) {
+                        // node e of the tree is key e; no key past 63
 #pragma unroll
-                            for (int e = 0; e < 64; ++e)
-                                if (hh == 1 || !((sees >> e) & 1ull)) x[e] = 0xff800000u;
-                        } else if (valid < kTile) {
-#pragma unroll
-                            for (int e = 0; e < 64; ++e)
-                                if (64 * hh + e >= valid) x[e] = 0xff800000u;
+                        for (int e = 0; e < 64; ++e) {
+                            if (!((sees >> e) & 1ull)) x[0][e] = 0xff800000u;
+                            x[1][e] = 0xff800000u;
                         }
-                    };
+                    } else if (valid < kTile) {
+#pragma unroll
+                        for (int e = 0; e < 64; ++e) {
+                            if (e >= valid) x[0][e] = 0xff800000u;
+                            if (64 + e >= valid) x[1][e] = 0xff800000u;
+                        }
+                    }
                     float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                    for (int hh = 1; hh >= 0; --hh) {
-                        load(hh);
+                    for (int e = 0; e < 64; e += 2)
 #pragma unroll
-                        for (int e = 0; e < 64; e += 4)
-#pragma unroll
-                            for (int b = 0; b < 2; ++b)
-                                mx[b] = ptx::max3(mx[b], __uint_as_float(x[e + 2 * b]),
-                                                  __uint_as_float(x[e + 2 * b + 1]));
-                    }
+                        for (int b = 0; b < 2; ++b)
+                            mx[b] = ptx::max3(mx[b], __uint_as_float(x[b][e]), __uint_as_float(x[b][e + 1]));
                     const float top = fmaxf(mx[0], mx[1]) * sc;
                     const bool raise = top > m + kSlack;
                     if (__any_sync(0xffffffffu, raise)) {
@@ -533,28 +577,36 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                     for (int hh = 0; hh < 2; ++hh) {
-                        if (hh == 1) load(1);
                         uint32_t p[32];
 #pragma unroll
                         for (int e = 0; e < 32; ++e) {
-                            const float2 z = ptx::fma2(make_float2(__uint_as_float(x[2 * e]),
-                                                                   __uint_as_float(x[2 * e + 1])),
+                            const float2 z = ptx::fma2(make_float2(__uint_as_float(x[hh][2 * e]),
+                                                                   __uint_as_float(x[hh][2 * e + 1])),
                                                        make_float2(sc, sc), make_float2(nm, nm));
                             const float2 y = make_float2(ptx::ex2_approx(z.x), ptx::ex2_approx(z.y));
                             sum[e & 1] = ptx::add2(sum[e & 1], y);
                             p[e] = ptx::pack_bf16x2(y.x, y.y);
                         }
                         ptx::tmem_st_32x32b_x32(t_s + 32 * hh, p);
+                        ptx::tmem_st_wait();
+                        ptx::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(sy.bar(L::B_P_FULL + 2 * slot + hh));
                     }
                     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-                    ptx::tmem_st_wait();
+                } else {
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        ptx::mbar_arrive(sy.bar(L::B_P_FULL + 2 * slot));
+                        ptx::mbar_arrive(sy.bar(L::B_P_FULL + 2 * slot + 1));
+                    }
                 }
-                ptx::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(sy.bar(L::B_P_FULL + slot));
             }
             if (!ok) break;
-            // ---- end of the segment
+            // ---- end of the segment; the next one's Q is on its way meanwhile
+            more = nx.next(k);
+            if (more) load_q(nx.u);
             if (!(ok = sy.wait(L::B_O_FULL, (uint32_t)(seg & 1), kSiteOFull))) break;
             ptx::tc_fence_after();
             // the slots that share a row tile tell each other (m, l) through
@@ -564,7 +616,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             if (!(ok = sync_sm())) break;
             // the next segment's mask (every read of it was before the last
             // segment's second sync, every write comes after the next one)
-            if (threadIdx.x == 64) odd_nodes[(seg + 1) & 1] = 0ull;
+            if (tid == 0) odd_nodes[(seg + 1) & 1] = 0ull;
             const bool whole = cu.t == 0 && tiles == cu.nt;
             constexpr int COLS = SPLIT_ROWS ? D : D / 2;         // columns this thread merges
             const int c0 = SPLIT_ROWS ? 0 : slot * COLS;
@@ -585,15 +637,15 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             const float inv = whole ? (l > 0.f || l != l ? 1.f / l : 0.f) : 1.f;
             if (!idle) {
 #pragma unroll 1
-                for (int cc = 0; cc < COLS; cc += 32) {
-                    uint32_t o0[32], o1[32];
+                for (int cc = 0; cc < COLS; cc += 16) {
+                    uint32_t o0[16], o1[16];
                     __syncwarp();
-                    ptx::tmem_ld_32x32b_x32(t_o0 + cc, o0);
-                    if (use1) ptx::tmem_ld_32x32b_x32(t_o0 + 128 + cc, o1);
+                    ptx::tmem_ld_32x32b_x16(t_o0 + cc, o0);
+                    if (use1) ptx::tmem_ld_32x32b_x16(t_o0 + 128 + cc, o1);
                     ptx::tmem_ld_wait();
-                    float v[32];
+                    float v[16];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
+                    for (int e = 0; e < 16; ++e) {
                         v[e] = __uint_as_float(o0[e]) * f0;
                         if (use1) v[e] = fmaf(__uint_as_float(o1[e]), f1, v[e]);
                     }
@@ -604,7 +656,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                                                       n * a.v_new.batch_stride + h * a.v_new.head_stride +
                                                       (int64_t)(__ffsll((long long)b) - 1) * a.v_new.token_stride;
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) {
+                            for (int e = 0; e < 16; ++e) {
                                 const float y = __bfloat162float(vr[c0 + cc + e]);
                                 if (!(fabsf(y) < INFINITY)) v[e] += y;
                             }
@@ -616,7 +668,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                                              (int64_t)(h * k.G + gg) * a.out.head_stride +
                                              (int64_t)node * a.out.token_stride + c0 + cc;
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8)
+                        for (int e = 0; e < 16; e += 8)
                             *reinterpret_cast<uint4*>(out + e) =
                                 make_uint4(ptx::pack_bf16x2(v[e] * inv, v[e + 1] * inv),
                                            ptx::pack_bf16x2(v[e + 2] * inv, v[e + 3] * inv),
@@ -626,7 +678,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                         float4* po = reinterpret_cast<float4*>(k.part_o) +
                                      (sgm * (D / 4) + (c0 + cc) / 4) * k.rows + r;
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4)
+                        for (int e = 0; e < 16; e += 4)
                             po[(int64_t)(e / 4) * k.rows] = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
                     }
                 }
@@ -635,9 +687,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             ptx::tc_fence_before();
             // O and Q's memory are read: the next segment may write them
             if (!(ok = sync_sm())) break;
-            w += tiles;
             g0 += tiles;
-            cu.next_unit(k);
         }
     }
     __syncthreads();
@@ -650,97 +700,93 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
 // Merges the segments of a unit that several CTAs shared, in CTA order:
 //   O = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i
 // Thread = 4 columns of a row, consecutive threads consecutive rows (how the
-// partials lie).  kWays threads share one such output, each taking every
-// kWays-th segment: with one layer at 128 k rows a unit has up to 76.
-constexpr int kWays = 8;
-constexpr int kMergeOut = 32;                // outputs per CTA
+// partials lie).  Where a unit has many segments (one layer at 128 k rows: up
+// to 76) kWays threads share an output, each taking every kWays-th segment;
+// with up to kFew one thread takes them all and no barrier is needed.
+constexpr int kMergeThreads = 256;
+constexpr int kWays = 8, kFew = 8;
 
-template <int D>
-__global__ void __launch_bounds__(kWays * kMergeOut) tree_combine_kernel(const __grid_constant__ TreeKernelArgs k) {
-    const statekv_tree_args& a = k.a;
-    const int per_unit = (k.rows * (D / 4) + kMergeOut - 1) / kMergeOut;
-    const int64_t u = blockIdx.x / per_unit;
-    const int part = (int)(blockIdx.x - u * per_unit);
-    const int64_t per_seq = (int64_t)a.layers * a.kv_heads * k.rb;
-    const int s = (int)(u / per_seq);
-    int64_t before, all;
-    sum_tiles(k, s, before, all);
-    const Plan plan = make_plan(k, all);
-    const int nt = seq_tiles(k, s);
-    const int64_t w = before * per_seq + (u - s * per_seq) * nt;
-    const int ca = plan.cta_of(w), cb = plan.cta_of(w + nt - 1);
-    if (ca == cb) return;                    // written by the one CTA
-    const int rblk = (int)(u % k.rb);
-    const int row_tile = k.R > kTile ? 2 * kTile : kTile;
-    const int rows = min(row_tile, k.R - rblk * row_tile);
-    const int out = part * kMergeOut + (threadIdx.x % kMergeOut), way = threadIdx.x / kMergeOut;
-    const int c4 = out / rows, r = out - c4 * rows;
-    const bool live = c4 < D / 4;
-    __shared__ float s_m[kWays][kMergeOut], s_l[kWays][kMergeOut];
-    __shared__ float4 s_o[kWays][kMergeOut];
+struct Merge {
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    // adds (m2, l2, o2)
+    __device__ void add(float m2, float l2, float4 o2) {
+        const float mn = fmaxf(m, m2);
+        const float f = m == -INFINITY ? 0.f : ptx::ex2_approx(m - mn);
+        const float g = m2 == -INFINITY ? 0.f : ptx::ex2_approx(m2 - mn);
+        l = l * f + l2 * g;
+        o.x = o.x * f + o2.x * g;
+        o.y = o.y * f + o2.y * g;
+        o.z = o.z * f + o2.z * g;
+        o.w = o.w * f + o2.w * g;
+        m = mn;
+    }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) tree_combine_kernel(const __grid_constant__ TreeKernelArgs k,
+                                                                     int per_unit) {
+    const statekv_tree_args& a = k.a;
+    const int u = blockIdx.x / per_unit, part = blockIdx.x - u * per_unit;
+    const int per_seq = a.layers * a.kv_heads * k.rb;
+    const int s = u / per_seq;
+    int64_t before, all;
+    sum_costs(k, s, before, all);
+    const Plan plan = make_plan(k, all);
+    const int nt = unit_tiles(seq_length(k, s));
+    const int64_t w = before * per_seq + (int64_t)(u - s * per_seq) * (nt + kUnitCost) + kUnitCost;
+    const int ca = plan.cta_of(w), segs = plan.cta_of(w + nt - 1) - ca + 1;
+    if (segs == 1) return;                   // written by the one CTA
+    const int nh = u / k.rb, rblk = u - nh * k.rb;
+    const int row_tile = k.R > kTile ? 2 * kTile : kTile;
+    const int rows = min(row_tile, k.R - rblk * row_tile);
+    const int n = nh / a.kv_heads, h = nh - n * a.kv_heads;
+    const int outs = rows * (D / 4);
+    const int ways = segs > kFew ? kWays : 1;
+    const int per_step = kMergeThreads / ways, x = threadIdx.x % per_step, way = threadIdx.x / per_step;
+    __shared__ Merge sh[kMergeThreads];
+    const float2* ml0 = k.part_ml + ((int64_t)ca + u) * k.rows;
+    const float4* po0 = reinterpret_cast<const float4*>(k.part_o) + ((int64_t)ca + u) * (D / 4) * k.rows;
     ptx::dep_wait();                         // the segments are written
-    if (live) {
-        const float2* ml = k.part_ml + (ca + u) * k.rows + r;
-        const float4* po = reinterpret_cast<const float4*>(k.part_o) + ((ca + u) * (D / 4) + c4) * k.rows + r;
-        const int n = cb - ca + 1;
-        constexpr int B = 4;
-        for (int i0 = way; i0 < n; i0 += B * kWays) {
-            float2 x[B];
-            float4 y[B];
+    for (int out0 = part * per_step; out0 < outs; out0 += per_unit * per_step) {
+        const int out = out0 + x, c4 = out / rows, r = out - c4 * rows;
+        const bool live = out < outs;
+        Merge acc;
+        if (live) {
+            constexpr int B = 4;
+            for (int i0 = way; i0 < segs; i0 += B * ways) {
+                float2 ml[B];
+                float4 y[B];
 #pragma unroll
-            for (int b = 0; b < B; ++b) {
-                const int i = i0 + b * kWays;
-                x[b] = make_float2(-INFINITY, 0.f);
-                y[b] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (i < n) {
-                    x[b] = ml[(int64_t)i * k.rows];
-                    y[b] = po[(int64_t)i * (D / 4) * k.rows];
+                for (int b = 0; b < B; ++b) {
+                    const int64_t i = i0 + b * ways;
+                    ml[b] = make_float2(-INFINITY, 0.f);
+                    y[b] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (i < segs) {
+                        ml[b] = ml0[i * k.rows + r];
+                        y[b] = po0[(i * (D / 4) + c4) * k.rows + r];
+                    }
                 }
-            }
 #pragma unroll
-            for (int b = 0; b < B; ++b) {
-                const float mn = fmaxf(m, x[b].x);
-                const float f = m == -INFINITY ? 0.f : ptx::ex2_approx(m - mn);
-                const float g = x[b].x == -INFINITY ? 0.f : ptx::ex2_approx(x[b].x - mn);
-                l = l * f + x[b].y * g;
-                o.x = o.x * f + y[b].x * g;
-                o.y = o.y * f + y[b].y * g;
-                o.z = o.z * f + y[b].z * g;
-                o.w = o.w * f + y[b].w * g;
-                m = mn;
+                for (int b = 0; b < B; ++b) acc.add(ml[b].x, ml[b].y, y[b]);
             }
         }
+        if (ways > 1) {
+            __syncthreads();                 // the last step's entries are read
+            sh[threadIdx.x] = acc;
+            __syncthreads();
+            if (way != 0) continue;
+#pragma unroll 1
+            for (int i = 1; i < kWays; ++i) acc.add(sh[i * per_step + x].m, sh[i * per_step + x].l, sh[i * per_step + x].o);
+        }
+        if (!live) continue;
+        const float inv = acc.l > 0.f || acc.l != acc.l ? 1.f / acc.l : 0.f;
+        const int row = rblk * row_tile + r, gg = row / a.tokens, j = row - gg * a.tokens;
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out.data) + n * a.out.batch_stride +
+                             (int64_t)(h * k.G + gg) * a.out.head_stride + (int64_t)j * a.out.token_stride + c4 * 4;
+        *reinterpret_cast<uint2*>(dst) = make_uint2(ptx::pack_bf16x2(acc.o.x * inv, acc.o.y * inv),
+                                                    ptx::pack_bf16x2(acc.o.z * inv, acc.o.w * inv));
     }
-    s_m[way][threadIdx.x % kMergeOut] = m;
-    s_l[way][threadIdx.x % kMergeOut] = l;
-    s_o[way][threadIdx.x % kMergeOut] = o;
-    __syncthreads();
-    if (way != 0 || !live) return;
-    const int x = threadIdx.x;
-    float mm = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < kWays; ++i) mm = fmaxf(mm, s_m[i][x]);
-    float ls = 0.f;
-    o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int i = 0; i < kWays; ++i) {
-        const float g = s_m[i][x] == -INFINITY ? 0.f : ptx::ex2_approx(s_m[i][x] - mm);
-        ls += s_l[i][x] * g;
-        o.x += s_o[i][x].x * g;
-        o.y += s_o[i][x].y * g;
-        o.z += s_o[i][x].z * g;
-        o.w += s_o[i][x].w * g;
-    }
-    const float inv = ls > 0.f || ls != ls ? 1.f / ls : 0.f;
-    const int64_t nh = u / k.rb;
-    const int n = (int)(nh / a.kv_heads), h = (int)(nh - (int64_t)n * a.kv_heads);
-    const int row = rblk * row_tile + r, gg = row / a.tokens, j = row - gg * a.tokens;
-    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out.data) + n * a.out.batch_stride +
-                         (int64_t)(h * k.G + gg) * a.out.head_stride + (int64_t)j * a.out.token_stride + c4 * 4;
-    *reinterpret_cast<uint2*>(dst) = make_uint2(ptx::pack_bf16x2(o.x * inv, o.y * inv),
-                                                ptx::pack_bf16x2(o.z * inv, o.w * inv));
 }
 
 struct TreeMaps {
@@ -758,19 +804,22 @@ cudaError_t launch_main(const TreeKernelArgs& k, const TreeMaps& m, cudaStream_t
 }
 
 template <int D>
-cudaError_t launch_combine(const TreeKernelArgs& k, int64_t units, cudaStream_t st) {
-    const int64_t per_unit = (k.rows * (D / 4) + kMergeOut - 1) / kMergeOut;
+cudaError_t launch_combine(const TreeKernelArgs& k, int64_t units, int sms, cudaStream_t st) {
+    // about eight CTAs per SM, but no more than there are steps of the
+    // many-segment form
+    const int64_t steps = (k.rows * (D / 4) + kMergeThreads / kWays - 1) / (kMergeThreads / kWays);
+    const int64_t per_unit = std::min<int64_t>(steps, std::max<int64_t>(1, 8 * sms / units));
     if (units * per_unit > 0x7fffffff) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(units * per_unit));
-    cfg.blockDim = dim3(kWays * kMergeOut);
+    cfg.blockDim = dim3(kMergeThreads);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, tree_combine_kernel<D>, k);
+    return cudaLaunchKernelEx(&cfg, tree_combine_kernel<D>, k, (int)per_unit);
 }
 
 // Sizes that follow from the arguments; false where they are refused.
@@ -864,8 +913,9 @@ extern "C" int statekv_tree_attention(const statekv_tree_args* args, void* cuda_
     k.G = z.G; k.R = z.R; k.rb = z.rb; k.rows = z.rows;
     k.scale_log2 = (float)(a.scale * 1.4426950408889634074);
     // no more CTAs than the longest cache could use
-    const int64_t most = z.units * (((int64_t)(a.lengths ? a.cache_rows : a.length) + kTile - 1) / kTile + 1);
-    k.grid = (int)std::min<int64_t>(sms, (most + kMinTiles - 1) / kMinTiles);
+    const int64_t most =
+        z.units * (((int64_t)(a.lengths ? a.cache_rows : a.length) + kTile - 1) / kTile + 1 + kUnitCost);
+    k.grid = (int)std::min<int64_t>(sms, (most + kMinShare - 1) / kMinShare);
     const int64_t segments = (int64_t)sms + z.units;
     k.part_o = static_cast<float*>(a.workspace);
     k.part_ml = reinterpret_cast<float2*>(k.part_o + segments * z.rows * a.head_dim);
@@ -875,6 +925,6 @@ extern "C" int statekv_tree_attention(const statekv_tree_args* args, void* cuda_
                                       : (two ? launch_main<64, true>(k, m, st) : launch_main<64, false>(k, m, st));
     // one CTA holds whole units only
     if (e == cudaSuccess && k.grid > 1)
-        e = a.head_dim == 128 ? launch_combine<128>(k, z.units, st) : launch_combine<64>(k, z.units, st);
+        e = a.head_dim == 128 ? launch_combine<128>(k, z.units, sms, st) : launch_combine<64>(k, z.units, sms, st);
     return e == cudaSuccess ? STATEKV_OK : view_cuda_fail();
 }
