@@ -56,7 +56,7 @@ constexpr int kMinShare = 4;                 // least share (in tiles' time) bef
 constexpr int kTreeThreads = 384;
 // registers a thread after the split: 128 threads of the first warpgroup and
 // 256 softmax threads, together the 168 x 384 of the launch
-constexpr int kRegsIssue = 56, kRegsSoftmax = 224;
+constexpr int kRegsIssue = 40, kRegsSoftmax = 232;
 static_assert(kRegsIssue + 2 * kRegsSoftmax <= 3 * 168, "registers of the launch");
 
 struct TreeKernelArgs {
@@ -65,8 +65,15 @@ struct TreeKernelArgs {
     float2* part_ml;                         // [segments][rows] (reference, sum)
     float scale_log2;
     int32_t G, R, rb, rows;                  // rows: most rows of a unit
+    uint32_t inv_tokens;                     // floor(2^32 / tokens) + 1
     int32_t grid;                            // CTAs of the main kernel
 };
+
+// r / tokens for a query row r < 65536: the high word of r * (2^32 / tokens,
+// rounded up) is off by less than r / 2^32 < 1 / tokens, so exact
+__device__ __forceinline__ int head_of(const TreeKernelArgs& k, int r) {
+    return k.a.tokens == 1 ? r : (int)__umulhi((uint32_t)r, k.inv_tokens);
+}
 
 // The schedule, from the sequences' lengths.  A unit of nt key tiles counts as
 // kUnitCost + nt tiles (it starts with kUnitCost of no content): without that
@@ -430,33 +437,27 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             sync_par ^= 1u;
             return r;
         };
-        // Q of a unit: rows r = g * tokens + j, zeros past the last; loaded
-        // into registers ahead of the previous unit's end, stored after it
+        // Q of a unit, rows r = g * tokens + j and zeros past the last: copied
+        // asynchronously while the previous unit's output is written (held in
+        // registers over that time, the loads were spilled one by one: 7 us)
         constexpr int UPR = D / 8;                               // 16-byte units per row
-        constexpr int QN = L::RT * kTile * UPR / 256;            // of them per thread
-        uint4 qv[QN];
         auto load_q = [&](int u) {
             const int nh = u / k.rb, n = nh / a.kv_heads, h = nh - n * a.kv_heads;
             const int row_base = (u - nh * k.rb) * L::RT * kTile;
-            const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q.data) + n * a.q.batch_stride;
-#pragma unroll
-            for (int i = 0; i < QN; ++i) {
-                const int r = row_base + (i * 256 + tid) / UPR, e = tid % UPR;
-                qv[i] = make_uint4(0u, 0u, 0u, 0u);
-                if (r < k.R) {
-                    const int g = r / a.tokens, j = r - g * a.tokens;
-                    qv[i] = *reinterpret_cast<const uint4*>(q + (int64_t)(h * k.G + g) * a.q.head_stride +
-                                                            j * a.q.token_stride + 8 * e);
-                }
+            const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q.data) + n * a.q.batch_stride +
+                                     (int64_t)(h * k.G) * a.q.head_stride + 8 * (tid % UPR);
+            const int e = tid % UPR;
+#pragma unroll 4
+            for (int r = tid / UPR; r < L::RT * kTile; r += 256 / UPR) {
+                const int rq = row_base + r, g = head_of(k, rq), j = rq - g * a.tokens;
+                const bool there = rq < k.R;
+                ptx::cp_async_16(sQ + (r / kTile) * L::TILE + (e >> 3) * L::CHUNK + (r % kTile) * 128 +
+                                     (((e & 7) ^ (r & 7)) << 4),
+                                 there ? q + g * a.q.head_stride + j * a.q.token_stride : q, there ? 16u : 0u);
             }
         };
-        auto store_q = [&]() {
-#pragma unroll
-            for (int i = 0; i < QN; ++i) {
-                const int r = (i * 256 + tid) / UPR, e = tid % UPR;
-                *reinterpret_cast<uint4*>(base + L::OFF_Q + (r / kTile) * L::TILE + (e >> 3) * L::CHUNK +
-                                          (r % kTile) * 128 + (((e & 7) ^ (r & 7)) << 4)) = qv[i];
-            }
+        auto q_ready = [&]() {
+            ptx::cp_async_wait();
             ptx::fence_proxy_async_smem();
             ptx::tc_fence_before();
             __syncwarp();
@@ -472,12 +473,13 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             const int n = nh / a.kv_heads, h = nh - n * a.kv_heads;
             const int row_base = rblk * L::RT * kTile;
             const int rows = min(L::RT * kTile, k.R - row_base); // rows of this unit
-            store_q();
+            q_ready();
             // this thread's row of the unit (both slots' threads have the
             // same row where they share the row tile)
             const int r = (SPLIT_ROWS ? slot * kTile : 0) + lrow;
             const bool live = r < rows;
-            const int node = live ? (row_base + r) % a.tokens : 0;
+            const int gg = head_of(k, row_base + r);                 // of the head group
+            const int node = live ? row_base + r - gg * a.tokens : 0;
             uint64_t sees = 0;
             if (live) sees = a.tree[(int64_t)cu.s * a.tree_stride + node];
             if (a.tokens < 64) sees &= (1ull << a.tokens) - 1ull;
@@ -604,19 +606,25 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                 }
             }
             if (!ok) break;
-            // ---- end of the segment; the next one's Q is on its way meanwhile
-            more = nx.next(k);
-            if (more) load_q(nx.u);
+            // ---- end of the segment
             if (!(ok = sy.wait(L::B_O_FULL, (uint32_t)(seg & 1), kSiteOFull))) break;
             ptx::tc_fence_after();
             // the slots that share a row tile tell each other (m, l) through
-            // Q's memory, which no product reads any more
-            float2* ml = reinterpret_cast<float2*>(base + L::OFF_Q);
-            if (!SPLIT_ROWS) ml[slot * kTile + lrow] = make_float2(m, l);
-            if (!(ok = sync_sm())) break;
+            // the scores' tensor memory, which no product uses any more
+            if (!SPLIT_ROWS) {
+                const uint32_t x[2] = {__float_as_uint(m), __float_as_uint(l)};
+                ptx::tmem_st_32x32b_x2(t_s, x);
+                ptx::tmem_st_wait();
+            }
             // the next segment's mask (every read of it was before the last
             // segment's second sync, every write comes after the next one)
             if (tid == 0) odd_nodes[(seg + 1) & 1] = 0ull;
+            ptx::tc_fence_before();
+            if (!(ok = sync_sm())) break;
+            ptx::tc_fence_after();
+            // Q's memory is free: the next unit's copy runs from here on
+            more = nx.next(k);
+            if (more) load_q(nx.u);
             const bool whole = cu.t == 0 && tiles == cu.nt;
             constexpr int COLS = SPLIT_ROWS ? D : D / 2;         // columns this thread merges
             const int c0 = SPLIT_ROWS ? 0 : slot * COLS;
@@ -624,7 +632,12 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             bool use1 = false;
             uint32_t t_o0 = t_o;
             if (!SPLIT_ROWS) {
-                const float2 x0 = ml[lrow], x1 = ml[kTile + lrow];
+                uint32_t y[4];
+                ptx::tmem_ld_32x32b_x2(tmem + L::TM_S + lane_base, y[0], y[1]);
+                ptx::tmem_ld_32x32b_x2(tmem + L::TM_S + 128 + lane_base, y[2], y[3]);
+                ptx::tmem_ld_wait();
+                const float2 x0 = make_float2(__uint_as_float(y[0]), __uint_as_float(y[1]));
+                const float2 x1 = make_float2(__uint_as_float(y[2]), __uint_as_float(y[3]));
                 use1 = tiles > 1;                                // slot 1 had a tile
                 m = fmaxf(x0.x, use1 ? x1.x : -INFINITY);
                 f0 = x0.x == -INFINITY ? 0.f : ptx::ex2_approx(x0.x - m);
@@ -663,7 +676,6 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                         }
                     }
                     if (live && whole) {
-                        const int gg = (row_base + r) / a.tokens;
                         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out.data) + n * a.out.batch_stride +
                                              (int64_t)(h * k.G + gg) * a.out.head_stride +
                                              (int64_t)node * a.out.token_stride + c0 + cc;
@@ -685,7 +697,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                 if (live && !whole && c0 == 0) k.part_ml[sgm * k.rows + r] = make_float2(m, l);
             }
             ptx::tc_fence_before();
-            // O and Q's memory are read: the next segment may write them
+            // O and the scores' memory are read: the next segment may write them
             if (!(ok = sync_sm())) break;
             g0 += tiles;
         }
@@ -781,7 +793,7 @@ __global__ void __launch_bounds__(kMergeThreads) tree_combine_kernel(const __gri
         }
         if (!live) continue;
         const float inv = acc.l > 0.f || acc.l != acc.l ? 1.f / acc.l : 0.f;
-        const int row = rblk * row_tile + r, gg = row / a.tokens, j = row - gg * a.tokens;
+        const int row = rblk * row_tile + r, gg = head_of(k, row), j = row - gg * a.tokens;
         __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out.data) + n * a.out.batch_stride +
                              (int64_t)(h * k.G + gg) * a.out.head_stride + (int64_t)j * a.out.token_stride + c4 * 4;
         *reinterpret_cast<uint2*>(dst) = make_uint2(ptx::pack_bf16x2(acc.o.x * inv, acc.o.y * inv),
@@ -911,6 +923,7 @@ extern "C" int statekv_tree_attention(const statekv_tree_args* args, void* cuda_
     TreeKernelArgs k{};
     k.a = a;
     k.G = z.G; k.R = z.R; k.rb = z.rb; k.rows = z.rows;
+    k.inv_tokens = (uint32_t)((1ull << 32) / (uint32_t)a.tokens + 1);
     k.scale_log2 = (float)(a.scale * 1.4426950408889634074);
     // no more CTAs than the longest cache could use
     const int64_t most =
