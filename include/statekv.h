@@ -229,10 +229,63 @@ int statekv_prefill_frames_host(statekv_handle* h, int32_t frames, const void* q
  * (n*T + decoded + tokens > max_frames*T).  Once a handle has decoded text,
  * the prefill entry points return E_INVALID_ARG until statekv_reset.  The
  * first call allocates the handle's decode scratch (partial results per
- * 2048-key chunk of D; E_OOM if that fails).
+ * 2048-key chunk of D; E_OOM if that fails).  The first call of this and the
+ * entry points below that allocate cannot be captured into a CUDA graph.
  */
 int statekv_decode(statekv_handle* h, int32_t tokens, const void* q, const void* k,
                    const void* v, void* o, void* cuda_stream);
+
+/*
+ * RMS norm of the heads of Q and K ahead of the rotation, for models that
+ * have one (Qwen3-VL): from this call on the prefill and decode entry points
+ * compute x * w / sqrt(mean(x^2) + eps) in fp32 for every head of q and k
+ * before they rotate it, w = q_weight or k_weight of the head's layer, float
+ * [num_layers][head_dim], DEVICE memory (16-byte aligned) copied on
+ * cuda_stream.  Both NULL turns the norm off again; one NULL is
+ * E_INVALID_ARG.  The first call allocates the handle's copy.
+ */
+int statekv_set_qk_norm(statekv_handle* h, const float* q_weight, const float* k_weight, float eps,
+                        void* cuda_stream);
+
+/*
+ * One verification step of speculative decoding over the detailed state: a
+ * tree of `tokens` (1..64, at most T) drafted tokens attends over every D row
+ * and, among itself, where its masks say.
+ *   tree:  uint64 DEVICE [num_streams][tokens], bit j of entry i set where node
+ *          i sees node j (its ancestors and itself);
+ *   depth: int32 DEVICE [num_streams][tokens]: node i is at position
+ *          position_offset + n*T + decoded text + depth[i].
+ * q, k, v, o as for statekv_decode.  The drafted K', V stay in the handle's
+ * own draft rows: D, its count and the text count do not change, so a call can
+ * be repeated, until statekv_accept takes a path over.  bf16, head_dim 64 or
+ * 128, G <= 64 (else E_UNSUPPORTED).  The first call allocates the draft rows
+ * and the workspace (E_OOM).
+ */
+int statekv_decode_tree(statekv_handle* h, int32_t tokens, const void* q, const void* k, const void* v,
+                        const uint64_t* tree, const int32_t* depth, void* o, void* cuda_stream);
+
+/*
+ * The accepted path of the last statekv_decode_tree becomes text: K', V of
+ * nodes path[s][0..count-1] (int32 DEVICE [num_streams][count], a path from a
+ * node of depth 0 down, so that node i of it is at depth i; the same count
+ * for every stream) are appended to D and the text count grows by count.
+ * E_INVALID_ARG without such a step before it, or count > its tokens;
+ * E_CAPACITY when the rows do not fit.  A node out of range is recorded in the
+ * device status and its row skipped.  count = 0 drops the draft.
+ */
+int statekv_accept(statekv_handle* h, int32_t count, const int32_t* path, void* cuda_stream);
+
+/*
+ * statekv_decode with block-sparse attention (statekv_sparse_attention below):
+ * each new token attends to the `top` (1..1024) 64-row blocks of D that 8-bit
+ * scores of its query choose per KV head, and to the rows since the last
+ * complete block.  Block summaries of D are kept by the handle and brought up
+ * to date by this call.  tokens 1..T; bf16, head_dim 64 or 128, G <= 16, D of
+ * at most 2,097,152 rows (else E_UNSUPPORTED).  The first call allocates the
+ * summaries (E_OOM).
+ */
+int statekv_decode_sparse(statekv_handle* h, int32_t tokens, int32_t top, const void* q, const void* k,
+                          const void* v, void* o, void* cuda_stream);
 
 /* Text tokens decoded since the last reset (-1 for a NULL handle). */
 int64_t statekv_text_tokens(const statekv_handle* h);
@@ -285,8 +338,8 @@ int statekv_get_scores(statekv_handle* h, int32_t s, int32_t layer,
                        int32_t* m, int32_t* pitch);
 
 /* Borrowed DEVICE pointer to the rotated queries Q' of the last frame step
- * ([S][L][Hq][T][d], storage dtype) or, after a text decode, of the last
- * decode step ([S][L][Hq][tokens][d]).  Valid until the next step. */
+ * ([S][L][Hq][T][d], storage dtype) or, after a text decode (dense, sparse or
+ * a tree), of the last such step ([S][L][Hq][tokens][d]).  Valid until the next step. */
 int statekv_get_rotated_query(statekv_handle* h, const void** q_rot);
 
 /* Set the frame index n (teacher forcing / resume); 0 <= n < max_frames. */
@@ -421,10 +474,13 @@ typedef struct statekv_view {
  * (element k with element k + head_dim/2), in fp32, rounded once.
  *   q -> q_out rows t; k -> k_out and v -> v_out rows out_rows[sequence] + t
  *   (row t where out_rows is NULL), of out_capacity rows.
- * q_weight, k_weight [head_dim] in weight_dtype, or NULL: no norm of that
- * tensor.  omega: float64 [head_dim/2], radians per position.  positions:
- * int32 [batch / position_layers][position_stride >= tokens], or
- * position_stride 0 for one row shared by all; NULL: position0 + t.  v.data
+ * q_weight, k_weight [weight_rows][head_dim] in weight_dtype (16-byte
+ * aligned), batch entry n using row n % weight_rows (1: one weight for all;
+ * the number of layers: one per layer); NULL: no norm of that tensor.  omega:
+ * float64 [head_dim/2], radians per position.  Token t is at position
+ * position0 + positions[n / position_layers][t] (int32, rows position_stride
+ * >= tokens apart, 0 for one row shared by all), position0 + t where
+ * positions is NULL.  v.data
  * and v_out.data may both be NULL.  Each output may be its own input (the
  * same view).  A sequence whose rows do not fit in k_out is recorded, and its
  * K and V are not stored.
@@ -441,7 +497,7 @@ typedef struct statekv_norm_rope_args {
     int64_t position0;
     int32_t position_stride, position_layers;
     int32_t batch, layers, q_heads, kv_heads, tokens, head_dim;
-    int32_t out_capacity;
+    int32_t out_capacity, weight_rows;
     int32_t dtype, weight_dtype;
     float eps;
 } statekv_norm_rope_args;

@@ -43,6 +43,7 @@ EXPORTS = (
     "statekv_norm_rope", "statekv_tree_attention", "statekv_tree_attention_workspace",
     "statekv_append_accepted", "statekv_block_summaries",
     "statekv_sparse_attention",
+    "statekv_set_qk_norm", "statekv_decode_tree", "statekv_accept", "statekv_decode_sparse",
 )
 
 BLOCK = 64          # STATEKV_BLOCK
@@ -76,7 +77,7 @@ NormRopeArgs = _struct(
     "NormRopeArgs", (View, "q k v q_out k_out v_out"),
     (C.c_void_p, "q_weight k_weight omega positions out_rows status"), (C.c_int64, "position0"),
     (C.c_int32, "position_stride position_layers batch layers q_heads kv_heads tokens head_dim "
-                "out_capacity dtype weight_dtype"), (C.c_float, "eps"))
+                "out_capacity weight_rows dtype weight_dtype"), (C.c_float, "eps"))
 TreeArgs = _struct(
     "TreeArgs", (View, "q out k_new v_new k_cache v_cache"),
     (C.c_void_p, "tree lengths status workspace"), (C.c_int64, "workspace_bytes"),
@@ -131,6 +132,10 @@ def load() -> C.CDLL:
         "statekv_frame_index": (C.c_int64, [h]),
         "statekv_decode": (C.c_int, [h, C.c_int32, _P, _P, _P, _P, _P]),
         "statekv_text_tokens": (C.c_int64, [h]),
+        "statekv_set_qk_norm": (C.c_int, [h, _P, _P, C.c_float, _P]),
+        "statekv_decode_tree": (C.c_int, [h, C.c_int32, _P, _P, _P, _P, _P, _P, _P]),
+        "statekv_accept": (C.c_int, [h, C.c_int32, _P, _P]),
+        "statekv_decode_sparse": (C.c_int, [h, C.c_int32, C.c_int32, _P, _P, _P, _P, _P]),
         "statekv_reset": (C.c_int, [h]),
         "statekv_check_device_status": (C.c_int, [h, _P]),
         "statekv_get_scores": (C.c_int, [h, C.c_int32, C.c_int32, _PP, _PP,

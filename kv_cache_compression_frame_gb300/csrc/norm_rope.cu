@@ -77,21 +77,31 @@ struct NormRopeKernelArgs {
     int64_t items;                   // batch * tokens * chunks
 };
 
-__device__ __forceinline__ float weight_at(const void* w, int dtype, int k) {
-    return dtype == STATEKV_F32 ? static_cast<const float*>(w)[k]
-                                : __bfloat162float(static_cast<const __nv_bfloat16*>(w)[k]);
+// VEC weights from element `at` on (an aligned multiple of VEC)
+template <int VEC>
+__device__ __forceinline__ void load_weights(const void* w, int dtype, int64_t at, float (&x)[VEC]) {
+    if (dtype == STATEKV_F32) {
+        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(w) + at);
+#pragma unroll
+        for (int i = 0; i < VEC / 4; ++i) {
+            const float4 f = p[i];
+            x[4 * i] = f.x; x[4 * i + 1] = f.y; x[4 * i + 2] = f.z; x[4 * i + 3] = f.w;
+        }
+    } else {
+        const uint2* p = reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(w) + at);
+#pragma unroll
+        for (int i = 0; i < VEC / 4; ++i) {
+            const uint2 u = p[i];
+            x[4 * i] = __uint_as_float(u.x << 16); x[4 * i + 1] = __uint_as_float(u.x & 0xffff0000u);
+            x[4 * i + 2] = __uint_as_float(u.y << 16); x[4 * i + 3] = __uint_as_float(u.y & 0xffff0000u);
+        }
+    }
 }
 
 template <typename E, int D>
 __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ NormRopeKernelArgs ka) {
     constexpr int VEC = Row<E>::N, HALF = D / 2, TPR = HALF / VEC;
     const statekv_norm_rope_args& a = ka.a;
-    __shared__ float s_w[2][D];                              // weights of Q and K (1 where none)
-    for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
-        const void* w = i < D ? a.q_weight : a.k_weight;
-        s_w[i / D][i % D] = w ? weight_at(w, a.weight_dtype, i % D) : 1.f;
-    }
-    __syncthreads();
     const int64_t item = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / TPR;
     const int j = threadIdx.x % TPR;
     // whole groups leave together: the shuffles below stay within a group
@@ -119,8 +129,8 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
         }
     }
     const int seq = (int)(n / a.layers);
-    const int64_t p = a.positions ? (int64_t)a.positions[n / a.position_layers * a.position_stride + t]
-                                  : a.position0 + t;
+    const int64_t p = a.position0 +
+                      (a.positions ? (int64_t)a.positions[n / a.position_layers * a.position_stride + t] : t);
     float c[VEC], s[VEC];
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
@@ -132,6 +142,8 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
     const bool fits = row0 >= 0 && row0 <= a.out_capacity - a.tokens;
     if (!fits && j == 0 && h0 == 0)
         record_error(a.status, (uint32_t)STATEKV_E_DEVICE, kSiteLength, (uint32_t)row0);
+    const int64_t w_row = n % a.weight_rows * D;             // weights of this entry's layer
+    float wl[VEC], wh[VEC];
 #pragma unroll
     for (int i = 0; i < kHeads; ++i) {
         const int h = h0 + i;
@@ -141,18 +153,22 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
             float x[VEC], y[VEC];
             Row<E>::unpack(lo[i], x);
             Row<E>::unpack(hi[i], y);
-            if (isq ? a.q_weight != nullptr : a.k_weight != nullptr) {
+            const void* weight = isq ? a.q_weight : a.k_weight;
+            if (weight) {
+                if (i == 0 || h == a.q_heads) {              // the first of its kind here
+                    load_weights<VEC>(weight, a.weight_dtype, w_row + k0, wl);
+                    load_weights<VEC>(weight, a.weight_dtype, w_row + HALF + k0, wh);
+                }
                 float ss = 0.f;
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) ss = fmaf(x[e], x[e], fmaf(y[e], y[e], ss));
 #pragma unroll
                 for (int off = TPR / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(group, ss, off);
                 const float r = rsqrtf(ss * (1.f / D) + a.eps);
-                const float* w = s_w[isq ? 0 : 1];
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
-                    x[e] *= r * w[k0 + e];
-                    y[e] *= r * w[HALF + k0 + e];
+                    x[e] *= r * wl[e];
+                    y[e] *= r * wh[e];
                 }
             }
 #pragma unroll
@@ -204,12 +220,14 @@ extern "C" int statekv_norm_rope(const statekv_norm_rope_args* args, void* cuda_
     if (a.dtype != STATEKV_BF16 && a.dtype != STATEKV_F32) return STATEKV_E_INVALID_ARG;
     if (a.weight_dtype != STATEKV_BF16 && a.weight_dtype != STATEKV_F32) return STATEKV_E_INVALID_ARG;
     if (a.batch < 0 || a.layers < 1 || a.batch % a.layers != 0 || a.tokens < 0 || a.q_heads < 0 ||
-        a.kv_heads < 0 || a.position_stride < 0 || a.position_layers < 1 || a.out_capacity < 0 || !(a.eps >= 0.f))
+        a.kv_heads < 0 || a.position_stride < 0 || a.position_layers < 1 || a.weight_rows < 1 || a.out_capacity < 0 || !(a.eps >= 0.f))
         return STATEKV_E_INVALID_ARG;
     if (a.head_dim != 64 && a.head_dim != 128) return STATEKV_E_UNSUPPORTED;
     if (!a.status || reinterpret_cast<uintptr_t>(a.status) % 4 || !a.omega ||
         reinterpret_cast<uintptr_t>(a.omega) % 8)
         return STATEKV_E_INVALID_ARG;
+    for (const void* w : {a.q_weight, a.k_weight})
+        if (w && !aligned16(w)) return STATEKV_E_INVALID_ARG;
     const int es = a.dtype == STATEKV_BF16 ? 2 : 4;
     if (a.q_heads > 0 && (!view_ok(a.q, es) || !view_ok(a.q_out, es))) return STATEKV_E_INVALID_ARG;
     if (a.kv_heads > 0) {

@@ -75,8 +75,10 @@ template <> struct Vec<float> {
 // 32-byte chunk pair of inputs in flight, so occupancy sets the bytes in
 // flight (5 CTAs at 48 registers: 15.4 us on the 2B stack, 6: 14.6 us; 8 at 32
 // registers spills: 17.9 us; two chunk pairs per thread: 16.6 us)
-template <typename E>
-__global__ void __launch_bounds__(256, 6) rope_kernel(RopeArgs a) {
+// NORM: the heads of Q and K are normalised first, x * w / sqrt(mean(x^2) +
+// eps); a row's tpr threads are neighbours in a warp and share the sum.
+template <typename E, bool NORM>
+__global__ void __launch_bounds__(256, NORM ? 4 : 6) rope_kernel(RopeArgs a) {
     constexpr int VEC = Vec<E>::N;
     // the attention kernel that follows may set itself up meanwhile; it
     // waits for this grid before it touches memory
@@ -106,6 +108,24 @@ __global__ void __launch_bounds__(256, 6) rope_kernel(RopeArgs a) {
     const E* base = src + (int64_t)src_row * a.d;
     Vec<E>::load(base + k0, x);
     Vec<E>::load(base + half + k0, y);
+    if (NORM && kind != 2) {
+        float ss = 0.f;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) ss = fmaf(x[e], x[e], fmaf(y[e], y[e], ss));
+        // (whole rows leave above, and a row is all Q, all K or all V)
+        const unsigned lanes = ((1u << tpr) - 1u) << ((threadIdx.x & 31u) & ~(unsigned)(tpr - 1));
+        for (int off = tpr / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(lanes, ss, off);
+        const float r = rsqrtf(ss / (float)a.d + a.eps);
+        const uint32_t layer = unit / (uint32_t)(kind == 0 ? a.q_heads : a.kv_heads) % (uint32_t)a.layers;
+        const float* w = (kind == 0 ? a.q_weight : a.k_weight) + layer * a.d;
+#pragma unroll
+        for (int e = 0; e < VEC; e += 4) {
+            const float4 wl = *reinterpret_cast<const float4*>(w + k0 + e);
+            const float4 wh = *reinterpret_cast<const float4*>(w + half + k0 + e);
+            x[e] *= r * wl.x; x[e + 1] *= r * wl.y; x[e + 2] *= r * wl.z; x[e + 3] *= r * wl.w;
+            y[e] *= r * wh.x; y[e + 1] *= r * wh.y; y[e + 2] *= r * wh.z; y[e + 3] *= r * wh.w;
+        }
+    }
     if (kind != 2) {
         // pairs 2p, 2p+1 of this thread: one 16-byte load (rope_cs_index)
         const float4* cs = reinterpret_cast<const float4*>(a.cs + (int64_t)i * half);
@@ -173,8 +193,12 @@ cudaError_t launch_rope(const RopeArgs& a, int dtype, cudaStream_t st, bool earl
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = early ? 1 : 0;
-    if (dtype == STATEKV_BF16) return cudaLaunchKernelEx(&cfg, rope_kernel<__nv_bfloat16>, a);
-    return cudaLaunchKernelEx(&cfg, rope_kernel<float>, a);
+    const bool norm = a.q_weight != nullptr;
+    if (dtype == STATEKV_BF16)
+        return norm ? cudaLaunchKernelEx(&cfg, rope_kernel<__nv_bfloat16, true>, a)
+                    : cudaLaunchKernelEx(&cfg, rope_kernel<__nv_bfloat16, false>, a);
+    return norm ? cudaLaunchKernelEx(&cfg, rope_kernel<float, true>, a)
+                : cudaLaunchKernelEx(&cfg, rope_kernel<float, false>, a);
 }
 
 }  // namespace statekv

@@ -27,6 +27,9 @@ using namespace statekv;
 
 namespace {
 
+// most drafted tokens of a tree
+constexpr int kMaxDraft = 64;
+
 // copy streams per direction of the batched host entry point
 constexpr int kCopyWays = 4;
 
@@ -64,6 +67,14 @@ struct statekv_handle {
     int num_sms = 0;
     float* dec_m = nullptr; float* dec_l = nullptr; float* dec_o = nullptr;  // decode partials
     int64_t dec_items = 0;              // capacity of the partials (items)
+    float* norm_w = nullptr;            // [2][L][d] weights of Q and K (statekv_set_qk_norm)
+    float norm_eps = 0.f;
+    bool norm = false;
+    void* draft_k = nullptr; void* draft_v = nullptr;   // [U][kMaxDraft][d] drafted tokens
+    void* tree_ws = nullptr; int64_t tree_ws_bytes = 0;
+    int32_t draft = 0;                  // tokens of the last tree, 0: nothing to accept
+    int8_t* codes = nullptr; float* code_scales = nullptr;   // block summaries of D
+    int64_t summarised = 0;             // D rows whose complete blocks have summaries
     int G = 0, U = 0, GT = 0, slots = 0, m_pad = 0, n_row_tiles = 0, esize = 0;
     int64_t det_pitch = 0;
     double mscale = 1.0;
@@ -106,6 +117,17 @@ struct statekv_handle {
     size_t kv_bytes() const {
         return (size_t)cfg.num_streams * cfg.num_layers * cfg.num_kv_heads * cfg.frame_tokens *
                cfg.head_dim * esize;
+    }
+    // [S*L][heads][tokens][d] of the storage dtype, rows `pitch` apart per head
+    statekv_view view(const void* p, int64_t heads, int64_t pitch) const {
+        const int64_t d = cfg.head_dim;
+        return {const_cast<void*>(p), heads * pitch * d, pitch * d, d};
+    }
+    void norm_args(RopeArgs& ra) const {
+        ra.q_weight = norm ? norm_w : nullptr;
+        ra.k_weight = norm ? norm_w + (size_t)cfg.num_layers * cfg.head_dim : nullptr;
+        ra.eps = norm_eps;
+        ra.layers = cfg.num_layers; ra.q_heads = cfg.num_q_heads; ra.kv_heads = cfg.num_kv_heads;
     }
     int c() const { return (int)std::min<int64_t>(cfg.budget, n * cfg.frame_tokens); }
 };
@@ -258,6 +280,7 @@ int run_front(statekv_handle* h, const void* q, const void* k, const void* v, vo
     ra.rows_kv = (int64_t)h->U * T;
     ra.T = T; ra.d = d; ra.slots = h->slots; ra.c = cc;
     ra.det_pitch = h->det_pitch; ra.det_row0 = h->n * T;
+    h->norm_args(ra);
     e = timed(h, STATEKV_KERNEL_ROPE, st, [&] { return launch_rope(ra, c.dtype, st, true); });
     if (e != cudaSuccess) return cuda_fail();
 
@@ -295,6 +318,7 @@ int run_back(statekv_handle* h, cudaStream_t st) {
     if (e != cudaSuccess) return cuda_fail();
 
     h->n += 1;
+    h->draft = 0;
     return STATEKV_OK;
 }
 
@@ -592,6 +616,7 @@ int statekv_decode(statekv_handle* h, int32_t tokens, const void* q, const void*
     ra.rows_kv = (int64_t)h->U * tokens;
     ra.T = tokens; ra.d = c.head_dim; ra.slots = h->slots; ra.c = 0;
     ra.det_pitch = h->det_pitch; ra.det_row0 = visible;
+    h->norm_args(ra);
     if (launch_rope(ra, c.dtype, st, false) != cudaSuccess) return cuda_fail();
     DecodeMaps maps;
     if (!make_decode_maps(&maps, h->q_rot, R, npad, h->det_k, h->det_v, h->det_pitch, h->U))
@@ -603,6 +628,173 @@ int statekv_decode(statekv_handle* h, int32_t tokens, const void* q, const void*
     da.scale_log2 = h->scale_log2;
     if (launch_decode(da, maps, st) != cudaSuccess) return cuda_fail();
     h->text += tokens;
+    h->draft = 0;
+    return STATEKV_OK;
+}
+
+int statekv_set_qk_norm(statekv_handle* h, const float* q_weight, const float* k_weight, float eps,
+                        void* cuda_stream) {
+    if (!h || (q_weight != nullptr) != (k_weight != nullptr)) return STATEKV_E_INVALID_ARG;
+    if (!q_weight) {
+        h->norm = false;
+        return STATEKV_OK;
+    }
+    if (check_ptr(q_weight) || check_ptr(k_weight) || !(eps >= 0.f)) return STATEKV_E_INVALID_ARG;
+    DeviceGuard g(h->cfg.device);
+    if (!g.ok) return cuda_fail();
+    const size_t n = (size_t)h->cfg.num_layers * h->cfg.head_dim, bytes = n * sizeof(float);
+    if (!h->norm_w && !dalloc(h, &h->norm_w, 2 * bytes)) return STATEKV_E_OOM;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(cuda_stream);
+    if (cudaMemcpyAsync(h->norm_w, q_weight, bytes, cudaMemcpyDeviceToDevice, st) != cudaSuccess ||
+        cudaMemcpyAsync(h->norm_w + n, k_weight, bytes, cudaMemcpyDeviceToDevice, st) != cudaSuccess)
+        return cuda_fail();
+    h->norm = true;
+    h->norm_eps = eps;
+    return STATEKV_OK;
+}
+
+int statekv_decode_tree(statekv_handle* h, int32_t tokens, const void* q, const void* k, const void* v,
+                        const uint64_t* tree, const int32_t* depth, void* o, void* cuda_stream) {
+    if (!h) return STATEKV_E_INVALID_ARG;
+    int r;
+    if ((r = check_ptr(q)) || (r = check_ptr(k)) || (r = check_ptr(v)) || (r = check_ptr(o))) return r;
+    const statekv_config& c = h->cfg;
+    if (tokens < 1 || tokens > c.frame_tokens || !tree || reinterpret_cast<uintptr_t>(tree) % 8 || !depth ||
+        reinterpret_cast<uintptr_t>(depth) % 4)
+        return STATEKV_E_INVALID_ARG;
+    if (tokens > kMaxDraft || c.dtype != STATEKV_BF16 || h->G > 64) return STATEKV_E_UNSUPPORTED;
+    const int64_t visible = h->n * c.frame_tokens + h->text;
+    DeviceGuard g(c.device);
+    if (!g.ok) return cuda_fail();
+    const int batch = c.num_streams * c.num_layers;
+    if (!h->tree_ws) {
+        const int most = std::min(kMaxDraft, (int)c.frame_tokens);
+        const int64_t need =
+            statekv_tree_attention_workspace(batch, c.num_q_heads, c.num_kv_heads, most, c.head_dim);
+        if (need < 0) return STATEKV_E_UNSUPPORTED;
+        const size_t rows = (size_t)h->U * kMaxDraft * c.head_dim * h->esize;
+        if ((!h->draft_k && !dalloc(h, &h->draft_k, rows)) || (!h->draft_v && !dalloc(h, &h->draft_v, rows)) ||
+            !dalloc(h, &h->tree_ws, (size_t)need))
+            return STATEKV_E_OOM;
+        h->tree_ws_bytes = need;
+    }
+    statekv_norm_rope_args na{};
+    na.q = h->view(q, c.num_q_heads, tokens);
+    na.k = h->view(k, c.num_kv_heads, tokens);
+    na.v = h->view(v, c.num_kv_heads, tokens);
+    na.q_out = h->view(h->q_rot, c.num_q_heads, tokens);
+    na.k_out = h->view(h->draft_k, c.num_kv_heads, kMaxDraft);
+    na.v_out = h->view(h->draft_v, c.num_kv_heads, kMaxDraft);
+    if (h->norm) {
+        na.q_weight = h->norm_w;
+        na.k_weight = h->norm_w + (size_t)c.num_layers * c.head_dim;
+    }
+    na.omega = h->omega;
+    na.positions = depth;
+    na.status = h->err;
+    na.position0 = c.position_offset + visible;
+    na.position_stride = tokens; na.position_layers = c.num_layers;
+    na.batch = batch; na.layers = c.num_layers; na.q_heads = c.num_q_heads; na.kv_heads = c.num_kv_heads;
+    na.tokens = tokens; na.head_dim = c.head_dim; na.out_capacity = kMaxDraft; na.weight_rows = c.num_layers;
+    na.dtype = c.dtype; na.weight_dtype = STATEKV_F32; na.eps = h->norm_eps;
+    if ((r = statekv_norm_rope(&na, cuda_stream)) != STATEKV_OK) return r;
+    statekv_tree_args ta{};
+    ta.q = na.q_out; ta.out = h->view(o, c.num_q_heads, tokens);
+    ta.k_new = na.k_out; ta.v_new = na.v_out;
+    ta.k_cache = h->view(h->det_k, c.num_kv_heads, h->det_pitch);
+    ta.v_cache = h->view(h->det_v, c.num_kv_heads, h->det_pitch);
+    ta.tree = tree; ta.status = h->err; ta.workspace = h->tree_ws; ta.workspace_bytes = h->tree_ws_bytes;
+    ta.scale = h->mscale * h->mscale / std::sqrt((double)c.head_dim);
+    ta.tree_stride = tokens; ta.length = (int32_t)visible;
+    ta.batch = batch; ta.layers = c.num_layers; ta.q_heads = c.num_q_heads; ta.kv_heads = c.num_kv_heads;
+    ta.tokens = tokens; ta.head_dim = c.head_dim; ta.cache_rows = (int32_t)h->det_pitch;
+    if ((r = statekv_tree_attention(&ta, cuda_stream)) != STATEKV_OK) return r;
+    h->draft = tokens;
+    return STATEKV_OK;
+}
+
+int statekv_accept(statekv_handle* h, int32_t count, const int32_t* path, void* cuda_stream) {
+    if (!h || count < 0 || h->draft < 1 || count > h->draft) return STATEKV_E_INVALID_ARG;
+    if (count == 0) {
+        h->draft = 0;
+        return STATEKV_OK;
+    }
+    if (!path || reinterpret_cast<uintptr_t>(path) % 4) return STATEKV_E_INVALID_ARG;
+    const statekv_config& c = h->cfg;
+    const int64_t visible = h->n * c.frame_tokens + h->text;
+    if (visible + count > h->det_pitch) return STATEKV_E_CAPACITY;
+    DeviceGuard g(c.device);
+    if (!g.ok) return cuda_fail();
+    statekv_append_args aa{};
+    aa.k_new = h->view(h->draft_k, c.num_kv_heads, kMaxDraft);
+    aa.v_new = h->view(h->draft_v, c.num_kv_heads, kMaxDraft);
+    aa.k_cache = h->view(h->det_k, c.num_kv_heads, h->det_pitch);
+    aa.v_cache = h->view(h->det_v, c.num_kv_heads, h->det_pitch);
+    aa.path = path; aa.status = h->err;
+    aa.path_stride = count; aa.path_len = count; aa.length = (int32_t)visible;
+    aa.batch = c.num_streams * c.num_layers; aa.layers = c.num_layers; aa.kv_heads = c.num_kv_heads;
+    aa.tokens = h->draft; aa.head_dim = c.head_dim; aa.cache_rows = (int32_t)h->det_pitch; aa.dtype = c.dtype;
+    const int r = statekv_append_accepted(&aa, cuda_stream);
+    if (r != STATEKV_OK) return r;
+    h->text += count;
+    h->draft = 0;
+    return STATEKV_OK;
+}
+
+int statekv_decode_sparse(statekv_handle* h, int32_t tokens, int32_t top, const void* q, const void* k,
+                          const void* v, void* o, void* cuda_stream) {
+    if (!h) return STATEKV_E_INVALID_ARG;
+    int r;
+    if ((r = check_ptr(q)) || (r = check_ptr(k)) || (r = check_ptr(v)) || (r = check_ptr(o))) return r;
+    const statekv_config& c = h->cfg;
+    if (tokens < 1 || tokens > c.frame_tokens || top < 1) return STATEKV_E_INVALID_ARG;
+    const int64_t blocks = h->det_pitch / STATEKV_BLOCK;
+    if (top > 1024 || c.dtype != STATEKV_BF16 || h->G > 16 || blocks > 32768) return STATEKV_E_UNSUPPORTED;
+    const int64_t visible = h->n * c.frame_tokens + h->text;
+    if (visible + tokens > h->det_pitch) return STATEKV_E_CAPACITY;
+    DeviceGuard g(c.device);
+    if (!g.ok) return cuda_fail();
+    if (!h->code_scales) {
+        if ((!h->codes && !dalloc(h, &h->codes, (size_t)h->U * blocks * c.head_dim)) ||
+            !dalloc(h, &h->code_scales, (size_t)h->U * blocks * sizeof(float)))
+            return STATEKV_E_OOM;
+    }
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(cuda_stream);
+    const int batch = c.num_streams * c.num_layers;
+    // blocks completed since the last call (those of frames, text or accepted drafts)
+    if (visible / STATEKV_BLOCK > h->summarised / STATEKV_BLOCK) {
+        statekv_summary_args sa{};
+        sa.k_cache = h->view(h->det_k, c.num_kv_heads, h->det_pitch);
+        sa.codes = h->codes; sa.scales = h->code_scales; sa.status = h->err;
+        sa.length = (int32_t)visible; sa.appended = (int32_t)(visible - h->summarised); sa.blocks = (int32_t)blocks;
+        sa.batch = batch; sa.layers = c.num_layers; sa.kv_heads = c.num_kv_heads; sa.head_dim = c.head_dim;
+        sa.cache_rows = (int32_t)h->det_pitch;
+        if ((r = statekv_block_summaries(&sa, cuda_stream)) != STATEKV_OK) return r;
+        h->summarised = visible;
+    }
+    RopeArgs ra{};
+    ra.q = q; ra.k = k; ra.v = v;
+    ra.q_rot = h->q_rot; ra.pool_k = nullptr; ra.pool_v = nullptr;
+    ra.det_k = h->det_k; ra.det_v = h->det_v;
+    ra.cs = h->cs + (size_t)visible * (c.head_dim / 2);
+    ra.rows_q = (int64_t)h->U * h->G * tokens;
+    ra.rows_kv = (int64_t)h->U * tokens;
+    ra.T = tokens; ra.d = c.head_dim; ra.slots = h->slots; ra.c = 0;
+    ra.det_pitch = h->det_pitch; ra.det_row0 = visible;
+    h->norm_args(ra);
+    if (launch_rope(ra, c.dtype, st, false) != cudaSuccess) return cuda_fail();
+    statekv_sparse_args pa{};
+    pa.q = h->view(h->q_rot, c.num_q_heads, tokens); pa.out = h->view(o, c.num_q_heads, tokens);
+    pa.k_cache = h->view(h->det_k, c.num_kv_heads, h->det_pitch);
+    pa.v_cache = h->view(h->det_v, c.num_kv_heads, h->det_pitch);
+    pa.codes = h->codes; pa.scales = h->code_scales; pa.status = h->err;
+    pa.scale = h->mscale * h->mscale / std::sqrt((double)c.head_dim);
+    pa.length = (int32_t)(visible + tokens); pa.top = top; pa.blocks = (int32_t)blocks;
+    pa.batch = batch; pa.layers = c.num_layers; pa.q_heads = c.num_q_heads; pa.kv_heads = c.num_kv_heads;
+    pa.tokens = tokens; pa.head_dim = c.head_dim; pa.cache_rows = (int32_t)h->det_pitch;
+    if ((r = statekv_sparse_attention(&pa, cuda_stream)) != STATEKV_OK) return r;
+    h->text += tokens;
+    h->draft = 0;
     return STATEKV_OK;
 }
 
@@ -641,6 +833,8 @@ int statekv_reset(statekv_handle* h) {
     if (!h) return STATEKV_E_INVALID_ARG;
     h->n = 0;
     h->text = 0;
+    h->draft = 0;
+    h->summarised = 0;
     return STATEKV_OK;
 }
 
@@ -682,6 +876,8 @@ int statekv_get_rotated_query(statekv_handle* h, const void** q_rot) {
 int statekv_set_frame_index(statekv_handle* h, int64_t n) {
     if (!h || n < 0 || n >= h->cfg.max_frames) return STATEKV_E_INVALID_ARG;
     h->n = n;
+    h->draft = 0;
+    h->summarised = 0;                  // D rows from here on may be written anew
     return STATEKV_OK;
 }
 

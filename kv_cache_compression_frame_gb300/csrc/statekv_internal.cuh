@@ -34,6 +34,10 @@ struct RopeArgs {
     int64_t rows_kv;     // S*L*Hkv*T
     int32_t T, d, slots, c;
     int64_t det_pitch, det_row0;                   // det row of token 0 = n*T
+    // per-head norm (both NULL: none): weights [L][d], eps
+    const float* q_weight; const float* k_weight;
+    float eps;
+    int32_t layers, q_heads, kv_heads;
 };
 
 struct RopeTableArgs {

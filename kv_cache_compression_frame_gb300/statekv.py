@@ -173,6 +173,60 @@ class StateKV:
     def decode(self, q, k, v, o=None, stream=None) -> torch.Tensor:
         """Text tokens over the detailed state: q [S][L][Hq][tok][d],
         k, v [S][L][Hkv][tok][d] (device, pre-RoPE).  Returns o like q."""
+        q, k, v, o, tok = self._text_in(q, k, v, o)
+        N.check(self._lib.statekv_decode(
+            self._h, tok, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+            _stream_ptr(stream, self.device)), "statekv_decode")
+        return o
+
+    def set_qk_norm(self, q_weight, k_weight, eps: float = 1e-6, stream=None) -> None:
+        """RMS norm of the heads of q and k ahead of the rotation, weights
+        [d] or [L][d] (copied); None, None turns it off."""
+        if q_weight is None or k_weight is None:
+            if q_weight is not None or k_weight is not None:
+                raise ValueError("set_qk_norm: both weights, or neither")
+            N.check(self._lib.statekv_set_qk_norm(self._h, None, None, 0.0, None), "statekv_set_qk_norm")
+            return
+        L, d = self.cfg.num_layers, self.cfg.head_dim
+        st = torch.cuda.current_stream(self.device) if stream is None else stream
+        with torch.cuda.device(self.device), torch.cuda.stream(st):
+            w = torch.stack([x.to(device=self.device, dtype=torch.float32).expand(L, d)
+                             for x in (q_weight, k_weight)])
+            N.check(self._lib.statekv_set_qk_norm(self._h, w[0].data_ptr(), w[1].data_ptr(), eps,
+                                                  st.cuda_stream), "statekv_set_qk_norm")
+
+    def decode_tree(self, q, k, v, tree, depth, o=None, stream=None) -> torch.Tensor:
+        """A tree of drafted tokens over the detailed state: q, k, v as for
+        decode, tree int64 masks and depth int32, both [S][tok] (tree_masks).
+        Nothing is appended until accept().  Returns o like q."""
+        q, k, v, o, tok = self._text_in(q, k, v, o)
+        for t, dt, name in ((tree, torch.int64, "tree"), (depth, torch.int32, "depth")):
+            if tuple(t.shape) != (self.cfg.num_streams, tok) or t.dtype != dt or not t.is_contiguous() \
+                    or t.device != self.device:
+                raise ValueError(f"{name}: want contiguous {dt} {(self.cfg.num_streams, tok)} on {self.device}")
+        N.check(self._lib.statekv_decode_tree(
+            self._h, tok, q.data_ptr(), k.data_ptr(), v.data_ptr(), tree.data_ptr(), depth.data_ptr(),
+            o.data_ptr(), _stream_ptr(stream, self.device)), "statekv_decode_tree")
+        return o
+
+    def accept(self, path, stream=None) -> None:
+        """Nodes path (int32 [S][count]) of the last decode_tree become text."""
+        if path.dim() != 2 or path.shape[0] != self.cfg.num_streams or path.dtype != torch.int32 \
+                or not path.is_contiguous() or path.device != self.device:
+            raise ValueError(f"path: want contiguous int32 [{self.cfg.num_streams}][count] on {self.device}")
+        N.check(self._lib.statekv_accept(self._h, path.shape[1], path.data_ptr(),
+                                         _stream_ptr(stream, self.device)), "statekv_accept")
+
+    def decode_sparse(self, q, k, v, top: int, o=None, stream=None) -> torch.Tensor:
+        """decode() over the `top` best 64-row blocks of the detailed state
+        per token and KV head."""
+        q, k, v, o, tok = self._text_in(q, k, v, o)
+        N.check(self._lib.statekv_decode_sparse(
+            self._h, tok, top, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+            _stream_ptr(stream, self.device)), "statekv_decode_sparse")
+        return o
+
+    def _text_in(self, q, k, v, o):
         tok = q.shape[3] if q.dim() == 5 else -1
         qs = self.q_shape[:3] + (tok, self.q_shape[4])
         ks = self.kv_shape[:3] + (tok, self.kv_shape[4])
@@ -182,10 +236,7 @@ class StateKV:
         if o is None:
             o = torch.empty(qs, dtype=self.torch_dtype, device=self.device)
         self._check_in(o, qs, "o")
-        N.check(self._lib.statekv_decode(
-            self._h, tok, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
-            _stream_ptr(stream, self.device)), "statekv_decode")
-        return o
+        return q, k, v, o, tok
 
     @property
     def text_tokens(self) -> int:

@@ -156,8 +156,9 @@ class _On:
 
 def qk_norm_rope(q, k, positions, omega, q_weight=None, k_weight=None, *, v=None, eps: float = 1e-6,
                  q_out=None, k_out=None, v_out=None, out_rows=None, stream=None):
-    """RMS norm of every head of q [n][Hq][t][d] and k [n][Hkv][t][d] (no norm
-    where the weight is None), rotation at `positions` (int32 [t] or [rows][t]
+    """RMS norm of every head of q [n][Hq][t][d] and k [n][Hkv][t][d] with
+    weights [d] or [layers][d] (the batch is sequences x layers; no norm where
+    the weight is None), rotation at `positions` (int32 [t] or [rows][t]
     with rows dividing n, or an int: that and the following ones) with omega
     float64 [d/2], in one pass.  v is copied.  k and v go to rows out_rows
     (int32 [sequences]) + t of k_out and v_out (default: new tensors, row t).
@@ -174,9 +175,13 @@ def qk_norm_rope(q, k, positions, omega, q_weight=None, k_weight=None, *, v=None
     for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
         if w is not None:
             wd = wd or w.dtype
-            if w.shape != (d,) or wd not in _DTYPES:
-                raise ValueError(f"{name}: want [{d}] of one of {list(_DTYPES)}")
-            setattr(a, name, _vector(w, name, wd, dev))
+            rows = w.shape[0] if w.dim() == 2 else 1
+            if w.shape[-1:] != (d,) or wd not in _DTYPES or rows < 1 or n % rows or a.weight_rows not in (0, rows):
+                raise ValueError(f"{name}: want [{d}] or [layers][{d}] of one of {list(_DTYPES)}, the same for "
+                                 "both weights, layers dividing the batch")
+            setattr(a, name, _vector(w, name, wd, dev, w.dim()))
+            a.weight_rows = rows
+    a.weight_rows = a.weight_rows or 1
     if omega.shape != (d // 2,):
         raise ValueError(f"omega: want [{d // 2}]")
     a.omega = _vector(omega, "omega", torch.float64, dev)

@@ -115,6 +115,23 @@ def test_norm_rope_positions_weights_and_zero_rows():
 
 
 @gpu
+@pytest.mark.parametrize("dtype,wdtype", [(BF16, BF16), (BF16, torch.float32), (torch.float32, torch.float32)])
+def test_norm_rope_weights_per_layer(dtype, wdtype):
+    g = gen(7)
+    seqs, layers, t, d = 2, 3, 6, 64
+    q, k = randn(g, seqs * layers, 3, t, d, dtype=dtype), randn(g, seqs * layers, 2, t, d, dtype=dtype)
+    qw, kw = (1 + randn(g, layers, d, dtype=wdtype) / 4 for _ in range(2))
+    pos = torch.randint(0, 5000, (t,), generator=g, device=DEV).to(torch.int32)
+    qo, ko = kv.qk_norm_rope(q, k, pos, omega_of(d), qw, kw)
+    for got, x, w in ((qo, q, qw), (ko, k, kw)):
+        for n in range(seqs * layers):
+            ref, mag = ref_norm_rope(x[n:n + 1], pos[None], omega_of(d), w[n % layers], 1e-6)
+            within(got[n:n + 1], ref, half_step(dtype) * ref.abs() + 2.0 ** -20 * mag)
+    with pytest.raises(ValueError, match="weight"):
+        kv.qk_norm_rope(q, k, pos, omega_of(d), qw, kw[:2].contiguous())
+
+
+@gpu
 def test_norm_rope_into_a_cache_and_in_place():
     """K and V land at each sequence's rows; every other row stays as it was."""
     g = gen(6)
@@ -716,14 +733,14 @@ def test_tree_refusals_before_device_work(bad, want):
     (dict(dtype=5), N.E_INVALID_ARG), (dict(weight_dtype=5), N.E_INVALID_ARG), (dict(head_dim=96), N.E_UNSUPPORTED),
     (dict(omega=None), N.E_INVALID_ARG), (dict(omega=20), N.E_INVALID_ARG), (dict(status=None), N.E_INVALID_ARG),
     (dict(q=view(8)), N.E_INVALID_ARG), (dict(k_out=view(b=4)), N.E_INVALID_ARG), (dict(v_out=view(None)), N.E_INVALID_ARG),
-    (dict(layers=0), N.E_INVALID_ARG), (dict(position_layers=0), N.E_INVALID_ARG), (dict(batch=3, layers=2), N.E_INVALID_ARG),
+    (dict(layers=0), N.E_INVALID_ARG), (dict(position_layers=0), N.E_INVALID_ARG), (dict(weight_rows=0), N.E_INVALID_ARG), (dict(q_weight=8), N.E_INVALID_ARG), (dict(batch=3, layers=2), N.E_INVALID_ARG),
     (dict(out_capacity=2), N.E_CAPACITY), (dict(eps=-1.0), N.E_INVALID_ARG), (dict(eps=math.nan), N.E_INVALID_ARG),
     (dict(tokens=-1), N.E_INVALID_ARG), (dict(q_heads=70000), N.E_UNSUPPORTED), (dict(tokens=0, out_capacity=0), N.OK),
     (dict(batch=0), N.OK),
 ])
 def test_norm_rope_refusals_before_device_work(bad, want):
     a = dict(q=view(), k=view(), v=view(), q_out=view(), k_out=view(), v_out=view(), omega=16, status=16,
-             position_layers=1, batch=2, layers=1, q_heads=4, kv_heads=2, tokens=3, head_dim=128, out_capacity=3,
+             position_layers=1, weight_rows=1, batch=2, layers=1, q_heads=4, kv_heads=2, tokens=3, head_dim=128, out_capacity=3,
              dtype=0, weight_dtype=0, eps=1e-6)
     a.update(bad)
     assert N.load().statekv_norm_rope(N.NormRopeArgs(**a), None) == want
