@@ -17,13 +17,13 @@
 //  2. after a cluster barrier every CTA selects for itself (radix select on the
 //     ordered scores, 11 + 11 + 10 bits; ties by index in the compaction), so
 //     no result has to travel;
-//  3. the chosen blocks and the tail's pieces go to the C * 8 warps in turn.
-//     A warp attends over 64 rows on its own: K and V come from global memory
+//  3. the halves of the chosen blocks and the tail's pieces go to the C * 8
+//     warps in turn.  A warp attends over 32 rows on its own: K and V come from global memory
 //     straight into matrix fragments (the order of d inside a product is free,
 //     so each lane's 16-byte loads are its fragments), the G <= 16 query rows
 //     are the 16 rows of m16n8k16, (m, l, O) stay in registers;
-//  4. the warps merge in shared memory, the CTAs through distributed shared
-//     memory, each CTA writing its share of the output.
+//  4. the warps merge in shared memory and store each part of the result in
+//     the CTA that writes it (distributed shared memory), which merges the CTAs.
 // m16n8k16 and not tcgen05: with at most 16 query rows a 128-row product would
 // waste 7/8 of the tensor core, and the data would have to pass through shared
 // memory first.
@@ -42,6 +42,7 @@ constexpr int kSparseWarps = kSparseThreads / 32;
 constexpr int kMaxTop = 1024;
 constexpr int kMaxBlocks = 32768;
 constexpr int kBins = 2048;
+constexpr int kRows = 32;                // cache rows per entry of the attention
 
 struct SparseKernelArgs {
     statekv_sparse_args a;
@@ -63,8 +64,9 @@ __device__ __forceinline__ uint32_t ordered(float x) {
     return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-// Exclusive prefix sum of one value per thread over the CTA, and the total.
-__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* s_warp, uint32_t* total) {
+// Exclusive prefix sum of one value per thread over the CTA.  One barrier; two
+// scans in a row need scratch of their own.
+__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* s_warp) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint32_t x = v;
 #pragma unroll
@@ -74,15 +76,31 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* s_warp, uin
     }
     if (lane == 31) s_warp[warp] = x;
     __syncthreads();
-    uint32_t before = 0, all = 0;
+    uint32_t before = 0;
 #pragma unroll
-    for (int w = 0; w < kSparseWarps; ++w) {
+    for (int w = 0; w < kSparseWarps - 1; ++w)
         if (w < warp) before += s_warp[w];
-        all += s_warp[w];
-    }
-    __syncthreads();
-    *total = all;
     return before + x - v;
+}
+
+// 8-bit codes of one block against the group's query codes: max over g.
+template <int D>
+__device__ __forceinline__ int best_dot(const uint4 (&w)[D / 16], const int8_t* s_q, int G) {
+    int best = INT32_MIN;
+    for (int g = 0; g < G; ++g) {
+        const uint4* qc = reinterpret_cast<const uint4*>(s_q + g * D);
+        int s = 0;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+            const uint4 x = qc[i];
+            s = __dp4a((int)w[i].x, (int)x.x, s);
+            s = __dp4a((int)w[i].y, (int)x.y, s);
+            s = __dp4a((int)w[i].z, (int)x.z, s);
+            s = __dp4a((int)w[i].w, (int)x.w, s);
+        }
+        best = max(best, s);
+    }
+    return best;
 }
 
 template <int D>
@@ -96,14 +114,14 @@ __global__ void __launch_bounds__(kSparseThreads, 1) sparse_kernel(const __grid_
     uint32_t* s_key = reinterpret_cast<uint32_t*>(smem);
     float* s_o = reinterpret_cast<float*>(smem);
     uint8_t* fixed = smem + ka.region;
-    float* s_part = reinterpret_cast<float*>(fixed);                    // [G][D] this CTA's O
-    float2* s_pml = reinterpret_cast<float2*>(s_part + 16 * D);         // [16] its (m, l)
-    float2* s_wml = s_pml + 16;                                         // [8][16] the warps' (m, l)
+    float* s_part = reinterpret_cast<float*>(fixed);                    // [C][slice] the CTAs' O of this CTA's slice
+    float2* s_pml = reinterpret_cast<float2*>(s_part + 16 * D + 64);    // [16][16] the CTAs' (m, l)
+    float2* s_wml = s_pml + 16 * 16;                                    // [8][16] the warps' (m, l)
     int* s_list = reinterpret_cast<int*>(s_wml + kSparseWarps * 16);    // [kMaxTop]
-    uint32_t* s_bin = reinterpret_cast<uint32_t*>(s_list + kMaxTop);    // [kBins]
-    int8_t* s_q = reinterpret_cast<int8_t*>(s_bin + kBins);             // [16][D] query codes
-    uint32_t* s_scan = reinterpret_cast<uint32_t*>(s_q + 16 * D);       // [8]
-    uint32_t* s_pick = s_scan + kSparseWarps;                           // [2] digit, keys above it
+    uint32_t* s_bins = reinterpret_cast<uint32_t*>(s_list + kMaxTop);   // [2][kBins]
+    int8_t* s_q = reinterpret_cast<int8_t*>(s_bins + 2 * kBins);        // [16][D] query codes
+    uint32_t* s_scan = reinterpret_cast<uint32_t*>(s_q + 16 * D);       // [2][8]
+    uint32_t* s_pick = s_scan + 2 * kSparseWarps;                       // [2][3] digit, keys above it, keys of it
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = C > 1 ? (int)ptx::cluster_ctarank() : 0;
@@ -120,116 +138,140 @@ __global__ void __launch_bounds__(kSparseThreads, 1) sparse_kernel(const __grid_
     // ---- the group's query rows, 8 bits, one scale
     const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q.data) + n * a.q.batch_stride +
                              (int64_t)(h * G) * a.q.head_stride + (int64_t)tok * a.q.token_stride;
+    int nsel = nb;
     if (choose) {
-        float top = 0.f;
-        for (int i = tid; i < G * D; i += kSparseThreads)
-            top = fmaxf(top, fabsf(__bfloat162float(q[(i / D) * a.q.head_stride + i % D])));
+        // the first block's codes are on their way while the query is rounded
+        uint4 w[D / 16];
+        float scale = 0.f;
+        int b = rank * kSparseThreads + tid;
+        auto load_codes = [&]() {
+            const int64_t at = unit * a.blocks + b;
+            const uint4* code = reinterpret_cast<const uint4*>(a.codes + at * D);
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) w[i] = code[i];
+            scale = a.scales[at];
+        };
+        if (b < a.blocks) load_codes();                      // (without waiting for the length)
+        // G * D / 8 <= 256 threads have 8 values of the query each
+        float x[8], top = 0.f;
+        const bool has_q = tid < G * (D / 8);
+        if (has_q) {
+            const uint4 u = *reinterpret_cast<const uint4*>(q + (tid / (D / 8)) * a.q.head_stride + tid % (D / 8) * 8);
+            const uint32_t uw[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[2 * i] = __uint_as_float(uw[i] << 16);
+                x[2 * i + 1] = __uint_as_float(uw[i] & 0xffff0000u);
+                top = fmaxf(top, fmaxf(fabsf(x[2 * i]), fabsf(x[2 * i + 1])));
+            }
+        }
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
         if (lane == 0) s_scan[warp] = __float_as_uint(top);
+        for (int i = tid; i < 2 * kBins; i += kSparseThreads) s_bins[i] = 0;
         __syncthreads();
 #pragma unroll
-        for (int w = 0; w < kSparseWarps; ++w) top = fmaxf(top, __uint_as_float(s_scan[w]));
+        for (int i = 0; i < kSparseWarps; ++i) top = fmaxf(top, __uint_as_float(s_scan[i]));
         const float inv = top > 0.f ? 127.f / top : 0.f;
-        for (int i = tid; i < G * D; i += kSparseThreads) {
-            const float x = rintf(__bfloat162float(q[(i / D) * a.q.head_stride + i % D]) * inv);
-            s_q[i] = (int8_t)(int)fminf(fmaxf(x, -127.f), 127.f);
+        if (has_q) {
+            uint32_t c[2] = {0u, 0u};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int code = (int)fminf(fmaxf(rintf(x[i] * inv), -127.f), 127.f);
+                c[i >> 2] |= (uint32_t)(code & 0xff) << (8 * (i & 3));
+            }
+            *reinterpret_cast<uint2*>(s_q + tid * 8) = make_uint2(c[0], c[1]);
         }
         __syncthreads();
-    }
-    if (C > 1) ptx::cluster_wait();                          // every CTA has started: its memory may be written
-    int nsel = nb;
-    if (choose) {
+        if (C > 1) ptx::cluster_wait();                      // every CTA has started: its memory may be written
         // ---- scores
-        for (int b = rank * kSparseThreads + tid; b < nb; b += C * kSparseThreads) {
-            const int64_t at = unit * a.blocks + b;
-            const uint4* code = reinterpret_cast<const uint4*>(a.codes + at * D);
-            uint4 w[D / 16];
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) w[i] = code[i];
-            const float scale = a.scales[at];
-            int best = INT32_MIN;
-            for (int g = 0; g < G; ++g) {
-                const uint4* qc = reinterpret_cast<const uint4*>(s_q + g * D);
-                int s = 0;
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                    const uint4 x = qc[i];
-                    s = __dp4a((int)w[i].x, (int)x.x, s);
-                    s = __dp4a((int)w[i].y, (int)x.y, s);
-                    s = __dp4a((int)w[i].z, (int)x.z, s);
-                    s = __dp4a((int)w[i].w, (int)x.w, s);
-                }
-                best = max(best, s);
-            }
-            const uint32_t key = ordered((float)best * scale);
+        while (b < nb) {
+            const uint32_t key = ordered((float)best_dot<D>(w, s_q, G) * scale);
             if (C == 1) s_key[b] = key;
             else
                 for (int r = 0; r < C; ++r)
                     ptx::st_cluster_u32(ptx::cluster_map(ptx::smem_u32(s_key + b), (uint32_t)r), key);
+            b += C * kSparseThreads;
+            if (b < nb) load_codes();
         }
         if (C > 1) ptx::cluster_sync();
         else __syncthreads();
-        // ---- the top-th largest key: digits of 11, 11 and 10 bits
+        // ---- the top-th largest key, digits of 11, 11 and 10 bits.  Often the
+        // second digit's keys are all wanted: then no third pass is needed.
         uint32_t prefix = 0, mask = 0, need = (uint32_t)a.top;
+        constexpr int PER = kBins / kSparseThreads;
 #pragma unroll 1
-        for (int shift = 21; shift >= 0; shift = shift == 21 ? 10 : shift == 10 ? 0 : -1) {
-            for (int i = tid; i < kBins; i += kSparseThreads) s_bin[i] = 0;
-            __syncthreads();
-            const uint32_t digits = shift == 0 ? 1023u : 2047u;
-            for (int b = tid; b < nb; b += kSparseThreads) {
-                const uint32_t key = s_key[b];
-                if ((key & mask) == prefix) atomicAdd(&s_bin[(key >> shift) & digits], 1u);
+        for (int pass = 0; pass < 3; ++pass) {
+            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+            const uint32_t digits = pass == 2 ? 1023u : 2047u;
+            uint32_t* bins = s_bins + (pass & 1) * kBins;
+            for (int i = tid; i < nb; i += kSparseThreads) {
+                const uint32_t key = s_key[i];
+                if ((key & mask) == prefix) atomicAdd(&bins[(key >> shift) & digits], 1u);
             }
             __syncthreads();
-            // thread t holds the bins 8 t' .. 8 t' + 7 of t' = 255 - t: larger digits first
-            uint32_t c[kBins / kSparseThreads], sum = 0, total;
+            // thread t holds the 8 bins from 8 (255 - t) on: larger digits first
+            static_assert(PER == 8, "two 16-byte loads");
+            uint4* mine = reinterpret_cast<uint4*>(bins + (kSparseThreads - 1 - tid) * PER);
+            const uint4 lo = mine[0], hi = mine[1];
+            mine[0] = mine[1] = make_uint4(0, 0, 0, 0);      // for the pass after the next
+            const uint32_t c[PER] = {hi.w, hi.z, hi.y, hi.x, lo.w, lo.z, lo.y, lo.x};
+            const uint32_t sum = (c[0] + c[1]) + (c[2] + c[3]) + ((c[4] + c[5]) + (c[6] + c[7]));
+            uint32_t above = block_scan(sum, s_scan + (pass & 1) * kSparseWarps);
+            uint32_t* pick = s_pick + (pass & 1) * 3;
 #pragma unroll
-            for (int i = 0; i < kBins / kSparseThreads; ++i) {
-                c[i] = s_bin[kBins - 1 - (tid * (kBins / kSparseThreads) + i)];
-                sum += c[i];
-            }
-            uint32_t above = block_scan(sum, s_scan, &total);
-#pragma unroll
-            for (int i = 0; i < kBins / kSparseThreads; ++i) {
+            for (int i = 0; i < PER; ++i) {
                 if (above < need && need <= above + c[i]) {
-                    s_pick[0] = (uint32_t)(kBins - 1 - (tid * (kBins / kSparseThreads) + i));
-                    s_pick[1] = above;
+                    pick[0] = (uint32_t)(kBins - 1 - (tid * PER + i));
+                    pick[1] = above;
+                    pick[2] = c[i];
                 }
                 above += c[i];
             }
             __syncthreads();
-            prefix |= s_pick[0] << shift;
+            prefix |= pick[0] << shift;
             mask |= digits << shift;
-            need -= s_pick[1];
-            __syncthreads();
+            need -= pick[1];
+            if (pick[2] == need) break;                      // (the same in every thread)
         }
-        // ---- in index order: keys above the threshold, and the first `need` equal to it
-        const int per = (nb + kSparseThreads - 1) / kSparseThreads;
-        const int b0 = min(nb, tid * per), b1 = min(nb, b0 + per);
-        uint32_t gt = 0, eq = 0, total;
-        for (int b = b0; b < b1; ++b) {
-            gt += s_key[b] > prefix;
-            eq += s_key[b] == prefix;
+        // ---- in index order: keys above the threshold, and the first `need`
+        // equal to it; a warp has consecutive blocks and counts by ballot
+        const int per = (nb + 32 * kSparseWarps - 1) / (32 * kSparseWarps) * 32;
+        const int b0 = min(nb, warp * per), b1 = min(nb, b0 + per);
+        // both counts in one word: fewer than top <= 1024 keys are above, at
+        // most 32768 equal
+        uint32_t count = 0;
+        for (int i = b0 + lane; i < b0 + per; i += 32) {
+            const uint32_t key = i < b1 ? s_key[i] & mask : 0u;
+            count += __popc(__ballot_sync(0xffffffffu, i < b1 && key > prefix)) << 16;
+            count += __popc(__ballot_sync(0xffffffffu, i < b1 && key == prefix));
         }
-        // (both counts are at most 32768)
-        uint32_t gt_before = block_scan(gt, s_scan, &total);
-        uint32_t eq_before = block_scan(eq, s_scan, &total);
-        for (int b = b0; b < b1; ++b) {
-            const uint32_t key = s_key[b];
-            const bool take = key > prefix || (key == prefix && eq_before < need);
-            if (take) s_list[gt_before + min(eq_before, need)] = b;
-            gt_before += key > prefix;
-            eq_before += key == prefix;
+        uint32_t* sums = s_scan + kSparseWarps;
+        if (lane == 0) sums[warp] = count;
+        __syncthreads();
+        uint32_t at = 0;
+#pragma unroll
+        for (int w2 = 0; w2 < kSparseWarps - 1; ++w2)
+            if (w2 < warp) at += sums[w2];
+        for (int i = b0 + lane; i < b0 + per; i += 32) {
+            const uint32_t key = i < b1 ? s_key[i] & mask : 0u;
+            const unsigned gt = __ballot_sync(0xffffffffu, i < b1 && key > prefix);
+            const unsigned eq = __ballot_sync(0xffffffffu, i < b1 && key == prefix);
+            const unsigned below = (1u << lane) - 1u;
+            const uint32_t n_gt = (at >> 16) + __popc(gt & below), n_eq = (at & 0xffffu) + __popc(eq & below);
+            if (((gt >> lane) & 1u) || (((eq >> lane) & 1u) && n_eq < need)) s_list[n_gt + min(n_eq, need)] = i;
+            at += (__popc(gt) << 16) + __popc(eq);
         }
         nsel = a.top;
         __syncthreads();                                     // the list is complete, the scores are read
+    } else if (C > 1) {
+        ptx::cluster_wait();
     }
     if (a.selected && rank == 0)
         for (int i = tid; i < a.top; i += kSparseThreads)
             a.selected[item * a.top + i] = i >= nsel || row < 0 ? -1 : choose ? s_list[i] : i;
 
-    // ---- attention: entries 0..nsel-1 are blocks, the rest pieces of the tail
+    // ---- attention over entries of 32 rows: two of every block, then the tail's
     const int quad = lane & 3, g8 = lane >> 2;
     uint32_t qf[D / 16][4];
     {
@@ -251,36 +293,74 @@ __global__ void __launch_bounds__(kSparseThreads, 1) sparse_kernel(const __grid_
     const __nv_bfloat16* vb = static_cast<const __nv_bfloat16*>(a.v_cache.data) + n * a.v_cache.batch_stride +
                               h * a.v_cache.head_stride + g8 * DJ;
     const int tail = row - nb * STATEKV_BLOCK + 1;           // rows since the last complete block
-    const int entries = nsel + (tail > 0 ? (tail + STATEKV_BLOCK - 1) / STATEKV_BLOCK : 0);
-    for (int e = row < 0 ? entries : warp * C + rank; e < entries; e += kSparseWarps * C) {
-        const int r0 = STATEKV_BLOCK * (e < nsel ? (choose ? s_list[e] : e) : nb + e - nsel);
-        const int valid = min(STATEKV_BLOCK, row + 1 - r0);  // 64 for a block
-        float s[8][4];
+    const int halves = 2 * nsel, entries = row < 0 ? 0 : halves + (max(tail, 0) + kRows - 1) / kRows;
+    // first row of entry e
+    auto row_of = [&](int e) -> int {
+        return e < halves ? STATEKV_BLOCK * (choose ? s_list[e >> 1] : e >> 1) + kRows * (e & 1)
+                          : STATEKV_BLOCK * nb + kRows * (e - halves);
+    };
+    // a warp's entries one after the other: the next one's keys are loaded
+    // while this one's probabilities are computed, its values while the next
+    // scores are
+    uint4 kf[kRows / 8][KI], vf[kRows / 16][4][DJ / 8];
+    auto load_k = [&](int r0) {
+        const int last = min(kRows, row + 1 - r0) - 1;       // rows past the token's own may not exist
 #pragma unroll
-        for (int t = 0; t < 8; ++t) {
+        for (int t = 0; t < kRows / 8; ++t) {
+            const __nv_bfloat16* p = kb + (int64_t)(r0 + min(8 * t + g8, last)) * a.k_cache.token_stride;
+#pragma unroll
+            for (int i = 0; i < KI; ++i) kf[t][i] = *reinterpret_cast<const uint4*>(p + i * 32);
+        }
+    };
+    auto load_v = [&](int r0) {
+        const int last = min(kRows, row + 1 - r0) - 1;
+        // of keys 16 ks + {2 quad, 2 quad + 1} and 8 further, columns g8 * DJ ..
+#pragma unroll
+        for (int ks = 0; ks < kRows / 16; ++ks)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const int key = 16 * ks + 2 * quad + (y & 1) + 8 * (y >> 1);
+                const __nv_bfloat16* p = vb + (int64_t)(r0 + min(key, last)) * a.v_cache.token_stride;
+#pragma unroll
+                for (int i = 0; i < DJ / 8; ++i) {
+                    vf[ks][y][i] = *reinterpret_cast<const uint4*>(p + 8 * i);
+                    if (key > last) vf[ks][y][i] = make_uint4(0, 0, 0, 0);
+                }
+            }
+    };
+    int e = warp * C + rank, r0 = 0;
+    if (e < entries) {
+        r0 = row_of(e);
+        load_k(r0);
+        load_v(r0);
+    }
+    while (e < entries) {
+        const int valid = row + 1 - r0;                      // at least kRows but in the tail
+        float s[kRows / 8][4];
+#pragma unroll
+        for (int t = 0; t < kRows / 8; ++t) {
             s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
-            // (rows past the token's own are not read: they may lie past the cache)
-            const int64_t r = r0 + min(8 * t + g8, valid - 1);
-            uint4 kf[KI];
-#pragma unroll
-            for (int i = 0; i < KI; ++i)
-                kf[i] = *reinterpret_cast<const uint4*>(kb + r * a.k_cache.token_stride + i * 32);
 #pragma unroll
             for (int i = 0; i < KI; ++i) {
-                mma16816(s[t], qf[2 * i], kf[i].x, kf[i].y);
-                mma16816(s[t], qf[2 * i + 1], kf[i].z, kf[i].w);
+                mma16816(s[t], qf[2 * i], kf[t][i].x, kf[t][i].y);
+                mma16816(s[t], qf[2 * i + 1], kf[t][i].z, kf[t][i].w);
             }
         }
-        if (valid < STATEKV_BLOCK) {
+        e += kSparseWarps * C;
+        if (e < entries) {
+            r0 = row_of(e);
+            load_k(r0);
+        }
+        if (valid < kRows) {
 #pragma unroll
-            for (int t = 0; t < 8; ++t)
+            for (int t = 0; t < kRows / 8; ++t)
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
                     if (8 * t + 2 * quad + (x & 1) >= valid) s[t][x] = -INFINITY;
         }
         float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int t = 0; t < 8; ++t) {
+        for (int t = 0; t < kRows / 8; ++t) {
             top[0] = ptx::max3(top[0], s[t][0], s[t][1]);
             top[1] = ptx::max3(top[1], s[t][2], s[t][3]);
         }
@@ -288,31 +368,24 @@ __global__ void __launch_bounds__(kSparseThreads, 1) sparse_kernel(const __grid_
         for (int x = 0; x < 2; ++x) {
             top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 1));
             top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 2));
-            const float mn = fmaxf(m[x], top[x] * ka.scale_log2);
-            const float f = m[x] == -INFINITY ? 0.f : ptx::ex2_approx(m[x] - mn);
-            m[x] = mn;
-            l[x] *= f;
+            top[x] = fmaxf(m[x], top[x] * ka.scale_log2);
+        }
+        if (__any_sync(0xffffffffu, top[0] > m[0] || top[1] > m[1])) {
 #pragma unroll
-            for (int j = 0; j < DJ; ++j) {
-                o[j][2 * x] *= f;
-                o[j][2 * x + 1] *= f;
+            for (int x = 0; x < 2; ++x) {
+                const float f = m[x] == -INFINITY ? 0.f : ptx::ex2_approx(m[x] - top[x]);
+                m[x] = top[x];
+                l[x] *= f;
+#pragma unroll
+                for (int j = 0; j < DJ; ++j) {
+                    o[j][2 * x] *= f;
+                    o[j][2 * x + 1] *= f;
+                }
             }
         }
         const float nm0 = m[0] == -INFINITY ? 0.f : -m[0], nm1 = m[1] == -INFINITY ? 0.f : -m[1];
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-            // V of keys 16 ks + {2 quad, 2 quad + 1} and 8 further, columns g8 * DJ ..
-            uint4 v[4][DJ / 8];
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                const int key = 16 * ks + 2 * quad + (y & 1) + 8 * (y >> 1);
-                const int64_t r = r0 + min(key, valid - 1);
-#pragma unroll
-                for (int i = 0; i < DJ / 8; ++i) {
-                    v[y][i] = *reinterpret_cast<const uint4*>(vb + r * a.v_cache.token_stride + 8 * i);
-                    if (key >= valid) v[y][i] = make_uint4(0, 0, 0, 0);
-                }
-            }
+        for (int ks = 0; ks < kRows / 16; ++ks) {
             uint32_t p[4];
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
@@ -326,6 +399,7 @@ __global__ void __launch_bounds__(kSparseThreads, 1) sparse_kernel(const __grid_
                 p[2 * t] = ptx::pack_bf16x2(p0, p1);
                 p[2 * t + 1] = ptx::pack_bf16x2(p2, p3);
             }
+            const uint4 (&v)[4][DJ / 8] = vf[ks];
 #pragma unroll
             for (int i = 0; i < DJ / 8; ++i) {
                 const uint32_t k0[4] = {v[0][i].x, v[0][i].y, v[0][i].z, v[0][i].w};
@@ -341,6 +415,7 @@ __global__ void __launch_bounds__(kSparseThreads, 1) sparse_kernel(const __grid_
                 }
             }
         }
+        if (e < entries) load_v(r0);
     }
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
@@ -360,83 +435,125 @@ __global__ void __launch_bounds__(kSparseThreads, 1) sparse_kernel(const __grid_
         }
     }
     __syncthreads();
-    // ---- the CTA's warps, in order
-    for (int i = tid; i < G * D; i += kSparseThreads) {
+    // ---- the CTA's warps, in order, 4 columns a thread; the result goes to
+    // the CTA of the cluster that writes this part of the output
+    const int slice = ((G * D + C - 1) / C + 3) / 4 * 4;
+    for (int i = 4 * tid; i < G * D; i += 4 * kSparseThreads) {
         const int r = i / D;
-        float mm = -INFINITY;
+        float mm = -INFINITY, ls = 0.f;
 #pragma unroll
         for (int w = 0; w < kSparseWarps; ++w) mm = fmaxf(mm, s_wml[w * 16 + r].x);
-        float acc = 0.f, ls = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kSparseWarps; ++w) {
             const float2 x = s_wml[w * 16 + r];
+            const float4 y = *reinterpret_cast<const float4*>(s_o + w * G * D + i);
             const float f = x.x == -INFINITY ? 0.f : ptx::ex2_approx(x.x - mm);
-            acc = fmaf(s_o[w * G * D + i], f, acc);
+            acc.x = fmaf(y.x, f, acc.x);
+            acc.y = fmaf(y.y, f, acc.y);
+            acc.z = fmaf(y.z, f, acc.z);
+            acc.w = fmaf(y.w, f, acc.w);
             ls = fmaf(x.y, f, ls);
         }
-        s_part[i] = acc;
-        if (i % D == 0) s_pml[r] = make_float2(mm, ls);
+        const int owner = i / slice;
+        float* part = s_part + rank * slice + i - owner * slice;
+        if (C == 1) *reinterpret_cast<float4*>(part) = acc;
+        else ptx::st_cluster_f32x4(ptx::cluster_map(ptx::smem_u32(part), (uint32_t)owner), acc);
+        if (i % D == 0) {
+            if (C == 1) s_pml[r] = make_float2(mm, ls);
+            else
+                for (int c = 0; c < C; ++c)
+                    ptx::st_cluster_f32x2(ptx::cluster_map(ptx::smem_u32(s_pml + rank * 16 + r), (uint32_t)c),
+                                          make_float2(mm, ls));
+        }
     }
-    if (C > 1) ptx::cluster_sync();
+    if (C > 1) ptx::cluster_sync();                          // the last access to another CTA's memory
     else __syncthreads();
-    // ---- the CTAs, in rank order; each writes its share of the output
-    for (int i = (rank * kSparseThreads + tid) * 2; i < G * D; i += C * kSparseThreads * 2) {
-        const int r = i / D;
-        float2 ml[8];
-        float mm = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-            if (c < C) {
-                const uint32_t at = ptx::cluster_map(ptx::smem_u32(s_pml + r), (uint32_t)c);
-                ml[c] = C > 1 ? ptx::ld_cluster_f32x2(at) : s_pml[r];
-                mm = fmaxf(mm, ml[c].x);
-            }
-        float2 acc = make_float2(0.f, 0.f);
-        float ls = 0.f;
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-            if (c < C) {
-                const uint32_t at = ptx::cluster_map(ptx::smem_u32(s_part + i), (uint32_t)c);
-                const float2 x = C > 1 ? ptx::ld_cluster_f32x2(at) : *reinterpret_cast<const float2*>(s_part + i);
-                const float f = ml[c].x == -INFINITY ? 0.f : ptx::ex2_approx(ml[c].x - mm);
-                acc.x = fmaf(x.x, f, acc.x);
-                acc.y = fmaf(x.y, f, acc.y);
-                ls = fmaf(ml[c].y, f, ls);
-            }
+    // ---- the CTAs, in rank order
+    for (int i = 4 * tid; i < slice; i += 4 * kSparseThreads) {
+        const int at = rank * slice + i, r = at / D;
+        if (at >= G * D) break;
+        float mm = -INFINITY, ls = 0.f;
+        for (int c = 0; c < C; ++c) mm = fmaxf(mm, s_pml[c * 16 + r].x);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = 0; c < C; ++c) {
+            const float2 x = s_pml[c * 16 + r];
+            const float4 y = *reinterpret_cast<const float4*>(s_part + c * slice + i);
+            const float f = x.x == -INFINITY ? 0.f : ptx::ex2_approx(x.x - mm);
+            acc.x = fmaf(y.x, f, acc.x);
+            acc.y = fmaf(y.y, f, acc.y);
+            acc.z = fmaf(y.z, f, acc.z);
+            acc.w = fmaf(y.w, f, acc.w);
+            ls = fmaf(x.y, f, ls);
+        }
         const float inv = ls > 0.f || ls != ls ? 1.f / ls : 0.f;
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out.data) + n * a.out.batch_stride +
-                             (int64_t)(h * G + r) * a.out.head_stride + (int64_t)tok * a.out.token_stride + i % D;
-        *reinterpret_cast<uint32_t*>(out) = ptx::pack_bf16x2(acc.x * inv, acc.y * inv);
+                             (int64_t)(h * G + r) * a.out.head_stride + (int64_t)tok * a.out.token_stride + at % D;
+        *reinterpret_cast<uint2*>(out) = make_uint2(ptx::pack_bf16x2(acc.x * inv, acc.y * inv),
+                                                    ptx::pack_bf16x2(acc.z * inv, acc.w * inv));
     }
-    if (C > 1) ptx::cluster_sync();                          // nobody leaves while its memory is read
+}
+
+template <int D>
+cudaLaunchConfig_t config(int64_t items, int cluster, size_t smem, cudaStream_t st, cudaLaunchAttribute (&attr)[1]) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(items * cluster));
+    cfg.blockDim = dim3(kSparseThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cfg;
+}
+
+// Clusters of 16 CTAs (more than the portable 8) that device dev holds at
+// once, one CTA per SM; cached, -1 before the first query.
+template <int D>
+int clusters_of_16(int dev) {
+    static std::atomic<int> cache[64];
+    static std::atomic<uint64_t> known{0};
+    if (dev < 0 || dev >= 64) return 0;
+    if (known.load(std::memory_order_acquire) >> dev & 1ull) return cache[dev].load(std::memory_order_relaxed);
+    int n = 0;
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = config<D>(1, 16, 64 * 1024, nullptr, attr);
+    const void* f = reinterpret_cast<const void*>(&sparse_kernel<D>);
+    if (cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+        cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, sparse_kernel<D>, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        n = 0;
+    }
+    cache[dev].store(n, std::memory_order_relaxed);
+    known.fetch_or(1ull << dev, std::memory_order_release);
+    return n;
 }
 
 // CTAs per (batch entry, KV head, token): as many as keep the device in one
-// wave, at most 8 (the portable cluster size).
-int cluster_for(int64_t items, int sms) {
+// wave, at most 16.  An SM takes in about 50 GB/s of scattered rows: the 4 MB
+// of one token in one layer want as many SMs as there are.
+template <int D>
+int cluster_for(int64_t items, int sms, int dev) {
+    if (items * 16 <= sms && items <= clusters_of_16<D>(dev)) return 16;
     int c = 8;
     while (c > 1 && items * c > sms) c /= 2;
     return c;
 }
 
 template <int D>
-cudaError_t launch(const SparseKernelArgs& ka, int64_t items, cudaStream_t st) {
-    const size_t smem = ka.region + 16 * D * 4 + 16 * 8 + kSparseWarps * 16 * 8 + kMaxTop * 4 + kBins * 4 + 16 * D +
-                        (kSparseWarps + 2) * 4;
-    cudaError_t e = cudaFuncSetAttribute(sparse_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+cudaError_t launch(SparseKernelArgs& ka, int64_t items, int dev, int sms, cudaStream_t st) {
+    ka.cluster = cluster_for<D>(items, sms, dev);
+    const size_t smem = ka.region + (16 * D + 64) * 4 + 16 * 16 * 8 + kSparseWarps * 16 * 8 + kMaxTop * 4 +
+                        2 * kBins * 4 + 16 * D + (2 * kSparseWarps + 6) * 4;
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(&sparse_kernel<D>), 227 * 1024, dev, done);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(items * ka.cluster));
-    cfg.blockDim = dim3(kSparseThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
     cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)ka.cluster;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    const cudaLaunchConfig_t cfg = config<D>(items, ka.cluster, smem, st, attr);
     return cudaLaunchKernelEx(&cfg, sparse_kernel<D>, ka);
 }
 
@@ -467,16 +584,13 @@ extern "C" int statekv_sparse_attention(const statekv_sparse_args* args, void* c
     if (most > a.top && (!aligned16(a.codes) || !a.scales || reinterpret_cast<uintptr_t>(a.scales) % 4))
         return STATEKV_E_INVALID_ARG;
     int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return view_cuda_fail();
+    if (!current_device(&dev, &sms)) return view_cuda_fail();
     SparseKernelArgs k{};
     k.a = a;
     k.G = a.q_heads / a.kv_heads;
     k.scale_log2 = (float)(a.scale * 1.4426950408889634074);
-    k.cluster = cluster_for(items, sms);
     k.region = (std::max(most > a.top ? most * 4 : 0, kSparseWarps * k.G * a.head_dim * 4) + 15) / 16 * 16;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(cuda_stream);
-    const cudaError_t e = a.head_dim == 128 ? launch<128>(k, items, st) : launch<64>(k, items, st);
+    const cudaError_t e = a.head_dim == 128 ? launch<128>(k, items, dev, sms, st) : launch<64>(k, items, dev, sms, st);
     return e == cudaSuccess ? STATEKV_OK : view_cuda_fail();
 }

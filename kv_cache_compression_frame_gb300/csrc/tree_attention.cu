@@ -806,10 +806,11 @@ struct TreeMaps {
 };
 
 template <int D, bool SPLIT_ROWS>
-cudaError_t launch_main(const TreeKernelArgs& k, const TreeMaps& m, cudaStream_t st) {
+cudaError_t launch_main(const TreeKernelArgs& k, const TreeMaps& m, int dev, cudaStream_t st) {
     using L = TreeLayout<D, SPLIT_ROWS>;
-    cudaError_t e = cudaFuncSetAttribute(tree_kernel<D, SPLIT_ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         L::SMEM);
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e =
+        allow_smem(reinterpret_cast<const void*>(&tree_kernel<D, SPLIT_ROWS>), L::SMEM, dev, done);
     if (e != cudaSuccess) return e;
     tree_kernel<D, SPLIT_ROWS><<<(unsigned)k.grid, kTreeThreads, L::SMEM, st>>>(m.k, m.v, m.kn, m.vn, k);
     return cudaGetLastError();
@@ -852,12 +853,6 @@ int tree_sizes(int batch, int q_heads, int kv_heads, int tokens, int head_dim, T
     return z->units > 0x7fffffff / 1024 ? STATEKV_E_UNSUPPORTED : STATEKV_OK;
 }
 
-bool device_sms(int* sms) {
-    int dev = 0;
-    return cudaGetDevice(&dev) == cudaSuccess &&
-           cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess;
-}
-
 int64_t workspace_for(const TreeSizes& z, int sms, int d) {
     // one segment per CTA and per unit; O, then (m, l)
     return ((int64_t)sms + z.units) * z.rows * (d * 4 + 8);
@@ -876,8 +871,8 @@ extern "C" int64_t statekv_tree_attention_workspace(int32_t batch, int32_t q_hea
     using namespace statekv;
     TreeSizes z;
     if (tree_sizes(batch, q_heads, kv_heads, tokens, head_dim, &z) != STATEKV_OK) return -1;
-    int sms = 0;
-    if (!device_sms(&sms)) {
+    int dev = 0, sms = 0;
+    if (!current_device(&dev, &sms)) {
         cudaGetLastError();
         return -1;
     }
@@ -907,8 +902,8 @@ extern "C" int statekv_tree_attention(const statekv_tree_args* args, void* cuda_
         (cached && (!spread(a.k_cache, a.batch, a.kv_heads, a.cache_rows) ||
                     !spread(a.v_cache, a.batch, a.kv_heads, a.cache_rows))))
         return STATEKV_E_INVALID_ARG;
-    int sms = 0;
-    if (!device_sms(&sms)) return view_cuda_fail();
+    int dev = 0, sms = 0;
+    if (!current_device(&dev, &sms)) return view_cuda_fail();
     if (!aligned16(a.workspace) || a.workspace_bytes < workspace_for(z, sms, a.head_dim))
         return STATEKV_E_INVALID_ARG;
     TreeMaps m;
@@ -934,8 +929,8 @@ extern "C" int statekv_tree_attention(const statekv_tree_args* args, void* cuda_
     k.part_ml = reinterpret_cast<float2*>(k.part_o + segments * z.rows * a.head_dim);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(cuda_stream);
     const bool two = z.R > kTile;
-    cudaError_t e = a.head_dim == 128 ? (two ? launch_main<128, true>(k, m, st) : launch_main<128, false>(k, m, st))
-                                      : (two ? launch_main<64, true>(k, m, st) : launch_main<64, false>(k, m, st));
+    cudaError_t e = a.head_dim == 128 ? (two ? launch_main<128, true>(k, m, dev, st) : launch_main<128, false>(k, m, dev, st))
+                                      : (two ? launch_main<64, true>(k, m, dev, st) : launch_main<64, false>(k, m, dev, st));
     // one CTA holds whole units only
     if (e == cudaSuccess && k.grid > 1)
         e = a.head_dim == 128 ? launch_combine<128>(k, z.units, sms, st) : launch_combine<64>(k, z.units, sms, st);

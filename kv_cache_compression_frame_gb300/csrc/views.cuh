@@ -3,9 +3,26 @@
 // views and the lookup of a sequence's cache length.
 #pragma once
 
+#include <atomic>
+
 #include "statekv_internal.cuh"
 
 namespace statekv {
+
+// Lets a kernel take `bytes` of dynamic shared memory on device dev, once per
+// device (`done`: one bit each; devices past 63 ask every time).
+inline cudaError_t allow_smem(const void* kernel, int bytes, int dev, std::atomic<uint64_t>& done) {
+    const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0ull;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
+
+inline bool current_device(int* dev, int* sms) {
+    return cudaGetDevice(dev) == cudaSuccess &&
+           cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev) == cudaSuccess;
+}
 
 // A failed CUDA call: clear the runtime's last-error state (a refused launch,
 // for instance, would otherwise be reported again by the next call that

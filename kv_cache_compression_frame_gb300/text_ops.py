@@ -16,27 +16,31 @@ mode is on.
 
 from __future__ import annotations
 
-import ctypes as C
+import struct
 
 import torch
 
 from . import _native as N
 
-_BF16, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
+_BF16, _F32, _I32, _I64, _I8 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.int8
 _DTYPES = {_BF16: N.BF16, _F32: N.F32}
-_NO_VIEW = N.View(None, 0, 0, 0)
-_status: dict[int, torch.Tensor] = {}
+_NO_VIEW = (0, 0, 0, 0)
+_status: dict[int, tuple] = {}              # device -> (status word, its address)
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 def _status_ptr(dev: int) -> int:
-    t = _status.get(dev)
-    if t is None:
-        if torch.cuda.is_current_stream_capturing():
-            # its zeros would be part of the graph, and its memory the graph's
-            raise RuntimeError("call a text operator once on this device before capturing one")
-        t = _status[dev] = torch.zeros(4, dtype=_I32, device=torch.device("cuda", dev))
-        torch.cuda.synchronize(dev)         # any stream may use it from here on
+    try:
+        return _status[dev][1]
+    except KeyError:
+        pass
+    if torch.cuda.is_current_stream_capturing():
+        # its zeros would be part of the graph, and its memory the graph's
+        raise RuntimeError("call a text operator once on this device before capturing one")
+    t = torch.zeros(4, dtype=_I32, device=torch.device("cuda", dev))
+    torch.cuda.synchronize(dev)             # any stream may use it from here on
+    _status[dev] = (t, t.data_ptr())
     return t.data_ptr()
 
 
@@ -47,9 +51,9 @@ def check_status(device: int | torch.device | None = None) -> None:
         if isinstance(device, int) else torch.device(device).index
     if dev is None:
         dev = torch.cuda.current_device()
-    t = _status.get(dev)
-    if t is None:
+    if dev not in _status:
         return
+    t = _status[dev][0]
     torch.cuda.synchronize(dev)
     code = int(t[0])
     if code:
@@ -82,41 +86,43 @@ def tree_masks(parents, device=None) -> tuple[torch.Tensor, torch.Tensor]:
             torch.tensor(depths, dtype=_I32, device=device))
 
 
-def _view(t: torch.Tensor, name: str, shape, dtype, dev) -> N.View:
+def _view(t: torch.Tensor, name: str, shape, dtype, dev: int) -> tuple:
+    """(pointer, batch, head and token stride) of a checked argument."""
     st = t.stride()
-    if t.dtype is not dtype or t.shape != shape or t.device != dev or (st[3] != 1 and shape[3] != 1):
-        raise ValueError(f"{name}: want {dtype} {tuple(shape)} on {dev} with a contiguous last dimension, "
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or (st[3] != 1 and shape[3] != 1):
+        raise ValueError(f"{name}: want {dtype} {tuple(shape)} on cuda:{dev} with a contiguous last dimension, "
                          f"got {t.dtype} {tuple(t.shape)} strides {st} on {t.device}")
     if t.requires_grad and torch.is_grad_enabled():
         raise ValueError(f"{name} requires grad: the text operators have no backward pass")
-    return N.View(t.data_ptr(), st[0], st[1], st[2])
+    return t.data_ptr(), st[0], st[1], st[2]
 
 
 def _shape4(t: torch.Tensor, name: str):
-    if t.dim() != 4 or not t.is_cuda:
+    s = t.shape
+    if len(s) != 4 or not t.is_cuda:
         raise ValueError(f"{name}: want a CUDA tensor [batch][heads][tokens][head_dim], got "
-                         f"{tuple(t.shape)} on {t.device}")
-    return t.shape
+                         f"{tuple(s)} on {t.device}")
+    return s
 
 
-def _vector(t: torch.Tensor, name: str, dtype, dev, dims: int = 1) -> int:
-    if t.dtype is not dtype or t.dim() != dims or t.device != dev or not t.is_contiguous():
-        raise ValueError(f"{name}: want a contiguous {dims}-D {dtype} tensor on {dev}, got {t.dtype} "
+def _vector(t: torch.Tensor, name: str, dtype, dev: int, dims: int = 1) -> int:
+    if t.dtype is not dtype or t.dim() != dims or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: want a contiguous {dims}-D {dtype} tensor on cuda:{dev}, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _lengths(lengths, batch: int, dev) -> tuple[int | None, int, int]:
-    """(pointer, common value, layers) of a lengths argument."""
+def _lengths(lengths, batch: int, dev: int) -> tuple[int, int, int]:
+    """(pointer, common value, layers; 0: not known) of a lengths argument."""
     if isinstance(lengths, torch.Tensor):
         p = _vector(lengths, "lengths", _I32, dev)
         seqs = lengths.shape[0]
         if seqs == 0 or batch % seqs:
             if batch == seqs == 0:
-                return None, 0, 1
+                return 0, 0, 1
             raise ValueError(f"lengths: {seqs} sequences do not divide a batch of {batch}")
         return p, 0, batch // seqs or 1
-    return None, int(lengths), 0
+    return 0, int(lengths), 0
 
 
 def _layers(found: int, rows: int, batch: int, name: str) -> int:
@@ -132,26 +138,51 @@ def _layers(found: int, rows: int, batch: int, name: str) -> int:
 
 
 class _On:
-    """The tensors' device and the stream of a call made current."""
+    """Makes the tensors' device and the call's stream current."""
 
-    def __init__(self, dev: torch.device, stream):
-        self.dev = dev.index
-        self.away = torch.cuda.current_device() != self.dev
-        self.stream = stream
+    def __init__(self, dev: int, stream):
+        self.guards = [torch.cuda.device(dev)] + ([torch.cuda.stream(stream)] if stream is not None else [])
 
-    def __enter__(self) -> int:
-        self.guards = []
-        if self.away:
-            self.guards.append(torch.cuda.device(self.dev))
-        if self.stream is not None:
-            self.guards.append(torch.cuda.stream(self.stream))
+    def __enter__(self):
         for g in self.guards:
             g.__enter__()
-        return _raw_stream(self.dev)
 
     def __exit__(self, *exc):
         for g in reversed(self.guards):
             g.__exit__(*exc)
+
+
+class _Here:
+    """The same where they are current already."""
+
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *exc):
+        pass
+
+
+_HERE = _Here()
+
+
+def _on(dev: int, stream):
+    return _HERE if stream is None and _current_device() == dev else _On(dev, stream)
+
+
+def _call(name: str, pack: struct.Struct, dev: int, *values) -> None:
+    if not N.packed:
+        N.load()
+    try:
+        args = pack.pack(*values)
+    except struct.error as e:
+        raise ValueError(f"{name}: a size is out of range ({e})") from None
+    status = N.packed[name](args, _raw_stream(dev))
+    if status:
+        N.check(status, name)
+
+
+def _empty(shape, dtype, like: torch.Tensor) -> torch.Tensor:
+    return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def qk_norm_rope(q, k, positions, omega, q_weight=None, k_weight=None, *, v=None, eps: float = 1e-6,
@@ -163,63 +194,65 @@ def qk_norm_rope(q, k, positions, omega, q_weight=None, k_weight=None, *, v=None
     float64 [d/2], in one pass.  v is copied.  k and v go to rows out_rows
     (int32 [sequences]) + t of k_out and v_out (default: new tensors, row t).
     Returns (q_out, k_out) or (q_out, k_out, v_out)."""
-    n, hq, t, d = _shape4(q, "q")
+    n, hq, t, d = qs = _shape4(q, "q")
     hkv = _shape4(k, "k")[1]
-    dev, dt = q.device, q.dtype
+    dt, dev = q.dtype, q.get_device()
     if dt not in _DTYPES:
         raise ValueError(f"q: {dt}, want one of {list(_DTYPES)}")
-    a = N.NormRopeArgs()
-    a.q = _view(q, "q", (n, hq, t, d), dt, dev)
-    a.k = _view(k, "k", (n, hkv, t, d), dt, dev)
-    wd = None
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+    ks = (n, hkv, t, d)
+    qv, kv_ = _view(q, "q", qs, dt, dev), _view(k, "k", ks, dt, dev)
+    wd, w_rows, w_ptr = None, 1, [0, 0]
+    for i, w in enumerate((q_weight, k_weight)):
         if w is not None:
-            wd = wd or w.dtype
             rows = w.shape[0] if w.dim() == 2 else 1
-            if w.shape[-1:] != (d,) or wd not in _DTYPES or rows < 1 or n % rows or a.weight_rows not in (0, rows):
-                raise ValueError(f"{name}: want [{d}] or [layers][{d}] of one of {list(_DTYPES)}, the same for "
-                                 "both weights, layers dividing the batch")
-            setattr(a, name, _vector(w, name, wd, dev, w.dim()))
-            a.weight_rows = rows
-    a.weight_rows = a.weight_rows or 1
+            if w.shape[-1:] != (d,) or w.dtype not in _DTYPES or rows < 1 or n % rows or \
+                    (wd is not None and (wd is not w.dtype or rows != w_rows)):
+                raise ValueError(f"{'qk'[i]}_weight: want [{d}] or [layers][{d}] of one of {list(_DTYPES)}, the "
+                                 "same for both weights, layers dividing the batch")
+            wd, w_rows = w.dtype, rows
+            w_ptr[i] = _vector(w, f"{'qk'[i]}_weight", wd, dev, w.dim())
     if omega.shape != (d // 2,):
         raise ValueError(f"omega: want [{d // 2}]")
-    a.omega = _vector(omega, "omega", torch.float64, dev)
-    a.position_layers = 1
+    om = _vector(omega, "omega", torch.float64, dev)
+    pos = p0 = p_stride = 0
+    p_layers = layers = 1
     if isinstance(positions, torch.Tensor):
-        a.positions = _vector(positions, "positions", _I32, dev, positions.dim() if positions.dim() == 2 else 1)
+        dims = positions.dim()
+        pos = _vector(positions, "positions", _I32, dev, dims if dims == 2 else 1)
         if positions.shape[-1] != t:
             raise ValueError(f"positions: want {t} per row")
-        if positions.dim() == 2 and positions.shape[0] != 1:
-            if n and (positions.shape[0] == 0 or n % positions.shape[0]):
-                raise ValueError(f"positions: {positions.shape[0]} rows do not divide a batch of {n}")
-            a.position_stride, a.position_layers = t, max(1, n // max(1, positions.shape[0]))
+        if dims == 2 and positions.shape[0] != 1:
+            rows = positions.shape[0]
+            if n and (rows == 0 or n % rows):
+                raise ValueError(f"positions: {rows} rows do not divide a batch of {n}")
+            p_stride, p_layers = t, max(1, n // max(1, rows))
     else:
-        a.position0 = int(positions)
-    a.layers = 1
+        p0 = int(positions)
+    at = 0
     if out_rows is not None:
-        a.out_rows, _, a.layers = _lengths(out_rows, n, dev)
+        if not isinstance(out_rows, torch.Tensor):
+            raise ValueError("out_rows: want int32 [sequences]")
+        at, _, layers = _lengths(out_rows, n, dev)
         if k_out is None or (v is not None and v_out is None):
             raise ValueError("out_rows needs k_out (and v_out)")
-    with _On(dev, stream) as st:
-        a.status = _status_ptr(dev.index)
+    if v is None and v_out is not None:
+        raise ValueError("v_out without v")
+    with _on(dev, stream):
+        status = _status_ptr(dev)
         if q_out is None:
-            q_out = torch.empty((n, hq, t, d), dtype=dt, device=dev)
+            q_out = _empty(qs, dt, q)
         if k_out is None:
-            k_out = torch.empty((n, hkv, t, d), dtype=dt, device=dev)
-        a.q_out = _view(q_out, "q_out", (n, hq, t, d), dt, dev)
+            k_out = _empty(ks, dt, q)
         cap = k_out.shape[2] if k_out.dim() == 4 else -1
-        a.k_out = _view(k_out, "k_out", (n, hkv, cap, d), dt, dev)
-        if v is not None:
-            a.v = _view(v, "v", (n, hkv, t, d), dt, dev)
-            if v_out is None:
-                v_out = torch.empty((n, hkv, cap, d), dtype=dt, device=dev)
-            a.v_out = _view(v_out, "v_out", (n, hkv, cap, d), dt, dev)
-        elif v_out is not None:
-            raise ValueError("v_out without v")
-        a.batch, a.q_heads, a.kv_heads, a.tokens, a.head_dim = n, hq, hkv, t, d
-        a.out_capacity, a.dtype, a.weight_dtype, a.eps = cap, _DTYPES[dt], _DTYPES[wd or dt], eps
-        N.check(N.load().statekv_norm_rope(C.byref(a), st), "statekv_norm_rope")
+        os_ = (n, hkv, cap, d)
+        if v is not None and v_out is None:
+            v_out = _empty(os_, dt, q)
+        _call("statekv_norm_rope", N.PACK_NORM_ROPE, dev,
+            *qv, *kv_, *(_NO_VIEW if v is None else _view(v, "v", ks, dt, dev)),
+            *_view(q_out, "q_out", qs, dt, dev), *_view(k_out, "k_out", os_, dt, dev),
+            *(_NO_VIEW if v is None else _view(v_out, "v_out", os_, dt, dev)),
+            w_ptr[0], w_ptr[1], om, pos, at, status, p0, p_stride, p_layers, n, layers, hq, hkv, t, d, cap,
+            w_rows, _DTYPES[dt], _DTYPES[wd or dt], eps)
     return (q_out, k_out) if v is None else (q_out, k_out, v_out)
 
 
@@ -231,39 +264,37 @@ def tree_attention(q, k_new, v_new, tree, k_cache, v_cache, lengths, *, scale: f
     themselves, where tree (int64 masks [tokens] or [sequences][tokens], see
     tree_masks) says.  bf16.  Returns out like q.  workspace: a uint8 CUDA
     tensor of tree_attention_workspace() bytes (default: allocated)."""
-    n, hq, tok, d = _shape4(q, "q")
-    hkv, rows = _shape4(k_cache, "k_cache")[1:3]
-    dev = q.device
-    a = N.TreeArgs()
-    a.q = _view(q, "q", (n, hq, tok, d), _BF16, dev)
-    a.k_new = _view(k_new, "k_new", (n, hkv, tok, d), _BF16, dev)
-    a.v_new = _view(v_new, "v_new", (n, hkv, tok, d), _BF16, dev)
-    a.k_cache = _view(k_cache, "k_cache", (n, hkv, rows, d), _BF16, dev)
-    a.v_cache = _view(v_cache, "v_cache", (n, hkv, rows, d), _BF16, dev)
-    a.lengths, a.length, layers = _lengths(lengths, n, dev)
+    n, hq, tok, d = qs = _shape4(q, "q")
+    _, hkv, rows, _ = _shape4(k_cache, "k_cache")
+    dev = q.get_device()
+    ns, cs = (n, hkv, tok, d), (n, hkv, rows, d)
+    views = (*_view(q, "q", qs, _BF16, dev), *_view(k_new, "k_new", ns, _BF16, dev),
+             *_view(v_new, "v_new", ns, _BF16, dev), *_view(k_cache, "k_cache", cs, _BF16, dev),
+             *_view(v_cache, "v_cache", cs, _BF16, dev))
+    lens, length, layers = _lengths(lengths, n, dev)
     dims = tree.dim()
-    a.tree = _vector(tree, "tree", _I64, dev, dims if dims == 2 else 1)
+    masks = _vector(tree, "tree", _I64, dev, dims if dims == 2 else 1)
     if tree.shape[-1] != tok:
         raise ValueError(f"tree: want {tok} masks per row")
+    t_stride = 0
     if dims == 2 and tree.shape[0] != 1:
         layers = _layers(layers, tree.shape[0], n, "tree")
-        a.tree_stride = tok
-    lib = N.load()
-    with _On(dev, stream) as st:
-        a.status = _status_ptr(dev.index)
+        t_stride = tok
+    with _on(dev, stream):
+        status = _status_ptr(dev)
         if out is None:
-            out = torch.empty((n, hq, tok, d), dtype=_BF16, device=dev)
-        a.out = _view(out, "out", (n, hq, tok, d), _BF16, dev)
+            out = _empty(qs, _BF16, q)
+        ws = size = 0
         if workspace is None:
-            size = lib.statekv_tree_attention_workspace(n, hq, hkv, tok, d)
+            size = N.load().statekv_tree_attention_workspace(n, hq, hkv, tok, d)
             if size > 0:
-                workspace = torch.empty(size, dtype=torch.uint8, device=dev)
-        if workspace is not None:
-            a.workspace = _vector(workspace, "workspace", torch.uint8, dev)
-            a.workspace_bytes = workspace.shape[0]
-        a.scale, a.layers = scale, layers or 1
-        a.batch, a.q_heads, a.kv_heads, a.tokens, a.head_dim, a.cache_rows = n, hq, hkv, tok, d, rows
-        N.check(lib.statekv_tree_attention(C.byref(a), st), "statekv_tree_attention")
+                workspace = _empty(size, torch.uint8, q)
+                ws = workspace.data_ptr()
+        else:
+            ws, size = _vector(workspace, "workspace", torch.uint8, dev), workspace.shape[0]
+        _call("statekv_tree_attention", N.PACK_TREE, dev,
+            *views[:4], *_view(out, "out", qs, _BF16, dev), *views[4:], masks, lens, status, ws, size, scale,
+            t_stride, length, n, layers or 1, hq, hkv, tok, d, rows)
     return out
 
 
@@ -280,39 +311,38 @@ def append_accepted(k_new, v_new, path, counts, k_cache, v_cache, lengths, *, st
     [n][Hkv][tokens][d] become cache rows lengths + i, i < counts (int32
     [sequences], or None: all steps).  Returns the new lengths (int32
     [sequences], or an int where lengths is an int and counts None)."""
-    n, hkv, tok, d = _shape4(k_new, "k_new")
+    n, hkv, tok, d = ns = _shape4(k_new, "k_new")
     rows = _shape4(k_cache, "k_cache")[2]
-    dev, dt = k_new.device, k_new.dtype
+    dt, dev = k_new.dtype, k_new.get_device()
     if dt not in _DTYPES:
         raise ValueError(f"k_new: {dt}, want one of {list(_DTYPES)}")
-    a = N.AppendArgs()
-    a.k_new = _view(k_new, "k_new", (n, hkv, tok, d), dt, dev)
-    a.v_new = _view(v_new, "v_new", (n, hkv, tok, d), dt, dev)
-    a.k_cache = _view(k_cache, "k_cache", (n, hkv, rows, d), dt, dev)
-    a.v_cache = _view(v_cache, "v_cache", (n, hkv, rows, d), dt, dev)
-    a.lengths, a.length, layers = _lengths(lengths, n, dev)
+    cs = (n, hkv, rows, d)
+    views = (*_view(k_new, "k_new", ns, dt, dev), *_view(v_new, "v_new", ns, dt, dev),
+             *_view(k_cache, "k_cache", cs, dt, dev), *_view(v_cache, "v_cache", cs, dt, dev))
+    lens, length, layers = _lengths(lengths, n, dev)
     dims = path.dim()
-    a.path = _vector(path, "path", _I32, dev, dims if dims == 2 else 1)
-    a.path_len = path.shape[-1]
+    pp = _vector(path, "path", _I32, dev, dims if dims == 2 else 1)
+    steps = path.shape[-1]
+    p_stride = cnt = 0
     if dims == 2 and path.shape[0] != 1:
         layers = _layers(layers, path.shape[0], n, "path")
-        a.path_stride = a.path_len
+        p_stride = steps
     if counts is not None:
-        a.counts = _vector(counts, "counts", _I32, dev)
+        cnt = _vector(counts, "counts", _I32, dev)
         if layers and counts.shape[0] * layers != n:
             raise ValueError(f"counts: {counts.shape[0]} for {n // layers} sequences")
         layers = layers or _layers(0, counts.shape[0], n, "counts")
     layers = layers or 1
-    with _On(dev, stream) as st:
-        a.status = _status_ptr(dev.index)
-        new = None
-        if a.lengths or a.counts:
-            new = torch.empty(n // layers, dtype=_I32, device=dev)
-            a.new_lengths = new.data_ptr()
-        a.layers, a.batch, a.kv_heads, a.tokens, a.head_dim = layers, n, hkv, tok, d
-        a.cache_rows, a.dtype = rows, _DTYPES[dt]
-        N.check(N.load().statekv_append_accepted(C.byref(a), st), "statekv_append_accepted")
-    return int(lengths) + path.shape[-1] if new is None else new
+    with _on(dev, stream):
+        status = _status_ptr(dev)
+        new, to = None, 0
+        if lens or cnt:
+            new = _empty(n // layers, _I32, k_new)
+            to = new.data_ptr()
+        _call("statekv_append_accepted", N.PACK_APPEND, dev,
+            *views, pp, cnt, lens, to, status, p_stride, steps, length, n, layers, hkv, tok, d, rows,
+            _DTYPES[dt])
+    return length + steps if new is None else new
 
 
 def block_summaries(k_cache, codes, scales, lengths, *, appended: int | None = None, stream=None) -> None:
@@ -320,21 +350,19 @@ def block_summaries(k_cache, codes, scales, lengths, *, appended: int | None = N
     [n][Hkv][blocks]) up to date for the complete 64-row blocks of k_cache
     [n][Hkv][rows][d] that the last `appended` rows (None: all) of the first
     `lengths` completed.  blocks >= rows // 64."""
-    n, hkv, rows, d = _shape4(k_cache, "k_cache")
-    dev = k_cache.device
-    a = N.SummaryArgs()
-    a.k_cache = _view(k_cache, "k_cache", (n, hkv, rows, d), _BF16, dev)
-    a.codes, a.scales, a.blocks = _summary_ptrs(codes, scales, n, hkv, d, dev)
-    a.lengths, a.length, layers = _lengths(lengths, n, dev)
-    a.appended = rows if appended is None else min(int(appended), rows)
-    with _On(dev, stream) as st:
-        a.status = _status_ptr(dev.index)
-        a.layers, a.batch, a.kv_heads, a.head_dim, a.cache_rows = layers or 1, n, hkv, d, rows
-        N.check(N.load().statekv_block_summaries(C.byref(a), st), "statekv_block_summaries")
+    n, hkv, rows, d = cs = _shape4(k_cache, "k_cache")
+    dev = k_cache.get_device()
+    view = _view(k_cache, "k_cache", cs, _BF16, dev)
+    pc, ps, blocks = _summary_ptrs(codes, scales, n, hkv, d, dev)
+    lens, length, layers = _lengths(lengths, n, dev)
+    appended = rows if appended is None else min(int(appended), rows)
+    with _on(dev, stream):
+        _call("statekv_block_summaries", N.PACK_SUMMARY, dev,
+            *view, pc, ps, lens, _status_ptr(dev), length, appended, blocks, n, layers or 1, hkv, d, rows)
 
 
-def _summary_ptrs(codes, scales, n: int, hkv: int, d: int, dev) -> tuple[int, int, int]:
-    pc = _vector(codes, "codes", torch.int8, dev, 4)
+def _summary_ptrs(codes, scales, n: int, hkv: int, d: int, dev: int) -> tuple[int, int, int]:
+    pc = _vector(codes, "codes", _I8, dev, 4)
     ps = _vector(scales, "scales", _F32, dev, 3)
     blocks = codes.shape[2]
     if codes.shape != (n, hkv, blocks, d) or scales.shape != (n, hkv, blocks):
@@ -351,26 +379,25 @@ def sparse_attention(q, k_cache, v_cache, codes, scales, lengths, top: int, *, s
     best for each token and KV head, and the rows since the last complete
     block.  bf16.  Returns (out like q, selected int32 [n][Hkv][tokens][top]:
     the chosen blocks in ascending order, then -1)."""
-    n, hq, tok, d = _shape4(q, "q")
-    hkv, rows = _shape4(k_cache, "k_cache")[1:3]
-    dev, top = q.device, int(top)
-    a = N.SparseArgs()
-    a.q = _view(q, "q", (n, hq, tok, d), _BF16, dev)
-    a.k_cache = _view(k_cache, "k_cache", (n, hkv, rows, d), _BF16, dev)
-    a.v_cache = _view(v_cache, "v_cache", (n, hkv, rows, d), _BF16, dev)
-    a.codes, a.scales, a.blocks = _summary_ptrs(codes, scales, n, hkv, d, dev)
-    a.lengths, a.length, layers = _lengths(lengths, n, dev)
-    with _On(dev, stream) as st:
-        a.status = _status_ptr(dev.index)
+    n, hq, tok, d = qs = _shape4(q, "q")
+    _, hkv, rows, _ = _shape4(k_cache, "k_cache")
+    dev, top = q.get_device(), int(top)
+    cs = (n, hkv, rows, d)
+    qv = _view(q, "q", qs, _BF16, dev)
+    kc, vc = _view(k_cache, "k_cache", cs, _BF16, dev), _view(v_cache, "v_cache", cs, _BF16, dev)
+    pc, ps, blocks = _summary_ptrs(codes, scales, n, hkv, d, dev)
+    lens, length, layers = _lengths(lengths, n, dev)
+    with _on(dev, stream):
+        status = _status_ptr(dev)
         if out is None:
-            out = torch.empty((n, hq, tok, d), dtype=_BF16, device=dev)
-        a.out = _view(out, "out", (n, hq, tok, d), _BF16, dev)
+            out = _empty(qs, _BF16, q)
+        ss = (n, hkv, tok, max(0, top))
         if selected is None:
-            selected = torch.empty((n, hkv, tok, max(0, top)), dtype=_I32, device=dev)
-        elif selected.shape != (n, hkv, tok, top):
-            raise ValueError(f"selected: want {(n, hkv, tok, top)}, got {tuple(selected.shape)}")
-        a.selected = _vector(selected, "selected", _I32, dev, 4)
-        a.scale, a.top, a.layers = scale, top, layers or 1
-        a.batch, a.q_heads, a.kv_heads, a.tokens, a.head_dim, a.cache_rows = n, hq, hkv, tok, d, rows
-        N.check(N.load().statekv_sparse_attention(C.byref(a), st), "statekv_sparse_attention")
+            selected = _empty(ss, _I32, q)
+        elif selected.shape != ss:
+            raise ValueError(f"selected: want {ss}, got {tuple(selected.shape)}")
+        _call("statekv_sparse_attention", N.PACK_SPARSE, dev,
+            *qv, *_view(out, "out", qs, _BF16, dev), *kc, *vc, pc, ps, lens,
+            _vector(selected, "selected", _I32, dev, 4), status, scale, length, top, blocks, n, layers or 1, hq,
+            hkv, tok, d, rows)
     return out, selected

@@ -14,6 +14,7 @@ Tolerances, all derived beforehand.
    (about 7 here): 1.1e-4 on the exponent, twice that on a quotient: 2^-12 A.
 """
 
+import ctypes as C
 import math
 
 import pytest
@@ -787,6 +788,22 @@ def test_sparse_refusals_before_device_work(bad, want):
              cache_rows=256)
     a.update(bad)
     assert N.load().statekv_sparse_attention(N.SparseArgs(**a), None) == want
+
+
+@pytest.mark.parametrize("pack,args", [(N.PACK_NORM_ROPE, N.NormRopeArgs), (N.PACK_TREE, N.TreeArgs),
+                                       (N.PACK_APPEND, N.AppendArgs), (N.PACK_SUMMARY, N.SummaryArgs),
+                                       (N.PACK_SPARSE, N.SparseArgs)])
+def test_packed_arguments_are_the_structures(pack, args):
+    flat, n = [], 0
+
+    def leaf(t):
+        nonlocal n
+        n += 1
+        flat.append(n / 2 if t in (C.c_float, C.c_double) else n)
+        return flat[-1]
+
+    a = args(**{f: N.View(*(leaf(x) for _, x in N.View._fields_)) if t is N.View else leaf(t) for f, t in args._fields_})
+    assert pack.size == C.sizeof(args) and pack.pack(*flat) == bytes(a)
 
 
 def test_null_arguments():
