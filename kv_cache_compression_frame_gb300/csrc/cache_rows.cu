@@ -58,14 +58,16 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
 // loads of a lane all independent.
 constexpr int kSumThreads = 128;
 
-__device__ __forceinline__ float2 neg2(float2 a) { return make_float2(-a.x, -a.y); }
+// a - b (a fused multiply-add by -1 is exact in the product; there is no
+// packed subtraction, and negating takes an instruction per half)
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) { return ptx::fma2(b, make_float2(-1.f, -1.f), a); }
 
 // hi + lo += b
 __device__ __forceinline__ void two_add(float2& hi, float2& lo, float2 b) {
     const float2 s = ptx::add2(hi, b);
-    const float2 bb = ptx::add2(s, neg2(hi));
-    const float2 ea = ptx::add2(hi, neg2(ptx::add2(s, neg2(bb))));
-    const float2 eb = ptx::add2(b, neg2(bb));
+    const float2 bb = sub2(s, hi);
+    const float2 ea = sub2(hi, sub2(s, bb));
+    const float2 eb = sub2(b, bb);
     lo = ptx::add2(lo, ptx::add2(ea, eb));
     hi = s;
 }

@@ -51,7 +51,8 @@ namespace {
 
 constexpr int kTile = 128;                   // keys per tile, query rows per row tile
 constexpr float kSlack = 8.f;                // raise the reference past 2^8
-constexpr int kUnitCost = 2;                 // a unit's start and end in key tiles' time
+constexpr int kUnitCost = 6;                 // a unit's start and end in key tiles' time
+constexpr int kWholeTiles = 8;               // key tiles up to which few units stay whole
 constexpr int kMinShare = 4;                 // least share (in tiles' time) before more CTAs join
 constexpr int kTreeThreads = 384;
 // registers a thread after the split: 128 threads of the first warpgroup and
@@ -67,6 +68,7 @@ struct TreeKernelArgs {
     int32_t G, R, rb, rows;                  // rows: most rows of a unit
     uint32_t inv_tokens;                     // floor(2^32 / tokens) + 1
     int32_t grid;                            // CTAs of the main kernel
+    int32_t whole;                           // a share is a unit: nothing to merge
 };
 
 // r / tokens for a query row r < 65536: the high word of r * (2^32 / tokens,
@@ -217,15 +219,17 @@ struct TreeLayout {
     static constexpr int B_K_EMPTY = B_K_FULL + KS;
     static constexpr int B_V_FULL = B_K_EMPTY + KS;
     static constexpr int B_V_EMPTY = B_V_FULL + VS;
-    static constexpr int B_Q_FULL = B_V_EMPTY + VS;      // Q of the segment stored (8 warps)
-    static constexpr int B_S_FULL = B_Q_FULL + 1;        // [2 slots]
+    static constexpr int B_Q_FULL = B_V_EMPTY + VS;      // Q of the segment stored (2 warps)
+    static constexpr int B_Q_FREE = B_Q_FULL + 1;        // the segment's last S is done
+    static constexpr int B_S_FULL = B_Q_FREE + 1;        // [2 slots]
     static constexpr int B_P_FULL = B_S_FULL + 2;        // [2 slots][2 halves of 64 keys] (4 warps)
     static constexpr int B_O_FULL = B_P_FULL + 4;        // the segment's products are done
     static constexpr int B_SYNC = B_O_FULL + 1;          // the 8 softmax warps
     static constexpr int B_DRAIN = B_SYNC + 1;
     static constexpr int NBAR = B_DRAIN + 1;
-    static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;  // TMEM address, abort flag, odd nodes [2]
-    static constexpr int SMEM = OFF_MISC + 24 + 1024;
+    static constexpr int OFF_ML = OFF_BAR + NBAR * 8;    // float2 [2 slots][128]: the slots' (m, l)
+    static constexpr int OFF_MISC = OFF_ML + 2048;       // TMEM address, abort flag, odd nodes [2]
+    static constexpr int SMEM = OFF_MISC + 24;
     static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
     static_assert(NBAR * 8 % 8 == 0 && OFF_MISC % 8 == 0, "the node mask is 8-byte aligned");
     static constexpr uint32_t TMEM_COLS = 512, TM_S = 0, TM_O = 256;
@@ -243,19 +247,30 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             const __grid_constant__ TreeKernelArgs k) {
     using L = TreeLayout<D, SPLIT_ROWS>;
     const statekv_tree_args& a = k.a;
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t raw_u32 = ptx::smem_u32(smem_raw);
-    const uint32_t sbase = (raw_u32 + 1023u) & ~1023u;
-    uint8_t* base = smem_raw + (sbase - raw_u32);
+    // the swizzled tiles need 1024-byte alignment; there is no room for slack
+    extern __shared__ __align__(1024) uint8_t base[];
+    const uint32_t sbase = ptx::smem_u32(base);
+    if (sbase & 1023u) {
+        if (threadIdx.x == 0) record_error(a.status, (uint32_t)STATEKV_E_DEVICE, kSiteDrain, sbase);
+        return;
+    }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     // every warp finds the CTA's share by itself
-    int64_t none, costs;
-    sum_costs(k, 0, none, costs);
-    const Plan plan = make_plan(k, costs);
     const int c = (int)blockIdx.x;
-    if (c >= plan.ctas) return;
-    const Walk first = find(k, plan.start(c), plan.start(c + 1));
+    Walk first{};
+    if (k.whole) {
+        first.next_u = c;
+        first.next_s = c / (a.layers * a.kv_heads * k.rb);
+        first.next_len = seq_length(k, first.next_s);
+        first.left = unit_tiles(first.next_len) + kUnitCost;
+    } else {
+        int64_t none, costs;
+        sum_costs(k, 0, none, costs);
+        const Plan plan = make_plan(k, costs);
+        if (c >= plan.ctas) return;
+        first = find(k, plan.start(c), plan.start(c + 1));
+    }
 
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + L::OFF_MISC);
     volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(base + L::OFF_MISC + 4);
@@ -270,7 +285,8 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             ptx::mbar_init(sy.bar(L::B_V_FULL + s), 1);
             ptx::mbar_init(sy.bar(L::B_V_EMPTY + s), 1);
         }
-        ptx::mbar_init(sy.bar(L::B_Q_FULL), 8);
+        ptx::mbar_init(sy.bar(L::B_Q_FULL), 2);
+        ptx::mbar_init(sy.bar(L::B_Q_FREE), 1);
         for (int s = 0; s < 2; ++s) {
             ptx::mbar_init(sy.bar(L::B_S_FULL + s), 1);
             ptx::mbar_init(sy.bar(L::B_P_FULL + 2 * s), 4);
@@ -354,7 +370,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         int g0 = 0, seg = 0;                             // tiles before this segment, segments done
         uint32_t p_par[2] = {0, 0};
         bool ok = true;
-        auto issue_s = [&](int j) -> bool {
+        auto issue_s = [&](int j, bool last) -> bool {
             const int slot = j & 1, g = g0 + (SPLIT_ROWS ? j >> 1 : j), s = g % L::KS;
             if (!sy.wait(L::B_K_FULL + s, (uint32_t)((g / L::KS) & 1), kSiteKvFull)) return false;
             ptx::tc_fence_after();
@@ -370,6 +386,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                                         (kc | ks) ? 1u : 0u);
                 ptx::umma_commit(sy.bar(L::B_S_FULL + slot));
                 if (!SPLIT_ROWS || slot == 1) ptx::umma_commit(sy.bar(L::B_K_EMPTY + s));
+                if (last) ptx::umma_commit(sy.bar(L::B_Q_FREE));
             }
             __syncwarp();
             return true;
@@ -399,11 +416,11 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             const int jobs = SPLIT_ROWS ? 2 * x.tiles : x.tiles;
             if (!(ok = sy.wait(L::B_Q_FULL, (uint32_t)(seg & 1), kSiteQFull))) break;
             ptx::tc_fence_after();
-            ok = issue_s(0);
-            if (ok && jobs > 1) ok = issue_s(1);
+            ok = issue_s(0, jobs == 1);
+            if (ok && jobs > 1) ok = issue_s(1, jobs == 2);
             for (int j = 0; ok && j < jobs; ++j) {
                 ok = issue_pv(j);
-                if (ok && j + 2 < jobs) ok = issue_s(j + 2);
+                if (ok && j + 2 < jobs) ok = issue_s(j + 2, j + 3 == jobs);
             }
             if (!ok) break;
             if (ptx::elect_one()) ptx::umma_commit(sy.bar(L::B_O_FULL));
@@ -413,6 +430,33 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         if (ptx::elect_one()) ptx::umma_commit(sy.bar(L::B_DRAIN));
         __syncwarp();
         sy.drain(L::B_DRAIN, 0);
+    } else {
+        // --------------------------------------------------------- Q copier
+        // (warps 2 and 3) a unit's rows r = g * tokens + j, zeros past the
+        // last, as soon as the unit before needs Q no more: its last softmax
+        // and its output hide the copy
+        constexpr int UPR = D / 8;                       // 16-byte units per row
+        const int qt = (int)threadIdx.x - 64, e = qt % UPR;
+        Walk x = first;
+        for (int seg = 0; x.next(k); ++seg) {
+            if (seg > 0 && !sy.wait(L::B_Q_FREE, (uint32_t)((seg - 1) & 1), kSiteQFull)) break;
+            const int nh = x.u / k.rb, n = nh / a.kv_heads, h = nh - n * a.kv_heads;
+            const int row_base = (x.u - nh * k.rb) * L::RT * kTile;
+            const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q.data) + n * a.q.batch_stride +
+                                     (int64_t)(h * k.G) * a.q.head_stride + 8 * e;
+#pragma unroll 4
+            for (int r = qt / UPR; r < L::RT * kTile; r += 64 / UPR) {
+                const int rq = row_base + r, g = head_of(k, rq), j = rq - g * a.tokens;
+                const bool there = rq < k.R;
+                ptx::cp_async_16(sQ + (r / kTile) * L::TILE + (e >> 3) * L::CHUNK + (r % kTile) * 128 +
+                                     (((e & 7) ^ (r & 7)) << 4),
+                                 there ? q + g * a.q.head_stride + j * a.q.token_stride : q, there ? 16u : 0u);
+            }
+            ptx::cp_async_wait();
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(sy.bar(L::B_Q_FULL));
+        }
     }
     } else {
         // ------------------------------------------------ softmax / epilogue
@@ -430,50 +474,26 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         bool ok = true;
         // barrier of the softmax warps (a bounded mbarrier wait: a warp that
         // gave up cannot leave the others blocked)
-        auto sync_sm = [&]() -> bool {
+        // (relaxed: orders no memory access.  An arrive with release semantics
+        // first waits for the warp's global stores: after the partials' stores
+        // that took 8 us while HBM was saturated)
+        auto sync_sm = [&](bool relaxed) -> bool {
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(sy.bar(L::B_SYNC));
+            if (lane == 0) {
+                if (relaxed) ptx::mbar_arrive_relaxed(sy.bar(L::B_SYNC));
+                else ptx::mbar_arrive(sy.bar(L::B_SYNC));
+            }
             const bool r = sy.wait(L::B_SYNC, sync_par, kSiteCol);
             sync_par ^= 1u;
             return r;
         };
-        // Q of a unit, rows r = g * tokens + j and zeros past the last: copied
-        // asynchronously while the previous unit's output is written (held in
-        // registers over that time, the loads were spilled one by one: 7 us)
-        constexpr int UPR = D / 8;                               // 16-byte units per row
-        auto load_q = [&](int u) {
-            const int nh = u / k.rb, n = nh / a.kv_heads, h = nh - n * a.kv_heads;
-            const int row_base = (u - nh * k.rb) * L::RT * kTile;
-            const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q.data) + n * a.q.batch_stride +
-                                     (int64_t)(h * k.G) * a.q.head_stride + 8 * (tid % UPR);
-            const int e = tid % UPR;
-#pragma unroll 4
-            for (int r = tid / UPR; r < L::RT * kTile; r += 256 / UPR) {
-                const int rq = row_base + r, g = head_of(k, rq), j = rq - g * a.tokens;
-                const bool there = rq < k.R;
-                ptx::cp_async_16(sQ + (r / kTile) * L::TILE + (e >> 3) * L::CHUNK + (r % kTile) * 128 +
-                                     (((e & 7) ^ (r & 7)) << 4),
-                                 there ? q + g * a.q.head_stride + j * a.q.token_stride : q, there ? 16u : 0u);
-            }
-        };
-        auto q_ready = [&]() {
-            ptx::cp_async_wait();
-            ptx::fence_proxy_async_smem();
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(sy.bar(L::B_Q_FULL));
-        };
-        Walk nx = first;                                         // one segment ahead
-        bool more = nx.next(k);
-        if (more) load_q(nx.u);
-        for (; ok && more; ++seg) {
-            const Walk cu = nx;
+        Walk cu = first;
+        for (; ok && cu.next(k); ++seg) {
             const int tiles = cu.tiles;
             const int nh = cu.u / k.rb, rblk = cu.u - nh * k.rb;
             const int n = nh / a.kv_heads, h = nh - n * a.kv_heads;
             const int row_base = rblk * L::RT * kTile;
             const int rows = min(L::RT * kTile, k.R - row_base); // rows of this unit
-            q_ready();
             // this thread's row of the unit (both slots' threads have the
             // same row where they share the row tile)
             const int r = (SPLIT_ROWS ? slot * kTile : 0) + lrow;
@@ -496,7 +516,8 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                 s_par ^= 1u;
                 __syncwarp();
                 ptx::tc_fence_after();
-                if (drafted || valid < kTile) {
+                const bool special = drafted || valid < kTile;
+                if (special) {
                     // V rows whose products with P = 0 must be 0.  (After S
                     // full, which implies that the slot's last P V is done
                     // and with it the load before this one in V's stage: a
@@ -593,7 +614,12 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                         ptx::tmem_st_wait();
                         ptx::tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive(sy.bar(L::B_P_FULL + 2 * slot + hh));
+                        // P itself is ordered by the tensor-memory wait and
+                        // fence; only cleaned rows of V need a release
+                        if (lane == 0) {
+                            if (special) ptx::mbar_arrive(sy.bar(L::B_P_FULL + 2 * slot + hh));
+                            else ptx::mbar_arrive_relaxed(sy.bar(L::B_P_FULL + 2 * slot + hh));
+                        }
                     }
                     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                 } else {
@@ -609,22 +635,14 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             // ---- end of the segment
             if (!(ok = sy.wait(L::B_O_FULL, (uint32_t)(seg & 1), kSiteOFull))) break;
             ptx::tc_fence_after();
-            // the slots that share a row tile tell each other (m, l) through
-            // the scores' tensor memory, which no product uses any more
-            if (!SPLIT_ROWS) {
-                const uint32_t x[2] = {__float_as_uint(m), __float_as_uint(l)};
-                ptx::tmem_st_32x32b_x2(t_s, x);
-                ptx::tmem_st_wait();
-            }
+            // the slots that share a row tile tell each other (m, l)
+            float2* ml = reinterpret_cast<float2*>(base + L::OFF_ML);
+            if (!SPLIT_ROWS) ml[slot * kTile + lrow] = make_float2(m, l);
             // the next segment's mask (every read of it was before the last
             // segment's second sync, every write comes after the next one)
             if (tid == 0) odd_nodes[(seg + 1) & 1] = 0ull;
             ptx::tc_fence_before();
-            if (!(ok = sync_sm())) break;
-            ptx::tc_fence_after();
-            // Q's memory is free: the next unit's copy runs from here on
-            more = nx.next(k);
-            if (more) load_q(nx.u);
+            if (!(ok = sync_sm(false))) break;
             const bool whole = cu.t == 0 && tiles == cu.nt;
             constexpr int COLS = SPLIT_ROWS ? D : D / 2;         // columns this thread merges
             const int c0 = SPLIT_ROWS ? 0 : slot * COLS;
@@ -632,12 +650,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             bool use1 = false;
             uint32_t t_o0 = t_o;
             if (!SPLIT_ROWS) {
-                uint32_t y[4];
-                ptx::tmem_ld_32x32b_x2(tmem + L::TM_S + lane_base, y[0], y[1]);
-                ptx::tmem_ld_32x32b_x2(tmem + L::TM_S + 128 + lane_base, y[2], y[3]);
-                ptx::tmem_ld_wait();
-                const float2 x0 = make_float2(__uint_as_float(y[0]), __uint_as_float(y[1]));
-                const float2 x1 = make_float2(__uint_as_float(y[2]), __uint_as_float(y[3]));
+                const float2 x0 = ml[lrow], x1 = ml[kTile + lrow];
                 use1 = tiles > 1;                                // slot 1 had a tile
                 m = fmaxf(x0.x, use1 ? x1.x : -INFINITY);
                 f0 = x0.x == -INFINITY ? 0.f : ptx::ex2_approx(x0.x - m);
@@ -650,15 +663,15 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             const float inv = whole ? (l > 0.f || l != l ? 1.f / l : 0.f) : 1.f;
             if (!idle) {
 #pragma unroll 1
-                for (int cc = 0; cc < COLS; cc += 16) {
-                    uint32_t o0[16], o1[16];
+                for (int cc = 0; cc < COLS; cc += 32) {
+                    uint32_t o0[32], o1[32];
                     __syncwarp();
-                    ptx::tmem_ld_32x32b_x16(t_o0 + cc, o0);
-                    if (use1) ptx::tmem_ld_32x32b_x16(t_o0 + 128 + cc, o1);
+                    ptx::tmem_ld_32x32b_x32(t_o0 + cc, o0);
+                    if (use1) ptx::tmem_ld_32x32b_x32(t_o0 + 128 + cc, o1);
                     ptx::tmem_ld_wait();
-                    float v[16];
+                    float v[32];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
+                    for (int e = 0; e < 32; ++e) {
                         v[e] = __uint_as_float(o0[e]) * f0;
                         if (use1) v[e] = fmaf(__uint_as_float(o1[e]), f1, v[e]);
                     }
@@ -669,7 +682,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                                                       n * a.v_new.batch_stride + h * a.v_new.head_stride +
                                                       (int64_t)(__ffsll((long long)b) - 1) * a.v_new.token_stride;
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) {
+                            for (int e = 0; e < 32; ++e) {
                                 const float y = __bfloat162float(vr[c0 + cc + e]);
                                 if (!(fabsf(y) < INFINITY)) v[e] += y;
                             }
@@ -680,7 +693,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                                              (int64_t)(h * k.G + gg) * a.out.head_stride +
                                              (int64_t)node * a.out.token_stride + c0 + cc;
 #pragma unroll
-                        for (int e = 0; e < 16; e += 8)
+                        for (int e = 0; e < 32; e += 8)
                             *reinterpret_cast<uint4*>(out + e) =
                                 make_uint4(ptx::pack_bf16x2(v[e] * inv, v[e + 1] * inv),
                                            ptx::pack_bf16x2(v[e + 2] * inv, v[e + 3] * inv),
@@ -690,15 +703,16 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                         float4* po = reinterpret_cast<float4*>(k.part_o) +
                                      (sgm * (D / 4) + (c0 + cc) / 4) * k.rows + r;
 #pragma unroll
-                        for (int e = 0; e < 16; e += 4)
+                        for (int e = 0; e < 32; e += 4)
                             po[(int64_t)(e / 4) * k.rows] = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
                     }
                 }
                 if (live && !whole && c0 == 0) k.part_ml[sgm * k.rows + r] = make_float2(m, l);
             }
             ptx::tc_fence_before();
-            // O and the scores' memory are read: the next segment may write them
-            if (!(ok = sync_sm())) break;
+            // O and ml are read (the values are in registers): the next segment
+            // may write them
+            if (!(ok = sync_sm(true))) break;
             g0 += tiles;
         }
     }
@@ -920,10 +934,14 @@ extern "C" int statekv_tree_attention(const statekv_tree_args* args, void* cuda_
     k.G = z.G; k.R = z.R; k.rb = z.rb; k.rows = z.rows;
     k.inv_tokens = (uint32_t)((1ull << 32) / (uint32_t)a.tokens + 1);
     k.scale_log2 = (float)(a.scale * 1.4426950408889634074);
-    // no more CTAs than the longest cache could use
-    const int64_t most =
-        z.units * (((int64_t)(a.lengths ? a.cache_rows : a.length) + kTile - 1) / kTile + 1 + kUnitCost);
-    k.grid = (int)std::min<int64_t>(sms, (most + kMinShare - 1) / kMinShare);
+    // A few short units are not cut: their 8 tiles one after the other take
+    // about as long as the second launch that would merge them (one layer, 300
+    // rows: 12.1 us cut, 10.9 us whole, and one launch less on the host).  Otherwise no more CTAs than the
+    // longest cache could use.
+    const int64_t tiles = ((int64_t)(a.lengths ? a.cache_rows : a.length) + kTile - 1) / kTile + 1;
+    k.whole = tiles <= kWholeTiles && z.units <= sms;
+    k.grid = k.whole ? (int)z.units
+                     : (int)std::min<int64_t>(sms, (z.units * (tiles + kUnitCost) + kMinShare - 1) / kMinShare);
     const int64_t segments = (int64_t)sms + z.units;
     k.part_o = static_cast<float*>(a.workspace);
     k.part_ml = reinterpret_cast<float2*>(k.part_o + segments * z.rows * a.head_dim);
@@ -932,7 +950,7 @@ extern "C" int statekv_tree_attention(const statekv_tree_args* args, void* cuda_
     cudaError_t e = a.head_dim == 128 ? (two ? launch_main<128, true>(k, m, dev, st) : launch_main<128, false>(k, m, dev, st))
                                       : (two ? launch_main<64, true>(k, m, dev, st) : launch_main<64, false>(k, m, dev, st));
     // one CTA holds whole units only
-    if (e == cudaSuccess && k.grid > 1)
+    if (e == cudaSuccess && !k.whole && k.grid > 1)
         e = a.head_dim == 128 ? launch_combine<128>(k, z.units, sms, st) : launch_combine<64>(k, z.units, sms, st);
     return e == cudaSuccess ? STATEKV_OK : view_cuda_fail();
 }
