@@ -1,6 +1,8 @@
 // Rows of a cache of keys and values: the accepted path of a drafted tree
 // joins the cache, and complete 64-row blocks get the summaries that
 // sparse_attention.cu selects them by.
+#include <algorithm>
+
 #include "views.cuh"
 #include "sm100_ptx.cuh"
 
@@ -54,9 +56,10 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
 // rank among the scores hangs on them), so the sum is exact to well below
 // half an fp32 ulp: two-term accumulation, s + b = fl(s + b) + e with e
 // recovered by Knuth's two-sum, in packed fp32 pairs.  Bound by HBM (each key
-// is read once): one warp per block, 16 bytes per lane and load, the block's
-// loads of a lane all independent.
+// is read once): a warp per block, 16 bytes per lane and load, eight loads on
+// their way while eight are summed, across blocks too.
 constexpr int kSumThreads = 128;
+constexpr int kSumCtas = 5;                                  // per SM: 102 registers a thread, 64 of them keys in flight
 
 // a - b (a fused multiply-add by -1 is exact in the product; there is no
 // packed subtraction, and negating takes an instruction per half)
@@ -73,69 +76,101 @@ __device__ __forceinline__ void two_add(float2& hi, float2& lo, float2 b) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kSumThreads) summary_kernel(const __grid_constant__ statekv_summary_args a,
-                                                              int window) {
+__global__ void __launch_bounds__(kSumThreads, kSumCtas) summary_kernel(const __grid_constant__ statekv_summary_args a,
+                                                                        int window) {
     constexpr int LPR = D / 8;                               // lanes per row
     constexpr int RPI = 32 / LPR;                            // rows per load
+    constexpr int GROUP = 8;                                 // loads of a lane per group
+    constexpr int GROUPS = STATEKV_BLOCK / RPI / GROUP;      // of a block: 4 or 2
+    static_assert(GROUPS % 2 == 0, "a block starts in buffer 0");
     const int lane = threadIdx.x & 31;
-    const int64_t item = (int64_t)blockIdx.x * (kSumThreads / 32) + (threadIdx.x >> 5);
-    const int64_t unit = item / window;
-    if (unit >= (int64_t)a.batch * a.kv_heads) return;
-    const int n = (int)(unit / a.kv_heads), h = (int)(unit - (int64_t)n * a.kv_heads);
-    const int len = cache_length(a.lengths, a.length, n / a.layers, a.cache_rows, a.status);
-    const int first = a.appended < len ? (len - a.appended) / STATEKV_BLOCK : 0;
-    const int b = first + (int)(item - unit * window);
-    if (b >= len / STATEKV_BLOCK) return;
-    const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(a.k_cache.data) + n * a.k_cache.batch_stride +
-                             h * a.k_cache.head_stride +
-                             ((int64_t)b * STATEKV_BLOCK + lane / LPR) * a.k_cache.token_stride +
-                             (lane % LPR) * 8;
-    float2 hi[4], lo[4];
+    const int64_t items = (int64_t)a.batch * a.kv_heads * window;
+    const int64_t step = (int64_t)gridDim.x * (kSumThreads / 32);
+    // the first block from item i on that the appended rows completed: its
+    // output index, and this lane's first key
+    int64_t i = (int64_t)blockIdx.x * (kSumThreads / 32) + (threadIdx.x >> 5);
+    int64_t out = 0;
+    const __nv_bfloat16* k = nullptr;
+    auto seek = [&]() -> bool {
+        for (; i < items; i += step) {
+            const int64_t unit = i / window;
+            const int n = (int)(unit / a.kv_heads), h = (int)(unit - (int64_t)n * a.kv_heads);
+            const int len = cache_length(a.lengths, a.length, n / a.layers, a.cache_rows, a.status);
+            const int first = a.appended < len ? (len - a.appended) / STATEKV_BLOCK : 0;
+            const int b = first + (int)(i - unit * window);
+            if (b >= len / STATEKV_BLOCK) continue;
+            out = unit * a.blocks + b;
+            k = static_cast<const __nv_bfloat16*>(a.k_cache.data) + n * a.k_cache.batch_stride +
+                h * a.k_cache.head_stride + ((int64_t)b * STATEKV_BLOCK + lane / LPR) * a.k_cache.token_stride +
+                (lane % LPR) * 8;
+            i += step;
+            return true;
+        }
+        return false;
+    };
+    uint4 u[2][GROUP];
+    auto load = [&](uint4 (&x)[GROUP], int g) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) hi[j] = lo[j] = make_float2(0.f, 0.f);
-#pragma unroll 8
-    for (int r = 0; r < STATEKV_BLOCK / RPI; ++r) {
-        const uint4 u = *reinterpret_cast<const uint4*>(k + (int64_t)r * RPI * a.k_cache.token_stride);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        for (int r = 0; r < GROUP; ++r)
+            x[r] = *reinterpret_cast<const uint4*>(k + (int64_t)((g * GROUP + r) * RPI) * a.k_cache.token_stride);
+    };
+    bool have = seek();
+    if (have) load(u[0], 0);
+    while (have) {
+        const int64_t at = out;
+        float2 hi[4], lo[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            two_add(hi[j], lo[j], make_float2(__uint_as_float(w[j] << 16),
-                                              __uint_as_float(w[j] & 0xffff0000u)));
-    }
+        for (int j = 0; j < 4; ++j) hi[j] = lo[j] = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int off = LPR; off < 32; off <<= 1)
+        for (int g = 0; g < GROUPS; ++g) {
+            // the next group, or the next block's first, is on its way
+            // while this one is summed
+            if (g + 1 < GROUPS) load(u[(g + 1) & 1], g + 1);
+            else if ((have = seek())) load(u[0], 0);
+#pragma unroll
+            for (int r = 0; r < GROUP; ++r) {
+                const uint4 x = u[g & 1][r];
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    two_add(hi[j], lo[j], make_float2(__uint_as_float(w[j] << 16),
+                                                      __uint_as_float(w[j] & 0xffff0000u)));
+            }
+        }
+#pragma unroll
+        for (int off = LPR; off < 32; off <<= 1)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 oh = make_float2(__shfl_xor_sync(0xffffffffu, hi[j].x, off),
+                                              __shfl_xor_sync(0xffffffffu, hi[j].y, off));
+                const float2 ol = make_float2(__shfl_xor_sync(0xffffffffu, lo[j].x, off),
+                                              __shfl_xor_sync(0xffffffffu, lo[j].y, off));
+                // symmetric in the two lanes, so that both hold the same bits
+                float2 e = make_float2(0.f, 0.f);
+                two_add(hi[j], e, oh);
+                lo[j] = ptx::add2(ptx::add2(lo[j], ol), e);
+            }
+        float m[8], top = 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const float2 oh = make_float2(__shfl_xor_sync(0xffffffffu, hi[j].x, off),
-                                          __shfl_xor_sync(0xffffffffu, hi[j].y, off));
-            const float2 ol = make_float2(__shfl_xor_sync(0xffffffffu, lo[j].x, off),
-                                          __shfl_xor_sync(0xffffffffu, lo[j].y, off));
-            // symmetric in the two lanes, so that both hold the same bits
-            float2 e = make_float2(0.f, 0.f);
-            two_add(hi[j], e, oh);
-            lo[j] = ptx::add2(ptx::add2(lo[j], ol), e);
+            m[2 * j] = (hi[j].x + lo[j].x) * (1.f / STATEKV_BLOCK);
+            m[2 * j + 1] = (hi[j].y + lo[j].y) * (1.f / STATEKV_BLOCK);
+            top = fmaxf(top, fmaxf(fabsf(m[2 * j]), fabsf(m[2 * j + 1])));
         }
-    float m[8], top = 0.f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        m[2 * j] = (hi[j].x + lo[j].x) * (1.f / STATEKV_BLOCK);
-        m[2 * j + 1] = (hi[j].y + lo[j].y) * (1.f / STATEKV_BLOCK);
-        top = fmaxf(top, fmaxf(fabsf(m[2 * j]), fabsf(m[2 * j + 1])));
-    }
+        for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+        const float inv = top > 0.f ? 127.f / top : 0.f;
+        if (lane < LPR) {
+            uint32_t w[2] = {0u, 0u};
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-    const float inv = top > 0.f ? 127.f / top : 0.f;
-    const int64_t out = unit * a.blocks + b;
-    if (lane < LPR) {
-        uint32_t w[2] = {0u, 0u};
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int code = (int)fminf(fmaxf(rintf(m[j] * inv), -127.f), 127.f);
-            w[j >> 2] |= (uint32_t)(code & 0xff) << (8 * (j & 3));
+            for (int j = 0; j < 8; ++j) {
+                const int code = (int)fminf(fmaxf(rintf(m[j] * inv), -127.f), 127.f);
+                w[j >> 2] |= (uint32_t)(code & 0xff) << (8 * (j & 3));
+            }
+            *reinterpret_cast<uint2*>(a.codes + at * D + lane * 8) = make_uint2(w[0], w[1]);
         }
-        *reinterpret_cast<uint2*>(a.codes + out * D + lane * 8) = make_uint2(w[0], w[1]);
+        if (lane == 0) a.scales[at] = top / 127.f;
     }
-    if (lane == 0) a.scales[out] = top / 127.f;
 }
 
 }  // namespace
@@ -149,8 +184,10 @@ cudaError_t launch_summary(const statekv_summary_args& a, cudaStream_t st) {
     // blocks that the appended rows can have completed
     const int window = a.appended / STATEKV_BLOCK + 1 < a.blocks ? a.appended / STATEKV_BLOCK + 1 : a.blocks;
     const int64_t items = (int64_t)a.batch * a.kv_heads * window;
-    const int64_t grid = (items + kSumThreads / 32 - 1) / (kSumThreads / 32);
-    if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    // one wave of CTAs, each warp walking the blocks
+    int dev = 0, sms = 0;
+    if (!current_device(&dev, &sms)) return cudaErrorInvalidDevice;
+    const int64_t grid = std::min<int64_t>((items + kSumThreads / 32 - 1) / (kSumThreads / 32), (int64_t)sms * kSumCtas);
     if (a.head_dim == 128) summary_kernel<128><<<(unsigned)grid, kSumThreads, 0, st>>>(a, window);
     else summary_kernel<64><<<(unsigned)grid, kSumThreads, 0, st>>>(a, window);
     return cudaGetLastError();
