@@ -181,8 +181,14 @@ def _call(name: str, pack: struct.Struct, dev: int, *values) -> None:
         N.check(status, name)
 
 
-def _empty(shape, dtype, like: torch.Tensor) -> torch.Tensor:
-    return torch.empty(shape, dtype=dtype, device=like.device)
+def _out(t, name: str, shape, dtype, like: torch.Tensor, dev: int) -> tuple:
+    """(tensor, its view): the caller's checked, or a new contiguous one."""
+    if t is not None:
+        return t, _view(t, name, shape, dtype, dev)
+    t = torch.empty(shape, dtype=dtype, device=like.device)
+    row = shape[3]
+    head = shape[2] * row
+    return t, (t.data_ptr(), shape[1] * head, head, row)
 
 
 def qk_norm_rope(q, k, positions, omega, q_weight=None, k_weight=None, *, v=None, eps: float = 1e-6,
@@ -239,20 +245,18 @@ def qk_norm_rope(q, k, positions, omega, q_weight=None, k_weight=None, *, v=None
         raise ValueError("v_out without v")
     with _on(dev, stream):
         status = _status_ptr(dev)
-        if q_out is None:
-            q_out = _empty(qs, dt, q)
-        if k_out is None:
-            k_out = _empty(ks, dt, q)
-        cap = k_out.shape[2] if k_out.dim() == 4 else -1
+        cap = t if k_out is None else k_out.shape[2] if k_out.dim() == 4 else -1
         os_ = (n, hkv, cap, d)
-        if v is not None and v_out is None:
-            v_out = _empty(os_, dt, q)
+        q_out, qo = _out(q_out, "q_out", qs, dt, q, dev)
+        k_out, ko = _out(k_out, "k_out", os_, dt, q, dev)
+        vv = vo = _NO_VIEW
+        if v is not None:
+            vv = _view(v, "v", ks, dt, dev)
+            v_out, vo = _out(v_out, "v_out", os_, dt, q, dev)
         _call("statekv_norm_rope", N.PACK_NORM_ROPE, dev,
-            *qv, *kv_, *(_NO_VIEW if v is None else _view(v, "v", ks, dt, dev)),
-            *_view(q_out, "q_out", qs, dt, dev), *_view(k_out, "k_out", os_, dt, dev),
-            *(_NO_VIEW if v is None else _view(v_out, "v_out", os_, dt, dev)),
-            w_ptr[0], w_ptr[1], om, pos, at, status, p0, p_stride, p_layers, n, layers, hq, hkv, t, d, cap,
-            w_rows, _DTYPES[dt], _DTYPES[wd or dt], eps)
+                  *qv, *kv_, *vv, *qo, *ko, *vo,
+                  w_ptr[0], w_ptr[1], om, pos, at, status, p0, p_stride, p_layers, n, layers, hq, hkv, t, d, cap,
+                  w_rows, _DTYPES[dt], _DTYPES[wd or dt], eps)
     return (q_out, k_out) if v is None else (q_out, k_out, v_out)
 
 
@@ -282,19 +286,18 @@ def tree_attention(q, k_new, v_new, tree, k_cache, v_cache, lengths, *, scale: f
         t_stride = tok
     with _on(dev, stream):
         status = _status_ptr(dev)
-        if out is None:
-            out = _empty(qs, _BF16, q)
+        out, ov = _out(out, "out", qs, _BF16, q, dev)
         ws = size = 0
         if workspace is None:
             size = N.load().statekv_tree_attention_workspace(n, hq, hkv, tok, d)
             if size > 0:
-                workspace = _empty(size, torch.uint8, q)
+                workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
                 ws = workspace.data_ptr()
         else:
             ws, size = _vector(workspace, "workspace", torch.uint8, dev), workspace.shape[0]
         _call("statekv_tree_attention", N.PACK_TREE, dev,
-            *views[:4], *_view(out, "out", qs, _BF16, dev), *views[4:], masks, lens, status, ws, size, scale,
-            t_stride, length, n, layers or 1, hq, hkv, tok, d, rows)
+                  *views[:4], *ov, *views[4:], masks, lens, status, ws, size, scale,
+                  t_stride, length, n, layers or 1, hq, hkv, tok, d, rows)
     return out
 
 
@@ -337,11 +340,11 @@ def append_accepted(k_new, v_new, path, counts, k_cache, v_cache, lengths, *, st
         status = _status_ptr(dev)
         new, to = None, 0
         if lens or cnt:
-            new = _empty(n // layers, _I32, k_new)
+            new = torch.empty(n // layers, dtype=_I32, device=k_new.device)
             to = new.data_ptr()
         _call("statekv_append_accepted", N.PACK_APPEND, dev,
-            *views, pp, cnt, lens, to, status, p_stride, steps, length, n, layers, hkv, tok, d, rows,
-            _DTYPES[dt])
+                  *views, pp, cnt, lens, to, status, p_stride, steps, length, n, layers, hkv, tok, d, rows,
+                  _DTYPES[dt])
     return length + steps if new is None else new
 
 
@@ -358,7 +361,7 @@ def block_summaries(k_cache, codes, scales, lengths, *, appended: int | None = N
     appended = rows if appended is None else min(int(appended), rows)
     with _on(dev, stream):
         _call("statekv_block_summaries", N.PACK_SUMMARY, dev,
-            *view, pc, ps, lens, _status_ptr(dev), length, appended, blocks, n, layers or 1, hkv, d, rows)
+                  *view, pc, ps, lens, _status_ptr(dev), length, appended, blocks, n, layers or 1, hkv, d, rows)
 
 
 def _summary_ptrs(codes, scales, n: int, hkv: int, d: int, dev: int) -> tuple[int, int, int]:
@@ -389,15 +392,14 @@ def sparse_attention(q, k_cache, v_cache, codes, scales, lengths, top: int, *, s
     lens, length, layers = _lengths(lengths, n, dev)
     with _on(dev, stream):
         status = _status_ptr(dev)
-        if out is None:
-            out = _empty(qs, _BF16, q)
+        out, ov = _out(out, "out", qs, _BF16, q, dev)
         ss = (n, hkv, tok, max(0, top))
         if selected is None:
-            selected = _empty(ss, _I32, q)
+            selected = torch.empty(ss, dtype=_I32, device=q.device)
         elif selected.shape != ss:
             raise ValueError(f"selected: want {ss}, got {tuple(selected.shape)}")
         _call("statekv_sparse_attention", N.PACK_SPARSE, dev,
-            *qv, *_view(out, "out", qs, _BF16, dev), *kc, *vc, pc, ps, lens,
-            _vector(selected, "selected", _I32, dev, 4), status, scale, length, top, blocks, n, layers or 1, hq,
-            hkv, tok, d, rows)
+                  *qv, *ov, *kc, *vc, pc, ps, lens,
+                  _vector(selected, "selected", _I32, dev, 4), status, scale, length, top, blocks, n, layers or 1, hq,
+                  hkv, tok, d, rows)
     return out, selected
