@@ -736,7 +736,7 @@ def test_tree_refusals_before_device_work(bad, want):
     (dict(q=view(8)), N.E_INVALID_ARG), (dict(k_out=view(b=4)), N.E_INVALID_ARG), (dict(v_out=view(None)), N.E_INVALID_ARG),
     (dict(layers=0), N.E_INVALID_ARG), (dict(position_layers=0), N.E_INVALID_ARG), (dict(weight_rows=0), N.E_INVALID_ARG), (dict(q_weight=8), N.E_INVALID_ARG), (dict(batch=3, layers=2), N.E_INVALID_ARG),
     (dict(out_capacity=2), N.E_CAPACITY), (dict(eps=-1.0), N.E_INVALID_ARG), (dict(eps=math.nan), N.E_INVALID_ARG),
-    (dict(tokens=-1), N.E_INVALID_ARG), (dict(q_heads=70000), N.E_UNSUPPORTED), (dict(tokens=0, out_capacity=0), N.OK),
+    (dict(tokens=-1), N.E_INVALID_ARG), (dict(q_heads=17000), N.E_UNSUPPORTED), (dict(tokens=0, out_capacity=0), N.OK),
     (dict(batch=0), N.OK),
 ])
 def test_norm_rope_refusals_before_device_work(bad, want):
