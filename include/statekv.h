@@ -516,8 +516,9 @@ int statekv_norm_rope(const statekv_norm_rope_args* args, void* cuda_stream);
  * bf16, head_dim 64 or 128, q_heads / kv_heads <= 64, cache_rows >= 0 rows
  * per head in the cache views.  workspace: device memory of
  * statekv_tree_attention_workspace() bytes, 16-byte aligned, contents
- * irrelevant; that function depends on the current device and returns -1 for
- * sizes that the call would refuse.  The results do not depend on the
+ * irrelevant (NULL where that is 0: a few short caches); the function depends
+ * on the current device, does not fall with any of its arguments but may rise
+ * with each, and returns -1 for sizes that the call would refuse.  The results do not depend on the
  * workspace or on the other calls, but sums are grouped by the whole batch:
  * they agree between batchings up to rounding.
  */
@@ -533,7 +534,7 @@ typedef struct statekv_tree_args {
     int32_t batch, layers, q_heads, kv_heads, tokens, head_dim, cache_rows;
 } statekv_tree_args;
 int64_t statekv_tree_attention_workspace(int32_t batch, int32_t q_heads, int32_t kv_heads,
-                                         int32_t tokens, int32_t head_dim);
+                                         int32_t tokens, int32_t head_dim, int32_t cache_rows);
 int statekv_tree_attention(const statekv_tree_args* args, void* cuda_stream);
 
 /*

@@ -172,7 +172,7 @@ def load() -> C.CDLL:
                        ("statekv_block_summaries", SummaryArgs),
                        ("statekv_sparse_attention", SparseArgs)):
         sig[name] = (C.c_int, [C.POINTER(args), _P])
-    sig["statekv_tree_attention_workspace"] = (C.c_int64, [C.c_int32] * 5)
+    sig["statekv_tree_attention_workspace"] = (C.c_int64, [C.c_int32] * 6)
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
         fn.restype = res

@@ -670,7 +670,8 @@ int statekv_decode_tree(statekv_handle* h, int32_t tokens, const void* q, const 
     if (!h->tree_ws) {
         const int most = std::min(kMaxDraft, (int)c.frame_tokens);
         const int64_t need =
-            statekv_tree_attention_workspace(batch, c.num_q_heads, c.num_kv_heads, most, c.head_dim);
+            statekv_tree_attention_workspace(batch, c.num_q_heads, c.num_kv_heads, most, c.head_dim,
+                                             (int32_t)h->det_pitch);
         if (need < 0) return STATEKV_E_UNSUPPORTED;
         const size_t rows = (size_t)h->U * kMaxDraft * c.head_dim * h->esize;
         if ((!h->draft_k && !dalloc(h, &h->draft_k, rows)) || (!h->draft_v && !dalloc(h, &h->draft_v, rows)) ||

@@ -867,6 +867,14 @@ int tree_sizes(int batch, int q_heads, int kv_heads, int tokens, int head_dim, T
     return z->units > 0x7fffffff / 1024 ? STATEKV_E_UNSUPPORTED : STATEKV_OK;
 }
 
+// A few short units are not cut: their 8 tiles one after the other take about
+// as long as the second launch that would merge them (one layer, 300 rows:
+// 12.1 us cut, 10.9 us whole, and one launch less on the host).
+int64_t most_tiles(int64_t cache_rows) { return (cache_rows + kTile - 1) / kTile + 1; }
+bool stays_whole(const TreeSizes& z, int64_t cache_rows, int sms) {
+    return most_tiles(cache_rows) <= kWholeTiles && z.units <= sms;
+}
+
 int64_t workspace_for(const TreeSizes& z, int sms, int d) {
     // one segment per CTA and per unit; O, then (m, l)
     return ((int64_t)sms + z.units) * z.rows * (d * 4 + 8);
@@ -881,16 +889,17 @@ bool spread(const statekv_view& v, int64_t batch, int64_t heads, int64_t rows) {
 }  // namespace statekv
 
 extern "C" int64_t statekv_tree_attention_workspace(int32_t batch, int32_t q_heads, int32_t kv_heads,
-                                                    int32_t tokens, int32_t head_dim) {
+                                                    int32_t tokens, int32_t head_dim, int32_t cache_rows) {
     using namespace statekv;
     TreeSizes z;
+    if (cache_rows < 0) return -1;
     if (tree_sizes(batch, q_heads, kv_heads, tokens, head_dim, &z) != STATEKV_OK) return -1;
     int dev = 0, sms = 0;
     if (!current_device(&dev, &sms)) {
         cudaGetLastError();
         return -1;
     }
-    return workspace_for(z, sms, head_dim);
+    return stays_whole(z, cache_rows, sms) ? 0 : workspace_for(z, sms, head_dim);
 }
 
 extern "C" int statekv_tree_attention(const statekv_tree_args* args, void* cuda_stream) {
@@ -918,7 +927,8 @@ extern "C" int statekv_tree_attention(const statekv_tree_args* args, void* cuda_
         return STATEKV_E_INVALID_ARG;
     int dev = 0, sms = 0;
     if (!current_device(&dev, &sms)) return view_cuda_fail();
-    if (!aligned16(a.workspace) || a.workspace_bytes < workspace_for(z, sms, a.head_dim))
+    const bool whole = stays_whole(z, a.cache_rows, sms);
+    if (!whole && (!aligned16(a.workspace) || a.workspace_bytes < workspace_for(z, sms, a.head_dim)))
         return STATEKV_E_INVALID_ARG;
     TreeMaps m;
     if (!encode_view4(&m.kn, a.k_new, a.head_dim, a.tokens, a.kv_heads, a.batch) ||
@@ -934,14 +944,10 @@ extern "C" int statekv_tree_attention(const statekv_tree_args* args, void* cuda_
     k.G = z.G; k.R = z.R; k.rb = z.rb; k.rows = z.rows;
     k.inv_tokens = (uint32_t)((1ull << 32) / (uint32_t)a.tokens + 1);
     k.scale_log2 = (float)(a.scale * 1.4426950408889634074);
-    // A few short units are not cut: their 8 tiles one after the other take
-    // about as long as the second launch that would merge them (one layer, 300
-    // rows: 12.1 us cut, 10.9 us whole, and one launch less on the host).  Otherwise no more CTAs than the
-    // longest cache could use.
-    const int64_t tiles = ((int64_t)(a.lengths ? a.cache_rows : a.length) + kTile - 1) / kTile + 1;
-    k.whole = tiles <= kWholeTiles && z.units <= sms;
-    k.grid = k.whole ? (int)z.units
-                     : (int)std::min<int64_t>(sms, (z.units * (tiles + kUnitCost) + kMinShare - 1) / kMinShare);
+    // otherwise no more CTAs than the longest cache could use
+    k.whole = whole;
+    const int64_t cost = most_tiles(a.lengths ? a.cache_rows : a.length) + kUnitCost;
+    k.grid = whole ? (int)z.units : (int)std::min<int64_t>(sms, (z.units * cost + kMinShare - 1) / kMinShare);
     const int64_t segments = (int64_t)sms + z.units;
     k.part_o = static_cast<float*>(a.workspace);
     k.part_ml = reinterpret_cast<float2*>(k.part_o + segments * z.rows * a.head_dim);

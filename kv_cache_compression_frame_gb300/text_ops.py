@@ -152,21 +152,9 @@ class _On:
             g.__exit__(*exc)
 
 
-class _Here:
-    """The same where they are current already."""
-
-    def __enter__(self):
-        pass
-
-    def __exit__(self, *exc):
-        pass
-
-
-_HERE = _Here()
-
-
-def _on(dev: int, stream):
-    return _HERE if stream is None and _current_device() == dev else _On(dev, stream)
+def _elsewhere(dev: int, stream) -> bool:
+    """Whether a call needs _On around it."""
+    return stream is not None or _current_device() != dev
 
 
 def _call(name: str, pack: struct.Struct, dev: int, *values) -> None:
@@ -203,6 +191,10 @@ def qk_norm_rope(q, k, positions, omega, q_weight=None, k_weight=None, *, v=None
     n, hq, t, d = qs = _shape4(q, "q")
     hkv = _shape4(k, "k")[1]
     dt, dev = q.dtype, q.get_device()
+    if _elsewhere(dev, stream):
+        with _On(dev, stream):
+            return qk_norm_rope(q, k, positions, omega, q_weight, k_weight, v=v, eps=eps, q_out=q_out,
+                                k_out=k_out, v_out=v_out, out_rows=out_rows)
     if dt not in _DTYPES:
         raise ValueError(f"q: {dt}, want one of {list(_DTYPES)}")
     ks = (n, hkv, t, d)
@@ -243,20 +235,19 @@ def qk_norm_rope(q, k, positions, omega, q_weight=None, k_weight=None, *, v=None
             raise ValueError("out_rows needs k_out (and v_out)")
     if v is None and v_out is not None:
         raise ValueError("v_out without v")
-    with _on(dev, stream):
-        status = _status_ptr(dev)
-        cap = t if k_out is None else k_out.shape[2] if k_out.dim() == 4 else -1
-        os_ = (n, hkv, cap, d)
-        q_out, qo = _out(q_out, "q_out", qs, dt, q, dev)
-        k_out, ko = _out(k_out, "k_out", os_, dt, q, dev)
-        vv = vo = _NO_VIEW
-        if v is not None:
-            vv = _view(v, "v", ks, dt, dev)
-            v_out, vo = _out(v_out, "v_out", os_, dt, q, dev)
-        _call("statekv_norm_rope", N.PACK_NORM_ROPE, dev,
-                  *qv, *kv_, *vv, *qo, *ko, *vo,
-                  w_ptr[0], w_ptr[1], om, pos, at, status, p0, p_stride, p_layers, n, layers, hq, hkv, t, d, cap,
-                  w_rows, _DTYPES[dt], _DTYPES[wd or dt], eps)
+    status = _status_ptr(dev)
+    cap = t if k_out is None else k_out.shape[2] if k_out.dim() == 4 else -1
+    os_ = (n, hkv, cap, d)
+    q_out, qo = _out(q_out, "q_out", qs, dt, q, dev)
+    k_out, ko = _out(k_out, "k_out", os_, dt, q, dev)
+    vv = vo = _NO_VIEW
+    if v is not None:
+        vv = _view(v, "v", ks, dt, dev)
+        v_out, vo = _out(v_out, "v_out", os_, dt, q, dev)
+    _call("statekv_norm_rope", N.PACK_NORM_ROPE, dev,
+              *qv, *kv_, *vv, *qo, *ko, *vo,
+              w_ptr[0], w_ptr[1], om, pos, at, status, p0, p_stride, p_layers, n, layers, hq, hkv, t, d, cap,
+              w_rows, _DTYPES[dt], _DTYPES[wd or dt], eps)
     return (q_out, k_out) if v is None else (q_out, k_out, v_out)
 
 
@@ -271,6 +262,10 @@ def tree_attention(q, k_new, v_new, tree, k_cache, v_cache, lengths, *, scale: f
     n, hq, tok, d = qs = _shape4(q, "q")
     _, hkv, rows, _ = _shape4(k_cache, "k_cache")
     dev = q.get_device()
+    if _elsewhere(dev, stream):
+        with _On(dev, stream):
+            return tree_attention(q, k_new, v_new, tree, k_cache, v_cache, lengths, scale=scale, out=out,
+                                  workspace=workspace)
     ns, cs = (n, hkv, tok, d), (n, hkv, rows, d)
     views = (*_view(q, "q", qs, _BF16, dev), *_view(k_new, "k_new", ns, _BF16, dev),
              *_view(v_new, "v_new", ns, _BF16, dev), *_view(k_cache, "k_cache", cs, _BF16, dev),
@@ -284,26 +279,27 @@ def tree_attention(q, k_new, v_new, tree, k_cache, v_cache, lengths, *, scale: f
     if dims == 2 and tree.shape[0] != 1:
         layers = _layers(layers, tree.shape[0], n, "tree")
         t_stride = tok
-    with _on(dev, stream):
-        status = _status_ptr(dev)
-        out, ov = _out(out, "out", qs, _BF16, q, dev)
-        ws = size = 0
-        if workspace is None:
-            size = N.load().statekv_tree_attention_workspace(n, hq, hkv, tok, d)
-            if size > 0:
-                workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
-                ws = workspace.data_ptr()
-        else:
-            ws, size = _vector(workspace, "workspace", torch.uint8, dev), workspace.shape[0]
-        _call("statekv_tree_attention", N.PACK_TREE, dev,
-                  *views[:4], *ov, *views[4:], masks, lens, status, ws, size, scale,
-                  t_stride, length, n, layers or 1, hq, hkv, tok, d, rows)
+    status = _status_ptr(dev)
+    out, ov = _out(out, "out", qs, _BF16, q, dev)
+    ws = size = 0
+    if workspace is None:
+        size = N.load().statekv_tree_attention_workspace(n, hq, hkv, tok, d, rows)
+        if size > 0:
+            workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+            ws = workspace.data_ptr()
+    else:
+        ws, size = _vector(workspace, "workspace", torch.uint8, dev), workspace.shape[0]
+    _call("statekv_tree_attention", N.PACK_TREE, dev,
+              *views[:4], *ov, *views[4:], masks, lens, status, ws, size, scale,
+              t_stride, length, n, layers or 1, hq, hkv, tok, d, rows)
     return out
 
 
-def tree_attention_workspace(batch: int, q_heads: int, kv_heads: int, tokens: int, head_dim: int) -> int:
-    """Bytes of workspace tree_attention needs on the current device."""
-    size = N.load().statekv_tree_attention_workspace(batch, q_heads, kv_heads, tokens, head_dim)
+def tree_attention_workspace(batch: int, q_heads: int, kv_heads: int, tokens: int, head_dim: int,
+                             cache_rows: int) -> int:
+    """Bytes of workspace tree_attention needs on the current device (0 for a
+    few short caches)."""
+    size = N.load().statekv_tree_attention_workspace(batch, q_heads, kv_heads, tokens, head_dim, cache_rows)
     if size < 0:
         raise N.StateKVError(N.E_UNSUPPORTED, "statekv_tree_attention_workspace")
     return size
@@ -317,6 +313,9 @@ def append_accepted(k_new, v_new, path, counts, k_cache, v_cache, lengths, *, st
     n, hkv, tok, d = ns = _shape4(k_new, "k_new")
     rows = _shape4(k_cache, "k_cache")[2]
     dt, dev = k_new.dtype, k_new.get_device()
+    if _elsewhere(dev, stream):
+        with _On(dev, stream):
+            return append_accepted(k_new, v_new, path, counts, k_cache, v_cache, lengths)
     if dt not in _DTYPES:
         raise ValueError(f"k_new: {dt}, want one of {list(_DTYPES)}")
     cs = (n, hkv, rows, d)
@@ -336,15 +335,14 @@ def append_accepted(k_new, v_new, path, counts, k_cache, v_cache, lengths, *, st
             raise ValueError(f"counts: {counts.shape[0]} for {n // layers} sequences")
         layers = layers or _layers(0, counts.shape[0], n, "counts")
     layers = layers or 1
-    with _on(dev, stream):
-        status = _status_ptr(dev)
-        new, to = None, 0
-        if lens or cnt:
-            new = torch.empty(n // layers, dtype=_I32, device=k_new.device)
-            to = new.data_ptr()
-        _call("statekv_append_accepted", N.PACK_APPEND, dev,
-                  *views, pp, cnt, lens, to, status, p_stride, steps, length, n, layers, hkv, tok, d, rows,
-                  _DTYPES[dt])
+    status = _status_ptr(dev)
+    new, to = None, 0
+    if lens or cnt:
+        new = torch.empty(n // layers, dtype=_I32, device=k_new.device)
+        to = new.data_ptr()
+    _call("statekv_append_accepted", N.PACK_APPEND, dev,
+              *views, pp, cnt, lens, to, status, p_stride, steps, length, n, layers, hkv, tok, d, rows,
+              _DTYPES[dt])
     return length + steps if new is None else new
 
 
@@ -355,13 +353,15 @@ def block_summaries(k_cache, codes, scales, lengths, *, appended: int | None = N
     `lengths` completed.  blocks >= rows // 64."""
     n, hkv, rows, d = cs = _shape4(k_cache, "k_cache")
     dev = k_cache.get_device()
+    if _elsewhere(dev, stream):
+        with _On(dev, stream):
+            return block_summaries(k_cache, codes, scales, lengths, appended=appended)
     view = _view(k_cache, "k_cache", cs, _BF16, dev)
     pc, ps, blocks = _summary_ptrs(codes, scales, n, hkv, d, dev)
     lens, length, layers = _lengths(lengths, n, dev)
     appended = rows if appended is None else min(int(appended), rows)
-    with _on(dev, stream):
-        _call("statekv_block_summaries", N.PACK_SUMMARY, dev,
-                  *view, pc, ps, lens, _status_ptr(dev), length, appended, blocks, n, layers or 1, hkv, d, rows)
+    _call("statekv_block_summaries", N.PACK_SUMMARY, dev,
+              *view, pc, ps, lens, _status_ptr(dev), length, appended, blocks, n, layers or 1, hkv, d, rows)
 
 
 def _summary_ptrs(codes, scales, n: int, hkv: int, d: int, dev: int) -> tuple[int, int, int]:
@@ -384,22 +384,26 @@ def sparse_attention(q, k_cache, v_cache, codes, scales, lengths, top: int, *, s
     the chosen blocks in ascending order, then -1)."""
     n, hq, tok, d = qs = _shape4(q, "q")
     _, hkv, rows, _ = _shape4(k_cache, "k_cache")
-    dev, top = q.get_device(), int(top)
+    dev = q.get_device()
+    if _elsewhere(dev, stream):
+        with _On(dev, stream):
+            return sparse_attention(q, k_cache, v_cache, codes, scales, lengths, top, scale=scale, out=out,
+                                    selected=selected)
+    top = int(top)
     cs = (n, hkv, rows, d)
     qv = _view(q, "q", qs, _BF16, dev)
     kc, vc = _view(k_cache, "k_cache", cs, _BF16, dev), _view(v_cache, "v_cache", cs, _BF16, dev)
     pc, ps, blocks = _summary_ptrs(codes, scales, n, hkv, d, dev)
     lens, length, layers = _lengths(lengths, n, dev)
-    with _on(dev, stream):
-        status = _status_ptr(dev)
-        out, ov = _out(out, "out", qs, _BF16, q, dev)
-        ss = (n, hkv, tok, max(0, top))
-        if selected is None:
-            selected = torch.empty(ss, dtype=_I32, device=q.device)
-        elif selected.shape != ss:
-            raise ValueError(f"selected: want {ss}, got {tuple(selected.shape)}")
-        _call("statekv_sparse_attention", N.PACK_SPARSE, dev,
-                  *qv, *ov, *kc, *vc, pc, ps, lens,
-                  _vector(selected, "selected", _I32, dev, 4), status, scale, length, top, blocks, n, layers or 1, hq,
-                  hkv, tok, d, rows)
+    status = _status_ptr(dev)
+    out, ov = _out(out, "out", qs, _BF16, q, dev)
+    ss = (n, hkv, tok, max(0, top))
+    if selected is None:
+        selected = torch.empty(ss, dtype=_I32, device=q.device)
+    elif selected.shape != ss:
+        raise ValueError(f"selected: want {ss}, got {tuple(selected.shape)}")
+    _call("statekv_sparse_attention", N.PACK_SPARSE, dev,
+              *qv, *ov, *kc, *vc, pc, ps, lens,
+              _vector(selected, "selected", _I32, dev, 4), status, scale, length, top, blocks, n, layers or 1, hq,
+              hkv, tok, d, rows)
     return out, selected

@@ -361,13 +361,13 @@ def test_tree_large_scores_and_order():
 def test_tree_views_workspace_stream_and_shared_tree():
     """Token-major caches and queries, one tree for all, own workspace, another stream."""
     g = gen(11)
-    n, hq, hkv, tok, d, rows = 2, 6, 3, 8, 128, 333
+    n, hq, hkv, tok, d, rows = 2, 6, 3, 8, 128, 1333
     q = randn(g, n, tok, hq + 2 * hkv, d).transpose(1, 2)
     q, kn, vn = q.split([hq, hkv, hkv], 1)
     pool = randn(g, n, rows, 2, hkv, d)
     kc, vc = pool[:, :, 0].transpose(1, 2), pool[:, :, 1].transpose(1, 2)
     tree = random_tree(tok, 1, 5)[0]
-    ws = torch.full((kv.tree_attention_workspace(n, hq, hkv, tok, d),), 255, dtype=torch.uint8, device=DEV)
+    ws = torch.full((kv.tree_attention_workspace(n, hq, hkv, tok, d, 5000),), 255, dtype=torch.uint8, device=DEV)
     out = torch.zeros(n, tok, hq, d, dtype=BF16, device=DEV).transpose(1, 2)
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
@@ -810,8 +810,8 @@ def test_null_arguments():
     lib = N.load()
     for f in ("norm_rope", "tree_attention", "append_accepted", "block_summaries", "sparse_attention"):
         assert getattr(lib, "statekv_" + f)(None, None) == N.E_INVALID_ARG
-    assert lib.statekv_tree_attention_workspace(1, 4, 2, 65, 128) == -1
-    assert lib.statekv_tree_attention_workspace(1, 3, 2, 4, 128) == -1
+    assert lib.statekv_tree_attention_workspace(1, 4, 2, 65, 128, 100) == -1
+    assert lib.statekv_tree_attention_workspace(1, 3, 2, 4, 128, 100) == -1
 
 
 @gpu
@@ -830,7 +830,9 @@ def test_python_checks_name_the_argument():
         call(q=q.clone().requires_grad_())
     with pytest.raises(kv.StateKVError):
         call(lengths=11)
+    call(workspace=torch.empty(16, dtype=torch.uint8, device=DEV))     # none needed: short caches
+    long = [torch.zeros(2, 2, 1200, 64, dtype=BF16, device=DEV) for _ in range(2)]
     with pytest.raises(kv.StateKVError):
-        call(workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+        call(k_cache=long[0], v_cache=long[1], workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
     with pytest.raises(kv.StateKVError):
         call(k_cache=kc[:, :1].expand(2, 2, 10, 64))
