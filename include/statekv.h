@@ -458,7 +458,7 @@ int statekv_attend_scores_static(const void* q_rot, const void* pool_k,
  *
  * Calls allocate nothing, keep nothing between calls and may be captured into
  * CUDA graphs.  Calls that overlap on the GPU need workspaces of their own;
- * they may share a status word.
+ * they may share a status word.  Scales of scores are in (1e-30, 1e30).
  */
 typedef struct statekv_view {
     void*   data;

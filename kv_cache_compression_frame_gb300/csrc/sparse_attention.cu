@@ -566,7 +566,7 @@ extern "C" int statekv_sparse_attention(const statekv_sparse_args* args, void* c
     const statekv_sparse_args& a = *args;
     if (a.batch < 0 || a.layers < 1 || a.batch % a.layers != 0 || a.kv_heads < 1 || a.q_heads < a.kv_heads ||
         a.q_heads % a.kv_heads != 0 || a.tokens < 0 || a.cache_rows < 0 || a.length < 0 || a.blocks < 0 || a.top < 1 ||
-        !(a.scale > 0.0) || !(a.scale < 1e30))
+        !(a.scale > 1e-30) || !(a.scale < 1e30))
         return STATEKV_E_INVALID_ARG;
     if ((a.head_dim != 64 && a.head_dim != 128) || a.q_heads / a.kv_heads > 16 || a.top > kMaxTop ||
         a.cache_rows / STATEKV_BLOCK > kMaxBlocks)

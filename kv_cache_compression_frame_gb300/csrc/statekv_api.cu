@@ -679,6 +679,7 @@ int statekv_decode_tree(statekv_handle* h, int32_t tokens, const void* q, const 
             return STATEKV_E_OOM;
         h->tree_ws_bytes = need;
     }
+    h->draft = 0;                       // the draft rows are written anew
     statekv_norm_rope_args na{};
     na.q = h->view(q, c.num_q_heads, tokens);
     na.k = h->view(k, c.num_kv_heads, tokens);

@@ -753,6 +753,9 @@ template <int D>
 __global__ void __launch_bounds__(kMergeThreads) tree_combine_kernel(const __grid_constant__ TreeKernelArgs k,
                                                                      int per_unit) {
     const statekv_tree_args& a = k.a;
+    // first of all, in every CTA: this grid must not end before the one whose
+    // end it stands for, even where there is nothing to merge
+    ptx::dep_wait();
     const int u = blockIdx.x / per_unit, part = blockIdx.x - u * per_unit;
     const int per_seq = a.layers * a.kv_heads * k.rb;
     const int s = u / per_seq;
@@ -773,7 +776,6 @@ __global__ void __launch_bounds__(kMergeThreads) tree_combine_kernel(const __gri
     __shared__ Merge sh[kMergeThreads];
     const float2* ml0 = k.part_ml + ((int64_t)ca + u) * k.rows;
     const float4* po0 = reinterpret_cast<const float4*>(k.part_o) + ((int64_t)ca + u) * (D / 4) * k.rows;
-    ptx::dep_wait();                         // the segments are written
     for (int out0 = part * per_step; out0 < outs; out0 += per_unit * per_step) {
         const int out = out0 + x, c4 = out / rows, r = out - c4 * rows;
         const bool live = out < outs;
@@ -907,7 +909,7 @@ extern "C" int statekv_tree_attention(const statekv_tree_args* args, void* cuda_
     if (!args) return STATEKV_E_INVALID_ARG;
     const statekv_tree_args& a = *args;
     if (a.layers < 1 || a.batch < 0 || a.batch % a.layers != 0 || a.cache_rows < 0 || a.length < 0 ||
-        a.tree_stride < 0 || !(a.scale > 0.0) || !(a.scale < 1e30))
+        a.tree_stride < 0 || !(a.scale > 1e-30) || !(a.scale < 1e30))
         return STATEKV_E_INVALID_ARG;
     TreeSizes z;
     int r = tree_sizes(a.batch, a.q_heads, a.kv_heads, a.tokens, a.head_dim, &z);

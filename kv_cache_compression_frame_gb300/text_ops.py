@@ -47,8 +47,7 @@ def _status_ptr(dev: int) -> int:
 def check_status(device: int | torch.device | None = None) -> None:
     """Synchronise the device and raise if a text operator recorded a failure
     there since the last check."""
-    dev = torch.cuda.current_device() if device is None else torch.device("cuda", device).index \
-        if isinstance(device, int) else torch.device(device).index
+    dev = device if isinstance(device, int) else None if device is None else torch.device(device).index
     if dev is None:
         dev = torch.cuda.current_device()
     if dev not in _status:
@@ -207,6 +206,8 @@ def qk_norm_rope(q, k, positions, omega, q_weight=None, k_weight=None, *, v=None
                     (wd is not None and (wd is not w.dtype or rows != w_rows)):
                 raise ValueError(f"{'qk'[i]}_weight: want [{d}] or [layers][{d}] of one of {list(_DTYPES)}, the "
                                  "same for both weights, layers dividing the batch")
+            if w.requires_grad and torch.is_grad_enabled():
+                raise ValueError(f"{'qk'[i]}_weight requires grad: the text operators have no backward pass")
             wd, w_rows = w.dtype, rows
             w_ptr[i] = _vector(w, f"{'qk'[i]}_weight", wd, dev, w.dim())
     if omega.shape != (d // 2,):

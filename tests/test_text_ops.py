@@ -380,6 +380,52 @@ def test_tree_views_workspace_stream_and_shared_tree():
 
 
 @gpu
+def test_tree_units_that_fill_the_device_exactly():
+    """One share per unit: nothing to merge, and what follows on the stream
+    still waits for the whole call."""
+    n = torch.cuda.get_device_properties(0).multi_processor_count
+    x = tree_inputs(13, n, 2, 1, 5, 128, 3000)
+    tree = random_tree(5, n, 1)
+    want = kv.tree_attention(*x[:3], tree, *x[3:], 3000, scale=0.1)
+    check_tree(*x[:3], tree, *x[3:], 3000, 0.1, want)
+    torch.cuda.synchronize()
+    got = kv.tree_attention(*x[:3], tree, *x[3:], 3000, scale=0.1)
+    x[3].fill_(7)
+    x[4].fill_(float("nan"))
+    assert torch.equal(got, want)
+
+
+@gpu
+def test_offsets_past_32_bits():
+    """The second batch entry of a cache lies 2^32 elements behind the first."""
+    far, rows, d = 1 << 32, 1500, 64
+    g = gen(14)
+    flat = torch.empty(far + rows * d, dtype=BF16, device=DEV)
+    cache = flat.as_strided((2, 1, rows, d), (far, rows * d, d, 1))
+    for i in range(2):
+        cache[i] = randn(g, 1, rows, d)
+    small = cache.contiguous()
+    q, k, v = randn(g, 2, 2, 6, d), randn(g, 2, 1, 6, d), randn(g, 2, 1, 6, d)
+    tree = random_tree(6, 2, 1)
+    assert torch.equal(kv.tree_attention(q, k, v, tree, cache, cache, rows, scale=0.1),
+                       kv.tree_attention(q, k, v, tree, small, small, rows, scale=0.1))
+    codes, scales = (torch.zeros((2, 1, 24, d), dtype=torch.int8, device=DEV), torch.zeros((2, 1, 24), device=DEV))
+    kv.block_summaries(cache, codes, scales, rows)
+    c, s = ref_summaries(small[:, :, :23 * 64])
+    assert torch.equal(codes[:, :, :23], c) and torch.equal(scales[:, :, :23], s)
+    for a, b in zip(kv.sparse_attention(q, cache, cache, codes, scales, rows, 3, scale=0.1),
+                    kv.sparse_attention(q, small, small, codes, scales, rows, 3, scale=0.1)):
+        assert torch.equal(a, b)
+    path = torch.tensor([5, 0], dtype=torch.int32, device=DEV)
+    kv.append_accepted(v, v, path, None, cache, cache, 700)
+    assert torch.equal(cache[:, :, 700:702], v[:, :, [5, 0]])
+    out = kv.qk_norm_rope(cache[:, :, :6], cache[:, :, 6:12], 3, omega_of(d))
+    want = kv.qk_norm_rope(cache[:, :, :6].contiguous(), cache[:, :, 6:12].contiguous(), 3, omega_of(d))
+    assert all(torch.equal(a, b) for a, b in zip(out, want))
+    kv.check_status()
+
+
+@gpu
 def test_tree_lengths_out_of_range_are_recorded():
     x = tree_inputs(12, 2, 2, 1, 3, 64, 50)
     tree = random_tree(3, 1, 1)[0]
@@ -719,7 +765,7 @@ def tree_args(**kw):
     (dict(tokens=0), N.E_INVALID_ARG), (dict(tokens=65), N.E_UNSUPPORTED), (dict(head_dim=96), N.E_UNSUPPORTED),
     (dict(q_heads=3), N.E_INVALID_ARG), (dict(kv_heads=0), N.E_INVALID_ARG), (dict(layers=3), N.E_INVALID_ARG),
     (dict(layers=0), N.E_INVALID_ARG), (dict(batch=-1), N.E_INVALID_ARG), (dict(scale=0.0), N.E_INVALID_ARG),
-    (dict(scale=math.nan), N.E_INVALID_ARG), (dict(scale=math.inf), N.E_INVALID_ARG),
+    (dict(scale=math.nan), N.E_INVALID_ARG), (dict(scale=math.inf), N.E_INVALID_ARG), (dict(scale=1e-40), N.E_INVALID_ARG),
     (dict(length=5), N.E_CAPACITY), (dict(length=-1), N.E_INVALID_ARG), (dict(status=None), N.E_INVALID_ARG),
     (dict(status=18), N.E_INVALID_ARG), (dict(tree=None), N.E_INVALID_ARG), (dict(tree=20), N.E_INVALID_ARG),
     (dict(q=view(8)), N.E_INVALID_ARG), (dict(q=view(t=4)), N.E_INVALID_ARG), (dict(out=view(h=-512)), N.E_INVALID_ARG),
