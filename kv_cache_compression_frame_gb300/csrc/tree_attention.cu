@@ -26,7 +26,8 @@
 // maximum and sum per row.  Thread = query row (TMEM lane): no reduction
 // across threads.  A "job" is one S = Q K^T, softmax, O += P V of a slot; the
 // issuer runs S two jobs ahead of P V, so one slot's exponentials overlap the
-// other's products.
+// other's products.  The next unit's first scores are computed while the last
+// one's output is written; two otherwise idle warps copy its Q.
 // P (bf16 pairs) overwrites its own S buffer: the products of one thread run
 // in issue order, and S of a slot's next job is issued after P V of its last.
 // That order also makes S(next) complete imply P V(last) complete, so a warp
@@ -41,6 +42,12 @@
 // past the cache's end are zeroed in shared memory, and non-finite values of
 // drafted V rows too (0 * NaN would reach rows that mask them) and put back
 // at the end for the rows that see them.
+//
+// Measured: 16 ragged streams of up to 32768 rows, 64 query rows a unit, 1.15
+// GB: 190 us = 6.0 TB/s (HBM).  28 layers x 131072 rows, 252 query rows a unit,
+// 3.76 GB and 0.95 TFLOP: 690 us on a cool chip, 705-775 us under the power
+// limit (1380 W, 1657 MHz), which is the bound there: variants that need fewer
+// cycles per tile were not faster.
 #include <algorithm>
 
 #include "pipeline.cuh"
