@@ -88,11 +88,13 @@ __device__ __forceinline__ int head_of(const TreeKernelArgs& k, int r) {
 // kUnitCost + nt tiles (it starts with kUnitCost of no content): without that
 // a CTA whose share held many short units took 1.5 times as long as the rest.
 struct Plan {
-    int64_t total;                           // tiles of all units
-    int ctas;                                // CTAs that get a share
-    __device__ int64_t start(int c) const { return total * c / ctas; }
-    // the CTA whose share holds tile w
-    __device__ int cta_of(int64_t w) const { return (int)(((w + 1) * ctas - 1) / total); }
+    uint32_t ctas, each, more;               // shares; tiles of a share, of the first `more` one more
+    __device__ uint32_t start(uint32_t c) const { return each * c + min(c, more); }
+    // the share that holds tile w
+    __device__ uint32_t cta_of(uint32_t w) const {
+        const uint32_t big = (each + 1) * more;
+        return w < big ? w / (each + 1) : more + (w - big) / each;
+    }
 };
 
 __device__ __forceinline__ int seq_length(const TreeKernelArgs& k, int s) {
@@ -105,33 +107,32 @@ __device__ __forceinline__ int unit_cost(const TreeKernelArgs& k, int s) {
 }
 
 // Cost of one unit of every sequence before s, and of all sequences; a whole
-// warp, the same result in every lane.
-__device__ __forceinline__ void sum_costs(const TreeKernelArgs& k, int s, int64_t& before, int64_t& all) {
+// warp, the same result in every lane.  (Totals are below 2^31, see the entry
+// point; 64-bit divisions by run-time values took 1 us of the prologue.)
+__device__ __forceinline__ void sum_costs(const TreeKernelArgs& k, int s, uint32_t& before, uint32_t& all) {
     const int seqs = k.a.batch / k.a.layers;
     if (!k.a.lengths) {
-        const int t = unit_cost(k, 0);
-        before = (int64_t)t * s;
-        all = (int64_t)t * seqs;
+        const uint32_t t = (uint32_t)unit_cost(k, 0);
+        before = t * (uint32_t)s;
+        all = t * (uint32_t)seqs;
         return;
     }
     before = all = 0;
     for (int i = threadIdx.x & 31; i < seqs; i += 32) {
-        const int t = unit_cost(k, i);
+        const uint32_t t = (uint32_t)unit_cost(k, i);
         all += t;
         if (i < s) before += t;
     }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        before += __shfl_xor_sync(0xffffffffu, before, off);
-        all += __shfl_xor_sync(0xffffffffu, all, off);
-    }
+    before = __reduce_add_sync(0xffffffffu, before);
+    all = __reduce_add_sync(0xffffffffu, all);
 }
 
-__device__ __forceinline__ Plan make_plan(const TreeKernelArgs& k, int64_t costs) {
+__device__ __forceinline__ Plan make_plan(const TreeKernelArgs& k, uint32_t costs) {
+    const uint32_t total = costs * (uint32_t)(k.a.layers * k.a.kv_heads * k.rb);
     Plan p;
-    p.total = costs * k.a.layers * k.a.kv_heads * k.rb;
-    const int64_t most = (p.total + kMinShare - 1) / kMinShare;
-    p.ctas = most < k.grid ? (int)most : k.grid;
+    p.ctas = min((total + kMinShare - 1) / kMinShare, (uint32_t)k.grid);
+    p.each = total / p.ctas;
+    p.more = total - p.each * p.ctas;
     return p;
 }
 
@@ -139,7 +140,7 @@ __device__ __forceinline__ Plan make_plan(const TreeKernelArgs& k, int64_t costs
 struct Walk {
     int next_s, next_len, v;                 // the next segment's sequence, its length, place in the unit
     int next_u;
-    int64_t left;                            // of the share
+    int left;                                // of the share
     // the current segment: sequence, cache rows, key tiles of the unit, unit,
     // first key tile and number of them
     int s, len, nt, u, t, tiles;
@@ -150,7 +151,7 @@ struct Walk {
             len = next_len;
             nt = unit_tiles(len);
             u = next_u;
-            const int take = (int)min((int64_t)(nt + kUnitCost - v), left);
+            const int take = min(nt + kUnitCost - v, left);
             t = max(v - kUnitCost, 0);
             tiles = max(v + take - kUnitCost, 0) - t;
             left -= take;
@@ -167,26 +168,26 @@ struct Walk {
 };
 
 // The walk of the share [w, w1) (a whole warp, the same result in every lane).
-__device__ __forceinline__ Walk find(const TreeKernelArgs& k, int64_t w, int64_t w1) {
-    const int64_t per_seq = (int64_t)k.a.layers * k.a.kv_heads * k.rb;
+__device__ __forceinline__ Walk find(const TreeKernelArgs& k, uint32_t w, uint32_t w1) {
+    const uint32_t per_seq = (uint32_t)(k.a.layers * k.a.kv_heads * k.rb);
     const int seqs = k.a.batch / k.a.layers;
     Walk c{};
-    c.left = w1 - w;
-    int cost;
+    c.left = (int)(w1 - w);
+    uint32_t cost;
     if (!k.a.lengths) {
         c.next_len = seq_length(k, 0);
-        cost = unit_tiles(c.next_len) + kUnitCost;
+        cost = (uint32_t)(unit_tiles(c.next_len) + kUnitCost);
         c.next_s = (int)(w / (cost * per_seq));
-        w -= c.next_s * (cost * per_seq);
+        w -= (uint32_t)c.next_s * (cost * per_seq);
     } else {
         const int lane = threadIdx.x & 31;
-        int64_t base = 0;
+        uint32_t base = 0;
         for (int s0 = 0; s0 < seqs; s0 += 32) {
-            const int64_t mine = s0 + lane < seqs ? unit_cost(k, s0 + lane) * per_seq : 0;
-            int64_t upto = mine;
+            const uint32_t mine = s0 + lane < seqs ? (uint32_t)unit_cost(k, s0 + lane) * per_seq : 0u;
+            uint32_t upto = mine;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
-                const int64_t x = __shfl_up_sync(0xffffffffu, upto, off);
+                const uint32_t x = __shfl_up_sync(0xffffffffu, upto, off);
                 if (lane >= off) upto += x;
             }
             const unsigned hit = __ballot_sync(0xffffffffu, base + upto > w);
@@ -200,10 +201,10 @@ __device__ __forceinline__ Walk find(const TreeKernelArgs& k, int64_t w, int64_t
         }
         w -= base;
         c.next_len = seq_length(k, c.next_s);
-        cost = unit_tiles(c.next_len) + kUnitCost;
+        cost = (uint32_t)(unit_tiles(c.next_len) + kUnitCost);
     }
-    const int64_t local = w / cost;
-    c.next_u = (int)(c.next_s * per_seq + local);
+    const uint32_t local = w / cost;
+    c.next_u = (int)((uint32_t)c.next_s * per_seq + local);
     c.v = (int)(w - local * cost);
     return c;
 }
@@ -272,17 +273,66 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         first.next_len = seq_length(k, first.next_s);
         first.left = unit_tiles(first.next_len) + kUnitCost;
     } else {
-        int64_t none, costs;
+        uint32_t none, costs;
         sum_costs(k, 0, none, costs);
         const Plan plan = make_plan(k, costs);
-        if (c >= plan.ctas) return;
-        first = find(k, plan.start(c), plan.start(c + 1));
+        if (c >= (int)plan.ctas) return;
+        first = find(k, plan.start((uint32_t)c), plan.start((uint32_t)c + 1));
     }
 
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + L::OFF_MISC);
     volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(base + L::OFF_MISC + 4);
     unsigned long long* odd_nodes = reinterpret_cast<unsigned long long*>(base + L::OFF_MISC + 8);
     Sync sy{sbase + (uint32_t)L::OFF_BAR, abort_flag, a.status};
+    const uint32_t sK = sbase + L::OFF_K, sV = sbase + L::OFF_V, sQ = sbase + L::OFF_Q;
+    // the next key tile of the share into its ring (thread 0); 1 loaded, 0 none
+    // left, -1 gave up
+    Walk wk = first, wv = first;
+    int kt = 0, vt = 0;                                  // tiles loaded
+    auto load = [&](bool is_v) -> int {
+        Walk& x = is_v ? wv : wk;
+        if (x.tiles == 0 && !x.next(k)) return 0;
+        int& cnt = is_v ? vt : kt;
+        const int ns = is_v ? L::VS : L::KS;
+        const int s = cnt % ns, j = cnt / ns;
+        if (!sy.wait((is_v ? L::B_V_EMPTY : L::B_K_EMPTY) + s, (uint32_t)(j & 1) ^ 1u, kSiteKvEmpty)) return -1;
+        const uint32_t fb = sy.bar((is_v ? L::B_V_FULL : L::B_K_FULL) + s);
+        ptx::mbar_arrive_expect_tx(fb, L::TILE);
+        const uint32_t dst = (is_v ? sV : sK) + s * L::TILE;
+        const bool drafted = x.t == x.nt - 1;
+        const CUtensorMap* map = drafted ? (is_v ? &tm_vn : &tm_kn) : (is_v ? &tm_v : &tm_k);
+        const int nh = x.u / k.rb, n = nh / a.kv_heads, h = nh - n * a.kv_heads;
+#pragma unroll
+        for (int kc = 0; kc < L::KCH; ++kc)
+            ptx::tma_load_4d(dst + kc * L::CHUNK, map, fb, kc * 64, drafted ? 0 : x.t * kTile, h, n);
+        ++cnt;
+        ++x.t;
+        --x.tiles;
+        return 1;
+    };
+    // a unit's rows r = g * tokens + j of Q, zeros past the last, into shared
+    // memory (warps 2 and 3, asynchronously)
+    auto copy_q = [&](int u) {
+        constexpr int UPR = D / 8;                       // 16-byte units per row
+        constexpr int STEP = 64 / UPR;                   // rows at a time: 4 or 8
+        const int qt = (int)threadIdx.x - 64, e = qt % UPR, r0 = qt / UPR;
+        const int nh = u / k.rb, n = nh / a.kv_heads, h = nh - n * a.kv_heads;
+        const int row_base = (u - nh * k.rb) * L::RT * kTile;
+        int g = head_of(k, row_base + r0), j = row_base + r0 - g * a.tokens;
+        const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(a.q.data) + n * a.q.batch_stride +
+                                 (int64_t)(h * k.G + g) * a.q.head_stride + j * a.q.token_stride + 8 * e;
+        const int64_t row = STEP * a.q.token_stride, wrap = a.q.head_stride - a.tokens * a.q.token_stride;
+        const int left = k.R - row_base;
+        const void* some = a.q.data;                     // (nothing is read for the zeros)
+#pragma unroll 4
+        for (int r = r0; r < L::RT * kTile; r += STEP) {
+            ptx::cp_async_16(sQ + (r / kTile) * L::TILE + (e >> 3) * L::CHUNK + (r % kTile) * 128 +
+                                 (((e & 7) ^ (r & 7)) << 4),
+                             r < left ? static_cast<const void*>(p) : some, r < left ? 16u : 0u);
+            p += row;
+            for (j += STEP; j >= a.tokens; j -= a.tokens) p += wrap;
+        }
+    };
     if (threadIdx.x == 0) {
         for (int s = 0; s < L::KS; ++s) {
             ptx::mbar_init(sy.bar(L::B_K_FULL + s), 1);
@@ -305,6 +355,15 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         *abort_flag = 0u;
         odd_nodes[0] = odd_nodes[1] = 0ull;
         ptx::fence_barrier_init();
+        // the first tiles are on their way while the rest is set up (the
+        // stages are empty: no wait)
+        static_assert(L::LEAD <= L::KS, "no wait before every barrier is visible");
+        for (int t = 0; t < L::LEAD; ++t) load(false);
+        load(true);
+    }
+    if (warp == 2 || warp == 3) {
+        Walk x = first;
+        if (x.next(k)) copy_q(x.u);
     }
     if (warp == 1) {
         ptx::tmem_alloc(ptx::smem_u32(tmem_slot), L::TMEM_COLS);
@@ -316,47 +375,14 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     const uint32_t tmem = *tmem_slot;
     // the merge may be launched now; it waits for this grid to end
     ptx::dep_trigger();
-    const uint32_t sK = sbase + L::OFF_K, sV = sbase + L::OFF_V, sQ = sbase + L::OFF_Q;
-
     if (warp < 4) {
         ptx::regs_dec<kRegsIssue>();
     if (warp == 0) {
         // ------------------------------------------------------ TMA producer
         if (lane == 0) {
-            ptx::tma_prefetch_desc(&tm_k);
-            ptx::tma_prefetch_desc(&tm_v);
-            Walk wk = first, wv = first;
-            wk.tiles = wv.tiles = 0;
-            int kt = 0, vt = 0;
-            // the next key tile of the share; 1 loaded, 0 none left, -1 gave up
-            auto load = [&](bool is_v) -> int {
-                Walk& x = is_v ? wv : wk;
-                if (x.tiles == 0 && !x.next(k)) return 0;
-                int& cnt = is_v ? vt : kt;
-                const int ns = is_v ? L::VS : L::KS;
-                const int s = cnt % ns, j = cnt / ns;
-                if (!sy.wait((is_v ? L::B_V_EMPTY : L::B_K_EMPTY) + s, (uint32_t)(j & 1) ^ 1u, kSiteKvEmpty))
-                    return -1;
-                const uint32_t fb = sy.bar((is_v ? L::B_V_FULL : L::B_K_FULL) + s);
-                ptx::mbar_arrive_expect_tx(fb, L::TILE);
-                const uint32_t dst = (is_v ? sV : sK) + s * L::TILE;
-                const bool drafted = x.t == x.nt - 1;
-                const CUtensorMap* map = drafted ? (is_v ? &tm_vn : &tm_kn) : (is_v ? &tm_v : &tm_k);
-                const int nh = x.u / k.rb, n = nh / a.kv_heads, h = nh - n * a.kv_heads;
-#pragma unroll
-                for (int kc = 0; kc < L::KCH; ++kc)
-                    ptx::tma_load_4d(dst + kc * L::CHUNK, map, fb, kc * 64, drafted ? 0 : x.t * kTile, h, n);
-                ++cnt;
-                ++x.t;
-                --x.tiles;
-                return 1;
-            };
-            int got = 1;
-            for (int t = 0; got == 1 && t < L::LEAD; ++t) got = load(false);
-            while (got >= 0) {
-                const int r = load(true);
-                if (r <= 0) break;
+            for (int got = 1; got >= 0;) {
                 got = load(false);
+                if (got >= 0 && load(true) <= 0) break;
             }
             // never leave a copy in flight into this CTA's shared memory
             for (int s = 0; s < L::KS && s < kt; ++s)
@@ -442,22 +468,11 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         // (warps 2 and 3) a unit's rows r = g * tokens + j, zeros past the
         // last, as soon as the unit before needs Q no more: its last softmax
         // and its output hide the copy
-        constexpr int UPR = D / 8;                       // 16-byte units per row
-        const int qt = (int)threadIdx.x - 64, e = qt % UPR;
         Walk x = first;
         for (int seg = 0; x.next(k); ++seg) {
-            if (seg > 0 && !sy.wait(L::B_Q_FREE, (uint32_t)((seg - 1) & 1), kSiteQFull)) break;
-            const int nh = x.u / k.rb, n = nh / a.kv_heads, h = nh - n * a.kv_heads;
-            const int row_base = (x.u - nh * k.rb) * L::RT * kTile;
-            const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q.data) + n * a.q.batch_stride +
-                                     (int64_t)(h * k.G) * a.q.head_stride + 8 * e;
-#pragma unroll 4
-            for (int r = qt / UPR; r < L::RT * kTile; r += 64 / UPR) {
-                const int rq = row_base + r, g = head_of(k, rq), j = rq - g * a.tokens;
-                const bool there = rq < k.R;
-                ptx::cp_async_16(sQ + (r / kTile) * L::TILE + (e >> 3) * L::CHUNK + (r % kTile) * 128 +
-                                     (((e & 7) ^ (r & 7)) << 4),
-                                 there ? q + g * a.q.head_stride + j * a.q.token_stride : q, there ? 16u : 0u);
+            if (seg > 0) {
+                if (!sy.wait(L::B_Q_FREE, (uint32_t)((seg - 1) & 1), kSiteQFull)) break;
+                copy_q(x.u);
             }
             ptx::cp_async_wait();
             ptx::fence_proxy_async_smem();
@@ -760,18 +775,18 @@ template <int D>
 __global__ void __launch_bounds__(kMergeThreads) tree_combine_kernel(const __grid_constant__ TreeKernelArgs k,
                                                                      int per_unit) {
     const statekv_tree_args& a = k.a;
-    // first of all, in every CTA: this grid must not end before the one whose
-    // end it stands for, even where there is nothing to merge
-    ptx::dep_wait();
     const int u = blockIdx.x / per_unit, part = blockIdx.x - u * per_unit;
     const int per_seq = a.layers * a.kv_heads * k.rb;
     const int s = u / per_seq;
-    int64_t before, all;
+    uint32_t before, all;
     sum_costs(k, s, before, all);
     const Plan plan = make_plan(k, all);
     const int nt = unit_tiles(seq_length(k, s));
-    const int64_t w = before * per_seq + (int64_t)(u - s * per_seq) * (nt + kUnitCost) + kUnitCost;
-    const int ca = plan.cta_of(w), segs = plan.cta_of(w + nt - 1) - ca + 1;
+    const uint32_t w = before * (uint32_t)per_seq + (uint32_t)((u - s * per_seq) * (nt + kUnitCost) + kUnitCost);
+    const int ca = (int)plan.cta_of(w), segs = (int)plan.cta_of(w + (uint32_t)nt - 1) - ca + 1;
+    // in every CTA, before it may leave: this grid must not end before the one
+    // whose end it stands for, even where there is nothing to merge
+    ptx::dep_wait();
     if (segs == 1) return;                   // written by the one CTA
     const int nh = u / k.rb, rblk = u - nh * k.rb;
     const int row_tile = k.R > kTile ? 2 * kTile : kTile;
@@ -956,6 +971,7 @@ extern "C" int statekv_tree_attention(const statekv_tree_args* args, void* cuda_
     // otherwise no more CTAs than the longest cache could use
     k.whole = whole;
     const int64_t cost = most_tiles(a.lengths ? a.cache_rows : a.length) + kUnitCost;
+    if (z.units * cost > 0x7fffffff) return STATEKV_E_UNSUPPORTED;   // the schedule counts in 32 bits
     k.grid = whole ? (int)z.units : (int)std::min<int64_t>(sms, (z.units * cost + kMinShare - 1) / kMinShare);
     const int64_t segments = (int64_t)sms + z.units;
     k.part_o = static_cast<float*>(a.workspace);
