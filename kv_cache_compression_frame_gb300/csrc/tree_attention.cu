@@ -218,7 +218,7 @@ struct TreeLayout {
     // as many stages as fit beside Q
     static constexpr int KS = D == 64 ? 6 : 3;
     static constexpr int VS = D == 64 ? 5 : (SPLIT_ROWS ? 2 : 3);
-    static constexpr int LEAD = SPLIT_ROWS ? 1 : 2;      // key tiles that S runs ahead of P V
+    static constexpr int LEAD = SPLIT_ROWS ? 1 : 2;      // K tiles loaded ahead of V, as S runs ahead of P V
     static constexpr int OFF_K = 0;
     static constexpr int OFF_V = OFF_K + KS * TILE;
     static constexpr int OFF_Q = OFF_V + VS * TILE;      // [RT] row tiles
@@ -377,109 +377,109 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     ptx::dep_trigger();
     if (warp < 4) {
         ptx::regs_dec<kRegsIssue>();
-    if (warp == 0) {
-        // ------------------------------------------------------ TMA producer
-        if (lane == 0) {
-            for (int got = 1; got >= 0;) {
-                got = load(false);
-                if (got >= 0 && load(true) <= 0) break;
+        if (warp == 0) {
+            // ------------------------------------------------------ TMA producer
+            if (lane == 0) {
+                for (int got = 1; got >= 0;) {
+                    got = load(false);
+                    if (got >= 0 && load(true) <= 0) break;
+                }
+                // never leave a copy in flight into this CTA's shared memory
+                for (int s = 0; s < L::KS && s < kt; ++s)
+                    sy.drain(L::B_K_FULL + s, (uint32_t)(((kt - 1 - s) / L::KS) & 1));
+                for (int s = 0; s < L::VS && s < vt; ++s)
+                    sy.drain(L::B_V_FULL + s, (uint32_t)(((vt - 1 - s) / L::VS) & 1));
             }
-            // never leave a copy in flight into this CTA's shared memory
-            for (int s = 0; s < L::KS && s < kt; ++s)
-                sy.drain(L::B_K_FULL + s, (uint32_t)(((kt - 1 - s) / L::KS) & 1));
-            for (int s = 0; s < L::VS && s < vt; ++s)
-                sy.drain(L::B_V_FULL + s, (uint32_t)(((vt - 1 - s) / L::VS) & 1));
-        }
-    } else if (warp == 1) {
-        // -------------------------------------------------------- MMA issuer
-        constexpr uint32_t idesc_s = ptx::idesc_bf16_f32(128, 128, false, false);
-        constexpr uint32_t idesc_o = ptx::idesc_bf16_f32(128, D, false, true);
-        const uint32_t kmaj_hi = (uint32_t)(ptx::sdesc_sw128(0, 16, 1024) >> 32);
-        const uint32_t v_hi = (uint32_t)(ptx::sdesc_sw128(0, L::CHUNK, 1024) >> 32);
-        const uint32_t kb0 = (uint32_t)ptx::sdesc_sw128(sK, 16, 1024);
-        const uint32_t qb0 = (uint32_t)ptx::sdesc_sw128(sQ, 16, 1024);
-        const uint32_t vb0 = (uint32_t)ptx::sdesc_sw128(sV, L::CHUNK, 1024);
-        Walk x = first;
-        int g0 = 0, seg = 0;                             // tiles before this segment, segments done
-        uint32_t p_par[2] = {0, 0};
-        bool ok = true;
-        auto issue_s = [&](int j, bool last) -> bool {
-            const int slot = j & 1, g = g0 + (SPLIT_ROWS ? j >> 1 : j), s = g % L::KS;
-            if (!sy.wait(L::B_K_FULL + s, (uint32_t)((g / L::KS) & 1), kSiteKvFull)) return false;
-            ptx::tc_fence_after();
-            if (ptx::elect_one()) {
-                const uint32_t kb = kb0 + (uint32_t)s * (L::TILE >> 4);
-                const uint32_t qb = qb0 + (SPLIT_ROWS ? (uint32_t)slot * (L::TILE >> 4) : 0u);
-#pragma unroll
-                for (int kc = 0; kc < L::KCH; ++kc)
-#pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)
-                        ptx::umma_ss_lh(tmem + L::TM_S + 128u * slot, qb + kc * (L::CHUNK >> 4) + 2 * ks, kmaj_hi,
-                                        kb + kc * (L::CHUNK >> 4) + 2 * ks, kmaj_hi, idesc_s,
-                                        (kc | ks) ? 1u : 0u);
-                ptx::umma_commit(sy.bar(L::B_S_FULL + slot));
-                if (!SPLIT_ROWS || slot == 1) ptx::umma_commit(sy.bar(L::B_K_EMPTY + s));
-                if (last) ptx::umma_commit(sy.bar(L::B_Q_FREE));
-            }
-            __syncwarp();
-            return true;
-        };
-        auto issue_pv = [&](int j) -> bool {
-            const int slot = j & 1, g = g0 + (SPLIT_ROWS ? j >> 1 : j), s = g % L::VS;
-            if (!sy.wait(L::B_V_FULL + s, (uint32_t)((g / L::VS) & 1), kSiteKvFull)) return false;
-            // the first 64 keys' products run while the other 64 are exponentiated
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                if (!sy.wait(L::B_P_FULL + 2 * slot + hf, p_par[slot], kSitePFull)) return false;
+        } else if (warp == 1) {
+            // -------------------------------------------------------- MMA issuer
+            constexpr uint32_t idesc_s = ptx::idesc_bf16_f32(128, 128, false, false);
+            constexpr uint32_t idesc_o = ptx::idesc_bf16_f32(128, D, false, true);
+            const uint32_t kmaj_hi = (uint32_t)(ptx::sdesc_sw128(0, 16, 1024) >> 32);
+            const uint32_t v_hi = (uint32_t)(ptx::sdesc_sw128(0, L::CHUNK, 1024) >> 32);
+            const uint32_t kb0 = (uint32_t)ptx::sdesc_sw128(sK, 16, 1024);
+            const uint32_t qb0 = (uint32_t)ptx::sdesc_sw128(sQ, 16, 1024);
+            const uint32_t vb0 = (uint32_t)ptx::sdesc_sw128(sV, L::CHUNK, 1024);
+            Walk x = first;
+            int g0 = 0, seg = 0;                             // tiles before this segment, segments done
+            uint32_t p_par[2] = {0, 0};
+            bool ok = true;
+            auto issue_s = [&](int j, bool last) -> bool {
+                const int slot = j & 1, g = g0 + (SPLIT_ROWS ? j >> 1 : j), s = g % L::KS;
+                if (!sy.wait(L::B_K_FULL + s, (uint32_t)((g / L::KS) & 1), kSiteKvFull)) return false;
                 ptx::tc_fence_after();
                 if (ptx::elect_one()) {
-                    const uint32_t vb = vb0 + (uint32_t)s * (L::TILE >> 4);
+                    const uint32_t kb = kb0 + (uint32_t)s * (L::TILE >> 4);
+                    const uint32_t qb = qb0 + (SPLIT_ROWS ? (uint32_t)slot * (L::TILE >> 4) : 0u);
 #pragma unroll
-                    for (int ks = 4 * hf; ks < 4 * hf + 4; ++ks)     // 16 keys per step
-                        ptx::umma_ts_lh(tmem + L::TM_O + 128u * slot, tmem + L::TM_S + 128u * slot + 8u * ks,
-                                        vb + 128u * ks, v_hi, idesc_o, (j > 1 || ks > 0) ? 1u : 0u);
-                    if (hf == 1 && (!SPLIT_ROWS || slot == 1)) ptx::umma_commit(sy.bar(L::B_V_EMPTY + s));
+                    for (int kc = 0; kc < L::KCH; ++kc)
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            ptx::umma_ss_lh(tmem + L::TM_S + 128u * slot, qb + kc * (L::CHUNK >> 4) + 2 * ks, kmaj_hi,
+                                            kb + kc * (L::CHUNK >> 4) + 2 * ks, kmaj_hi, idesc_s,
+                                            (kc | ks) ? 1u : 0u);
+                    ptx::umma_commit(sy.bar(L::B_S_FULL + slot));
+                    if (!SPLIT_ROWS || slot == 1) ptx::umma_commit(sy.bar(L::B_K_EMPTY + s));
+                    if (last) ptx::umma_commit(sy.bar(L::B_Q_FREE));
                 }
                 __syncwarp();
+                return true;
+            };
+            auto issue_pv = [&](int j) -> bool {
+                const int slot = j & 1, g = g0 + (SPLIT_ROWS ? j >> 1 : j), s = g % L::VS;
+                if (!sy.wait(L::B_V_FULL + s, (uint32_t)((g / L::VS) & 1), kSiteKvFull)) return false;
+                // the first 64 keys' products run while the other 64 are exponentiated
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    if (!sy.wait(L::B_P_FULL + 2 * slot + hf, p_par[slot], kSitePFull)) return false;
+                    ptx::tc_fence_after();
+                    if (ptx::elect_one()) {
+                        const uint32_t vb = vb0 + (uint32_t)s * (L::TILE >> 4);
+#pragma unroll
+                        for (int ks = 4 * hf; ks < 4 * hf + 4; ++ks)     // 16 keys per step
+                            ptx::umma_ts_lh(tmem + L::TM_O + 128u * slot, tmem + L::TM_S + 128u * slot + 8u * ks,
+                                            vb + 128u * ks, v_hi, idesc_o, (j > 1 || ks > 0) ? 1u : 0u);
+                        if (hf == 1 && (!SPLIT_ROWS || slot == 1)) ptx::umma_commit(sy.bar(L::B_V_EMPTY + s));
+                    }
+                    __syncwarp();
+                }
+                p_par[slot] ^= 1u;
+                return true;
+            };
+            for (; ok && x.next(k); ++seg) {
+                const int jobs = SPLIT_ROWS ? 2 * x.tiles : x.tiles;
+                if (!(ok = sy.wait(L::B_Q_FULL, (uint32_t)(seg & 1), kSiteQFull))) break;
+                ptx::tc_fence_after();
+                ok = issue_s(0, jobs == 1);
+                if (ok && jobs > 1) ok = issue_s(1, jobs == 2);
+                for (int j = 0; ok && j < jobs; ++j) {
+                    ok = issue_pv(j);
+                    if (ok && j + 2 < jobs) ok = issue_s(j + 2, j + 3 == jobs);
+                }
+                if (!ok) break;
+                if (ptx::elect_one()) ptx::umma_commit(sy.bar(L::B_O_FULL));
+                __syncwarp();
+                g0 += x.tiles;
             }
-            p_par[slot] ^= 1u;
-            return true;
-        };
-        for (; ok && x.next(k); ++seg) {
-            const int jobs = SPLIT_ROWS ? 2 * x.tiles : x.tiles;
-            if (!(ok = sy.wait(L::B_Q_FULL, (uint32_t)(seg & 1), kSiteQFull))) break;
-            ptx::tc_fence_after();
-            ok = issue_s(0, jobs == 1);
-            if (ok && jobs > 1) ok = issue_s(1, jobs == 2);
-            for (int j = 0; ok && j < jobs; ++j) {
-                ok = issue_pv(j);
-                if (ok && j + 2 < jobs) ok = issue_s(j + 2, j + 3 == jobs);
-            }
-            if (!ok) break;
-            if (ptx::elect_one()) ptx::umma_commit(sy.bar(L::B_O_FULL));
+            if (ptx::elect_one()) ptx::umma_commit(sy.bar(L::B_DRAIN));
             __syncwarp();
-            g0 += x.tiles;
-        }
-        if (ptx::elect_one()) ptx::umma_commit(sy.bar(L::B_DRAIN));
-        __syncwarp();
-        sy.drain(L::B_DRAIN, 0);
-    } else {
-        // --------------------------------------------------------- Q copier
-        // (warps 2 and 3) a unit's rows r = g * tokens + j, zeros past the
-        // last, as soon as the unit before needs Q no more: its last softmax
-        // and its output hide the copy
-        Walk x = first;
-        for (int seg = 0; x.next(k); ++seg) {
-            if (seg > 0) {
-                if (!sy.wait(L::B_Q_FREE, (uint32_t)((seg - 1) & 1), kSiteQFull)) break;
-                copy_q(x.u);
+            sy.drain(L::B_DRAIN, 0);
+        } else {
+            // --------------------------------------------------------- Q copier
+            // (warps 2 and 3) a unit's rows r = g * tokens + j, zeros past the
+            // last, as soon as the unit before needs Q no more: its last softmax
+            // and its output hide the copy
+            Walk x = first;
+            for (int seg = 0; x.next(k); ++seg) {
+                if (seg > 0) {
+                    if (!sy.wait(L::B_Q_FREE, (uint32_t)((seg - 1) & 1), kSiteQFull)) break;
+                    copy_q(x.u);
+                }
+                ptx::cp_async_wait();
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(sy.bar(L::B_Q_FULL));
             }
-            ptx::cp_async_wait();
-            ptx::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(sy.bar(L::B_Q_FULL));
         }
-    }
     } else {
         // ------------------------------------------------ softmax / epilogue
         ptx::regs_inc<kRegsSoftmax>();
@@ -495,10 +495,10 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         uint32_t s_par = 0, sync_par = 0;
         bool ok = true;
         // barrier of the softmax warps (a bounded mbarrier wait: a warp that
-        // gave up cannot leave the others blocked)
-        // (relaxed: orders no memory access.  An arrive with release semantics
-        // first waits for the warp's global stores: after the partials' stores
-        // that took 8 us while HBM was saturated)
+        // gave up cannot leave the others blocked).  relaxed: it orders no
+        // memory access.  An arrive with release semantics first waits for the
+        // warp's global stores, 8 us behind the partials' stores while HBM was
+        // saturated.
         auto sync_sm = [&](bool relaxed) -> bool {
             __syncwarp();
             if (lane == 0) {
