@@ -140,6 +140,11 @@ template <int N> __device__ __forceinline__ void regs_inc() {
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint32_t have) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(have) : "memory");
 }
+// Closes a group of this thread's copies; waits until at most N groups are open.
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_async_wait_group() {
+    asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory");
+}
 // This thread's copies are done.
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 

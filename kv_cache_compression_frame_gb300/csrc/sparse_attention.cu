@@ -17,23 +17,24 @@
 //  2. after a cluster barrier every CTA selects for itself (radix select on the
 //     ordered scores, 11 + 11 + 10 bits; ties by index in the compaction), so
 //     no result has to travel;
-//  3. the halves of the chosen blocks and the tail's pieces go to the C * 8
-//     warps in turn.  A warp attends over 32 rows on its own: K and V come
-//     from global memory straight into matrix fragments (the order of d inside
-//     a product is free, so each lane's 16-byte loads are its fragments), the
-//     G <= 16 query rows are the 16 rows of m16n8k16, (m, l, O) stay in
+//  3. the quarters of the chosen blocks and the tail's pieces go to the C * 8
+//     warps in turn.  A warp attends over 16 rows on its own, while the next 32
+//     are copied into its ring in shared memory; a lane's 16-byte loads are
+//     matrix fragments as they are (the order of d inside a product is free),
+//     the G <= 16 query rows are the 16 rows of m16n8k16, (m, l, O) stay in
 //     registers;
 //  4. the warps merge in shared memory and store each part of the result in
 //     the CTA that writes it (distributed shared memory), which merges the CTAs.
 // m16n8k16 and not tcgen05: with at most 16 query rows a 128-row product would
-// waste 7/8 of the tensor core, and the data would have to pass through shared
-// memory first.
+// waste 7/8 of the tensor core; it is busy for less than a fifth of the time.
 // Scores, softmax statistics and O are fp32; P is rounded to bf16 for the
 // product, l sums the unrounded P.
 // Measured, 64 blocks a token: one token in one layer of 2 KV heads over 131072
-// rows 15.0 us (initial loads 2.5, scores and exchange 1.7, selection 3,
-// attention 4.3, merges 2); 16 ragged streams x 8 KV heads x 3 tokens, 0.82 GB,
-// 147 us = 5.6 TB/s.
+// rows 14.7 us (initial loads 2.5, scores and exchange 1.7, selection 3,
+// attention 4, merges 2); 16 ragged streams x 8 KV heads x 3 tokens, 0.82 GB of
+// blocks counted per token, 114.5 us.  The rings are what counts there: with
+// rows of 32 straight from global memory into registers, which leave no room
+// for a second entry in flight, it was 147.
 #include <algorithm>
 
 #include "views.cuh"
@@ -47,13 +48,14 @@ constexpr int kSparseWarps = kSparseThreads / 32;
 constexpr int kMaxTop = 1024;
 constexpr int kMaxBlocks = 32768;
 constexpr int kBins = 2048;
-constexpr int kRows = 32;                // cache rows per entry of the attention
+constexpr int kRows = 16;                // cache rows per entry of the attention
+constexpr int kStages = 3;               // entries of a warp in shared memory
 
 struct SparseKernelArgs {
     statekv_sparse_args a;
     float scale_log2;
     int32_t G, cluster;
-    int32_t region;                  // bytes of shared memory used first for scores, then for partials
+    int32_t region;                  // bytes of shared memory used for the selection, the rows, the partials
 };
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -115,16 +117,17 @@ __global__ void __launch_bounds__(kSparseThreads, 1) sparse_kernel(const __grid_
     const statekv_sparse_args& a = ka.a;
     const int G = ka.G, C = ka.cluster;
     extern __shared__ __align__(16) uint8_t smem[];
-    // region: scores [blocks] + bins, later the warps' O [8][G][D]
-    uint32_t* s_key = reinterpret_cast<uint32_t*>(smem);
+    // region, one after the other: bins and scores; the warps' rows of K and V
+    // [8][kStages][2][kRows][D]; the warps' O [8][G][D]
+    uint32_t* s_bins = reinterpret_cast<uint32_t*>(smem);               // [2][kBins]
+    uint32_t* s_key = s_bins + 2 * kBins;                               // [blocks]
     float* s_o = reinterpret_cast<float*>(smem);
     uint8_t* fixed = smem + ka.region;
     float* s_part = reinterpret_cast<float*>(fixed);                    // [C][slice] the CTAs' O of this CTA's slice
     float2* s_pml = reinterpret_cast<float2*>(s_part + 16 * D + 64);    // [16][16] the CTAs' (m, l)
     float2* s_wml = s_pml + 16 * 16;                                    // [8][16] the warps' (m, l)
     int* s_list = reinterpret_cast<int*>(s_wml + kSparseWarps * 16);    // [kMaxTop]
-    uint32_t* s_bins = reinterpret_cast<uint32_t*>(s_list + kMaxTop);   // [2][kBins]
-    int8_t* s_q = reinterpret_cast<int8_t*>(s_bins + 2 * kBins);        // [16][D] query codes
+    int8_t* s_q = reinterpret_cast<int8_t*>(s_list + kMaxTop);          // [16][D] query codes
     uint32_t* s_scan = reinterpret_cast<uint32_t*>(s_q + 16 * D);       // [2][8]
     uint32_t* s_pick = s_scan + 2 * kSparseWarps;                       // [2][3] digit, keys above it, keys of it
 
@@ -276,7 +279,7 @@ __global__ void __launch_bounds__(kSparseThreads, 1) sparse_kernel(const __grid_
         for (int i = tid; i < a.top; i += kSparseThreads)
             a.selected[item * a.top + i] = i >= nsel || row < 0 ? -1 : choose ? s_list[i] : i;
 
-    // ---- attention over entries of 32 rows: two of every block, then the tail's
+    // ---- attention over entries of 16 rows: four of every block, then the tail's
     const int quad = lane & 3, g8 = lane >> 2;
     uint32_t qf[D / 16][4];
     {
@@ -293,84 +296,80 @@ __global__ void __launch_bounds__(kSparseThreads, 1) sparse_kernel(const __grid_
     float o[DJ][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < DJ; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-    const __nv_bfloat16* kb = static_cast<const __nv_bfloat16*>(a.k_cache.data) + n * a.k_cache.batch_stride +
-                              h * a.k_cache.head_stride + quad * 8;
-    const __nv_bfloat16* vb = static_cast<const __nv_bfloat16*>(a.v_cache.data) + n * a.v_cache.batch_stride +
-                              h * a.v_cache.head_stride + g8 * DJ;
     const int tail = row - nb * STATEKV_BLOCK + 1;           // rows since the last complete block
-    const int halves = 2 * nsel, entries = row < 0 ? 0 : halves + (max(tail, 0) + kRows - 1) / kRows;
-    // first row of entry e
-    auto row_of = [&](int e) -> int {
-        return e < halves ? STATEKV_BLOCK * (choose ? s_list[e >> 1] : e >> 1) + kRows * (e & 1)
-                          : STATEKV_BLOCK * nb + kRows * (e - halves);
+    constexpr int PER_BLOCK = STATEKV_BLOCK / kRows;
+    const int of_blocks = PER_BLOCK * nsel, entries = row < 0 ? 0 : of_blocks + (max(tail, 0) + kRows - 1) / kRows;
+    auto row_of = [&](int e) -> int {                        // first row of entry e
+        return e < of_blocks
+                   ? STATEKV_BLOCK * (choose ? s_list[e / PER_BLOCK] : e / PER_BLOCK) + kRows * (e % PER_BLOCK)
+                   : STATEKV_BLOCK * nb + kRows * (e - of_blocks);
     };
-    // a warp's entries one after the other: the next one's keys are loaded
-    // while this one's probabilities are computed, its values while the next
-    // scores are
-    uint4 kf[kRows / 8][KI], vf[kRows / 16][4][DJ / 8];
-    auto load_k = [&](int r0) {
-        const int last = min(kRows, row + 1 - r0) - 1;       // rows past the token's own may not exist
-#pragma unroll
-        for (int t = 0; t < kRows / 8; ++t) {
-            const __nv_bfloat16* p = kb + (int64_t)(r0 + min(8 * t + g8, last)) * a.k_cache.token_stride;
-#pragma unroll
-            for (int i = 0; i < KI; ++i) kf[t][i] = *reinterpret_cast<const uint4*>(p + i * 32);
-        }
+    // Each warp has a ring of its own.  Its rows are copied asynchronously in
+    // 16-byte units; a unit's place in its row is XOR-ed with bits of the row,
+    // so that the 8 lanes of a quarter warp, which read units of 2 rows of K or
+    // of 4 rows of V, meet no bank twice.
+    constexpr int UPR = D / 8, TILE = kRows * D * 2;         // units of a row, bytes of K or V of an entry
+    auto k_unit = [](int r, int u) { return u ^ ((r & 1) << 2); };
+    auto v_unit = [](int r, int u) {
+        const int y = (r >> 1) & 3;
+        return u ^ (D == 128 ? (y & 1) | (y >> 1 << 2) : y << 1);
     };
-    auto load_v = [&](int r0) {
-        const int last = min(kRows, row + 1 - r0) - 1;
-        // of keys 16 ks + {2 quad, 2 quad + 1} and 8 further, columns g8 * DJ ..
+    uint8_t* ring = smem + warp * (kStages * 2 * TILE);
+    const uint32_t ring_u32 = ptx::smem_u32(ring);
+    const __nv_bfloat16* kb = static_cast<const __nv_bfloat16*>(a.k_cache.data) + n * a.k_cache.batch_stride +
+                              h * a.k_cache.head_stride + lane % UPR * 8;
+    const __nv_bfloat16* vb = static_cast<const __nv_bfloat16*>(a.v_cache.data) + n * a.v_cache.batch_stride +
+                              h * a.v_cache.head_stride + lane % UPR * 8;
+    auto copy = [&](int e, int stage) {
+        if (e < entries) {
+            const int r0 = row_of(e), valid = row + 1 - r0;  // rows past the token's own may not exist: zeros
+            const uint32_t at = ring_u32 + stage * 2 * TILE;
 #pragma unroll
-        for (int ks = 0; ks < kRows / 16; ++ks)
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                const int key = 16 * ks + 2 * quad + (y & 1) + 8 * (y >> 1);
-                const __nv_bfloat16* p = vb + (int64_t)(r0 + min(key, last)) * a.v_cache.token_stride;
-#pragma unroll
-                for (int i = 0; i < DJ / 8; ++i) {
-                    vf[ks][y][i] = *reinterpret_cast<const uint4*>(p + 8 * i);
-                    if (key > last) vf[ks][y][i] = make_uint4(0, 0, 0, 0);
-                }
+            for (int i = 0; i < kRows * UPR / 32; ++i) {
+                const int r = (i * 32 + lane) / UPR, u = lane % UPR;
+                const int64_t src = r0 + min(r, valid - 1);
+                const uint32_t have = r < valid ? 16u : 0u;
+                ptx::cp_async_16(at + r * (D * 2) + 16 * k_unit(r, u), kb + src * a.k_cache.token_stride, have);
+                ptx::cp_async_16(at + TILE + r * (D * 2) + 16 * v_unit(r, u), vb + src * a.v_cache.token_stride, have);
             }
+        }
+        ptx::cp_async_commit();                              // (one group per entry, empty ones too)
     };
-    int e = warp * C + rank, r0 = 0;
-    if (e < entries) {
-        r0 = row_of(e);
-        load_k(r0);
-        load_v(r0);
-    }
-    while (e < entries) {
-        const int valid = row + 1 - r0;                      // at least kRows but in the tail
-        float s[kRows / 8][4];
+    const int step = kSparseWarps * C;
+    int e = warp * C + rank, stage = 0;
 #pragma unroll
-        for (int t = 0; t < kRows / 8; ++t) {
+    for (int i = 0; i < kStages - 1; ++i) copy(e + i * step, i);
+    for (; e < entries; e += step) {
+        ptx::cp_async_wait_group<kStages - 2>();
+        __syncwarp();                                        // every lane's copies; the stage before this one is read
+        copy(e + (kStages - 1) * step, stage == 0 ? kStages - 1 : stage - 1);
+        const uint8_t* kt = ring + stage * 2 * TILE;
+        const uint8_t* vt = kt + TILE;
+        stage = stage == kStages - 1 ? 0 : stage + 1;
+        const int valid = row + 1 - row_of(e);               // at least kRows but in the tail
+        float s[2][4];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
             s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+            const int r = 8 * t + g8;
 #pragma unroll
             for (int i = 0; i < KI; ++i) {
-                mma16816(s[t], qf[2 * i], kf[t][i].x, kf[t][i].y);
-                mma16816(s[t], qf[2 * i + 1], kf[t][i].z, kf[t][i].w);
+                const uint4 kf = *reinterpret_cast<const uint4*>(kt + r * (D * 2) + 16 * k_unit(r, 4 * i + quad));
+                mma16816(s[t], qf[2 * i], kf.x, kf.y);
+                mma16816(s[t], qf[2 * i + 1], kf.z, kf.w);
             }
-        }
-        e += kSparseWarps * C;
-        if (e < entries) {
-            r0 = row_of(e);
-            load_k(r0);
         }
         if (valid < kRows) {
 #pragma unroll
-            for (int t = 0; t < kRows / 8; ++t)
+            for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
                     if (8 * t + 2 * quad + (x & 1) >= valid) s[t][x] = -INFINITY;
         }
-        float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-        for (int t = 0; t < kRows / 8; ++t) {
-            top[0] = ptx::max3(top[0], s[t][0], s[t][1]);
-            top[1] = ptx::max3(top[1], s[t][2], s[t][3]);
-        }
+        float top[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
+            top[x] = fmaxf(fmaxf(s[0][2 * x], s[0][2 * x + 1]), fmaxf(s[1][2 * x], s[1][2 * x + 1]));
             top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 1));
             top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 2));
             top[x] = fmaxf(m[x], top[x] * ka.scale_log2);
@@ -389,39 +388,39 @@ __global__ void __launch_bounds__(kSparseThreads, 1) sparse_kernel(const __grid_
             }
         }
         const float nm0 = m[0] == -INFINITY ? 0.f : -m[0], nm1 = m[1] == -INFINITY ? 0.f : -m[1];
+        uint32_t p[4];
 #pragma unroll
-        for (int ks = 0; ks < kRows / 16; ++ks) {
-            uint32_t p[4];
+        for (int t = 0; t < 2; ++t) {
+            const float p0 = ptx::ex2_approx(fmaf(s[t][0], ka.scale_log2, nm0));
+            const float p1 = ptx::ex2_approx(fmaf(s[t][1], ka.scale_log2, nm0));
+            const float p2 = ptx::ex2_approx(fmaf(s[t][2], ka.scale_log2, nm1));
+            const float p3 = ptx::ex2_approx(fmaf(s[t][3], ka.scale_log2, nm1));
+            l[0] += p0 + p1;
+            l[1] += p2 + p3;
+            p[2 * t] = ptx::pack_bf16x2(p0, p1);
+            p[2 * t + 1] = ptx::pack_bf16x2(p2, p3);
+        }
+        // V of keys {2 quad, 2 quad + 1} and 8 further, columns g8 * DJ ..
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const float* x = s[2 * ks + t];
-                const float p0 = ptx::ex2_approx(fmaf(x[0], ka.scale_log2, nm0));
-                const float p1 = ptx::ex2_approx(fmaf(x[1], ka.scale_log2, nm0));
-                const float p2 = ptx::ex2_approx(fmaf(x[2], ka.scale_log2, nm1));
-                const float p3 = ptx::ex2_approx(fmaf(x[3], ka.scale_log2, nm1));
-                l[0] += p0 + p1;
-                l[1] += p2 + p3;
-                p[2 * t] = ptx::pack_bf16x2(p0, p1);
-                p[2 * t + 1] = ptx::pack_bf16x2(p2, p3);
+        for (int i = 0; i < DJ / 8; ++i) {
+            uint32_t v[4][4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const int r = 2 * quad + (y & 1) + 8 * (y >> 1);
+                const uint4 x = *reinterpret_cast<const uint4*>(vt + r * (D * 2) + 16 * v_unit(r, g8 * (DJ / 8) + i));
+                v[y][0] = x.x; v[y][1] = x.y; v[y][2] = x.z; v[y][3] = x.w;
             }
-            const uint4 (&v)[4][DJ / 8] = vf[ks];
 #pragma unroll
-            for (int i = 0; i < DJ / 8; ++i) {
-                const uint32_t k0[4] = {v[0][i].x, v[0][i].y, v[0][i].z, v[0][i].w};
-                const uint32_t k1[4] = {v[1][i].x, v[1][i].y, v[1][i].z, v[1][i].w};
-                const uint32_t k2[4] = {v[2][i].x, v[2][i].y, v[2][i].z, v[2][i].w};
-                const uint32_t k3[4] = {v[3][i].x, v[3][i].y, v[3][i].z, v[3][i].w};
-#pragma unroll
-                for (int wd = 0; wd < 4; ++wd) {
-                    mma16816(o[8 * i + 2 * wd], p, __byte_perm(k0[wd], k1[wd], 0x5410),
-                             __byte_perm(k2[wd], k3[wd], 0x5410));
-                    mma16816(o[8 * i + 2 * wd + 1], p, __byte_perm(k0[wd], k1[wd], 0x7632),
-                             __byte_perm(k2[wd], k3[wd], 0x7632));
-                }
+            for (int wd = 0; wd < 4; ++wd) {
+                mma16816(o[8 * i + 2 * wd], p, __byte_perm(v[0][wd], v[1][wd], 0x5410),
+                         __byte_perm(v[2][wd], v[3][wd], 0x5410));
+                mma16816(o[8 * i + 2 * wd + 1], p, __byte_perm(v[0][wd], v[1][wd], 0x7632),
+                         __byte_perm(v[2][wd], v[3][wd], 0x7632));
             }
         }
-        if (e < entries) load_v(r0);
     }
+    ptx::cp_async_wait_group<0>();
+    __syncthreads();                                         // the rings become the warps' partials
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
         l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
@@ -516,7 +515,7 @@ cudaLaunchConfig_t config(int64_t items, int cluster, size_t smem, cudaStream_t 
 }
 
 // Clusters of 16 CTAs (more than the portable 8) that device dev holds at
-// once, one CTA per SM; cached, -1 before the first query.
+// once, one CTA per SM; asked for once.
 template <int D>
 int clusters_of_16(int dev) {
     static std::atomic<int> cache[64];
@@ -525,7 +524,7 @@ int clusters_of_16(int dev) {
     if (known.load(std::memory_order_acquire) >> dev & 1ull) return cache[dev].load(std::memory_order_relaxed);
     int n = 0;
     cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t cfg = config<D>(1, 16, 64 * 1024, nullptr, attr);
+    const cudaLaunchConfig_t cfg = config<D>(1, 16, 227 * 1024, nullptr, attr);
     const void* f = reinterpret_cast<const void*>(&sparse_kernel<D>);
     if (cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
         cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess ||
@@ -553,7 +552,7 @@ template <int D>
 cudaError_t launch(SparseKernelArgs& ka, int64_t items, int dev, int sms, cudaStream_t st) {
     ka.cluster = cluster_for<D>(items, sms, dev);
     const size_t smem = ka.region + (16 * D + 64) * 4 + 16 * 16 * 8 + kSparseWarps * 16 * 8 + kMaxTop * 4 +
-                        2 * kBins * 4 + 16 * D + (2 * kSparseWarps + 6) * 4;
+                        16 * D + (2 * kSparseWarps + 6) * 4;
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = allow_smem(reinterpret_cast<const void*>(&sparse_kernel<D>), 227 * 1024, dev, done);
     if (e != cudaSuccess) return e;
@@ -594,7 +593,9 @@ extern "C" int statekv_sparse_attention(const statekv_sparse_args* args, void* c
     k.a = a;
     k.G = a.q_heads / a.kv_heads;
     k.scale_log2 = (float)(a.scale * 1.4426950408889634074);
-    k.region = (std::max(most > a.top ? most * 4 : 0, kSparseWarps * k.G * a.head_dim * 4) + 15) / 16 * 16;
+    const int select = most > a.top ? 2 * kBins * 4 + (most * 4 + 15) / 16 * 16 : 0;
+    const int rings = kSparseWarps * kStages * 2 * kRows * a.head_dim * 2;
+    k.region = std::max({select, rings, kSparseWarps * k.G * a.head_dim * 4});
     cudaStream_t st = reinterpret_cast<cudaStream_t>(cuda_stream);
     const cudaError_t e = a.head_dim == 128 ? launch<128>(k, items, dev, sms, st) : launch<64>(k, items, dev, sms, st);
     return e == cudaSuccess ? STATEKV_OK : view_cuda_fail();
