@@ -440,12 +440,14 @@ int statekv_attend_scores_static(const void* q_rot, const void* pool_k,
  * run the same kernels over D.
  *
  * Tensors are views [batch][heads][tokens][head_dim] of DEVICE memory on the
- * current device: the last dimension contiguous, the other strides free (in
- * elements), every row on a 16-byte boundary.  The batch is sequences x
- * layers: batch entry n belongs to sequence n / layers, and lengths, trees,
- * paths and destination rows have one entry per sequence.  Query head j uses
- * KV head j / (q_heads / kv_heads).  Outputs must not overlap inputs unless
- * said otherwise.
+ * current device: the last dimension contiguous, the other strides (in
+ * elements) free but not negative, every row on a 16-byte boundary.  An input
+ * may repeat its entries (stride 0), but for the keys and values of
+ * statekv_tree_attention, which are read in tiles; an output may not
+ * (E_INVALID_ARG).  The batch is sequences x layers: batch entry n belongs to sequence
+ * n / layers, and lengths, trees, paths and destination rows have one entry
+ * per sequence.  Query head j uses KV head j / (q_heads / kv_heads).  Outputs
+ * must not overlap inputs unless said otherwise.
  *
  * `lengths` (int32, device) gives each sequence's rows in the cache; where it
  * is NULL every sequence has `length` rows.  A length, count, row or node out

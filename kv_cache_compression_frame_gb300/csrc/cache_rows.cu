@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
 // their way while eight are summed, across blocks too: 131072 rows of 8 heads,
 // 270 MB, in 50 us = 5.4 TB/s (62 us with a warp per block and no overlap).
 constexpr int kSumThreads = 128;
-constexpr int kSumCtas = 5;                                  // per SM: 102 registers a thread, 64 of them keys in flight
+constexpr int kSumCtas = 5;                                  // per SM: 96 registers a thread, 64 of them keys in flight
 
 // a - b (a fused multiply-add by -1 is exact in the product; there is no
 // packed subtraction, and negating takes an instruction per half)
@@ -188,7 +188,8 @@ cudaError_t launch_summary(const statekv_summary_args& a, cudaStream_t st) {
     // one wave of CTAs, each warp walking the blocks
     int dev = 0, sms = 0;
     if (!current_device(&dev, &sms)) return cudaErrorInvalidDevice;
-    const int64_t grid = std::min<int64_t>((items + kSumThreads / 32 - 1) / (kSumThreads / 32), (int64_t)sms * kSumCtas);
+    const int64_t grid =
+        std::min<int64_t>((items + kSumThreads / 32 - 1) / (kSumThreads / 32), (int64_t)sms * kSumCtas);
     if (a.head_dim == 128) summary_kernel<128><<<(unsigned)grid, kSumThreads, 0, st>>>(a, window);
     else summary_kernel<64><<<(unsigned)grid, kSumThreads, 0, st>>>(a, window);
     return cudaGetLastError();
@@ -210,7 +211,10 @@ extern "C" int statekv_append_accepted(const statekv_append_args* args, void* cu
     if (!a.status || reinterpret_cast<uintptr_t>(a.status) % 4) return STATEKV_E_INVALID_ARG;
     if (a.batch == 0) return STATEKV_OK;
     if (a.path_len > 0 && (!a.path || !view_ok(a.k_new, es) || !view_ok(a.v_new, es))) return STATEKV_E_INVALID_ARG;
-    if (a.cache_rows > 0 && (!view_ok(a.k_cache, es) || !view_ok(a.v_cache, es))) return STATEKV_E_INVALID_ARG;
+    if (a.cache_rows > 0 && (!view_ok(a.k_cache, es) || !view_ok(a.v_cache, es) ||
+                             !spread(a.k_cache, a.batch, a.kv_heads, a.cache_rows) ||
+                             !spread(a.v_cache, a.batch, a.kv_heads, a.cache_rows)))
+        return STATEKV_E_INVALID_ARG;
     // the sequence's length is read by every head's CTA while one writes the new one
     if (a.new_lengths && (a.new_lengths == a.lengths || a.new_lengths == a.counts)) return STATEKV_E_INVALID_ARG;
     if (!a.lengths && !a.counts && (int64_t)a.length + a.path_len > a.cache_rows) return STATEKV_E_CAPACITY;

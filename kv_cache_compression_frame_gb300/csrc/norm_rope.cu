@@ -124,7 +124,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_rope_kernel(const __grid
         const void* w = i < D ? a.q_weight : a.k_weight;
         const int k = i % D;
         if (w)
-            s_w[i / D][k / HALF][table_at<VEC, HALF>(k % HALF)] = weight_at(w, a.weight_dtype, n % a.weight_rows * D + k);
+            s_w[i / D][k / HALF][table_at<VEC, HALF>(k % HALF)] =
+                weight_at(w, a.weight_dtype, n % a.weight_rows * D + k);
     }
     const int row0 = a.out_rows ? a.out_rows[seq] : 0;
     const bool fits = row0 >= 0 && row0 <= a.out_capacity - a.tokens;
@@ -230,7 +231,8 @@ extern "C" int statekv_norm_rope(const statekv_norm_rope_args* args, void* cuda_
     if (a.dtype != STATEKV_BF16 && a.dtype != STATEKV_F32) return STATEKV_E_INVALID_ARG;
     if (a.weight_dtype != STATEKV_BF16 && a.weight_dtype != STATEKV_F32) return STATEKV_E_INVALID_ARG;
     if (a.batch < 0 || a.layers < 1 || a.batch % a.layers != 0 || a.tokens < 0 || a.q_heads < 0 ||
-        a.kv_heads < 0 || a.position_stride < 0 || a.position_layers < 1 || a.weight_rows < 1 || a.out_capacity < 0 || !(a.eps >= 0.f))
+        a.kv_heads < 0 || a.position_stride < 0 || a.position_layers < 1 || a.weight_rows < 1 || a.out_capacity < 0 ||
+        !(a.eps >= 0.f))
         return STATEKV_E_INVALID_ARG;
     if (a.head_dim != 64 && a.head_dim != 128) return STATEKV_E_UNSUPPORTED;
     if (!a.status || reinterpret_cast<uintptr_t>(a.status) % 4 || !a.omega ||
@@ -239,11 +241,16 @@ extern "C" int statekv_norm_rope(const statekv_norm_rope_args* args, void* cuda_
     for (const void* w : {a.q_weight, a.k_weight})
         if (w && !aligned16(w)) return STATEKV_E_INVALID_ARG;
     const int es = a.dtype == STATEKV_BF16 ? 2 : 4;
-    if (a.q_heads > 0 && (!view_ok(a.q, es) || !view_ok(a.q_out, es))) return STATEKV_E_INVALID_ARG;
+    if (a.q_heads > 0 &&
+        (!view_ok(a.q, es) || !view_ok(a.q_out, es) || !spread(a.q_out, a.batch, a.q_heads, a.tokens)))
+        return STATEKV_E_INVALID_ARG;
     if (a.kv_heads > 0) {
-        if (!view_ok(a.k, es) || !view_ok(a.k_out, es)) return STATEKV_E_INVALID_ARG;
+        if (!view_ok(a.k, es) || !view_ok(a.k_out, es) || !spread(a.k_out, a.batch, a.kv_heads, a.out_capacity))
+            return STATEKV_E_INVALID_ARG;
         if ((a.v.data != nullptr) != (a.v_out.data != nullptr)) return STATEKV_E_INVALID_ARG;
-        if (a.v.data && (!view_ok(a.v, es) || !view_ok(a.v_out, es))) return STATEKV_E_INVALID_ARG;
+        if (a.v.data && (!view_ok(a.v, es) || !view_ok(a.v_out, es) ||
+                         !spread(a.v_out, a.batch, a.kv_heads, a.out_capacity)))
+            return STATEKV_E_INVALID_ARG;
         if (!a.out_rows && a.out_capacity < a.tokens) return STATEKV_E_CAPACITY;
     } else if (a.v.data || a.v_out.data) {
         return STATEKV_E_INVALID_ARG;

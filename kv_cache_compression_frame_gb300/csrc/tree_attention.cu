@@ -680,7 +680,8 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                 l = x0.y * f0 + (use1 ? x1.y * f1 : 0.f);
                 t_o0 = tmem + L::TM_O + lane_base + c0;
             }
-            const uint64_t odd = live ? *reinterpret_cast<volatile unsigned long long*>(odd_nodes + (seg & 1)) & sees : 0ull;
+            const uint64_t odd =
+                live ? *reinterpret_cast<volatile unsigned long long*>(odd_nodes + (seg & 1)) & sees : 0ull;
             const int64_t sgm = (int64_t)c + cu.u;               // segment number
             const float inv = whole ? (l > 0.f || l != l ? 1.f / l : 0.f) : 1.f;
             if (!idle) {
@@ -827,7 +828,8 @@ __global__ void __launch_bounds__(kMergeThreads) tree_combine_kernel(const __gri
             __syncthreads();
             if (way != 0) continue;
 #pragma unroll 1
-            for (int i = 1; i < kWays; ++i) acc.add(sh[i * per_step + x].m, sh[i * per_step + x].l, sh[i * per_step + x].o);
+            for (int i = 1; i < kWays; ++i)
+                acc.add(sh[i * per_step + x].m, sh[i * per_step + x].l, sh[i * per_step + x].o);
         }
         if (!live) continue;
         const float inv = acc.l > 0.f || acc.l != acc.l ? 1.f / acc.l : 0.f;
@@ -904,11 +906,6 @@ int64_t workspace_for(const TreeSizes& z, int sms, int d) {
     return ((int64_t)sms + z.units) * z.rows * (d * 4 + 8);
 }
 
-// A dimension of several entries that share their memory has no TMA view.
-bool spread(const statekv_view& v, int64_t batch, int64_t heads, int64_t rows) {
-    return (batch < 2 || v.batch_stride > 0) && (heads < 2 || v.head_stride > 0) && (rows < 2 || v.token_stride > 0);
-}
-
 }  // namespace
 }  // namespace statekv
 
@@ -945,7 +942,9 @@ extern "C" int statekv_tree_attention(const statekv_tree_args* args, void* cuda_
     // an empty cache needs no memory: its maps are never read
     const bool cached = a.cache_rows > 0;
     if (cached && (!view_ok(a.k_cache, 2) || !view_ok(a.v_cache, 2))) return STATEKV_E_INVALID_ARG;
-    if (!spread(a.k_new, a.batch, a.kv_heads, a.tokens) || !spread(a.v_new, a.batch, a.kv_heads, a.tokens) ||
+    // entries that share their memory have no TMA view
+    if (!spread(a.out, a.batch, a.q_heads, a.tokens) || !spread(a.k_new, a.batch, a.kv_heads, a.tokens) ||
+        !spread(a.v_new, a.batch, a.kv_heads, a.tokens) ||
         (cached && (!spread(a.k_cache, a.batch, a.kv_heads, a.cache_rows) ||
                     !spread(a.v_cache, a.batch, a.kv_heads, a.cache_rows))))
         return STATEKV_E_INVALID_ARG;
@@ -978,8 +977,9 @@ extern "C" int statekv_tree_attention(const statekv_tree_args* args, void* cuda_
     k.part_ml = reinterpret_cast<float2*>(k.part_o + segments * z.rows * a.head_dim);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(cuda_stream);
     const bool two = z.R > kTile;
-    cudaError_t e = a.head_dim == 128 ? (two ? launch_main<128, true>(k, m, dev, st) : launch_main<128, false>(k, m, dev, st))
-                                      : (two ? launch_main<64, true>(k, m, dev, st) : launch_main<64, false>(k, m, dev, st));
+    cudaError_t e = a.head_dim == 128 ? two ? launch_main<128, true>(k, m, dev, st) : launch_main<128, false>(k, m, dev, st)
+                    : two             ? launch_main<64, true>(k, m, dev, st)
+                                      : launch_main<64, false>(k, m, dev, st);
     // one CTA holds whole units only
     if (e == cudaSuccess && !k.whole && k.grid > 1)
         e = a.head_dim == 128 ? launch_combine<128>(k, z.units, sms, st) : launch_combine<64>(k, z.units, sms, st);

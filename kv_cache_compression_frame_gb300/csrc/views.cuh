@@ -43,6 +43,11 @@ inline bool view_ok(const statekv_view& v, int esize) {
     return true;
 }
 
+// No entries of the view share their memory: what an output needs.
+inline bool spread(const statekv_view& v, int64_t batch, int64_t heads, int64_t rows) {
+    return (batch < 2 || v.batch_stride > 0) && (heads < 2 || v.head_stride > 0) && (rows < 2 || v.token_stride > 0);
+}
+
 #ifdef __CUDACC__
 // Rows of sequence s, from the array or the common value.  A negative length
 // or one past `most` is recorded and clamped, so that every access that

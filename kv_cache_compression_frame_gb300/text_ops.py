@@ -3,13 +3,15 @@
 Thin marshalling over the handle-free entry points of include/statekv.h, which
 states the mathematics, limits and errors of each.  Tensors are CUDA tensors
 [batch][heads][tokens][head_dim] of any strides with a contiguous last
-dimension and rows on 16-byte boundaries; the batch is sequences x layers, and
+dimension and rows on 16-byte boundaries (expanded ones are inputs only, and
+not tree attention's keys and values); the batch is sequences x layers, and
 lengths, trees, paths and destination rows have one entry per sequence.
 
 Work is enqueued on `stream` (default: the current stream of the tensors'
 device).  Outputs and workspaces that are not passed in are allocated there.
 Failures that only the device can see (a length out of range, a wait that gave
-up) are kept in one status word per device, which check_status() reads.
+up) are kept in one status word per device, which check_status() reads; a
+device's first call allocates it and must not be inside a graph capture.
 There is no backward pass: inputs that require grad are refused while grad
 mode is on.
 """

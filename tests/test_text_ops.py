@@ -852,6 +852,55 @@ def test_packed_arguments_are_the_structures(pack, args):
     assert pack.size == C.sizeof(args) and pack.pack(*flat) == bytes(a)
 
 
+@pytest.mark.parametrize("where", [dict(b=0), dict(h=0), dict(t=0)])
+def test_outputs_that_share_memory_are_refused(where):
+    """Entries of an output that lie on one another, where there are several."""
+    lib, bad = N.load(), view(**where)
+    ins = {f: view() for f in ("q", "k", "v", "k_new", "v_new", "k_cache", "v_cache")}
+    sizes = dict(batch=2, layers=1, q_heads=4, kv_heads=2, tokens=3, head_dim=128, status=16)
+    of = lambda args, **kw: args(**{f: x for f, x in {**ins, **sizes, **kw}.items()  # noqa: E731
+                                    if f in dict(args._fields_)})
+    for name in ("q_out", "k_out", "v_out"):
+        outs = {**{f: view() for f in ("q_out", "k_out", "v_out")}, name: bad}
+        a = of(N.NormRopeArgs, **outs, omega=16, position_layers=1, weight_rows=1, out_capacity=3, eps=1e-6)
+        assert lib.statekv_norm_rope(a, None) == N.E_INVALID_ARG, name
+    assert lib.statekv_tree_attention(tree_args(out=bad), None) == N.E_INVALID_ARG
+    for name in ("k_cache", "v_cache"):
+        a = of(N.AppendArgs, **{name: bad}, path=16, path_len=2, length=2, cache_rows=4)
+        assert lib.statekv_append_accepted(a, None) == N.E_INVALID_ARG, name
+    a = of(N.SparseArgs, out=bad, codes=16, scales=16, scale=0.1, length=256, top=2, blocks=4, cache_rows=256)
+    assert lib.statekv_sparse_attention(a, None) == N.E_INVALID_ARG
+
+
+@gpu
+def test_inputs_may_repeat_their_entries():
+    """Expanded inputs give what their copies give."""
+    g = gen(62)
+    q, k, v = (randn(g, 1, 1, 5, 64).expand(2, h, 5, 64) for h in (6, 2, 2))
+    om = omega_of(64)
+    for a, b in zip(kv.qk_norm_rope(q, k, 7, om, v=v),
+                    kv.qk_norm_rope(q.contiguous(), k.contiguous(), 7, om, v=v.contiguous())):
+        assert torch.equal(a, b)
+    path = torch.tensor([4, 1], dtype=torch.int32, device=DEV)
+    caches = [torch.zeros(2, 2, 9, 64, dtype=BF16, device=DEV) for _ in range(4)]
+    kv.append_accepted(k, v, path, None, *caches[:2], 3)
+    kv.append_accepted(k.contiguous(), v.contiguous(), path, None, *caches[2:], 3)
+    assert torch.equal(caches[0], caches[2]) and torch.equal(caches[1], caches[3])
+    cache = randn(g, 1, 1, 1000, 64).expand(2, 2, 1000, 64)
+    codes, scales = torch.zeros(2, 2, 15, 64, dtype=torch.int8, device=DEV), torch.zeros(2, 2, 15, device=DEV)
+    kv.block_summaries(cache, codes, scales, 1000)
+    assert torch.equal(codes, codes[:1, :1].expand_as(codes)) and scales.min() == scales[0, 0].min() > 0
+    got = kv.sparse_attention(q, cache, cache, codes, scales, 1000, 4, scale=0.1)
+    want = kv.sparse_attention(q.contiguous(), cache.contiguous(), cache.contiguous(), codes, scales, 1000, 4,
+                               scale=0.1)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    tree = random_tree(5, 1, 1)[0]
+    new = k.contiguous()
+    assert torch.equal(kv.tree_attention(q, new, new, tree, *caches[:2], 9, scale=0.1),
+                       kv.tree_attention(q.contiguous(), new, new, tree, *caches[:2], 9, scale=0.1))
+    kv.check_status()
+
+
 def test_null_arguments():
     lib = N.load()
     for f in ("norm_rope", "tree_attention", "append_accepted", "block_summaries", "sparse_attention"):
