@@ -177,7 +177,10 @@ cudaError_t launch_rope_table(const RopeTableArgs& a, cudaStream_t st) {
 // that attention has then ended, so Q' (read by it) may be rewritten at
 // once, and the pool rows the selection reads are written after
 // dep_wait().  Inputs q, k, v were written before the selection was queued
-// or by an operation between the two, which then orders them as usual.
+// or by an operation between the two, which then orders them as usual: any
+// kernel but the selection must leave the release of its dependents to its
+// end, as the last kernel of every other entry point does (a reader of Q' or
+// D that triggered early would have both rewritten under its loads).
 cudaError_t launch_rope(const RopeArgs& a, int dtype, cudaStream_t st, bool early) {
     int vec = dtype == STATEKV_BF16 ? 8 : 4;
     int64_t threads = (a.rows_q + 2 * a.rows_kv) * (a.d / 2 / vec);

@@ -76,6 +76,7 @@ struct TreeKernelArgs {
     uint32_t inv_tokens;                     // floor(2^32 / tokens) + 1
     int32_t grid;                            // CTAs of the main kernel
     int32_t whole;                           // a share is a unit: nothing to merge
+    int32_t merge;                           // tree_combine_kernel follows
 };
 
 // r / tokens for a query row r < 65536: the high word of r * (2^32 / tokens,
@@ -373,8 +374,11 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    // the merge may be launched now; it waits for this grid to end
-    ptx::dep_trigger();
+    // The merge, where there is one, may be launched now; it waits for this
+    // grid to end.  Otherwise the next kernel is not ours to release: it may
+    // be one that starts early and relies on this grid's end (launch_rope
+    // writes Q' and D rows at once), so it gets the implicit release there.
+    if (k.merge) ptx::dep_trigger();
     if (warp < 4) {
         ptx::regs_dec<kRegsIssue>();
         if (warp == 0) {
@@ -972,6 +976,7 @@ extern "C" int statekv_tree_attention(const statekv_tree_args* args, void* cuda_
     const int64_t cost = most_tiles(a.lengths ? a.cache_rows : a.length) + kUnitCost;
     if (z.units * cost > 0x7fffffff) return STATEKV_E_UNSUPPORTED;   // the schedule counts in 32 bits
     k.grid = whole ? (int)z.units : (int)std::min<int64_t>(sms, (z.units * cost + kMinShare - 1) / kMinShare);
+    k.merge = !whole && k.grid > 1;          // one CTA holds whole units only
     const int64_t segments = (int64_t)sms + z.units;
     k.part_o = static_cast<float*>(a.workspace);
     k.part_ml = reinterpret_cast<float2*>(k.part_o + segments * z.rows * a.head_dim);
@@ -980,8 +985,7 @@ extern "C" int statekv_tree_attention(const statekv_tree_args* args, void* cuda_
     cudaError_t e = a.head_dim == 128 ? two ? launch_main<128, true>(k, m, dev, st) : launch_main<128, false>(k, m, dev, st)
                     : two             ? launch_main<64, true>(k, m, dev, st)
                                       : launch_main<64, false>(k, m, dev, st);
-    // one CTA holds whole units only
-    if (e == cudaSuccess && !k.whole && k.grid > 1)
+    if (e == cudaSuccess && k.merge)
         e = a.head_dim == 128 ? launch_combine<128>(k, z.units, sms, st) : launch_combine<64>(k, z.units, sms, st);
     return e == cudaSuccess ? STATEKV_OK : view_cuda_fail();
 }

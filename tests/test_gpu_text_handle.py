@@ -205,6 +205,44 @@ def test_tree_rules():
     assert e.value.status == -2
 
 
+@pytest.mark.parametrize("restart", [False, True])
+@pytest.mark.parametrize("frames,merged", [(6, False), (20, True)])
+def test_a_frame_behind_a_tree_step_waits_for_it(frames, merged, restart):
+    """The rotation of a frame rewrites Q' and, after a restart, D's first rows:
+    the tree step enqueued just before still reads them as they were.  Short
+    caches have no merging kernel between the two."""
+    h = handle(max_frames=frames, num_layers=4)
+    c, g = h.cfg, gen(20)
+    T = c.frame_tokens
+    assert (frames * T > 896) == merged
+    frame = text(h, g, T)
+    out = [torch.empty(h.q_shape, dtype=h.torch_dtype, device=DEV) for _ in range(2)]
+    tok = 21                                          # more than one copy of Q per thread
+    tree, depth = kv.tree_masks([[-1] + list(range(tok - 1))] * 2, DEV)
+    x = text(h, g, tok)
+    rows = [text(h, g, T) for _ in range(frames - 1)]
+    o = torch.empty_like(x[0])
+
+    def step(wait):
+        h.reset()
+        for r in rows:
+            h.prefill_frame(*r, out[0])
+        torch.cuda.synchronize()
+        h.decode_tree(*x, tree, depth, o=o)
+        if wait:
+            torch.cuda.synchronize()
+        if restart:
+            h.reset()
+        h.prefill_frame(*frame, out[1])
+        torch.cuda.synchronize()
+        return o.clone(), out[1].clone()
+
+    want = step(True)
+    for _ in range(10):
+        assert all(torch.equal(a, b) for a, b in zip(step(False), want))
+    h.check_device_status()
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_sparse_decode(d):
     """After frames, after decoded text and after an accepted draft; the same
