@@ -156,14 +156,25 @@ void free_all(statekv_handle* h) {
     destroy_pipeline(h);
 }
 
+// Memory of the handle, contents undefined: for buffers allocated on first use,
+// all of which are written before they are read.
 template <typename T>
 bool dalloc(statekv_handle* h, T** p, size_t bytes) {
     void* q = nullptr;
     if (bytes == 0) bytes = 16;
     if (cudaMalloc(&q, bytes) != cudaSuccess) { cudaGetLastError(); return false; }
-    if (cudaMemset(q, 0, bytes) != cudaSuccess) { cudaGetLastError(); cudaFree(q); return false; }
     h->allocs.push_back(q);
     *p = reinterpret_cast<T*>(q);
+    return true;
+}
+
+// The same, zeroed on the default stream: nothing orders that before work on a
+// non-blocking stream, so the caller has to synchronise before the first use
+// (statekv_create does).
+template <typename T>
+bool dalloc_zero(statekv_handle* h, T** p, size_t bytes) {
+    if (!dalloc(h, p, bytes)) return false;
+    if (cudaMemset(*p, 0, bytes ? bytes : 16) != cudaSuccess) { cudaGetLastError(); return false; }
     return true;
 }
 
@@ -380,26 +391,26 @@ int statekv_create(const statekv_config* cfg, statekv_handle** out) {
     const int d = c.head_dim, T = c.frame_tokens;
     const size_t row = (size_t)d * h->esize;
     bool ok = true;
-    ok = ok && dalloc(h, &h->omega, sizeof(double) * d / 2);
-    ok = ok && dalloc(h, &h->cs, sizeof(float2) * (size_t)h->det_pitch * d / 2);
-    ok = ok && dalloc(h, &h->pool_k, (size_t)h->U * h->slots * row);
-    ok = ok && dalloc(h, &h->pool_v, (size_t)h->U * h->slots * row);
-    ok = ok && dalloc(h, &h->pos, sizeof(int32_t) * (size_t)h->U * h->slots);
-    ok = ok && dalloc(h, &h->det_k, (size_t)h->U * h->det_pitch * row);
-    ok = ok && dalloc(h, &h->det_v, (size_t)h->U * h->det_pitch * row);
-    ok = ok && dalloc(h, &h->q_rot, (size_t)h->U * h->GT * row);
-    ok = ok && dalloc(h, &h->colsum, sizeof(float) * (size_t)h->U * h->n_row_tiles * h->m_pad);
-    ok = ok && dalloc(h, &h->scores, sizeof(float) * (size_t)h->U * h->m_pad);
-    ok = ok && dalloc(h, &h->score_pos, sizeof(int32_t) * (size_t)h->U * h->m_pad);
-    ok = ok && dalloc(h, &h->err, sizeof(uint32_t) * kErrWords);
-    ok = ok && dalloc(h, &h->stage_q, h->q_bytes());
-    ok = ok && dalloc(h, &h->stage_k, h->kv_bytes());
-    ok = ok && dalloc(h, &h->stage_v, h->kv_bytes());
-    ok = ok && dalloc(h, &h->stage_o, h->q_bytes());
-    ok = ok && dalloc(h, &h->stage2_q, h->q_bytes());
-    ok = ok && dalloc(h, &h->stage2_k, h->kv_bytes());
-    ok = ok && dalloc(h, &h->stage2_v, h->kv_bytes());
-    ok = ok && dalloc(h, &h->stage2_o, h->q_bytes());
+    ok = ok && dalloc_zero(h, &h->omega, sizeof(double) * d / 2);
+    ok = ok && dalloc_zero(h, &h->cs, sizeof(float2) * (size_t)h->det_pitch * d / 2);
+    ok = ok && dalloc_zero(h, &h->pool_k, (size_t)h->U * h->slots * row);
+    ok = ok && dalloc_zero(h, &h->pool_v, (size_t)h->U * h->slots * row);
+    ok = ok && dalloc_zero(h, &h->pos, sizeof(int32_t) * (size_t)h->U * h->slots);
+    ok = ok && dalloc_zero(h, &h->det_k, (size_t)h->U * h->det_pitch * row);
+    ok = ok && dalloc_zero(h, &h->det_v, (size_t)h->U * h->det_pitch * row);
+    ok = ok && dalloc_zero(h, &h->q_rot, (size_t)h->U * h->GT * row);
+    ok = ok && dalloc_zero(h, &h->colsum, sizeof(float) * (size_t)h->U * h->n_row_tiles * h->m_pad);
+    ok = ok && dalloc_zero(h, &h->scores, sizeof(float) * (size_t)h->U * h->m_pad);
+    ok = ok && dalloc_zero(h, &h->score_pos, sizeof(int32_t) * (size_t)h->U * h->m_pad);
+    ok = ok && dalloc_zero(h, &h->err, sizeof(uint32_t) * kErrWords);
+    ok = ok && dalloc_zero(h, &h->stage_q, h->q_bytes());
+    ok = ok && dalloc_zero(h, &h->stage_k, h->kv_bytes());
+    ok = ok && dalloc_zero(h, &h->stage_v, h->kv_bytes());
+    ok = ok && dalloc_zero(h, &h->stage_o, h->q_bytes());
+    ok = ok && dalloc_zero(h, &h->stage2_q, h->q_bytes());
+    ok = ok && dalloc_zero(h, &h->stage2_k, h->kv_bytes());
+    ok = ok && dalloc_zero(h, &h->stage2_v, h->kv_bytes());
+    ok = ok && dalloc_zero(h, &h->stage2_o, h->q_bytes());
     if (!ok) { free_all(h); delete h; return STATEKV_E_OOM; }
     if (cudaMemcpy(h->omega, om.data(), sizeof(double) * om.size(), cudaMemcpyHostToDevice) !=
         cudaSuccess) {

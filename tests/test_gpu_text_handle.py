@@ -243,6 +243,47 @@ def test_a_frame_behind_a_tree_step_waits_for_it(frames, merged, restart):
     h.check_device_status()
 
 
+def test_first_calls_on_a_stream_of_their_own():
+    """Buffers allocated on first use hold what the call's stream writes, whatever
+    is pending on the default stream."""
+    g = gen(21)
+    outs = []
+    for side in (False, True):
+        g.manual_seed(21)
+        h = handle(max_frames=20)
+        c, T = h.cfg, h.cfg.frame_tokens
+        qw, kw = (1 + randn(g, c.num_layers, c.head_dim, dtype=torch.float32) / 4 for _ in range(2))
+        frames = [text(h, g, T) for _ in range(18)]
+        xs = [text(h, g, tok) for tok in (1, 4, 2, 3)]
+        tree, depth = kv.tree_masks([[-1, 0, 0, 2]] * 2, DEV)
+        path = torch.tensor([[0, 2], [0, 1]], dtype=torch.int32, device=DEV)
+        got = []
+
+        def run():
+            h.set_qk_norm(qw, kw)
+            for f in frames:
+                h.prefill_frame(*f)
+            got.append(h.decode_sparse(*xs[0], 3))
+            got.append(h.decode_tree(*xs[1], tree, depth))
+            h.accept(path)
+            got.append(h.decode(*xs[2]))
+            got.append(h.decode_sparse(*xs[3], 3))
+
+        torch.cuda.synchronize()
+        if side:
+            torch.cuda._sleep(400_000_000)            # about 0.2 s of the default stream
+            with torch.cuda.stream(torch.cuda.Stream()):
+                run()
+        else:
+            run()
+        torch.cuda.synchronize()
+        got += [h.decode_sparse(*xs[3], 3), rows_of(h, "k"), rows_of(h, "v")]
+        h.check_device_status()
+        outs.append(got)
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+    assert all(o.float().abs().sum() > 0 for o in outs[0])
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_sparse_decode(d):
     """After frames, after decoded text and after an accepted draft; the same
