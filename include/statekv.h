@@ -566,7 +566,9 @@ int statekv_append_accepted(const statekv_append_args* args, void* cuda_stream);
  * Summaries of the complete blocks of STATEKV_BLOCK cache rows, block b =
  * rows [64 b, 64 b + 64): the mean key (fp32, from a sum exact to fp32) as
  * 8-bit codes of one scale,
- *   scale = max |mean| / 127,  code = round_to_even(mean * (127 / max |mean|)).
+ *   scale = max |mean| / 127,  code = round_to_even(mean * (127 / max |mean|)),
+ * in fp32 (where max |mean| < 2^-100, mean and maximum are multiplied by 2^64
+ * for the code, so that the factor stays finite; zeros give zeros).
  * Brings up to date the blocks that the last `appended` rows completed, [
  * (length - appended) / 64, length / 64 ); the others are left as they are.
  * codes: int8 [batch][kv_heads][blocks][head_dim] (8-byte aligned), scales:
@@ -590,7 +592,7 @@ int statekv_block_summaries(const statekv_summary_args* args, void* cuda_stream)
  * first = length - tokens, each token and KV head
  *   1. scores the complete blocks of rows [0, first): the head group's query
  *      rows are rounded to 8 bits with one scale, qi = round_to_even(q * (127 /
- *      max |q|)), and score_b = float(max over the group of qi . code_b) *
+ *      max |q|)) as for the summaries, and score_b = float(max over the group of qi . code_b) *
  *      scale_b.  The products are whole numbers, so the scores, and the choice,
  *      do not depend on the order of summation;
  *   2. keeps the `top` best (1..1024), ties to the lower block;

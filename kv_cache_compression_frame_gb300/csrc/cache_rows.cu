@@ -160,12 +160,12 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtas) summary_kernel(const __
         }
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-        const float inv = top > 0.f ? 127.f / top : 0.f;
+        const float up = code_range(top), inv = top > 0.f ? 127.f / (top * up) : 0.f;
         if (lane < LPR) {
             uint32_t w[2] = {0u, 0u};
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const int code = (int)fminf(fmaxf(rintf(m[j] * inv), -127.f), 127.f);
+                const int code = (int)fminf(fmaxf(rintf(m[j] * up * inv), -127.f), 127.f);
                 w[j >> 2] |= (uint32_t)(code & 0xff) << (8 * (j & 3));
             }
             *reinterpret_cast<uint2*>(a.codes + at * D + lane * 8) = make_uint2(w[0], w[1]);

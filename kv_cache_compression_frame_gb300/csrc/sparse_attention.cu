@@ -180,12 +180,12 @@ __global__ void __launch_bounds__(kSparseThreads, 1) sparse_kernel(const __grid_
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kSparseWarps; ++i) top = fmaxf(top, __uint_as_float(s_scan[i]));
-        const float inv = top > 0.f ? 127.f / top : 0.f;
+        const float up = code_range(top), inv = top > 0.f ? 127.f / (top * up) : 0.f;
         if (has_q) {
             uint32_t c[2] = {0u, 0u};
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const int code = (int)fminf(fmaxf(rintf(x[i] * inv), -127.f), 127.f);
+                const int code = (int)fminf(fmaxf(rintf(x[i] * up * inv), -127.f), 127.f);
                 c[i >> 2] |= (uint32_t)(code & 0xff) << (8 * (i & 3));
             }
             *reinterpret_cast<uint2*>(s_q + tid * 8) = make_uint2(c[0], c[1]);

@@ -49,6 +49,11 @@ inline bool spread(const statekv_view& v, int64_t batch, int64_t heads, int64_t 
 }
 
 #ifdef __CUDACC__
+// Rounding to 8 bits with one scale multiplies by 127 / max |x|, which passes
+// fp32's range for maxima below 2^-121 (zeros would become inf * 0).  Values
+// and maximum times this power of two, exact, give the same codes without that.
+__device__ __forceinline__ float code_range(float top) { return top < 0x1p-100f ? 0x1p64f : 1.f; }
+
 // Rows of sequence s, from the array or the common value.  A negative length
 // or one past `most` is recorded and clamped, so that every access that
 // follows from it stays in bounds.

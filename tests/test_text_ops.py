@@ -531,6 +531,27 @@ def test_block_summaries(d, token_major):
     kv.check_status()
 
 
+@gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_codes_of_tiny_keys(d):
+    """Blocks whose factor 127 / max |mean| would pass fp32's range: the codes of
+    the same block times 2^64, and zeros for zeros."""
+    g = gen(33)
+    sizes = [2.0 ** e for e in (-99, -100, -101, -110, -119, -121, -122, -126, -131, -133)]
+    nb = len(sizes)
+    k = randn(g, 1, 2, nb, 64, d, dtype=torch.float32) + 2 * randn(g, 1, 2, nb, 1, d, dtype=torch.float32)
+    k[..., ::3] = 0
+    k = (k * torch.tensor(sizes, device=DEV)[:, None, None]).flatten(2, 3).to(BF16)
+    codes, scales = torch.zeros(1, 2, nb, d, dtype=torch.int8, device=DEV), torch.zeros(1, 2, nb, device=DEV)
+    kv.block_summaries(k, codes, scales, nb * 64)
+    m = k.unflatten(-2, (-1, 64)).double().sum(-2).float() / 64
+    top = m.abs().amax(-1)
+    up = torch.where(top < 2.0 ** -100, 2.0 ** 64, 1.0)
+    want = torch.round(m * up[..., None] * (127 / (top * up).double()).float()[..., None]).to(torch.int8)
+    assert torch.equal(codes, want) and torch.equal(scales, (top.double() / 127).float())
+    assert (codes[..., ::3] == 0).all() and (codes.abs().amax(-1) == 127).all()
+
+
 # ------------------------------------------------------------------- sparse
 def ref_choice(q, codes, scales, nb, top):
     """q [g][d] of one token and KV head -> the chosen blocks, ascending."""
@@ -626,6 +647,22 @@ def test_sparse_ties_and_full_attention():
                              kc, vc, rows - 2, scale=0.1)
     # two results, each within its tolerance of the same value (|v| < 8)
     assert (got.double() - full.double()).abs().max() < 2 * (2 * 2.0 ** -8 + 2.0 ** -12) * 8
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_sparse_choice_of_tiny_queries(d):
+    """A power of two times a query chooses the same blocks, and a query's zeros
+    stay zeros, as small as it may be."""
+    q, kc, vc, codes, scales = sparse_inputs(34, 1, 4, 2, 3, d, 2000)
+    q[..., ::2] = 0
+    for e in (-90, -101, -120, -126):
+        tiny = (q.float() * 2.0 ** e).to(BF16)
+        selected = kv.sparse_attention(tiny, kc, vc, codes, scales, 2000, 5, scale=0.1)[1]
+        for h in range(2):
+            for t in range(3):
+                qs = (tiny[0, 2 * h:2 * h + 2, t].float() * 2.0 ** 64).to(BF16)
+                assert selected[0, h, t].tolist() == ref_choice(qs, codes[0, h], scales[0, h], (2000 - 3) // 64, 5), e
 
 
 @gpu
