@@ -188,6 +188,9 @@ class StateKV:
             N.check(self._lib.statekv_set_qk_norm(self._h, None, None, 0.0, None), "statekv_set_qk_norm")
             return
         L, d = self.cfg.num_layers, self.cfg.head_dim
+        for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+            if tuple(w.shape) not in ((d,), (L, d)):
+                raise ValueError(f"{name}: want [{d}] or [{L}][{d}], got {tuple(w.shape)}")
         st = torch.cuda.current_stream(self.device) if stream is None else stream
         with torch.cuda.device(self.device), torch.cuda.stream(st):
             w = torch.stack([x.to(device=self.device, dtype=torch.float32).expand(L, d)

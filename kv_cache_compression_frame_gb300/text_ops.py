@@ -204,7 +204,7 @@ def qk_norm_rope(q, k, positions, omega, q_weight=None, k_weight=None, *, v=None
     for i, w in enumerate((q_weight, k_weight)):
         if w is not None:
             rows = w.shape[0] if w.dim() == 2 else 1
-            if w.shape[-1:] != (d,) or w.dtype not in _DTYPES or rows < 1 or n % rows or \
+            if w.dim() not in (1, 2) or w.shape[-1] != d or w.dtype not in _DTYPES or rows < 1 or n % rows or \
                     (wd is not None and (wd is not w.dtype or rows != w_rows)):
                 raise ValueError(f"{'qk'[i]}_weight: want [{d}] or [layers][{d}] of one of {list(_DTYPES)}, the "
                                  "same for both weights, layers dividing the batch")

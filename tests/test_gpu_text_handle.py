@@ -109,6 +109,17 @@ def test_qk_norm_in_prefill_and_decode(dtype, d):
     assert torch.equal(h.rotated_query(), plain.rotated_query())
 
 
+@pytest.mark.parametrize("shape", [(), (1,), (3, 1), (1, 128), (3, 1, 128), (128, 3)])
+def test_qk_norm_weights_of_other_shapes_are_refused(shape):
+    h = handle()
+    right, wrong = torch.ones(128), torch.ones(shape)
+    with pytest.raises(ValueError, match="q_weight"):
+        h.set_qk_norm(wrong, right)
+    with pytest.raises(ValueError, match="k_weight"):
+        h.set_qk_norm(right, wrong)
+    h.set_qk_norm(right, right.expand(3, 128))
+
+
 @pytest.mark.parametrize("d,norm", [(128, False), (128, True), (64, True)])
 def test_tree_step_and_acceptance(d, norm):
     h = handle(head_dim=d)

@@ -133,6 +133,18 @@ def test_norm_rope_weights_per_layer(dtype, wdtype):
 
 
 @gpu
+def test_norm_rope_weights_of_other_shapes_are_refused():
+    g = gen(63)
+    q, k, om = randn(g, 4, 2, 3, 64), randn(g, 4, 1, 3, 64), omega_of(64)
+    for shape in ((2, 1, 64), (1, 1, 64), (1,), (4, 1), (3, 64), (0, 64), (2, 128), ()):
+        w = torch.ones(shape, dtype=BF16, device=DEV)
+        with pytest.raises(ValueError, match="q_weight"):
+            kv.qk_norm_rope(q, k, 0, om, w)
+        with pytest.raises(ValueError, match="k_weight"):
+            kv.qk_norm_rope(q, k, 0, om, None, w)
+
+
+@gpu
 def test_norm_rope_into_a_cache_and_in_place():
     """K and V land at each sequence's rows; every other row stays as it was."""
     g = gen(6)
