@@ -19,6 +19,7 @@ mode is on.
 from __future__ import annotations
 
 import struct
+import threading
 
 import torch
 
@@ -28,6 +29,7 @@ _BF16, _F32, _I32, _I64, _I8 = torch.bfloat16, torch.float32, torch.int32, torch
 _DTYPES = {_BF16: N.BF16, _F32: N.F32}
 _NO_VIEW = (0, 0, 0, 0)
 _status: dict[int, tuple] = {}              # device -> (status word, its address)
+_status_lock = threading.Lock()
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
 
@@ -40,10 +42,13 @@ def _status_ptr(dev: int) -> int:
     if torch.cuda.is_current_stream_capturing():
         # its zeros would be part of the graph, and its memory the graph's
         raise RuntimeError("call a text operator once on this device before capturing one")
-    t = torch.zeros(4, dtype=_I32, device=torch.device("cuda", dev))
-    torch.cuda.synchronize(dev)             # any stream may use it from here on
-    _status[dev] = (t, t.data_ptr())
-    return t.data_ptr()
+    # one word per device, whichever thread comes first: kernels keep its address
+    with _status_lock:
+        if dev not in _status:
+            t = torch.zeros(4, dtype=_I32, device=torch.device("cuda", dev))
+            torch.cuda.synchronize(dev)     # any stream may use it from here on
+            _status[dev] = (t, t.data_ptr())
+        return _status[dev][1]
 
 
 def check_status(device: int | torch.device | None = None) -> None:

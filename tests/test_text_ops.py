@@ -950,6 +950,35 @@ def test_inputs_may_repeat_their_entries():
     kv.check_status()
 
 
+def test_first_calls_of_two_threads_share_a_status_word(monkeypatch):
+    """The address a thread gets is that of the word that is kept."""
+    import threading
+    import time
+
+    from kv_cache_compression_frame_gb300 import text_ops
+
+    def zeros(*a, **kw):
+        time.sleep(0.05)                            # another thread runs meanwhile
+        return torch.empty(4, dtype=torch.int32)
+
+    monkeypatch.setattr(text_ops, "_status", {})
+    monkeypatch.setattr(torch, "zeros", zeros)
+    monkeypatch.setattr(torch.cuda, "synchronize", lambda *a: time.sleep(0.05))
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    got, start = [], threading.Barrier(4)
+
+    def call():
+        start.wait()
+        got.append(text_ops._status_ptr(5))
+
+    threads = [threading.Thread(target=call) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert got == [text_ops._status[5][0].data_ptr()] * 4
+
+
 def test_null_arguments():
     lib = N.load()
     for f in ("norm_rope", "tree_attention", "append_accepted", "block_summaries", "sparse_attention"):
