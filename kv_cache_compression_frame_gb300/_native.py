@@ -177,10 +177,12 @@ def load() -> C.CDLL:
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args
+    ready = {}
     for name in PACKED:
         fn = lib[name]                  # a function object of its own
         fn.restype, fn.argtypes = C.c_int, [_P, _P]
-        packed[name] = fn
+        ready[name] = fn
+    packed.update(ready)                # all at once: another thread may look meanwhile
     _lib = lib
     return lib
 

@@ -979,6 +979,29 @@ def test_first_calls_of_two_threads_share_a_status_word(monkeypatch):
     assert got == [text_ops._status[5][0].data_ptr()] * 4
 
 
+def test_a_half_loaded_library_is_not_seen(monkeypatch):
+    """A thread that finds packed entry points finds all of them."""
+    seen_while_loading, cdll = [], C.CDLL
+
+    class Lib:
+        def __init__(self, path):
+            self.lib = cdll(path)
+
+        def __getattr__(self, name):
+            return getattr(self.lib, name)
+
+        def __getitem__(self, name):
+            seen_while_loading.append(len(N.packed))
+            return self.lib[name]
+
+    N.load()
+    monkeypatch.setattr(N, "packed", {})
+    monkeypatch.setattr(N, "_lib", None)
+    monkeypatch.setattr(N.C, "CDLL", Lib)
+    N.load()
+    assert seen_while_loading == [0] * len(N.PACKED) and sorted(N.packed) == sorted(N.PACKED)
+
+
 def test_null_arguments():
     lib = N.load()
     for f in ("norm_rope", "tree_attention", "append_accepted", "block_summaries", "sparse_attention"):
