@@ -12,8 +12,8 @@ device).  Outputs and workspaces that are not passed in are allocated there.
 Failures that only the device can see (a length out of range, a wait that gave
 up) are kept in one status word per device, which check_status() reads; a
 device's first call allocates it and must not be inside a graph capture.
-There is no backward pass: inputs that require grad are refused while grad
-mode is on.
+There is no derivative: inputs that require grad are refused while grad mode is
+on, and inputs with a forward-mode tangent always.
 """
 
 from __future__ import annotations
@@ -22,6 +22,7 @@ import struct
 import threading
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _native as N
 
@@ -98,9 +99,21 @@ def _view(t: torch.Tensor, name: str, shape, dtype, dev: int) -> tuple:
     if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or (st[3] != 1 and shape[3] != 1):
         raise ValueError(f"{name}: want {dtype} {tuple(shape)} on cuda:{dev} with a contiguous last dimension, "
                          f"got {t.dtype} {tuple(t.shape)} strides {st} on {t.device}")
+    if t.requires_grad:
+        _no_grad(t, name)
+    return t.data_ptr(), st[0], st[1], st[2]
+
+
+def _no_grad(t: torch.Tensor, name: str) -> None:
     if t.requires_grad and torch.is_grad_enabled():
         raise ValueError(f"{name} requires grad: the text operators have no backward pass")
-    return t.data_ptr(), st[0], st[1], st[2]
+
+
+def _no_tangents(**inputs) -> None:
+    # (called inside of a dual level only: outside no tensor has a tangent)
+    for name, t in inputs.items():
+        if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+            raise ValueError(f"{name} has a tangent: the text operators have no forward-mode derivative")
 
 
 def _shape4(t: torch.Tensor, name: str):
@@ -197,6 +210,8 @@ def qk_norm_rope(q, k, positions, omega, q_weight=None, k_weight=None, *, v=None
     n, hq, t, d = qs = _shape4(q, "q")
     hkv = _shape4(k, "k")[1]
     dt, dev = q.dtype, q.get_device()
+    if forward_ad._current_level >= 0:
+        _no_tangents(q=q, k=k, v=v, q_weight=q_weight, k_weight=k_weight, omega=omega)
     if _elsewhere(dev, stream):
         with _On(dev, stream):
             return qk_norm_rope(q, k, positions, omega, q_weight, k_weight, v=v, eps=eps, q_out=q_out,
@@ -213,12 +228,12 @@ def qk_norm_rope(q, k, positions, omega, q_weight=None, k_weight=None, *, v=None
                     (wd is not None and (wd is not w.dtype or rows != w_rows)):
                 raise ValueError(f"{'qk'[i]}_weight: want [{d}] or [layers][{d}] of one of {list(_DTYPES)}, the "
                                  "same for both weights, layers dividing the batch")
-            if w.requires_grad and torch.is_grad_enabled():
-                raise ValueError(f"{'qk'[i]}_weight requires grad: the text operators have no backward pass")
+            _no_grad(w, f"{'qk'[i]}_weight")
             wd, w_rows = w.dtype, rows
             w_ptr[i] = _vector(w, f"{'qk'[i]}_weight", wd, dev, w.dim())
     if omega.shape != (d // 2,):
         raise ValueError(f"omega: want [{d // 2}]")
+    _no_grad(omega, "omega")
     om = _vector(omega, "omega", torch.float64, dev)
     pos = p0 = p_stride = 0
     p_layers = layers = 1
@@ -274,6 +289,8 @@ def tree_attention(q, k_new, v_new, tree, k_cache, v_cache, lengths, *, scale: f
         with _On(dev, stream):
             return tree_attention(q, k_new, v_new, tree, k_cache, v_cache, lengths, scale=scale, out=out,
                                   workspace=workspace)
+    if forward_ad._current_level >= 0:
+        _no_tangents(q=q, k_new=k_new, v_new=v_new, k_cache=k_cache, v_cache=v_cache)
     ns, cs = (n, hkv, tok, d), (n, hkv, rows, d)
     views = (*_view(q, "q", qs, _BF16, dev), *_view(k_new, "k_new", ns, _BF16, dev),
              *_view(v_new, "v_new", ns, _BF16, dev), *_view(k_cache, "k_cache", cs, _BF16, dev),
@@ -321,6 +338,8 @@ def append_accepted(k_new, v_new, path, counts, k_cache, v_cache, lengths, *, st
     n, hkv, tok, d = ns = _shape4(k_new, "k_new")
     rows = _shape4(k_cache, "k_cache")[2]
     dt, dev = k_new.dtype, k_new.get_device()
+    if forward_ad._current_level >= 0:
+        _no_tangents(k_new=k_new, v_new=v_new, k_cache=k_cache, v_cache=v_cache)
     if _elsewhere(dev, stream):
         with _On(dev, stream):
             return append_accepted(k_new, v_new, path, counts, k_cache, v_cache, lengths)
@@ -361,6 +380,8 @@ def block_summaries(k_cache, codes, scales, lengths, *, appended: int | None = N
     `lengths` completed.  blocks >= rows // 64."""
     n, hkv, rows, d = cs = _shape4(k_cache, "k_cache")
     dev = k_cache.get_device()
+    if forward_ad._current_level >= 0:
+        _no_tangents(k_cache=k_cache, scales=scales)
     if _elsewhere(dev, stream):
         with _On(dev, stream):
             return block_summaries(k_cache, codes, scales, lengths, appended=appended)
@@ -374,6 +395,7 @@ def block_summaries(k_cache, codes, scales, lengths, *, appended: int | None = N
 
 def _summary_ptrs(codes, scales, n: int, hkv: int, d: int, dev: int) -> tuple[int, int, int]:
     pc = _vector(codes, "codes", _I8, dev, 4)
+    _no_grad(scales, "scales")
     ps = _vector(scales, "scales", _F32, dev, 3)
     blocks = codes.shape[2]
     if codes.shape != (n, hkv, blocks, d) or scales.shape != (n, hkv, blocks):
@@ -397,6 +419,8 @@ def sparse_attention(q, k_cache, v_cache, codes, scales, lengths, top: int, *, s
         with _On(dev, stream):
             return sparse_attention(q, k_cache, v_cache, codes, scales, lengths, top, scale=scale, out=out,
                                     selected=selected)
+    if forward_ad._current_level >= 0:
+        _no_tangents(q=q, k_cache=k_cache, v_cache=v_cache, scales=scales)
     top = int(top)
     cs = (n, hkv, rows, d)
     qv = _view(q, "q", qs, _BF16, dev)

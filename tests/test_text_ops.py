@@ -1011,6 +1011,40 @@ def test_null_arguments():
 
 
 @gpu
+def test_derivatives_are_refused():
+    """Reverse mode while grad mode is on, forward mode always, for every input
+    that could have one."""
+    from torch.autograd import forward_ad as fw
+    g = gen(64)
+    q, k, v = (randn(g, 2, h, 3, 64) for h in (4, 2, 2))
+    kc, vc = randn(g, 2, 2, 256, 64), randn(g, 2, 2, 256, 64)
+    codes, scales = ref_summaries(kc)
+    om, w = omega_of(64), torch.ones(64, device=DEV)
+    path = torch.zeros(1, dtype=torch.int32, device=DEV)
+    tree = random_tree(3, 1, 1)[0]
+    calls = [
+        (kv.qk_norm_rope, dict(q=q, k=k, omega=om, q_weight=w, k_weight=w, v=v), dict(positions=0)),
+        (kv.tree_attention, dict(q=q, k_new=k, v_new=v, k_cache=kc, v_cache=vc),
+         dict(tree=tree, lengths=256, scale=0.1)),
+        (kv.append_accepted, dict(k_new=k, v_new=v), dict(path=path, counts=None, k_cache=kc.clone(),
+                                                          v_cache=vc.clone(), lengths=3)),
+        (kv.block_summaries, dict(k_cache=kc), dict(codes=codes.clone(), scales=scales.clone(), lengths=256)),
+        (kv.sparse_attention, dict(q=q, k_cache=kc, v_cache=vc, scales=scales),
+         dict(codes=codes, lengths=256, top=1, scale=0.1)),
+    ]
+    for f, ins, rest in calls:
+        for name, x in ins.items():
+            with pytest.raises(ValueError, match=f"{name} requires grad"):
+                f(**{**ins, **rest, name: x.clone().requires_grad_()})
+            with fw.dual_level():
+                dual = fw.make_dual(x, torch.ones_like(x))
+                with torch.no_grad(), pytest.raises(ValueError, match=f"{name} has a tangent"):
+                    f(**{**ins, **rest, name: dual})
+                f(**ins, **rest)                    # no tangent: as outside
+    kv.check_status()
+
+
+@gpu
 def test_python_checks_name_the_argument():
     q, kn, vn, kc, vc = tree_inputs(1, 2, 4, 2, 3, 64, 10)
     tree = random_tree(3, 1, 1)
