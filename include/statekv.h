@@ -441,7 +441,8 @@ int statekv_attend_scores_static(const void* q_rot, const void* pool_k,
  *
  * Tensors are views [batch][heads][tokens][head_dim] of DEVICE memory on the
  * current device: the last dimension contiguous, the other strides (in
- * elements) free but not negative, every row on a 16-byte boundary.  An input
+ * elements) free but not negative, every row on a 16-byte boundary (the stride
+ * of a dimension of one entry is not looked at).  An input
  * may repeat its entries (stride 0), but for the keys and values of
  * statekv_tree_attention, which are read in tiles; an output may not
  * (E_INVALID_ARG).  The batch is sequences x layers: batch entry n belongs to sequence

@@ -210,8 +210,11 @@ extern "C" int statekv_append_accepted(const statekv_append_args* args, void* cu
     if ((int64_t)a.batch * a.kv_heads > 0x7fffffffll) return STATEKV_E_UNSUPPORTED;
     if (!a.status || reinterpret_cast<uintptr_t>(a.status) % 4) return STATEKV_E_INVALID_ARG;
     if (a.batch == 0) return STATEKV_OK;
-    if (a.path_len > 0 && (!a.path || !view_ok(a.k_new, es) || !view_ok(a.v_new, es))) return STATEKV_E_INVALID_ARG;
-    if (a.cache_rows > 0 && (!view_ok(a.k_cache, es) || !view_ok(a.v_cache, es) ||
+    if (a.path_len > 0 && (!a.path || !view_ok(a.k_new, es, a.batch, a.kv_heads, a.tokens) ||
+                           !view_ok(a.v_new, es, a.batch, a.kv_heads, a.tokens)))
+        return STATEKV_E_INVALID_ARG;
+    if (a.cache_rows > 0 && (!view_ok(a.k_cache, es, a.batch, a.kv_heads, a.cache_rows) ||
+                             !view_ok(a.v_cache, es, a.batch, a.kv_heads, a.cache_rows) ||
                              !spread(a.k_cache, a.batch, a.kv_heads, a.cache_rows) ||
                              !spread(a.v_cache, a.batch, a.kv_heads, a.cache_rows)))
         return STATEKV_E_INVALID_ARG;
@@ -233,8 +236,8 @@ extern "C" int statekv_block_summaries(const statekv_summary_args* args, void* c
     if (!a.status || reinterpret_cast<uintptr_t>(a.status) % 4) return STATEKV_E_INVALID_ARG;
     if (a.blocks < a.cache_rows / STATEKV_BLOCK) return STATEKV_E_CAPACITY;
     if (a.batch == 0 || a.cache_rows < STATEKV_BLOCK) return STATEKV_OK;
-    if (!view_ok(a.k_cache, 2) || !a.codes || reinterpret_cast<uintptr_t>(a.codes) % 8 || !a.scales ||
-        reinterpret_cast<uintptr_t>(a.scales) % 4)
+    if (!view_ok(a.k_cache, 2, a.batch, a.kv_heads, a.cache_rows) || !a.codes ||
+        reinterpret_cast<uintptr_t>(a.codes) % 8 || !a.scales || reinterpret_cast<uintptr_t>(a.scales) % 4)
         return STATEKV_E_INVALID_ARG;
     if (launch_summary(a, reinterpret_cast<cudaStream_t>(cuda_stream)) != cudaSuccess) return view_cuda_fail();
     return STATEKV_OK;

@@ -242,13 +242,17 @@ extern "C" int statekv_norm_rope(const statekv_norm_rope_args* args, void* cuda_
         if (w && !aligned16(w)) return STATEKV_E_INVALID_ARG;
     const int es = a.dtype == STATEKV_BF16 ? 2 : 4;
     if (a.q_heads > 0 &&
-        (!view_ok(a.q, es) || !view_ok(a.q_out, es) || !spread(a.q_out, a.batch, a.q_heads, a.tokens)))
+        (!view_ok(a.q, es, a.batch, a.q_heads, a.tokens) || !view_ok(a.q_out, es, a.batch, a.q_heads, a.tokens) ||
+         !spread(a.q_out, a.batch, a.q_heads, a.tokens)))
         return STATEKV_E_INVALID_ARG;
     if (a.kv_heads > 0) {
-        if (!view_ok(a.k, es) || !view_ok(a.k_out, es) || !spread(a.k_out, a.batch, a.kv_heads, a.out_capacity))
+        if (!view_ok(a.k, es, a.batch, a.kv_heads, a.tokens) ||
+            !view_ok(a.k_out, es, a.batch, a.kv_heads, a.out_capacity) ||
+            !spread(a.k_out, a.batch, a.kv_heads, a.out_capacity))
             return STATEKV_E_INVALID_ARG;
         if ((a.v.data != nullptr) != (a.v_out.data != nullptr)) return STATEKV_E_INVALID_ARG;
-        if (a.v.data && (!view_ok(a.v, es) || !view_ok(a.v_out, es) ||
+        if (a.v.data && (!view_ok(a.v, es, a.batch, a.kv_heads, a.tokens) ||
+                         !view_ok(a.v_out, es, a.batch, a.kv_heads, a.out_capacity) ||
                          !spread(a.v_out, a.batch, a.kv_heads, a.out_capacity)))
             return STATEKV_E_INVALID_ARG;
         if (!a.out_rows && a.out_capacity < a.tokens) return STATEKV_E_CAPACITY;

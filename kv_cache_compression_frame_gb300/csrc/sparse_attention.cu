@@ -580,10 +580,12 @@ extern "C" int statekv_sparse_attention(const statekv_sparse_args* args, void* c
     if (!a.status || reinterpret_cast<uintptr_t>(a.status) % 4) return STATEKV_E_INVALID_ARG;
     if (a.blocks < a.cache_rows / STATEKV_BLOCK || (!a.lengths && a.length > a.cache_rows)) return STATEKV_E_CAPACITY;
     if (items == 0) return STATEKV_OK;
-    if (!view_ok(a.q, 2) || !view_ok(a.out, 2) || !spread(a.out, a.batch, a.q_heads, a.tokens) ||
-        reinterpret_cast<uintptr_t>(a.selected) % 4)
+    if (!view_ok(a.q, 2, a.batch, a.q_heads, a.tokens) || !view_ok(a.out, 2, a.batch, a.q_heads, a.tokens) ||
+        !spread(a.out, a.batch, a.q_heads, a.tokens) || reinterpret_cast<uintptr_t>(a.selected) % 4)
         return STATEKV_E_INVALID_ARG;
-    if (a.cache_rows > 0 && (!view_ok(a.k_cache, 2) || !view_ok(a.v_cache, 2))) return STATEKV_E_INVALID_ARG;
+    if (a.cache_rows > 0 && (!view_ok(a.k_cache, 2, a.batch, a.kv_heads, a.cache_rows) ||
+                             !view_ok(a.v_cache, 2, a.batch, a.kv_heads, a.cache_rows)))
+        return STATEKV_E_INVALID_ARG;
     // the summaries are read only where there is something to choose
     const int most = (a.lengths ? a.cache_rows : a.length) / STATEKV_BLOCK;
     if (most > a.top && (!aligned16(a.codes) || !a.scales || reinterpret_cast<uintptr_t>(a.scales) % 4))

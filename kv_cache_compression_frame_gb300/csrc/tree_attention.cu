@@ -940,12 +940,15 @@ extern "C" int statekv_tree_attention(const statekv_tree_args* args, void* cuda_
     if (!a.status || reinterpret_cast<uintptr_t>(a.status) % 4) return STATEKV_E_INVALID_ARG;
     if (!a.lengths && a.length > a.cache_rows) return STATEKV_E_CAPACITY;
     if (a.batch == 0) return STATEKV_OK;
-    if (!a.tree || reinterpret_cast<uintptr_t>(a.tree) % 8 || !view_ok(a.q, 2) || !view_ok(a.out, 2) ||
-        !view_ok(a.k_new, 2) || !view_ok(a.v_new, 2))
+    if (!a.tree || reinterpret_cast<uintptr_t>(a.tree) % 8 || !view_ok(a.q, 2, a.batch, a.q_heads, a.tokens) ||
+        !view_ok(a.out, 2, a.batch, a.q_heads, a.tokens) || !view_ok(a.k_new, 2, a.batch, a.kv_heads, a.tokens) ||
+        !view_ok(a.v_new, 2, a.batch, a.kv_heads, a.tokens))
         return STATEKV_E_INVALID_ARG;
     // an empty cache needs no memory: its maps are never read
     const bool cached = a.cache_rows > 0;
-    if (cached && (!view_ok(a.k_cache, 2) || !view_ok(a.v_cache, 2))) return STATEKV_E_INVALID_ARG;
+    if (cached && (!view_ok(a.k_cache, 2, a.batch, a.kv_heads, a.cache_rows) ||
+                   !view_ok(a.v_cache, 2, a.batch, a.kv_heads, a.cache_rows)))
+        return STATEKV_E_INVALID_ARG;
     // entries that share their memory have no TMA view
     if (!spread(a.out, a.batch, a.q_heads, a.tokens) || !spread(a.k_new, a.batch, a.kv_heads, a.tokens) ||
         !spread(a.v_new, a.batch, a.kv_heads, a.tokens) ||

@@ -34,13 +34,13 @@ inline int view_cuda_fail() {
 
 inline bool aligned16(const void* p) { return p && reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
-// Every row of the view starts on a 16-byte boundary (what 16-byte loads and
-// TMA need), and no stride is negative.
-inline bool view_ok(const statekv_view& v, int esize) {
+// Every row of the view [batch][heads][rows] starts on a 16-byte boundary (what
+// 16-byte loads and TMA need), and no stride is negative.  The stride of a
+// dimension of one entry leads nowhere and may be anything.
+inline bool view_ok(const statekv_view& v, int esize, int64_t batch, int64_t heads, int64_t rows) {
     if (!aligned16(v.data)) return false;
-    for (int64_t s : {v.batch_stride, v.head_stride, v.token_stride})
-        if (s < 0 || (s * esize) % 16 != 0) return false;
-    return true;
+    auto ok = [&](int64_t n, int64_t s) { return n < 2 || (s >= 0 && s * esize % 16 == 0); };
+    return ok(batch, v.batch_stride) && ok(heads, v.head_stride) && ok(rows, v.token_stride);
 }
 
 // No entries of the view share their memory: what an output needs.

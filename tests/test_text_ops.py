@@ -1002,6 +1002,46 @@ def test_a_half_loaded_library_is_not_seen(monkeypatch):
     assert seen_while_loading == [0] * len(N.PACKED) and sorted(N.packed) == sorted(N.PACKED)
 
 
+@gpu
+def test_strides_of_single_entries_do_not_matter():
+    """One token, one head or one batch entry may have any stride: what contiguous
+    copies give."""
+    g = gen(65)
+    d, rows = 64, 300
+
+    def odd(x):                                     # the same values, odd strides where a dimension is 1
+        st = [s if n > 1 else 3 + 2 * i for i, (n, s) in enumerate(zip(x.shape, x.stride()))]
+        return x.as_strided(x.shape, (*st[:3], 1))
+
+    for n, hq, hkv, tok in ((1, 1, 1, 1), (2, 1, 1, 1), (1, 4, 2, 1), (1, 2, 1, 3), (1, 1, 1, 5)):
+        q, k, v = (randn(g, n, h, tok, d) for h in (hq, hkv, hkv))
+        kc, vc = randn(g, n, hkv, rows, d), randn(g, n, hkv, rows, d)
+        assert any(a != b for a, b in zip(odd(q).stride(), q.stride()))
+        out = torch.zeros_like(q)
+        om, tree = omega_of(d), random_tree(tok, 1, 1)[0]
+        for a, b in zip(kv.qk_norm_rope(odd(q), odd(k), 9, om, v=odd(v), q_out=odd(out)),
+                        kv.qk_norm_rope(q, k, 9, om, v=v)):
+            assert torch.equal(a, b)
+        assert torch.equal(kv.tree_attention(odd(q), odd(k), odd(v), tree, odd(kc), odd(vc), rows, scale=0.1,
+                                             out=odd(out)),
+                           kv.tree_attention(q, k, v, tree, kc, vc, rows, scale=0.1))
+        codes, scales = (torch.zeros(n, hkv, 4, d, dtype=torch.int8, device=DEV), torch.zeros(n, hkv, 4, device=DEV))
+        kv.block_summaries(odd(kc), codes, scales, rows)
+        c, s = ref_summaries(kc[:, :, :256])
+        assert torch.equal(codes, c) and torch.equal(scales, s)
+        assert torch.equal(kv.sparse_attention(odd(q), odd(kc), odd(vc), codes, scales, rows, 2, scale=0.1,
+                                               out=odd(out))[0],
+                           kv.sparse_attention(q, kc, vc, codes, scales, rows, 2, scale=0.1)[0])
+        path = torch.tensor([tok - 1], dtype=torch.int32, device=DEV)
+        kv.append_accepted(odd(k), odd(v), path, None, odd(kc), odd(vc), 7)
+        assert torch.equal(kc[:, :, 7], k[:, :, -1]) and torch.equal(vc[:, :, 7], v[:, :, -1])
+    # a cache of one row
+    one = torch.zeros(1, 1, 1, d, dtype=BF16, device=DEV)
+    kv.append_accepted(odd(k), odd(v), path, None, odd(one), odd(one.clone()), 0)
+    assert torch.equal(one[0, 0, 0], k[0, 0, -1])
+    kv.check_status()
+
+
 def test_null_arguments():
     lib = N.load()
     for f in ("norm_rope", "tree_attention", "append_accepted", "block_summaries", "sparse_attention"):
