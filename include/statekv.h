@@ -444,8 +444,9 @@ int statekv_attend_scores_static(const void* q_rot, const void* pool_k,
  * elements) free but not negative, every row on a 16-byte boundary (the stride
  * of a dimension of one entry is not looked at).  An input
  * may repeat its entries (stride 0), but for the keys and values of
- * statekv_tree_attention, which are read in tiles; an output may not
- * (E_INVALID_ARG).  The batch is sequences x layers: batch entry n belongs to sequence
+ * statekv_tree_attention, which are read in tiles; no two rows of an output may
+ * share memory (E_INVALID_ARG unless, taken from the smallest up, each stride
+ * spans all that the smaller ones reach).  The batch is sequences x layers: batch entry n belongs to sequence
  * n / layers, and lengths, trees, paths and destination rows have one entry
  * per sequence.  Query head j uses KV head j / (q_heads / kv_heads).  Outputs
  * must not overlap inputs unless said otherwise.

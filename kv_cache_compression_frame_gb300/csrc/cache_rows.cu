@@ -215,8 +215,8 @@ extern "C" int statekv_append_accepted(const statekv_append_args* args, void* cu
         return STATEKV_E_INVALID_ARG;
     if (a.cache_rows > 0 && (!view_ok(a.k_cache, es, a.batch, a.kv_heads, a.cache_rows) ||
                              !view_ok(a.v_cache, es, a.batch, a.kv_heads, a.cache_rows) ||
-                             !spread(a.k_cache, a.batch, a.kv_heads, a.cache_rows) ||
-                             !spread(a.v_cache, a.batch, a.kv_heads, a.cache_rows)))
+                             !apart(a.k_cache, a.batch, a.kv_heads, a.cache_rows, a.head_dim) ||
+                             !apart(a.v_cache, a.batch, a.kv_heads, a.cache_rows, a.head_dim)))
         return STATEKV_E_INVALID_ARG;
     // the sequence's length is read by every head's CTA while one writes the new one
     if (a.new_lengths && (a.new_lengths == a.lengths || a.new_lengths == a.counts)) return STATEKV_E_INVALID_ARG;

@@ -242,18 +242,15 @@ extern "C" int statekv_norm_rope(const statekv_norm_rope_args* args, void* cuda_
         if (w && !aligned16(w)) return STATEKV_E_INVALID_ARG;
     const int es = a.dtype == STATEKV_BF16 ? 2 : 4;
     if (a.q_heads > 0 &&
-        (!view_ok(a.q, es, a.batch, a.q_heads, a.tokens) || !view_ok(a.q_out, es, a.batch, a.q_heads, a.tokens) ||
-         !spread(a.q_out, a.batch, a.q_heads, a.tokens)))
+        (!view_ok(a.q, es, a.batch, a.q_heads, a.tokens) || !view_ok(a.q_out, es, a.batch, a.q_heads, a.tokens)))
         return STATEKV_E_INVALID_ARG;
     if (a.kv_heads > 0) {
         if (!view_ok(a.k, es, a.batch, a.kv_heads, a.tokens) ||
-            !view_ok(a.k_out, es, a.batch, a.kv_heads, a.out_capacity) ||
-            !spread(a.k_out, a.batch, a.kv_heads, a.out_capacity))
+            !view_ok(a.k_out, es, a.batch, a.kv_heads, a.out_capacity))
             return STATEKV_E_INVALID_ARG;
         if ((a.v.data != nullptr) != (a.v_out.data != nullptr)) return STATEKV_E_INVALID_ARG;
         if (a.v.data && (!view_ok(a.v, es, a.batch, a.kv_heads, a.tokens) ||
-                         !view_ok(a.v_out, es, a.batch, a.kv_heads, a.out_capacity) ||
-                         !spread(a.v_out, a.batch, a.kv_heads, a.out_capacity)))
+                         !view_ok(a.v_out, es, a.batch, a.kv_heads, a.out_capacity)))
             return STATEKV_E_INVALID_ARG;
         if (!a.out_rows && a.out_capacity < a.tokens) return STATEKV_E_CAPACITY;
     } else if (a.v.data || a.v_out.data) {
@@ -262,6 +259,10 @@ extern "C" int statekv_norm_rope(const statekv_norm_rope_args* args, void* cuda_
     const int64_t heads = (int64_t)a.q_heads + 2ll * a.kv_heads;
     if (heads > 16384) return STATEKV_E_UNSUPPORTED;         // rows of a CTA times heads below 2^32
     if (a.batch == 0 || a.tokens == 0 || heads == 0) return STATEKV_OK;
+    if (!apart(a.q_out, a.batch, a.q_heads, a.tokens, a.head_dim) ||
+        !apart(a.k_out, a.batch, a.kv_heads, a.out_capacity, a.head_dim) ||
+        (a.v.data && !apart(a.v_out, a.batch, a.kv_heads, a.out_capacity, a.head_dim)))
+        return STATEKV_E_INVALID_ARG;
     if (launch_norm_rope(a, reinterpret_cast<cudaStream_t>(cuda_stream)) != cudaSuccess)
         return view_cuda_fail();
     return STATEKV_OK;

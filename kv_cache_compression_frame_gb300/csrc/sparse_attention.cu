@@ -581,7 +581,7 @@ extern "C" int statekv_sparse_attention(const statekv_sparse_args* args, void* c
     if (a.blocks < a.cache_rows / STATEKV_BLOCK || (!a.lengths && a.length > a.cache_rows)) return STATEKV_E_CAPACITY;
     if (items == 0) return STATEKV_OK;
     if (!view_ok(a.q, 2, a.batch, a.q_heads, a.tokens) || !view_ok(a.out, 2, a.batch, a.q_heads, a.tokens) ||
-        !spread(a.out, a.batch, a.q_heads, a.tokens) || reinterpret_cast<uintptr_t>(a.selected) % 4)
+        !apart(a.out, a.batch, a.q_heads, a.tokens, a.head_dim) || reinterpret_cast<uintptr_t>(a.selected) % 4)
         return STATEKV_E_INVALID_ARG;
     if (a.cache_rows > 0 && (!view_ok(a.k_cache, 2, a.batch, a.kv_heads, a.cache_rows) ||
                              !view_ok(a.v_cache, 2, a.batch, a.kv_heads, a.cache_rows)))

@@ -949,8 +949,8 @@ extern "C" int statekv_tree_attention(const statekv_tree_args* args, void* cuda_
     if (cached && (!view_ok(a.k_cache, 2, a.batch, a.kv_heads, a.cache_rows) ||
                    !view_ok(a.v_cache, 2, a.batch, a.kv_heads, a.cache_rows)))
         return STATEKV_E_INVALID_ARG;
-    // entries that share their memory have no TMA view
-    if (!spread(a.out, a.batch, a.q_heads, a.tokens) || !spread(a.k_new, a.batch, a.kv_heads, a.tokens) ||
+    // (entries of K and V that share their memory have no TMA view)
+    if (!apart(a.out, a.batch, a.q_heads, a.tokens, a.head_dim) || !spread(a.k_new, a.batch, a.kv_heads, a.tokens) ||
         !spread(a.v_new, a.batch, a.kv_heads, a.tokens) ||
         (cached && (!spread(a.k_cache, a.batch, a.kv_heads, a.cache_rows) ||
                     !spread(a.v_cache, a.batch, a.kv_heads, a.cache_rows))))

@@ -3,7 +3,9 @@
 // views and the lookup of a sequence's cache length.
 #pragma once
 
+#include <algorithm>
 #include <atomic>
+#include <cstdint>
 
 #include "statekv_internal.cuh"
 
@@ -43,9 +45,26 @@ inline bool view_ok(const statekv_view& v, int esize, int64_t batch, int64_t hea
     return ok(batch, v.batch_stride) && ok(heads, v.head_stride) && ok(rows, v.token_stride);
 }
 
-// No entries of the view share their memory: what an output needs.
+// No two entries of the view start at the same place (what a TMA view needs).
 inline bool spread(const statekv_view& v, int64_t batch, int64_t heads, int64_t rows) {
     return (batch < 2 || v.batch_stride > 0) && (heads < 2 || v.head_stride > 0) && (rows < 2 || v.token_stride > 0);
+}
+
+// No entries of the view of rows of d elements share memory: what an output
+// needs.  Taken from the smallest stride up, each has to span all that the
+// smaller ones reach, as in any slice or permutation of an ordinary tensor.
+inline bool apart(const statekv_view& v, int64_t batch, int64_t heads, int64_t rows, int64_t d) {
+    if (batch < 1 || heads < 1 || rows < 1) return true;
+    struct Dim { int64_t n, stride; } dims[3] = {{rows, v.token_stride}, {heads, v.head_stride}, {batch, v.batch_stride}};
+    std::sort(dims, dims + 3, [](const Dim& x, const Dim& y) { return x.stride < y.stride; });
+    int64_t reach = d;
+    for (const Dim& x : dims) {
+        if (x.n < 2) continue;
+        if (x.stride < reach) return false;
+        if (x.stride > (INT64_MAX - reach) / (x.n - 1)) return false;
+        reach += x.stride * (x.n - 1);
+    }
+    return true;
 }
 
 #ifdef __CUDACC__

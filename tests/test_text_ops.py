@@ -921,6 +921,31 @@ def test_outputs_that_share_memory_are_refused(where):
     assert lib.statekv_sparse_attention(a, None) == N.E_INVALID_ARG
 
 
+@pytest.mark.parametrize("where", [dict(t=64), dict(h=256), dict(h=0), dict(b=896), dict(h=128, t=128, b=1 << 20),
+                                   dict(h=128, t=248), dict(b=128, h=248), dict(b=1 << 62, h=1 << 62)])
+def test_outputs_whose_rows_overlap_are_refused(where):
+    """Rows of 128 that reach into one another with strides that need not be 0:
+    2 batch entries of 4 heads (K and V: 2) of 3 tokens (of a cache: 4)."""
+    lib, good = N.load(), view(b=4096, h=512)
+    bad = view(**{**dict(b=4096, h=512), **where})
+    sizes = dict(batch=2, layers=1, q_heads=4, kv_heads=2, tokens=3, head_dim=128, status=16)
+    views = {f: good for f in ("q", "k", "v", "k_new", "v_new", "k_cache", "v_cache", "out", "q_out", "k_out", "v_out")}
+
+    def of(args, **kw):
+        return args(**{f: x for f, x in {**views, **sizes, **kw}.items() if f in dict(args._fields_)})
+
+    for name in ("q_out", "k_out", "v_out"):
+        a = of(N.NormRopeArgs, **{name: bad}, omega=16, position_layers=1, weight_rows=1, out_capacity=4, eps=1e-6)
+        assert lib.statekv_norm_rope(a, None) == N.E_INVALID_ARG, name
+    a = of(N.TreeArgs, out=bad, tree=16, workspace=16, workspace_bytes=1 << 40, scale=0.1, length=2, cache_rows=4)
+    assert lib.statekv_tree_attention(a, None) == N.E_INVALID_ARG
+    for name in ("k_cache", "v_cache"):
+        a = of(N.AppendArgs, **{name: bad}, path=16, path_len=2, length=2, cache_rows=4)
+        assert lib.statekv_append_accepted(a, None) == N.E_INVALID_ARG, name
+    a = of(N.SparseArgs, out=bad, codes=16, scales=16, scale=0.1, length=256, top=2, blocks=4, cache_rows=256)
+    assert lib.statekv_sparse_attention(a, None) == N.E_INVALID_ARG
+
+
 @gpu
 def test_inputs_may_repeat_their_entries():
     """Expanded inputs give what their copies give."""
