@@ -28,22 +28,31 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
     const int row_units = a.head_dim * (a.dtype == STATEKV_BF16 ? 2 : 4) / 16;
     const int es = a.dtype == STATEKV_BF16 ? 2 : 4;
     const int32_t* path = a.path + (int64_t)seq * a.path_stride;
-    for (int i = threadIdx.x; i < 2 * count * row_units; i += kAppendThreads) {
-        const int r = i / row_units, x = i - r * row_units;
+    // thread i takes the i-th 16 bytes of every 256: unit x of row r, all K rows
+    // and then all V rows (their number, and the units', may pass 32 bits)
+    const int dr = kAppendThreads / row_units, dx = kAppendThreads % row_units;
+    int x = threadIdx.x % row_units;
+    for (int64_t r = threadIdx.x / row_units; r < 2 * (int64_t)count;) {
         const bool is_v = r >= count;
-        const int step = is_v ? r - count : r;
+        const int step = (int)(is_v ? r - count : r);
         const int node = path[step];
         if (node < 0 || node >= a.tokens) {
             record_error(a.status, (uint32_t)STATEKV_E_DEVICE, kSiteNode, (uint32_t)node);
-            continue;
+        } else {
+            const statekv_view& s = is_v ? a.v_new : a.k_new;
+            const statekv_view& d = is_v ? a.v_cache : a.k_cache;
+            const char* src = static_cast<const char*>(s.data) +
+                              (n * s.batch_stride + h * s.head_stride + node * s.token_stride) * es;
+            char* dst = static_cast<char*>(d.data) +
+                        (n * d.batch_stride + h * d.head_stride + (int64_t)(len + step) * d.token_stride) * es;
+            reinterpret_cast<uint4*>(dst)[x] = reinterpret_cast<const uint4*>(src)[x];
         }
-        const statekv_view& s = is_v ? a.v_new : a.k_new;
-        const statekv_view& d = is_v ? a.v_cache : a.k_cache;
-        const char* src = static_cast<const char*>(s.data) +
-                          (n * s.batch_stride + h * s.head_stride + node * s.token_stride) * es;
-        char* dst = static_cast<char*>(d.data) +
-                    (n * d.batch_stride + h * d.head_stride + (int64_t)(len + step) * d.token_stride) * es;
-        reinterpret_cast<uint4*>(dst)[x] = reinterpret_cast<const uint4*>(src)[x];
+        r += dr;
+        x += dx;
+        if (x >= row_units) {
+            x -= row_units;
+            ++r;
+        }
     }
     if (a.new_lengths && h == 0 && n == seq * a.layers && threadIdx.x == 0) a.new_lengths[seq] = len + count;
 }

@@ -494,6 +494,27 @@ def test_append_accepted(dtype, d, layers):
     assert torch.equal(kc, k0) and torch.equal(vc, v0)
 
 
+@gpu
+def test_append_of_more_units_than_32_bits_count():
+    """One head's K and V rows are more than 2^31 units of 16 bytes: 34 GB."""
+    g = gen(32)
+    steps, d = (1 << 23) + 5001, 512
+    kn, vn = (randn(g, 1, 1, 2, d, dtype=torch.float32) for _ in range(2))
+    kc, vc = (torch.empty(1, 1, steps + 3, d, device=DEV) for _ in range(2))
+    for c in (kc, vc):
+        c[:, :, :1] = c[:, :, -2:] = 7
+    path = torch.arange(steps, device=DEV, dtype=torch.int32) % 2
+    assert 2 * steps * (d * 4 // 16) > 1 << 31
+    assert kv.append_accepted(kn, vn, path, None, kc, vc, 1) == steps + 1
+    kv.check_status()
+    for c, x in ((kc, kn), (vc, vn)):
+        assert (c[:, :, 0] == 7).all() and (c[:, :, -2:] == 7).all()
+        for part in (c[:, :, 1:-2:997], c[:, :, -1003:-2]):
+            first = (steps - 1001 if part.shape[2] == 1001 else 0)
+            at = (first + torch.arange(part.shape[2], device=DEV) * (1 if first else 997)) % 2
+            assert torch.equal(part, x[:, :, at])
+
+
 # ---------------------------------------------------------------- summaries
 def ref_summaries(k):
     """[..., blocks * 64, d] -> int8 codes and scales, as the header defines them."""
