@@ -213,11 +213,13 @@ extern "C" int statekv_append_accepted(const statekv_append_args* args, void* cu
     if (a.dtype != STATEKV_BF16 && a.dtype != STATEKV_F32) return STATEKV_E_INVALID_ARG;
     const int es = a.dtype == STATEKV_BF16 ? 2 : 4;
     if (a.batch < 0 || a.layers < 1 || a.batch % a.layers != 0 || a.kv_heads < 1 || a.tokens < 0 ||
-        a.path_len < 0 || a.path_stride < 0 || a.cache_rows < 0 || a.length < 0)
+        a.path_len < 0 || !rows_ok(a.path_stride, a.path_len) || a.cache_rows < 0 || a.length < 0)
         return STATEKV_E_INVALID_ARG;
     if (a.head_dim < 8 || a.head_dim > 512 || a.head_dim * es % 16 != 0) return STATEKV_E_UNSUPPORTED;
     if ((int64_t)a.batch * a.kv_heads > 0x7fffffffll) return STATEKV_E_UNSUPPORTED;
-    if (!a.status || reinterpret_cast<uintptr_t>(a.status) % 4) return STATEKV_E_INVALID_ARG;
+    if (!a.status || !ints_ok(a.status) || !ints_ok(a.path) || !ints_ok(a.counts) || !ints_ok(a.lengths) ||
+        !ints_ok(a.new_lengths))
+        return STATEKV_E_INVALID_ARG;
     if (a.batch == 0) return STATEKV_OK;
     if (a.path_len > 0 && (!a.path || !view_ok(a.k_new, es, a.batch, a.kv_heads, a.tokens) ||
                            !view_ok(a.v_new, es, a.batch, a.kv_heads, a.tokens)))
@@ -242,7 +244,7 @@ extern "C" int statekv_block_summaries(const statekv_summary_args* args, void* c
         a.cache_rows < 0 || a.length < 0 || a.appended < 0)
         return STATEKV_E_INVALID_ARG;
     if (a.head_dim != 64 && a.head_dim != 128) return STATEKV_E_UNSUPPORTED;
-    if (!a.status || reinterpret_cast<uintptr_t>(a.status) % 4) return STATEKV_E_INVALID_ARG;
+    if (!a.status || !ints_ok(a.status) || !ints_ok(a.lengths)) return STATEKV_E_INVALID_ARG;
     if (a.blocks < a.cache_rows / STATEKV_BLOCK) return STATEKV_E_CAPACITY;
     if (a.batch == 0 || a.cache_rows < STATEKV_BLOCK) return STATEKV_OK;
     if (!view_ok(a.k_cache, 2, a.batch, a.kv_heads, a.cache_rows) || !a.codes ||

@@ -577,7 +577,7 @@ extern "C" int statekv_sparse_attention(const statekv_sparse_args* args, void* c
         return STATEKV_E_UNSUPPORTED;
     const int64_t items = (int64_t)a.batch * a.kv_heads * a.tokens;
     if (items > 0x7fffffffll / 8) return STATEKV_E_UNSUPPORTED;
-    if (!a.status || reinterpret_cast<uintptr_t>(a.status) % 4) return STATEKV_E_INVALID_ARG;
+    if (!a.status || !ints_ok(a.status) || !ints_ok(a.lengths)) return STATEKV_E_INVALID_ARG;
     if (a.blocks < a.cache_rows / STATEKV_BLOCK || (!a.lengths && a.length > a.cache_rows)) return STATEKV_E_CAPACITY;
     if (items == 0) return STATEKV_OK;
     if (!view_ok(a.q, 2, a.batch, a.q_heads, a.tokens) || !view_ok(a.out, 2, a.batch, a.q_heads, a.tokens) ||

@@ -932,12 +932,12 @@ extern "C" int statekv_tree_attention(const statekv_tree_args* args, void* cuda_
     if (!args) return STATEKV_E_INVALID_ARG;
     const statekv_tree_args& a = *args;
     if (a.layers < 1 || a.batch < 0 || a.batch % a.layers != 0 || a.cache_rows < 0 || a.length < 0 ||
-        a.tree_stride < 0 || !(a.scale > 1e-30) || !(a.scale < 1e30))
+        !rows_ok(a.tree_stride, a.tokens) || !(a.scale > 1e-30) || !(a.scale < 1e30))
         return STATEKV_E_INVALID_ARG;
     TreeSizes z;
     int r = tree_sizes(a.batch, a.q_heads, a.kv_heads, a.tokens, a.head_dim, &z);
     if (r != STATEKV_OK) return r;
-    if (!a.status || reinterpret_cast<uintptr_t>(a.status) % 4) return STATEKV_E_INVALID_ARG;
+    if (!a.status || !ints_ok(a.status) || !ints_ok(a.lengths)) return STATEKV_E_INVALID_ARG;
     if (!a.lengths && a.length > a.cache_rows) return STATEKV_E_CAPACITY;
     if (a.batch == 0) return STATEKV_OK;
     if (!a.tree || reinterpret_cast<uintptr_t>(a.tree) % 8 || !view_ok(a.q, 2, a.batch, a.q_heads, a.tokens) ||

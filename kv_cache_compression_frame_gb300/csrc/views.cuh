@@ -36,6 +36,12 @@ inline int view_cuda_fail() {
 
 inline bool aligned16(const void* p) { return p && reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
+// An array of 32-bit entries, or none.
+inline bool ints_ok(const void* p) { return reinterpret_cast<uintptr_t>(p) % 4 == 0; }
+
+// Rows of `len` entries `stride` apart, or one row (0) for all.
+inline bool rows_ok(int32_t stride, int32_t len) { return stride == 0 || stride >= len; }
+
 // Every row of the view [batch][heads][rows] starts on a 16-byte boundary (what
 // 16-byte loads and TMA need), and no stride is negative.  The stride of a
 // dimension of one entry leads nowhere and may be anything.

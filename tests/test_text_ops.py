@@ -906,6 +906,33 @@ def test_sparse_refusals_before_device_work(bad, want):
     assert N.load().statekv_sparse_attention(N.SparseArgs(**a), None) == want
 
 
+def test_arrays_that_reach_past_their_rows_or_lie_between_words_are_refused():
+    """Rows of an array closer together than they are long would be read past the
+    array's end; an odd address faults on the device."""
+    lib, g = N.load(), view(b=4096, h=512)
+    sizes = dict(batch=2, layers=1, kv_heads=2, tokens=3, head_dim=128, status=16)
+    norm = dict(sizes, **{f: g for f in ("q", "k", "v", "q_out", "k_out", "v_out")}, omega=16, position_layers=1,
+                weight_rows=1, q_heads=4, out_capacity=3, eps=1e-6, positions=16)
+    tree = dict(sizes, **{f: g for f in ("q", "out", "k_new", "v_new", "k_cache", "v_cache")}, tree=16, workspace=16,
+                workspace_bytes=1 << 40, scale=0.1, length=2, q_heads=4, cache_rows=4)
+    append = dict(sizes, **{f: g for f in ("k_new", "v_new", "k_cache", "v_cache")}, path=16, path_len=2, length=2,
+                  cache_rows=4)
+    summary = dict({k: x for k, x in sizes.items() if k != "tokens"}, k_cache=g, codes=16, scales=16, length=128,
+                   appended=64, blocks=2, cache_rows=128)
+    sparse = dict(sizes, **{f: g for f in ("q", "out", "k_cache", "v_cache")}, codes=16, scales=16, scale=0.1,
+                  length=256, top=2, blocks=4, q_heads=4, cache_rows=256)
+    for f, args, good, bads in (
+            (lib.statekv_norm_rope, N.NormRopeArgs, norm,
+             [dict(position_stride=2), dict(positions=18), dict(out_rows=18)]),
+            (lib.statekv_tree_attention, N.TreeArgs, tree, [dict(tree_stride=2), dict(lengths=18)]),
+            (lib.statekv_append_accepted, N.AppendArgs, append,
+             [dict(path_stride=1), dict(path=18), dict(counts=18), dict(lengths=18), dict(new_lengths=18)]),
+            (lib.statekv_block_summaries, N.SummaryArgs, summary, [dict(lengths=18)]),
+            (lib.statekv_sparse_attention, N.SparseArgs, sparse, [dict(lengths=18)])):
+        for bad in bads:
+            assert f(args(**{**good, **bad}), None) == N.E_INVALID_ARG, bad
+
+
 @pytest.mark.parametrize("pack,args", [(N.PACK_NORM_ROPE, N.NormRopeArgs), (N.PACK_TREE, N.TreeArgs),
                                        (N.PACK_APPEND, N.AppendArgs), (N.PACK_SUMMARY, N.SummaryArgs),
                                        (N.PACK_SPARSE, N.SparseArgs)])
