@@ -240,6 +240,9 @@ extern "C" int statekv_norm_rope(const statekv_norm_rope_args* args, void* cuda_
         return STATEKV_E_INVALID_ARG;
     for (const void* w : {a.q_weight, a.k_weight})
         if (w && !aligned16(w)) return STATEKV_E_INVALID_ARG;
+    const int64_t heads = (int64_t)a.q_heads + 2ll * a.kv_heads;
+    if (heads > 16384) return STATEKV_E_UNSUPPORTED;         // rows of a CTA times heads below 2^32
+    if (a.batch == 0 || a.tokens == 0 || heads == 0) return STATEKV_OK;
     const int es = a.dtype == STATEKV_BF16 ? 2 : 4;
     if (a.q_heads > 0 &&
         (!view_ok(a.q, es, a.batch, a.q_heads, a.tokens) || !view_ok(a.q_out, es, a.batch, a.q_heads, a.tokens)))
@@ -256,9 +259,6 @@ extern "C" int statekv_norm_rope(const statekv_norm_rope_args* args, void* cuda_
     } else if (a.v.data || a.v_out.data) {
         return STATEKV_E_INVALID_ARG;
     }
-    const int64_t heads = (int64_t)a.q_heads + 2ll * a.kv_heads;
-    if (heads > 16384) return STATEKV_E_UNSUPPORTED;         // rows of a CTA times heads below 2^32
-    if (a.batch == 0 || a.tokens == 0 || heads == 0) return STATEKV_OK;
     if (!apart(a.q_out, a.batch, a.q_heads, a.tokens, a.head_dim) ||
         !apart(a.k_out, a.batch, a.kv_heads, a.out_capacity, a.head_dim) ||
         (a.v.data && !apart(a.v_out, a.batch, a.kv_heads, a.out_capacity, a.head_dim)))

@@ -151,6 +151,8 @@ def _layers(found: int, rows: int, batch: int, name: str) -> int:
         if rows not in (1, batch // found):
             raise ValueError(f"{name}: {rows} rows for {batch // found} sequences")
         return found
+    if rows == batch == 0:
+        return 1
     if rows == 0 or batch % rows:
         raise ValueError(f"{name}: {rows} rows do not divide a batch of {batch}")
     return max(1, batch // rows)
@@ -364,7 +366,7 @@ def append_accepted(k_new, v_new, path, counts, k_cache, v_cache, lengths, *, st
     layers = layers or 1
     status = _status_ptr(dev)
     new, to = None, 0
-    if lens or cnt:
+    if counts is not None or isinstance(lengths, torch.Tensor):
         new = torch.empty(n // layers, dtype=_I32, device=k_new.device)
         to = new.data_ptr()
     _call("statekv_append_accepted", N.PACK_APPEND, dev,

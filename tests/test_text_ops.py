@@ -1076,6 +1076,35 @@ def test_a_half_loaded_library_is_not_seen(monkeypatch):
 
 
 @gpu
+def test_empty_batches_and_tokens():
+    """Nothing to do: outputs of the right shape and type, and no error."""
+    z, c = (torch.zeros(0, 2, t, 64, dtype=BF16, device=DEV) for t in (3, 640))
+    none, two = torch.zeros(0, dtype=torch.int32, device=DEV), torch.zeros(2, dtype=torch.int32, device=DEV)
+    codes, scales = torch.zeros(0, 2, 10, 64, dtype=torch.int8, device=DEV), torch.zeros(0, 2, 10, device=DEV)
+    for lengths in (3, none):
+        for counts in (None, none):
+            got = kv.append_accepted(z, z, two, counts, c, c, lengths)
+            if lengths is none or counts is none:
+                assert got.shape == (0,) and got.dtype == torch.int32
+            else:
+                assert got == 5
+        for tree in (torch.ones(3, dtype=torch.int64, device=DEV), torch.ones(0, 3, dtype=torch.int64, device=DEV)):
+            assert kv.tree_attention(z, z, z, tree, c, c, lengths, scale=0.1).shape == z.shape
+        kv.block_summaries(c, codes, scales, lengths)
+        out, sel = kv.sparse_attention(z, c, c, codes, scales, lengths, 4, scale=0.1)
+        assert out.shape == z.shape and sel.shape == (0, 2, 3, 4)
+    for q in (z, torch.zeros(2, 2, 0, 64, dtype=BF16, device=DEV)):
+        got = kv.qk_norm_rope(q, q, 7, omega_of(64), v=q)
+        assert all(x.shape == q.shape for x in got)
+    q = torch.zeros(2, 2, 0, 64, dtype=BF16, device=DEV)
+    c = torch.zeros(2, 2, 640, 64, dtype=BF16, device=DEV)
+    codes, scales = torch.zeros(2, 2, 10, 64, dtype=torch.int8, device=DEV), torch.zeros(2, 2, 10, device=DEV)
+    assert kv.sparse_attention(q, c, c, codes, scales, 9, 4, scale=0.1)[0].shape == q.shape
+    assert kv.append_accepted(q, q, two[:0], None, c, c, 9) == 9
+    kv.check_status()
+
+
+@gpu
 def test_strides_of_single_entries_do_not_matter():
     """One token, one head or one batch entry may have any stride: what contiguous
     copies give."""
