@@ -175,6 +175,8 @@ class _On:
 
 def _elsewhere(dev: int, stream) -> bool:
     """Whether a call needs _On around it."""
+    if stream is not None and stream.device_index != dev:
+        raise ValueError(f"stream: of device {stream.device_index}, the tensors are on cuda:{dev}")
     return stream is not None or _current_device() != dev
 
 

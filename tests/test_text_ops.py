@@ -1105,6 +1105,24 @@ def test_empty_batches_and_tokens():
 
 
 @gpu
+def test_streams_of_another_device_are_refused():
+    """They would leave the work on the current stream of the tensors' device."""
+    class Elsewhere(torch.cuda.Stream):
+        device_index = 1
+
+    s = Elsewhere()
+    z, path = torch.zeros(1, 1, 1, 64, dtype=BF16, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+    codes, scales = torch.zeros(1, 1, 0, 64, dtype=torch.int8, device=DEV), torch.zeros(1, 1, 0, device=DEV)
+    for call in (lambda: kv.qk_norm_rope(z, z, 0, omega_of(64), stream=s),
+                 lambda: kv.tree_attention(z, z, z, path.long(), z, z, 1, scale=0.1, stream=s),
+                 lambda: kv.append_accepted(z, z, path, None, z.clone(), z.clone(), 0, stream=s),
+                 lambda: kv.block_summaries(z, codes, scales, 1, stream=s),
+                 lambda: kv.sparse_attention(z, z, z, codes, scales, 1, 1, scale=0.1, stream=s)):
+        with pytest.raises(ValueError, match="stream"):
+            call()
+
+
+@gpu
 def test_strides_of_single_entries_do_not_matter():
     """One token, one head or one batch entry may have any stride: what contiguous
     copies give."""
