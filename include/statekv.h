@@ -521,10 +521,12 @@ int statekv_norm_rope(const statekv_norm_rope_args* args, void* cuda_stream);
  * per head in the cache views.  workspace: device memory of
  * statekv_tree_attention_workspace() bytes, 16-byte aligned, contents
  * irrelevant (NULL where that is 0: a few short caches); the function depends
- * on the current device, does not fall with any of its arguments but may rise
- * with each, and returns -1 for sizes that the call would refuse.  The results do not depend on the
- * workspace or on the other calls, but sums are grouped by the whole batch:
- * they agree between batchings up to rounding.
+ * on the current device and returns -1 for sizes that the call would refuse.
+ * With the same kv_heads it rises or stays with every other argument, so one
+ * workspace for the largest serves all; with more KV heads for the same query
+ * heads it may fall.  The results do not depend on the workspace or on the
+ * other calls, but sums are grouped by the whole batch: they agree between
+ * batchings up to rounding.
  */
 typedef struct statekv_tree_args {
     statekv_view q, out, k_new, v_new, k_cache, v_cache;

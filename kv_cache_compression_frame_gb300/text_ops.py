@@ -327,7 +327,8 @@ def tree_attention(q, k_new, v_new, tree, k_cache, v_cache, lengths, *, scale: f
 def tree_attention_workspace(batch: int, q_heads: int, kv_heads: int, tokens: int, head_dim: int,
                              cache_rows: int) -> int:
     """Bytes of workspace tree_attention needs on the current device (0 for a
-    few short caches)."""
+    few short caches).  With the same kv_heads it never falls as another
+    argument rises; with more KV heads it may."""
     size = N.load().statekv_tree_attention_workspace(batch, q_heads, kv_heads, tokens, head_dim, cache_rows)
     if size < 0:
         raise N.StateKVError(N.E_UNSUPPORTED, "statekv_tree_attention_workspace")

@@ -392,6 +392,18 @@ def test_tree_views_workspace_stream_and_shared_tree():
 
 
 @gpu
+@pytest.mark.parametrize("kv_heads", [1, 2, 8])
+def test_tree_workspace_rises_with_all_but_kv_heads(kv_heads):
+    """One workspace for the largest arguments serves every call of a model."""
+    base = dict(batch=3, q_heads=16, kv_heads=kv_heads, tokens=8, head_dim=64, cache_rows=2000)
+    for name, values in dict(batch=range(0, 200), q_heads=range(kv_heads, 64 * kv_heads + 1, kv_heads),
+                             tokens=range(1, 65), head_dim=(64, 128), cache_rows=range(0, 4000, 50)).items():
+        for other in (dict(), dict(batch=40), dict(tokens=40), dict(cache_rows=600)):
+            sizes = [kv.tree_attention_workspace(**{**base, **other, name: x}) for x in values]
+            assert sizes == sorted(sizes), (name, other)
+
+
+@gpu
 def test_tree_units_that_fill_the_device_exactly():
     """One share per unit: nothing to merge, and what follows on the stream
     still waits for the whole call."""
