@@ -231,6 +231,8 @@ int statekv_prefill_frames_host(statekv_handle* h, int32_t frames, const void* q
  * first call allocates the handle's decode scratch (partial results per
  * 2048-key chunk of D; E_OOM if that fails).  The first call of this and the
  * entry points below that allocate cannot be captured into a CUDA graph.
+ * A captured call counts as made: its graph has to be replayed once before the
+ * handle's next call, and a further replay repeats it at the same positions.
  */
 int statekv_decode(statekv_handle* h, int32_t tokens, const void* q, const void* k,
                    const void* v, void* o, void* cuda_stream);
@@ -515,6 +517,8 @@ int statekv_norm_rope(const statekv_norm_rope_args* args, void* cuda_stream);
  * allowed).  q and k_new are already rotated.  A key that is masked, and
  * cache rows from `length` on, contribute nothing whatever they hold
  * (infinities and NaN included); a row that sees no key at all gets zeros.
+ * Scores, softmax sums and the output are fp32; the probabilities are rounded
+ * to bf16 (2^-8 of each) for the product with V, their sum takes them unrounded.
  * tree: uint64 [sequences][tree_stride >= tokens], or tree_stride 0 for one
  * tree shared by all; bits from `tokens` on are ignored.
  * bf16, head_dim 64 or 128, q_heads / kv_heads <= 64, cache_rows >= 0 rows
@@ -577,7 +581,7 @@ int statekv_append_accepted(const statekv_append_args* args, void* cuda_stream);
  * (length - appended) / 64, length / 64 ); the others are left as they are.
  * codes: int8 [batch][kv_heads][blocks][head_dim] (8-byte aligned), scales:
  * float [batch][kv_heads][blocks], blocks >= cache_rows / 64 (else
- * E_CAPACITY).  Keys must be finite.  bf16, head_dim 64 or 128.
+ * E_CAPACITY).  Keys, and their sums over a block in fp32, must be finite.  bf16, head_dim 64 or 128.
  */
 typedef struct statekv_summary_args {
     statekv_view k_cache;
@@ -602,7 +606,8 @@ int statekv_block_summaries(const statekv_summary_args* args, void* cuda_stream)
  *   2. keeps the `top` best (1..1024), ties to the lower block;
  *   3. attends over those blocks' rows, the rows since the last complete block
  *      and, causally, the new rows.
- * With top >= first / 64 this is full attention.  selected, if not NULL:
+ * With top >= first / 64 this is full attention.  Precision of the attention as
+ * in statekv_tree_attention.  selected, if not NULL:
  * int32 [batch][kv_heads][tokens][top], the chosen blocks in ascending order,
  * -1 from the last one on.  codes and scales as statekv_block_summaries
  * writes them, up to date for every complete block before `first`, codes

@@ -5,8 +5,8 @@
 //   score_b = float(max_g qi_g . code_b) * scale_b      (whole-number products)
 //   o = softmax(scale * q K_S^T) V_S,  S = rows of the top blocks and the tail
 //
-// After a 512-frame video one token of the dense step reads 67 MB of keys and
-// values per layer with 2 KV heads; here it reads 0.5 MB of codes and 2 MB of
+// After a 512-frame video one token of the dense step reads 134 MB of keys and
+// values per layer with 2 KV heads; here it reads 0.5 MB of codes and 4.2 MB of
 // the 64 best blocks.  The bound is latency: a chain of four dependent loads
 // (query, codes, keys, values) and a selection in between.
 //
@@ -35,6 +35,9 @@
 // blocks counted per token, 114.5 us.  The rings are what counts there: with
 // rows of 32 straight from global memory into registers, which leave no room
 // for a second entry in flight, it was 147.
+// One token in all 28 layers through a handle, rotation and summaries included:
+// 43 us with 2 KV heads (56 items, clusters of 2), 127 us with 8 (224 items, no
+// clusters); the bytes alone would take 20 and 79.
 #include <algorithm>
 
 #include "views.cuh"
