@@ -448,9 +448,9 @@ int statekv_attend_scores_static(const void* q_rot, const void* pool_k,
  * may repeat its entries (stride 0), but for the keys and values of
  * statekv_tree_attention, which are read in tiles; no two rows of an output may
  * share memory (E_INVALID_ARG unless, taken from the smallest up, each stride
- * spans all that the smaller ones reach).  The batch is sequences x layers: batch entry n belongs to sequence
- * n / layers, and lengths, trees, paths and destination rows have one entry
- * per sequence.  Query head j uses KV head j / (q_heads / kv_heads).  Outputs
+ * spans all that the smaller ones reach).  The batch is sequences x layers:
+ * batch entry n belongs to sequence n / layers, and lengths, trees, paths and
+ * destination rows have one entry per sequence.  Query head j uses KV head j / (q_heads / kv_heads).  Outputs
  * must not overlap inputs unless said otherwise.
  *
  * `lengths` (int32, device) gives each sequence's rows in the cache; where it
@@ -581,7 +581,8 @@ int statekv_append_accepted(const statekv_append_args* args, void* cuda_stream);
  * (length - appended) / 64, length / 64 ); the others are left as they are.
  * codes: int8 [batch][kv_heads][blocks][head_dim] (8-byte aligned), scales:
  * float [batch][kv_heads][blocks], blocks >= cache_rows / 64 (else
- * E_CAPACITY).  Keys, and their sums over a block in fp32, must be finite.  bf16, head_dim 64 or 128.
+ * E_CAPACITY).  Keys, and their sums over a block in fp32, must be finite.
+ * bf16, head_dim 64 or 128.
  */
 typedef struct statekv_summary_args {
     statekv_view k_cache;
@@ -600,8 +601,8 @@ int statekv_block_summaries(const statekv_summary_args* args, void* cuda_stream)
  * first = length - tokens, each token and KV head
  *   1. scores the complete blocks of rows [0, first): the head group's query
  *      rows are rounded to 8 bits with one scale, qi = round_to_even(q * (127 /
- *      max |q|)) as for the summaries, and score_b = float(max over the group of qi . code_b) *
- *      scale_b.  The products are whole numbers, so the scores, and the choice,
+ *      max |q|)) as for the summaries, and score_b = float(max over the group
+ *      of qi . code_b) * scale_b.  The products are whole numbers, so the scores, and the choice,
  *      do not depend on the order of summation;
  *   2. keeps the `top` best (1..1024), ties to the lower block;
  *   3. attends over those blocks' rows, the rows since the last complete block

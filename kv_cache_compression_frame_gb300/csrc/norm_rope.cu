@@ -231,8 +231,8 @@ extern "C" int statekv_norm_rope(const statekv_norm_rope_args* args, void* cuda_
     if (a.dtype != STATEKV_BF16 && a.dtype != STATEKV_F32) return STATEKV_E_INVALID_ARG;
     if (a.weight_dtype != STATEKV_BF16 && a.weight_dtype != STATEKV_F32) return STATEKV_E_INVALID_ARG;
     if (a.batch < 0 || a.layers < 1 || a.batch % a.layers != 0 || a.tokens < 0 || a.q_heads < 0 ||
-        a.kv_heads < 0 || !rows_ok(a.position_stride, a.tokens) || a.position_layers < 1 || a.weight_rows < 1 || a.out_capacity < 0 ||
-        !(a.eps >= 0.f))
+        a.kv_heads < 0 || a.position_stride < 0 || (a.positions && !rows_ok(a.position_stride, a.tokens)) ||
+        a.position_layers < 1 || a.weight_rows < 1 || a.out_capacity < 0 || !(a.eps >= 0.f))
         return STATEKV_E_INVALID_ARG;
     if (a.head_dim != 64 && a.head_dim != 128) return STATEKV_E_UNSUPPORTED;
     if (!a.status || reinterpret_cast<uintptr_t>(a.status) % 4 || !a.omega ||

@@ -943,6 +943,9 @@ def test_arrays_that_reach_past_their_rows_or_lie_between_words_are_refused():
             (lib.statekv_sparse_attention, N.SparseArgs, sparse, [dict(lengths=18)])):
         for bad in bads:
             assert f(args(**{**good, **bad}), None) == N.E_INVALID_ARG, bad
+    # a stride that belongs to no array is not looked at
+    assert lib.statekv_norm_rope(N.NormRopeArgs(**{**norm, "positions": None, "position_stride": 2, "batch": 0}),
+                                 None) == N.OK
 
 
 @pytest.mark.parametrize("pack,args", [(N.PACK_NORM_ROPE, N.NormRopeArgs), (N.PACK_TREE, N.TreeArgs),
