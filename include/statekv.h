@@ -151,7 +151,8 @@ const char* statekv_status_string(int status);
  * its positions [S][L][Hkv][B+T] int32, the detailed state
  * [S][L][Hkv][N_max*T][d] for K and V, scratch (rotated queries, per-tile key
  * column sums, scores) and one frame of staging for the host-buffer entry
- * point.  All device memory is zero-filled.  The handle owns it all.
+ * point.  This memory is zero-filled (buffers that later calls allocate on
+ * first use are not).  The handle owns it all.
  * On failure *out is set to NULL and nothing is leaked.
  */
 int statekv_create(const statekv_config* cfg, statekv_handle** out);
@@ -175,6 +176,10 @@ int statekv_destroy(statekv_handle* h);
  *   k, v : [S][L][Hkv][T][d]     (pre-RoPE keys; values)
  * q/k/v must not alias o or handle memory.  Returns E_CAPACITY when
  * n == max_frames.  On success the frame index advances by one.
+ * The rotation may start as soon as the kernel before it on the stream
+ * releases its dependents (programmatic dependent launch).  This library's own
+ * kernels do so only where that is safe; a caller's kernel that writes q, k or
+ * v, or reads handle memory, has to leave it to its end (the default).
  */
 int statekv_prefill_frame(statekv_handle* h, const void* q, const void* k,
                           const void* v, void* o, void* cuda_stream);
