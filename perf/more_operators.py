@@ -349,7 +349,7 @@ def _plain_verify(s):
             left = torch.where(yes, 1.0, torch.where(no, rest, left))
             used = used.masked_fill(yes, 0.0)
         else:
-            left = torch.where(yes, 1.0, torch.where(no, left - r, left))
+            left = torch.where(yes, 1.0, torch.where(no, (left - r).clamp(min=0.0), left))
             refused = refused & ~yes[:, None]
             refused[b, x[:, i]] |= no
         at = torch.where(yes, i + 1, at)
@@ -505,8 +505,8 @@ def _exact_verify(case, s):
             for child in (i for i in range(tok) if parent[i] == at):
                 x = drafted[child]
                 if q is None:
-                    whole = 1.0 - sum(float(s["target"][b, at + 1, t]) for t in
-                                      {drafted[i] for i in range(child) if parent[i] == at})
+                    tried = {drafted[i] for i in range(child) if parent[i] == at}
+                    whole = max(0.0, 1.0 - sum(float(s["target"][b, at + 1, t]) for t in tried))
                     if u[child] * whole < float(rest[x]):
                         break
                     rest[x] = 0.0
