@@ -634,6 +634,202 @@ typedef struct statekv_sparse_args {
 } statekv_sparse_args;
 int statekv_sparse_attention(const statekv_sparse_args* args, void* cuda_stream);
 
+/*
+ * ------------------------------------------------------ paged caches
+ *
+ * A pool of pages holds the rows of many sequences: views
+ * [pages][kv_heads][page_rows][head_dim] (batch_stride is the stride of a
+ * page), num_pages of them.  table: int32 [batch][table_stride], row i of batch
+ * entry n is row i % page_rows of page table[n][i / page_rows]; a table row
+ * holds table_pages <= table_stride entries, so a sequence at most table_pages
+ * * page_rows < 2^31 rows.  Entries past the last page in use are not looked
+ * at; one in use that is out of [0, num_pages) is recorded (E_DEVICE): its rows
+ * read as zeros, and nothing is written there.  Pages may be shared by entries
+ * that only read them.  page_rows is a multiple of 16.  table NULL: a plain
+ * cache, batch entry n is page n (num_pages >= batch), of any number of rows.
+ * lengths (or length) and counts have one entry per sequence, as above; counts
+ * NULL: `tokens` for all.  A count below 0, or past `tokens`, is recorded and
+ * clamped.
+ */
+
+/*
+ * New rows join their sequences: for i < counts[sequence],
+ *   cache row length + i = new row i,
+ * K and V of every layer and head; other rows stay as they are.  new_lengths,
+ * if not NULL, receives length + count (memory of its own).  A sequence whose
+ * rows do not fit in its table row appends nothing (recorded).  Batch entries
+ * that write one page write the same row of it in any order: pages that are
+ * appended to are not shared.  k_pages and v_pages do not overlap each other or
+ * the new rows.  Any head_dim of whole 16-byte units up to 512; dtype
+ * STATEKV_BF16 or STATEKV_F32.
+ */
+typedef struct statekv_paged_append_args {
+    statekv_view k_new, v_new, k_pages, v_pages;
+    const int32_t* table;
+    const int32_t* lengths;
+    const int32_t* counts;
+    int32_t* new_lengths;
+    uint32_t* status;
+    int32_t length, table_stride, table_pages, num_pages, page_rows;
+    int32_t batch, layers, kv_heads, tokens, head_dim, dtype;
+} statekv_paged_append_args;
+int statekv_paged_append(const statekv_paged_append_args* args, void* cuda_stream);
+
+/*
+ * Attention of the last tokens of each sequence over the cache they are already
+ * part of: with first = length - count, token j < count is row first + j and
+ * sees the rows up to itself,
+ *   o = softmax(q K[:first + j + 1]^T * scale) V[:first + j + 1],
+ *   lse = log(sum over those rows of exp(q . k * scale)).
+ * Any number of tokens (one, or a whole prompt), q already rotated.  Tokens from
+ * count on (a padded batch), and those of a sequence shorter than its count
+ * (recorded) past its length, give zeros and -infinity.  Rows that a token does
+ * not see contribute nothing to it whatever they hold (infinities and NaN
+ * included); a row whose scores are all -infinity gives zeros.
+ * Scores, softmax sums and the output are fp32; the probabilities are rounded
+ * to bf16 (2^-8 of each) for the product with V, their sum takes them unrounded.
+ * lse, if not NULL: float [batch][q_heads][tokens].
+ * bf16, head_dim 64 or 128, q_heads / kv_heads <= 64.  K and V are read in tiles:
+ * their entries do not share memory (strides above 0).  workspace: device memory of
+ * statekv_paged_attention_workspace() bytes, 16-byte aligned, contents
+ * irrelevant (NULL where that is 0: a few short caches; cache_rows: the most that
+ * a sequence can hold); the size depends on the current device and, with the
+ * same kv_heads, rises or stays with every argument (-1 for sizes that the call
+ * would refuse).  The results do not
+ * depend on the workspace or on other calls, but sums are grouped by the whole
+ * batch: they agree between batchings up to rounding.
+ */
+typedef struct statekv_paged_attention_args {
+    statekv_view q, out, k_pages, v_pages;
+    const int32_t* table;
+    const int32_t* lengths;
+    const int32_t* counts;
+    float* lse;
+    uint32_t* status;
+    void* workspace;
+    int64_t workspace_bytes;
+    double scale;
+    int32_t length, table_stride, table_pages, num_pages, page_rows;
+    int32_t batch, layers, q_heads, kv_heads, tokens, head_dim;
+} statekv_paged_attention_args;
+int64_t statekv_paged_attention_workspace(int32_t batch, int32_t q_heads, int32_t kv_heads,
+                                          int32_t tokens, int32_t head_dim, int32_t cache_rows);
+int statekv_paged_attention(const statekv_paged_attention_args* args, void* cuda_stream);
+
+/*
+ * What attention every cache row received from the tokens of a
+ * statekv_paged_attention call, from its queries and log-sum-exps:
+ *   out[row] = before[row] + sum over the head group's queries that see the row
+ *              of exp(q . k * scale - lse),
+ * rows from the length on as before.  q, lengths and counts as for that call;
+ * a query whose lse is -infinity adds nothing.  before, out: float
+ * [batch][kv_heads][weight_rows] (before NULL: zeros; out may be before),
+ * weight_rows at least the rows a sequence can hold (E_CAPACITY).  Scores and sums in
+ * fp32, each row's sum in a fixed order (the same bits on every run).
+ * bf16, head_dim 64 or 128, q_heads / kv_heads <= 64; q and K are read in tiles:
+ * their entries do not share memory.  No workspace.
+ */
+typedef struct statekv_attention_weights_args {
+    statekv_view q, k_pages;
+    const int32_t* table;
+    const int32_t* lengths;
+    const int32_t* counts;
+    const float* lse;
+    const float* before;
+    float* out;
+    uint32_t* status;
+    double scale;
+    int32_t length, table_stride, table_pages, num_pages, page_rows, weight_rows;
+    int32_t batch, layers, q_heads, kv_heads, tokens, head_dim;
+} statekv_attention_weights_args;
+int statekv_attention_weights(const statekv_attention_weights_args* args, void* cuda_stream);
+
+/*
+ * Eviction by accumulated weight: every batch entry and KV head keeps
+ * min(length, keep) of its rows, and they become, in their order, rows 0.. of
+ * the pages that out_table names.  Rows below `sinks` and the last `recent`
+ * stay (sinks + recent <= keep); of the others those of the largest weight,
+ * ties to the lower row, NaN below all.
+ * k_out and v_out are pools of their own, or k_pages and v_pages themselves;
+ * pages that out_table names are read by no entry of the call and named once.
+ * (The rows move to fresh pages so that pages shared with other sequences stay as
+ * they are.)  Rows of out pages past the last kept row stay as they are.
+ *   weights      float [batch][kv_heads][weight_rows], weight_rows at least the
+ *                rows a sequence can hold
+ *   weights_out  float [batch][kv_heads][out_rows]: the kept rows' weights, then zeros
+ *   kept         int32 [batch][kv_heads][keep]: the kept rows, then -1
+ *   new_lengths  int32 [sequences]: min(length, keep), if not NULL
+ * none of which shares memory with another or an input.  out_rows >= keep; the
+ * out table holds out_table_pages * page_rows >= keep rows (E_CAPACITY; both
+ * pools have the same page_rows); out_table NULL: batch entry n's
+ * rows go to page n of pools that are not the source's.  Any head_dim of whole
+ * 16-byte units up to 512; dtype STATEKV_BF16 or STATEKV_F32; a sequence holds at
+ * most 2^22 rows.
+ */
+typedef struct statekv_evict_args {
+    statekv_view k_pages, v_pages, k_out, v_out;
+    const int32_t* table;
+    const int32_t* out_table;
+    const int32_t* lengths;
+    const float* weights;
+    float* weights_out;
+    int32_t* kept;
+    int32_t* new_lengths;
+    uint32_t* status;
+    int32_t length, table_stride, table_pages, num_pages, page_rows, weight_rows;
+    int32_t out_table_stride, out_table_pages, out_num_pages, out_page_rows, out_rows;
+    int32_t keep, sinks, recent;
+    int32_t batch, layers, kv_heads, head_dim, dtype;
+} statekv_evict_args;
+int statekv_evict_rows(const statekv_evict_args* args, void* cuda_stream);
+
+/*
+ * Verification of a drafted tree against the target's probabilities, with
+ * random numbers from the caller: which path of it stands, and the token after
+ * it, so that the tokens are distributed as if drawn from the target one by one.
+ *   tree     uint64 [sequences][tree_stride >= tokens] (0: one for all), as for
+ *            statekv_tree_attention; node i's parent is the highest lower node
+ *            that its mask names, none: it follows the text so far
+ *   target   float, rows [sequences][tokens + 1][vocab] (strides in elements):
+ *            the target's probabilities after the text (row 0) and after node i (row i + 1)
+ *   draft    the same of the draft's, from which the children of a node were
+ *            drawn independently; rows of nodes without children are not read.  NULL: the
+ *            children of a node are proposals without probabilities
+ *   drafted  int32 [sequences][tokens], the nodes' tokens
+ *   uniforms float [sequences][tokens + 1] in [0, 1): one per node, then one for
+ *            the token at the end
+ * From the text on, with p and q the current node's rows, c = 0 and R = 1, for
+ * its children x in ascending order, u their uniforms:
+ *   r(v) = max(p(v) - c q(v), 0);  if u q(x) R < r(x), x stands and is the
+ *   current node; else c += R, R = sum of max(p(v) - c q(v), 0) over v.
+ * Without q: if u R < r(x), r = p without the refused tokens, x stands; else
+ * R = max(R - r(x), 0).
+ * When no child is left, the token is the lowest v with
+ *   sum over w <= v of r(w) > u * sum of r
+ * (where that sum is 0, of p instead of r; where that is 0 too, token 0).
+ * Products and sums in 64 bits.  Probabilities are in [0, 1] and sum to 1 up to
+ * rounding; NaN and negative ones count as 0, uniforms are clamped to [0, 1).
+ *   path     int32 [sequences][tokens]: the accepted nodes, then -1
+ *   counts   int32 [sequences], how many
+ *   next     int32 [sequences]
+ * as statekv_append_accepted takes them.  A drafted token out of [0, vocab) is recorded and
+ * refused.  tokens 1..64, vocab below 2^26.
+ */
+typedef struct statekv_verify_args {
+    const float* target;
+    const float* draft;
+    const int32_t* drafted;
+    const uint64_t* tree;
+    const float* uniforms;
+    int32_t* path;
+    int32_t* counts;
+    int32_t* next;
+    uint32_t* status;
+    int64_t target_stride, target_row, draft_stride, draft_row;   /* of a sequence, of a row */
+    int32_t tree_stride, sequences, tokens, vocab;
+} statekv_verify_args;
+int statekv_verify_tree(const statekv_verify_args* args, void* cuda_stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -45,6 +45,8 @@ EXPORTS = (
     "statekv_append_accepted", "statekv_block_summaries",
     "statekv_sparse_attention",
     "statekv_set_qk_norm", "statekv_decode_tree", "statekv_accept", "statekv_decode_sparse",
+    "statekv_paged_append", "statekv_paged_attention", "statekv_paged_attention_workspace",
+    "statekv_attention_weights", "statekv_evict_rows", "statekv_verify_tree",
 )
 
 BLOCK = 64          # STATEKV_BLOCK
@@ -96,6 +98,28 @@ SparseArgs = _struct(
     "SparseArgs", (View, "q out k_cache v_cache"), (C.c_void_p, "codes scales lengths selected status"),
     (C.c_double, "scale"),
     (C.c_int32, "length top blocks batch layers q_heads kv_heads tokens head_dim cache_rows"))
+_PAGED = "length table_stride table_pages num_pages page_rows "
+PagedAppendArgs = _struct(
+    "PagedAppendArgs", (View, "k_new v_new k_pages v_pages"),
+    (C.c_void_p, "table lengths counts new_lengths status"),
+    (C.c_int32, _PAGED + "batch layers kv_heads tokens head_dim dtype"))
+PagedAttentionArgs = _struct(
+    "PagedAttentionArgs", (View, "q out k_pages v_pages"),
+    (C.c_void_p, "table lengths counts lse status workspace"), (C.c_int64, "workspace_bytes"),
+    (C.c_double, "scale"), (C.c_int32, _PAGED + "batch layers q_heads kv_heads tokens head_dim"))
+AttentionWeightsArgs = _struct(
+    "AttentionWeightsArgs", (View, "q k_pages"),
+    (C.c_void_p, "table lengths counts lse before out status"), (C.c_double, "scale"),
+    (C.c_int32, _PAGED + "weight_rows batch layers q_heads kv_heads tokens head_dim"))
+EvictArgs = _struct(
+    "EvictArgs", (View, "k_pages v_pages k_out v_out"),
+    (C.c_void_p, "table out_table lengths weights weights_out kept new_lengths status"),
+    (C.c_int32, _PAGED + "weight_rows out_table_stride out_table_pages out_num_pages out_page_rows out_rows "
+                "keep sinks recent batch layers kv_heads head_dim dtype"))
+VerifyArgs = _struct(
+    "VerifyArgs", (C.c_void_p, "target draft drafted tree uniforms path counts next status"),
+    (C.c_int64, "target_stride target_row draft_stride draft_row"),
+    (C.c_int32, "tree_stride sequences tokens vocab"))
 
 # The same structures packed from flat values, a view as (pointer, batch, head,
 # token stride): a fifth of the time it takes to fill a ctypes structure.
@@ -105,9 +129,15 @@ PACK_TREE = struct.Struct("@" + 6 * _V + "4Pqd9i0q")
 PACK_APPEND = struct.Struct("@" + 4 * _V + "5P10i0q")
 PACK_SUMMARY = struct.Struct("@" + _V + "4P8i0q")
 PACK_SPARSE = struct.Struct("@" + 4 * _V + "5Pd10i0q")
+PACK_PAGED_APPEND = struct.Struct("@" + 4 * _V + "5P11i0q")
+PACK_PAGED_ATTENTION = struct.Struct("@" + 4 * _V + "6Pqd11i0q")
+PACK_WEIGHTS = struct.Struct("@" + 2 * _V + "7Pd12i0q")
+PACK_EVICT = struct.Struct("@" + 4 * _V + "8P19i0q")
+PACK_VERIFY = struct.Struct("@9P4q4i0q")
 # entry points that take such a packed structure and a stream; set by load()
 PACKED = ("statekv_norm_rope", "statekv_tree_attention", "statekv_append_accepted",
-          "statekv_block_summaries", "statekv_sparse_attention")
+          "statekv_block_summaries", "statekv_sparse_attention", "statekv_paged_append",
+          "statekv_paged_attention", "statekv_attention_weights", "statekv_evict_rows", "statekv_verify_tree")
 packed: dict = {}
 
 
@@ -170,9 +200,14 @@ def load() -> C.CDLL:
     for name, args in (("statekv_norm_rope", NormRopeArgs), ("statekv_tree_attention", TreeArgs),
                        ("statekv_append_accepted", AppendArgs),
                        ("statekv_block_summaries", SummaryArgs),
-                       ("statekv_sparse_attention", SparseArgs)):
+                       ("statekv_sparse_attention", SparseArgs),
+                       ("statekv_paged_append", PagedAppendArgs),
+                       ("statekv_paged_attention", PagedAttentionArgs),
+                       ("statekv_attention_weights", AttentionWeightsArgs),
+                       ("statekv_evict_rows", EvictArgs), ("statekv_verify_tree", VerifyArgs)):
         sig[name] = (C.c_int, [C.POINTER(args), _P])
-    sig["statekv_tree_attention_workspace"] = (C.c_int64, [C.c_int32] * 6)
+    for name in ("statekv_tree_attention_workspace", "statekv_paged_attention_workspace"):
+        sig[name] = (C.c_int64, [C.c_int32] * 6)
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
         fn.restype = res

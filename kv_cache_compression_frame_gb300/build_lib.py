@@ -29,7 +29,8 @@ LIB = os.path.join(PKG, "libstatekv.so")
 
 SOURCES = ["statekv_api.cu", "rope.cu", "attn_tc.cu", "attn_simt.cu", "select.cu",
            "attend_static.cu", "decode.cu", "norm_rope.cu", "cache_rows.cu", "tree_attention.cu",
-           "sparse_attention.cu"]
+           "sparse_attention.cu", "paged_rows.cu", "paged_attention.cu", "attention_weights.cu",
+           "verify_tree.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
                  "-I", INCLUDE, "-I", CSRC]

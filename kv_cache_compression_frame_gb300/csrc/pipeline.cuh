@@ -72,8 +72,8 @@ bool encode_view(CUtensorMap* m, const void* base, int d, int64_t rows, int64_t 
                  int box_rows);
 // The same for a strided view [batch][heads][rows][d] (bf16, every stride a
 // multiple of 16 bytes): coordinates (column, row, head, batch), boxes of 64
-// columns x 128 rows.
+// columns x box_rows rows x box_heads heads (rows innermost).
 bool encode_view4(CUtensorMap* m, const statekv_view& v, int d, int64_t rows, int64_t heads,
-                  int64_t batch);
+                  int64_t batch, int box_rows = 128, int box_heads = 1);
 
 }  // namespace statekv

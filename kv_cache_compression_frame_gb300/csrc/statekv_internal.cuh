@@ -19,7 +19,7 @@ enum ErrSite : uint32_t {
     kSiteQFull = 1, kSiteKvFull, kSiteKvEmpty, kSiteSFull, kSiteSEmpty,
     kSitePFull, kSitePEmpty, kSiteOFull, kSiteDrain, kSiteTmemAddr, kSiteCol,
     kSiteSelect = 32,
-    kSiteLength = 40, kSiteNode,
+    kSiteLength = 40, kSiteNode, kSitePage,
 };
 
 // ------------------------------------------------------------- launchers
