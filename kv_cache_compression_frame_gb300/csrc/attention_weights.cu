@@ -10,17 +10,23 @@
 // each sum has a fixed order, and nothing is written but one number per row.
 //
 // Work: an item is 256 rows of one (batch entry, KV head), two 128-row tiles,
-// each with a slot of four warps and two S buffers of its own.  Items are dealt
-// to the CTAs in turn (one CTA per SM): ragged lengths and the causal triangle
-// even out.  The item's queries stream through shared memory in blocks of
-// floor(128 / G) tokens x G heads, one TMA box each, shared by both tiles.
+// each with a slot of warps, an issuer and two S buffers of its own.  Items are
+// dealt to the CTAs in turn (one CTA per SM): ragged lengths and the causal
+// triangle even out.  The item's queries stream through shared memory in blocks
+// of floor(128 / G) tokens x G heads, one TMA box each, shared by both tiles.
+//
+// The log-sum-exp is part of the product: a ninth k-step multiplies a row of ones
+// with -lse / scale in three bf16 terms (24 bits), so S comes out as q . k - lse /
+// scale and a column costs one multiplication, one exponential and one addition.
+// Read from shared memory for each column it took twice the time: the products
+// take all of its bandwidth (8 KB per 64 cycles), and the reads wait for them.
 //
 // Bound: by HBM for a few tokens (K once, 256 bytes a row and 8 of weights), by
-// the exponentials for a prompt (16384 per tile and block against 512 cycles of
-// tensor work).
+// the exponentials (16384 per tile and block at 32 a cycle) and the tensor cores
+// (576 cycles) for a prompt.
 //
-// Scores and sums in fp32.  Tokens behind the count, columns that no query has
-// and queries that saw nothing are selected away, not added as zeros.
+// Scores and sums in fp32.  In blocks with tokens behind the count, with queries
+// that saw nothing, or over rows that not every token sees, columns are selected.
 #include <algorithm>
 
 #include "paged.cuh"
@@ -31,24 +37,21 @@ namespace {
 
 constexpr int kTile = 128;
 constexpr int kItem = 2 * kTile;             // rows of an item
-constexpr int kWeightThreads = 384;
+constexpr int kWeightThreads = 672;          // five warps of their own roles, sixteen (4..19) that add up
+constexpr int kRest = 512;                  // rows of a piece of what is copied
 
 struct WeightKernelArgs {
     statekv_attention_weights_args a;
-    float scale_log2;
+    float scale_log2, minus_inv_scale;
     int32_t G, tb;                           // query heads of a KV head, tokens of a query block
     int32_t cols, n;                         // queries of a block; columns of a product (a multiple of 16)
     int32_t box, page_boxes;                 // rows of a TMA box of K, boxes of a page
     int32_t capacity;
 };
 
-struct Seq {
-    int len, count;                          // rows to weigh (0 where there is no token), new tokens
-};
+// (no rows to weigh where there is no token)
 __device__ __forceinline__ Seq seq_of(const WeightKernelArgs& k, int s) {
-    Seq q;
-    q.len = cache_length(k.a.lengths, k.a.length, s, k.capacity, k.a.status);
-    q.count = new_tokens(k.a.counts, k.a.tokens, s, q.len, k.a.status);
+    Seq q = sequence_of(k.a, k.capacity, s);
     if (q.count == 0) q.len = 0;
     return q;
 }
@@ -86,38 +89,48 @@ struct Walk {
     }
 };
 
-template <int D>
+// WIDE: more than 64 columns, in two halves of eight warps each.
+template <int D, bool WIDE>
 struct WeightLayout {
     static constexpr int KCH = D / 64;
     static constexpr int CHUNK = 128 * 128;              // [128 rows][64 bf16], 128B-swizzled
     static constexpr int TILE = KCH * CHUNK;
-    static constexpr int KS = D == 64 ? 6 : 4;           // tiles of K: two or three items
-    static constexpr int QS = D == 64 ? 4 : 3;           // blocks of queries
+    static constexpr int QCHUNK = WIDE ? CHUNK : CHUNK / 2;
+    static constexpr int QTILE = KCH * QCHUNK;
+    // Tiles of K (an item has two), and blocks of queries.  KS is even: each slot
+    // has stages of its own.  Sharing them, an issuer two items ahead of the other
+    // could wait for a phase after one that is not complete, and pass.
+    static constexpr int KS = D == 64 ? 8 : 4;
+    static constexpr int QS = 2;                         // a helper each
+    static_assert(KS % 2 == 0, "stages per slot");
     static constexpr int OFF_K = 0;
     static constexpr int OFF_Q = OFF_K + KS * TILE;
-    static constexpr int OFF_LSE = OFF_Q + QS * TILE;    // [QS][128] log-sum-exps in log2 units
-    static constexpr int OFF_TOK = OFF_LSE + QS * 512;   // [128] token of a column in its block (255: none)
+    static constexpr int OFF_LSE = OFF_Q + QS * QTILE;   // [128 rows][4 slices of 16 bf16]: lse terms of QS blocks, 3 ones
+    static constexpr int OFF_PART = OFF_LSE + CHUNK;     // [2 slots][128] sums of the second half of the columns
+    static constexpr int OFF_BLIND = OFF_PART + (WIDE ? 1024 : 0);   // [8 blocks][4]: columns that saw nothing
+    static constexpr int OFF_TOK = OFF_BLIND + 128;      // [128] token of a column in its block (255: none)
     static constexpr int OFF_BAR = OFF_TOK + 128;
     static constexpr int B_K_FULL = 0;
     static constexpr int B_K_EMPTY = B_K_FULL + KS;
-    static constexpr int B_Q_FULL = B_K_EMPTY + KS;
-    static constexpr int B_L_FULL = B_Q_FULL + QS;       // log-sum-exps stored (1 warp)
-    static constexpr int B_Q_EMPTY = B_L_FULL + QS;      // both products done, 8 warps done
+    static constexpr int B_Q_FULL = B_K_EMPTY + KS;      // queries there, lse terms stored
+    static constexpr int B_Q_EMPTY = B_Q_FULL + QS;      // products done (2 slots)
     static constexpr int B_S_FULL = B_Q_EMPTY + QS;      // [2 slots][2 buffers]
-    static constexpr int B_S_EMPTY = B_S_FULL + 4;       // (4 warps)
-    static constexpr int B_DRAIN = B_S_EMPTY + 4;
-    static constexpr int NBAR = B_DRAIN + 1;
-    static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;  // TMEM address, abort flag, [QS] a query saw nothing
-    static constexpr int SMEM = OFF_MISC + 8 + QS * 4;
+    static constexpr int B_S_EMPTY = B_S_FULL + 4;       // (the slot's warps)
+    static constexpr int B_PART = B_S_EMPTY + 4;         // [2 slots] the second half's sums stored (4 warps)
+    static constexpr int B_TAKEN = B_PART + 2;           // [2 slots] and taken (4 warps)
+    static constexpr int B_DRAIN = B_TAKEN + 2;
+    static constexpr int NBAR = B_DRAIN + 2;             // [2 slots]
+    static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;  // TMEM address, abort flag, rest
+    static constexpr int SMEM = OFF_MISC + 12;
     static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
     static constexpr uint32_t TMEM_COLS = 512;
 };
 
-template <int D>
+template <int D, bool WIDE>
 __global__ void __launch_bounds__(kWeightThreads, 1)
 weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q,
                const __grid_constant__ WeightKernelArgs k) {
-    using L = WeightLayout<D>;
+    using L = WeightLayout<D, WIDE>;
     const statekv_attention_weights_args& a = k.a;
     extern __shared__ __align__(1024) uint8_t base[];
     const uint32_t sbase = ptx::smem_u32(base);
@@ -128,10 +141,12 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + L::OFF_MISC);
     volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(base + L::OFF_MISC + 4);
-    uint32_t* blind = reinterpret_cast<uint32_t*>(base + L::OFF_MISC + 8);
+    uint32_t* rest = reinterpret_cast<uint32_t*>(base + L::OFF_MISC + 8);
+    volatile uint32_t* blind = reinterpret_cast<volatile uint32_t*>(base + L::OFF_BLIND);
     uint8_t* tok = base + L::OFF_TOK;
     Sync sy{sbase + (uint32_t)L::OFF_BAR, abort_flag, a.status};
     const uint32_t sK = sbase + L::OFF_K, sQ = sbase + L::OFF_Q;
+    constexpr bool split = WIDE;
     if (threadIdx.x == 0) {
         for (int s = 0; s < L::KS; ++s) {
             ptx::mbar_init(sy.bar(L::B_K_FULL + s), 1);
@@ -139,15 +154,17 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         }
         for (int s = 0; s < L::QS; ++s) {
             ptx::mbar_init(sy.bar(L::B_Q_FULL + s), 1);
-            ptx::mbar_init(sy.bar(L::B_L_FULL + s), 1);
-            ptx::mbar_init(sy.bar(L::B_Q_EMPTY + s), 9);
+            ptx::mbar_init(sy.bar(L::B_Q_EMPTY + s), 2);
         }
         for (int s = 0; s < 4; ++s) {
             ptx::mbar_init(sy.bar(L::B_S_FULL + s), 1);
-            ptx::mbar_init(sy.bar(L::B_S_EMPTY + s), 4);
+            ptx::mbar_init(sy.bar(L::B_S_EMPTY + s), WIDE ? 8 : 4);
+            ptx::mbar_init(sy.bar(L::B_PART + s), 4);       // (and B_TAKEN)
         }
         ptx::mbar_init(sy.bar(L::B_DRAIN), 1);
+        ptx::mbar_init(sy.bar(L::B_DRAIN + 1), 1);
         *abort_flag = 0u;
+        *rest = 0u;
         ptx::fence_barrier_init();
     }
     if (warp == 1) {
@@ -156,12 +173,50 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     }
     if (warp == 2)
         for (int i = lane; i < 128; i += 32) tok[i] = (uint8_t)(i < k.cols ? i % k.tb : 255);
+    // Rows of Q that no query fills are zeros, columns that no query has get a
+    // score of -2^127: both once and for all.
+    for (int i = threadIdx.x; i < L::QS * L::QTILE / 16; i += kWeightThreads)
+        reinterpret_cast<uint4*>(base + L::OFF_Q)[i] = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = threadIdx.x; i < 128 * 8; i += kWeightThreads) {
+        const int r = i >> 3, e = i & 7;                         // 16-byte unit e of row r
+        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+        if (e == 6) x = make_uint4(0x3f803f80u, 0x3f80u, 0u, 0u);            // 1, 1, 1
+        else if (e % 2 == 0 && r >= k.cols) x.x = 0xff00u;                   // -2^127
+        *reinterpret_cast<uint4*>(base + L::OFF_LSE + r * 128 + ((e ^ (r & 7)) << 4)) = x;
+    }
+    ptx::fence_proxy_async_smem();
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     Walk x;
     x.begin();
+    // Rows that no query sees stay as before.  One step copies the next kRest of
+    // the CTA's; false: none left.  The warps that have no columns
+    // take them from the start, the others what is left when they are done.
+    const int pieces = a.out == a.before ? 0 : (a.weight_rows + kRest - 1) / kRest;
+    const int64_t all = (int64_t)a.batch * a.kv_heads * pieces;
+    auto copy_step = [&]() -> bool {
+        int64_t p = 0;
+        if (lane == 0) p = (int64_t)atomicAdd(rest, 1u) * gridDim.x + blockIdx.x;
+        p = __shfl_sync(0xffffffffu, p, 0);
+        if (p >= all) return false;
+        const int u = (int)(p / pieces), r0 = (int)(p - (int64_t)u * pieces) * kRest;
+        const int r1 = min(a.weight_rows, r0 + kRest), from = max(r0, seq_of(k, u / a.kv_heads / a.layers).len);
+        const int64_t o = (int64_t)u * a.weight_rows;
+        float v[kRest / 32];
+#pragma unroll
+        for (int e = 0; e < kRest / 32; ++e) {
+            const int i = r0 + lane + 32 * e;
+            v[e] = a.before && i >= from && i < r1 ? a.before[o + i] : 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < kRest / 32; ++e) {
+            const int i = r0 + lane + 32 * e;
+            if (i >= from && i < r1) a.out[o + i] = v[e];
+        }
+        return true;
+    };
     if (warp == 0) {
         // ------------------------------------------------------------- K tiles
         // lane i holds the table entry of box i of the item (at most 16), and of
@@ -204,160 +259,223 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         }
         for (int s = 0; s < L::KS && s < kt; ++s)
             sy.drain(L::B_K_FULL + s, (uint32_t)(((kt - 1 - s) / L::KS) & 1));
-    } else if (warp == 1) {
-        // ----------------------------------------------------------- MMA issuer
+    } else if (warp == 1 || warp == 3) {
+        // ---------------------------------------------------------- MMA issuers
+        // one per slot: an issuer shares its scheduler with five other warps and
+        // takes about 800 cycles between two products, which is twice a product's time
+        const int slot = warp >> 1;
         const uint32_t idesc = ptx::idesc_bf16_f32(128, 16, false, false) - (uint32_t)((16 >> 3) << 17) +
                                ((uint32_t)(k.n >> 3) << 17);
         const uint32_t hi = (uint32_t)(ptx::sdesc_sw128(0, 16, 1024) >> 32);
         const uint32_t kb0 = (uint32_t)ptx::sdesc_sw128(sK, 16, 1024);
         const uint32_t qb0 = (uint32_t)ptx::sdesc_sw128(sQ, 16, 1024);
-        int kt = 0, qt = 0;
+        const uint32_t lb0 = (uint32_t)ptx::sdesc_sw128(sbase + L::OFF_LSE, 16, 1024);
+        int ks = slot, qs = 0;
+        uint32_t k_par = 0, q_par = 0, s_par = 1, buf = 0;
         bool ok = true;
         while (ok && x.next(k)) {
-            for (int b = x.b0; ok && b < x.blocks; ++b, ++qt) {
-                const int qs = qt % L::QS, buf = qt & 1;
-                if (!(ok = sy.wait(L::B_Q_FULL + qs, (uint32_t)((qt / L::QS) & 1), kSiteQFull))) break;
-                for (int slot = 0; ok && slot < 2; ++slot) {
-                    const int ks = (kt + slot) % L::KS;
-                    if (b == x.b0 &&
-                        !(ok = sy.wait(L::B_K_FULL + ks, (uint32_t)(((kt + slot) / L::KS) & 1), kSiteKvFull)))
-                        break;
-                    if (!(ok = sy.wait(L::B_S_EMPTY + 2 * slot + buf, (uint32_t)((qt >> 1) & 1) ^ 1u, kSiteSEmpty)))
-                        break;
-                    ptx::tc_fence_after();
-                    if (ptx::elect_one()) {
-                        const uint32_t kb = kb0 + (uint32_t)ks * (L::TILE >> 4), qb = qb0 + (uint32_t)qs * (L::TILE >> 4);
-#pragma unroll
-                        for (int kc = 0; kc < L::KCH; ++kc)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                ptx::umma_ss_lh(tmem + 256u * slot + 128u * buf, kb + kc * (L::CHUNK >> 4) + 2 * i, hi,
-                                                qb + kc * (L::CHUNK >> 4) + 2 * i, hi, idesc, (kc | i) ? 1u : 0u);
-                        ptx::umma_commit(sy.bar(L::B_S_FULL + 2 * slot + buf));
-                        if (slot == 1) ptx::umma_commit(sy.bar(L::B_Q_EMPTY + qs));
-                        if (b == x.blocks - 1) ptx::umma_commit(sy.bar(L::B_K_EMPTY + ks));
-                    }
-                    __syncwarp();
-                }
-            }
-            kt += 2;
-        }
-        if (ptx::elect_one()) ptx::umma_commit(sy.bar(L::B_DRAIN));
-        __syncwarp();
-        sy.drain(L::B_DRAIN, 0);
-    } else if (warp == 2) {
-        // ----------------------------------------------- queries and their lse
-        const uint32_t bytes = (uint32_t)k.cols * D * 2;
-        int qt = 0;
-        bool ok = true;
-        while (ok && x.next(k)) {
-            for (int b = x.b0; b < x.blocks; ++b, ++qt) {
-                const int s = qt % L::QS;
-                if (!(ok = sy.wait(L::B_Q_EMPTY + s, (uint32_t)((qt / L::QS) & 1) ^ 1u, kSiteKvEmpty))) break;
-                __syncwarp();
-                if (lane == 0) {
-                    ptx::mbar_arrive_expect_tx(sy.bar(L::B_Q_FULL + s), bytes);
+            if (!(ok = sy.wait(L::B_K_FULL + ks, k_par, kSiteKvFull))) break;
+            const uint32_t kb = kb0 + (uint32_t)ks * (L::TILE >> 4);
+            for (int left = x.blocks - x.b0; left > 0; --left) {
+                if (!(ok = sy.wait(L::B_Q_FULL + qs, q_par, kSiteQFull))) break;
+                if (!(ok = sy.wait(L::B_S_EMPTY + 2 * slot + (int)buf, s_par, kSiteSEmpty))) break;
+                ptx::tc_fence_after();
+                if (ptx::elect_one()) {
+                    const uint32_t qb = qb0 + (uint32_t)qs * (L::QTILE >> 4);
 #pragma unroll
                     for (int kc = 0; kc < L::KCH; ++kc)
-                        ptx::tma_load_4d(sQ + s * L::TILE + kc * L::CHUNK, &tm_q, sy.bar(L::B_Q_FULL + s), kc * 64,
-                                         b * k.tb, x.h * k.G, x.n);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            ptx::umma_ss_lh(tmem + 256u * slot + 128u * buf, kb + kc * (L::CHUNK >> 4) + 2 * i, hi,
+                                            qb + kc * (L::QCHUNK >> 4) + 2 * i, hi, idesc, (kc | i) ? 1u : 0u);
+                    ptx::umma_ss_lh(tmem + 256u * slot + 128u * buf, lb0 + 6, hi, lb0 + 2 * qs, hi, idesc, 1u);
+                    ptx::umma_commit(sy.bar(L::B_S_FULL + 2 * slot + (int)buf));
+                    ptx::umma_commit(sy.bar(L::B_Q_EMPTY + qs));
+                    if (left == 1) ptx::umma_commit(sy.bar(L::B_K_EMPTY + ks));
                 }
-                float* lse2 = reinterpret_cast<float*>(base + L::OFF_LSE) + s * 128;
-                bool none = false;
-                for (int i = lane; i < k.cols; i += 32) {
-                    const int g = i / k.tb, j = b * k.tb + tok[i];
-                    float v = INFINITY;
-                    if (j < x.q.count) {
-                        v = a.lse[((int64_t)x.n * a.q_heads + x.h * k.G + g) * a.tokens + j] * 1.4426950408889634f;
-                        if (v == -INFINITY) {
-                            v = INFINITY;
-                            none = true;
-                        }
-                    }
-                    lse2[i] = v;
-                }
-                none = __any_sync(0xffffffffu, none);
-                if (lane == 0) blind[s] = none;
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(sy.bar(L::B_L_FULL + s));
+                s_par ^= buf;
+                buf ^= 1u;
+                if (++qs == L::QS) {
+                    qs = 0;
+                    q_par ^= 1u;
+                }
+            }
+            if ((ks += 2) >= L::KS) {
+                ks -= L::KS;
+                k_par ^= 1u;
             }
         }
-        for (int s = 0; s < L::QS && s < qt; ++s)
-            sy.drain(L::B_Q_FULL + s, (uint32_t)(((qt - 1 - s) / L::QS) & 1));
-    } else if (warp == 3) {
-        // --------------------------------- rows that no query sees stay as before
-        if (a.out != a.before) {
-            const int units = a.batch * a.kv_heads;
-            for (int u = blockIdx.x; u < units; u += gridDim.x) {
-                const Seq q = seq_of(k, u / a.kv_heads / a.layers);
-                const int64_t o = (int64_t)u * a.weight_rows;
-#pragma unroll 8
-                for (int i = q.len + lane; i < a.weight_rows; i += 32) a.out[o + i] = a.before ? a.before[o + i] : 0.f;
-            }
+        if (ptx::elect_one()) ptx::umma_commit(sy.bar(L::B_DRAIN + slot));
+        __syncwarp();
+        sy.drain(L::B_DRAIN + slot, 0);
+        while (copy_step()) {}
+    } else if (warp == 2 || warp == 20) {
+        // -------------------------------------------- queries and log-sum-exps
+        // A block costs a warp 1700 cycles (the splitting, the stores, the latency
+        // of the next block's values), so there are two, with a stage each.
+        const int mine = warp == 2 ? 0 : 1;
+        const uint32_t bytes = (uint32_t)k.cols * D * 2;
+        int off[4];                                              // of this lane's columns in a block
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int i = lane + 32 * e;
+            off[e] = i < k.cols ? i / k.tb * a.tokens + tok[i] : -1;
         }
+        int b = 0, head = 0, n = 0, qt = 0;
+        uint32_t q_par = 1;
+        const float* src = nullptr;
+        auto item = [&]() -> bool {
+            if (!x.next(k)) return false;
+            b = x.b0;
+            head = x.h * k.G;
+            n = x.n;
+            src = a.lse + ((int64_t)n * a.q_heads + head) * a.tokens + b * k.tb;
+            return true;
+        };
+        bool have = item();
+        auto advance = [&](int count) {
+            for (; have && count > 0; --count) {
+                ++qt;
+                src += k.tb;
+                if (++b == x.blocks) have = item();
+            }
+        };
+        advance(mine);
+        auto read = [&](float (&v)[4]) {
+            const int upto = x.q.count - b * k.tb;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                v[e] = off[e] >= 0 && (upto >= k.tb || tok[lane + 32 * e] < upto) ? src[off[e]] : 0.f;
+        };
+        // one block: its log-sum-exps are in v, the next one's go to w
+        auto step = [&](const float (&v)[4], float (&w)[4]) -> bool {
+            const int at = qt, b_at = b, head_at = head, n_at = n;
+            advance(L::QS);
+            if (have) read(w);
+            if (!sy.wait(L::B_Q_EMPTY + mine, q_par, kSiteKvEmpty)) return false;
+            if (ptx::elect_one()) {
+                ptx::mbar_expect_tx(sy.bar(L::B_Q_FULL + mine), bytes);
+#pragma unroll
+                for (int kc = 0; kc < L::KCH; ++kc)
+                    ptx::tma_load_4d(sQ + mine * L::QTILE + kc * L::QCHUNK, &tm_q, sy.bar(L::B_Q_FULL + mine), kc * 64,
+                                     b_at * k.tb, head_at, n_at);
+            }
+            __syncwarp();
+            uint32_t none = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int r = lane + 32 * e;
+                if (off[e] >= 0) {
+                    // -lse / scale = hi + mid + lo
+                    const float y = v[e] * k.minus_inv_scale;
+                    const float hi = __bfloat162float(__float2bfloat16(y)), y1 = y - hi;
+                    const float mid = __bfloat162float(__float2bfloat16(y1));
+                    *reinterpret_cast<uint2*>(base + L::OFF_LSE + r * 128 + (((2 * mine) ^ (r & 7)) << 4)) =
+                        make_uint2(ptx::pack_bf16x2(hi, mid), ptx::pack_bf16x2(y1 - mid, 0.f));
+                }
+                const uint32_t who = __ballot_sync(0xffffffffu, fabsf(v[e]) == INFINITY);
+                if (lane == e) none = who;
+            }
+            if (lane < 4) blind[4 * (at & 7) + lane] = none;
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(sy.bar(L::B_Q_FULL + mine));
+            q_par ^= 1u;
+            return have;
+        };
+        // (two sets by turns: moving one to the other would wait for its loads)
+        float v[4], w[4];
+        if (have) read(v);
+        while (have && step(v, w) && step(w, v)) {}
+        // never leave a copy in flight into this CTA's shared memory
+        sy.drain(L::B_Q_FULL + mine, q_par);
+        while (copy_step()) {}
     } else {
         // --------------------------------------------------------- exponentials
-        const int slot = (warp - 4) >> 2, q4 = warp & 3;
+        // slot and half of its columns
+        const int slot = (warp >> 2) - 1 & 1, half = (warp - 4) >> 3, q4 = warp & 3;
         const int lrow = q4 * 32 + lane;                         // key of the tile = TMEM lane
         const uint32_t t_s = tmem + 256u * slot + ((uint32_t)(q4 * 32) << 16);
-        const float2 sc = make_float2(k.scale_log2, k.scale_log2);
-        int qt = 0;
-        bool ok = true;
-        while (ok && x.next(k)) {
+        const float sc = k.scale_log2;
+        volatile float* part = reinterpret_cast<volatile float*>(base + L::OFF_PART) + slot * 128 + lrow;
+        const int c_begin = 64 * half, c_end = split && half == 0 ? 64 : k.n;
+        uint32_t s_par = 0, item = 0, buf = 0, qt = 0;
+        bool ok = split || half == 0;
+        for (; ok && x.next(k); ++item) {
             const int row = x.row0 + slot * kTile + lrow;
             const int64_t at = ((int64_t)x.n * a.kv_heads + x.h) * a.weight_rows + row;
-            const bool live = row < x.q.len;
+            const bool live = half == 0 && row < x.q.len;
             const float before = live && a.before ? a.before[at] : 0.f;
             const int first_new = x.q.len - x.q.count;
             float total = 0.f;
-            for (int b = x.b0; b < x.blocks; ++b, ++qt) {
-                const int s = qt % L::QS, buf = qt & 1;
-                if (!(ok = sy.wait(L::B_L_FULL + s, (uint32_t)((qt / L::QS) & 1), kSiteQFull))) break;
-                if (!(ok = sy.wait(L::B_S_FULL + 2 * slot + buf, (uint32_t)((qt >> 1) & 1), kSiteSFull))) break;
+            for (int b = x.b0; b < x.blocks; ++b) {
+                if (!(ok = sy.wait(L::B_S_FULL + 2 * slot + (int)buf, s_par, kSiteSFull))) break;
                 __syncwarp();
                 ptx::tc_fence_after();
-                const float* lse2 = reinterpret_cast<const float*>(base + L::OFF_LSE) + s * 128;
+                const uint32_t t_b = t_s + 128u * buf;
                 const int j0 = b * k.tb;
                 // tokens of the block that see this row: from `from` to `upto`
                 const int from = row - first_new - j0, upto = x.q.count - j0;
-                const bool special = x.row0 + kItem > first_new + j0 + 1 || upto < k.tb || blind[s] != 0u;
+                volatile uint32_t* unseen = blind + 4 * (qt & 7);
                 float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                if (x.row0 + kItem > first_new + j0 + 1 || upto < k.tb ||
+                    (unseen[0] | unseen[1] | unseen[2] | unseen[3]) != 0u) {
 #pragma unroll 1
-                for (int c0 = 0; c0 < k.cols; c0 += 32) {
-                    uint32_t v[32];
-                    ptx::tmem_ld_32x32b_x32(t_s + 128u * buf + c0, v);
-                    ptx::tmem_ld_wait();
-                    if (special || c0 + 32 > k.cols) {
+                    for (int c = c_begin; c < c_end; c += 16) {
+                        uint32_t v[16];
+                        __syncwarp();
+                        ptx::tmem_ld_32x32b_x16(t_b + c, v);
+                        ptx::tmem_ld_wait();
+                        const uint32_t gone = unseen[c >> 5] >> (c & 31);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const int j = tok[c0 + e];
-                            const float m = lse2[c0 + e];
-                            const float y = ptx::ex2_approx(fmaf(__uint_as_float(v[e]), sc.x, -m));
-                            if (c0 + e < k.cols && j >= from && j < upto && m != INFINITY) sum[e & 1].x += y;
-                        }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            const float4 m = *reinterpret_cast<const float4*>(lse2 + c0 + e);
-                            const float2 z0 = ptx::fma2(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sc,
-                                                        make_float2(-m.x, -m.y));
-                            const float2 z1 = ptx::fma2(make_float2(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])),
-                                                        sc, make_float2(-m.z, -m.w));
-                            sum[0] = ptx::add2(sum[0], make_float2(ptx::ex2_approx(z0.x), ptx::ex2_approx(z0.y)));
-                            sum[1] = ptx::add2(sum[1], make_float2(ptx::ex2_approx(z1.x), ptx::ex2_approx(z1.y)));
+                        for (int e = 0; e < 16; ++e) {
+                            const int j = tok[c + e];
+                            const float y = ptx::ex2_approx(__uint_as_float(v[e]) * sc);
+                            sum[e & 1].x += c + e < k.cols && j >= from && j < upto && !(gone >> e & 1u) ? y : 0.f;
                         }
                     }
-                }
-                ptx::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    ptx::mbar_arrive(sy.bar(L::B_S_EMPTY + 2 * slot + buf));
-                    ptx::mbar_arrive(sy.bar(L::B_Q_EMPTY + s));
+                } else {
+                    // the next 16 columns are on their way while these are added
+                    uint32_t v[2][16];
+                    ptx::tmem_ld_32x32b_x16(t_b + c_begin, v[0]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int c = c_begin + 16 * i;
+                        if (c >= c_end) break;
+                        ptx::tmem_ld_wait();
+                        if (i < 3 && c + 16 < c_end) ptx::tmem_ld_32x32b_x16(t_b + c + 16, v[(i + 1) & 1]);
+                        const uint32_t (&x16)[16] = v[i & 1];
+#pragma unroll
+                        for (int e = 0; e < 16; e += 2)
+                            sum[(e >> 1) & 1] = ptx::add2(sum[(e >> 1) & 1],
+                                                          make_float2(ptx::ex2_approx(__uint_as_float(x16[e]) * sc),
+                                                                      ptx::ex2_approx(__uint_as_float(x16[e + 1]) * sc)));
+                    }
                 }
                 total += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(sy.bar(L::B_S_EMPTY + 2 * slot + (int)buf));
+                s_par ^= buf;
+                buf ^= 1u;
+                ++qt;
+            }
+            if (ok && split) {
+                // the second half's sum joins the first's
+                if (half == 1) {
+                    if (!(ok = sy.wait(L::B_TAKEN + slot, (item & 1u) ^ 1u, kSiteCol))) break;
+                    *part = total;
+                } else {
+                    if (!(ok = sy.wait(L::B_PART + slot, item & 1u, kSiteCol))) break;
+                    total += *part;
+                }
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(sy.bar((half == 1 ? L::B_PART : L::B_TAKEN) + slot));
             }
             if (ok && live) a.out[at] = before + total;
         }
+        while (copy_step()) {}
     }
     __syncthreads();
     if (warp == 1) {
@@ -366,14 +484,14 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     }
 }
 
-template <int D>
+template <int D, bool WIDE>
 cudaError_t launch_weights(const WeightKernelArgs& k, const CUtensorMap& mk, const CUtensorMap& mq, int dev, int grid,
                            cudaStream_t st) {
-    using L = WeightLayout<D>;
+    using L = WeightLayout<D, WIDE>;
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(&weights_kernel<D>), L::SMEM, dev, done);
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(&weights_kernel<D, WIDE>), L::SMEM, dev, done);
     if (e != cudaSuccess) return e;
-    weights_kernel<D><<<(unsigned)grid, kWeightThreads, L::SMEM, st>>>(mk, mq, k);
+    weights_kernel<D, WIDE><<<(unsigned)grid, kWeightThreads, L::SMEM, st>>>(mk, mq, k);
     return cudaGetLastError();
 }
 
@@ -414,6 +532,7 @@ extern "C" int statekv_attention_weights(const statekv_attention_weights_args* a
     k.cols = k.tb * G;
     k.n = (k.cols + 15) / 16 * 16;
     k.scale_log2 = (float)(a.scale * 1.4426950408889634074);
+    k.minus_inv_scale = (float)(-1.0 / a.scale);
     k.capacity = cached ? (int)pg.capacity() : 0;
     k.box = kTile;
     if (a.table)
@@ -427,7 +546,10 @@ extern "C" int statekv_attention_weights(const statekv_attention_weights_args* a
     const int64_t items = (int64_t)a.batch * a.kv_heads * ((most + kItem - 1) / kItem);
     const int grid = (int)std::min<int64_t>(sms, std::max<int64_t>(items, (int64_t)a.batch * a.kv_heads));
     cudaStream_t st = reinterpret_cast<cudaStream_t>(cuda_stream);
-    const cudaError_t e = a.head_dim == 128 ? launch_weights<128>(k, mk, mq, dev, grid, st)
-                                            : launch_weights<64>(k, mk, mq, dev, grid, st);
+    const bool wide = k.cols > 64;
+    const cudaError_t e = a.head_dim == 128 ? wide ? launch_weights<128, true>(k, mk, mq, dev, grid, st)
+                                                   : launch_weights<128, false>(k, mk, mq, dev, grid, st)
+                          : wide            ? launch_weights<64, true>(k, mk, mq, dev, grid, st)
+                                            : launch_weights<64, false>(k, mk, mq, dev, grid, st);
     return e == cudaSuccess ? STATEKV_OK : view_cuda_fail();
 }

@@ -42,16 +42,21 @@ __device__ __forceinline__ int page_at(const Paging& p, int n, int i, uint32_t* 
     return -1;
 }
 
-// New tokens of sequence s among its len rows: the array's entry or `tokens`,
-// recorded and clamped where it is out of range.
-__device__ __forceinline__ int new_tokens(const int32_t* counts, int tokens, int s, int len, uint32_t* err) {
-    const int most = tokens < len ? tokens : len;
-    int c = counts ? counts[s] : tokens;
-    if (c < 0 || c > most) {
-        record_error(err, (uint32_t)STATEKV_E_DEVICE, kSiteLength, (uint32_t)c);
-        c = c < 0 ? 0 : most;
-    }
-    return c;
+// Rows of a sequence in the cache, and the new tokens among them.
+struct Seq {
+    int len, count;
+};
+// Of sequence s: the arrays' entries (both read at once) or the common values,
+// recorded and clamped where they are out of range.
+template <class Args>
+__device__ __forceinline__ Seq sequence_of(const Args& a, int capacity, int s) {
+    int len = a.lengths ? a.lengths[s] : a.length, count = a.counts ? a.counts[s] : a.tokens;
+    const int len0 = len, count0 = count;
+    len = min(max(len, 0), capacity);
+    count = min(max(count, 0), min(a.tokens, len));
+    if (len != len0 || count != count0)
+        record_error(a.status, (uint32_t)STATEKV_E_DEVICE, kSiteLength, (uint32_t)(len != len0 ? len0 : count0));
+    return {len, count};
 }
 #endif
 

@@ -26,18 +26,17 @@
 // A "job" is one S = Q K^T, softmax, O += P V of a slot; the issuer runs S two
 // jobs ahead of P V, so one slot's exponentials overlap the other's products.
 // The next unit's first scores are computed while the last one's output is
-// written; two otherwise idle warps copy its Q.  P (bf16 pairs) overwrites its
+// written; a warp copies its Q.  P (bf16 pairs) overwrites its
 // own S buffer: the products of one thread run in issue order, and S of a
 // slot's next job is issued after P V of its last.  That order also makes
 // S(next) complete imply P V(last) complete, so a warp that raises its
 // reference may rescale O right away.
 //
 // Pages: a tile is copied in boxes of the largest power of two of rows (16..128)
-// that divides a page, so no box crosses a page's end.  Each lane of the
-// producer warp holds the place of one of the next 32 boxes and the table entry
-// of one of the 32 after them: table reads are off the critical path but at a
-// unit's start (a serial lookup per tile would cost a load's latency, half of a
-// tile's time).  Boxes past the sequence's end are asked for at a page that does
+// that divides a page, so no box crosses a page's end.  K and V have a producer
+// warp each (the same code, once in the instruction cache).  Each lane holds the
+// page of one of the next 32 boxes and the table entry of one of the 32 after
+// them: table reads are off the critical path but at a unit's start.  Boxes past the sequence's end are asked for at a page that does
 // not exist, which TMA fills with zeros without reading anything.
 //
 // Precision: S, m, l and O in fp32; P is rounded to bf16 for the product (as
@@ -94,15 +93,7 @@ __device__ __forceinline__ int token_of(const PagedKernelArgs& k, int r) {
     return k.G == 1 ? r : (int)__umulhi((uint32_t)r, k.inv_group);
 }
 
-struct Seq {
-    int len, count;                          // rows in the cache, new tokens among them
-};
-__device__ __forceinline__ Seq seq_of(const PagedKernelArgs& k, int s) {
-    Seq q;
-    q.len = cache_length(k.a.lengths, k.a.length, s, k.capacity, k.a.status);
-    q.count = new_tokens(k.a.counts, k.a.tokens, s, q.len, k.a.status);
-    return q;
-}
+__device__ __forceinline__ Seq seq_of(const PagedKernelArgs& k, int s) { return sequence_of(k.a, k.capacity, s); }
 
 // Cache rows that block b's last token sees (0: no token in it), and their tiles.
 __device__ __forceinline__ int block_keys(const PagedKernelArgs& k, Seq q, int b) {
@@ -156,10 +147,10 @@ __device__ __forceinline__ Plan make_plan(const PagedKernelArgs& k) {
     return p;
 }
 
-// A place in the schedule: unit (s, head nh of layers x KV heads, block b), and
-// how far into its cost.
+// A place in the schedule: unit (sequence s, batch entry n, KV head h, block b),
+// and how far into its cost.
 struct Place {
-    int s, nh, b, v;
+    int s, n, h, b, v;
     Seq q;
 };
 
@@ -205,8 +196,11 @@ __device__ __forceinline__ Place find(const PagedKernelArgs& k, uint32_t w) {
             w -= cost * heads;
         }
     }
-    p.nh = (int)(w / cost);
-    w -= (uint32_t)p.nh * cost;
+    const int nh = (int)(w / cost);
+    w -= (uint32_t)nh * cost;
+    p.n = nh / k.a.kv_heads;
+    p.h = nh - p.n * k.a.kv_heads;
+    p.n += p.s * k.a.layers;
     if (k.rb > 1) {
         uint32_t base = 0;
         for (int b0 = 0; b0 < k.rb; b0 += 32) {
@@ -244,9 +238,8 @@ struct Walk {
     Seq q;
     __device__ bool next(const PagedKernelArgs& k) {
         while (left > 0) {
-            n = at.nh / k.a.kv_heads;
-            h = at.nh - n * k.a.kv_heads;
-            n += at.s * k.a.layers;
+            n = at.n;
+            h = at.h;
             b = at.b;
             q = at.q;
             keys = block_keys(k, q, b);
@@ -263,9 +256,9 @@ struct Walk {
                 later = true;
                 if (++at.b == k.rb) {
                     at.b = 0;
-                    if (++at.nh == k.a.layers * k.a.kv_heads) {
-                        at.nh = 0;
-                        if (++at.s < k.a.batch / k.a.layers) at.q = seq_of(k, at.s);
+                    if (++at.h == k.a.kv_heads) {
+                        at.h = 0;
+                        if (++at.n == (at.s + 1) * k.a.layers && at.n < k.a.batch) at.q = seq_of(k, ++at.s);
                     }
                 }
             }
@@ -318,7 +311,6 @@ struct PagedLayout {
     // as many stages as fit beside Q
     static constexpr int KS = D == 64 ? 6 : 3;
     static constexpr int VS = D == 64 ? 5 : (SPLIT_ROWS ? 2 : 3);
-    static constexpr int LEAD = SPLIT_ROWS ? 1 : 2;      // K tiles loaded ahead of V, as S runs ahead of P V
     static constexpr int OFF_K = 0;
     static constexpr int OFF_V = OFF_K + KS * TILE;
     static constexpr int OFF_Q = OFF_V + VS * TILE;      // [RT] row tiles
@@ -327,7 +319,7 @@ struct PagedLayout {
     static constexpr int B_K_EMPTY = B_K_FULL + KS;
     static constexpr int B_V_FULL = B_K_EMPTY + KS;
     static constexpr int B_V_EMPTY = B_V_FULL + VS;
-    static constexpr int B_Q_FULL = B_V_EMPTY + VS;      // Q of the segment stored (2 warps)
+    static constexpr int B_Q_FULL = B_V_EMPTY + VS;      // Q of the segment stored
     static constexpr int B_Q_FREE = B_Q_FULL + 1;        // the segment's last S is done
     static constexpr int B_S_FULL = B_Q_FREE + 1;        // [2 slots]
     static constexpr int B_P_FULL = B_S_FULL + 2;        // [2 slots][2 halves of 64 keys] (4 warps)
@@ -363,123 +355,35 @@ paged_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
     }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    // every warp finds the CTA's share by itself
-    const int c = (int)blockIdx.x;
-    Walk first{};
-    if (k.whole) {
-        const int per_seq = a.layers * a.kv_heads * k.rb;
-        first.at.s = c / per_seq;
-        first.at.nh = (c - first.at.s * per_seq) / k.rb;
-        first.at.b = c % k.rb;
-        first.at.q = seq_of(k, first.at.s);
-        first.left = block_tiles(k, first.at.q, first.at.b) + kUnitCost;
-    } else {
-        const Plan plan = make_plan(k);
-        if (c >= (int)plan.ctas) return;
-        first.at = find(k, plan.start((uint32_t)c));
-        first.left = (int)(plan.start((uint32_t)c + 1) - plan.start((uint32_t)c));
-    }
-
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + L::OFF_MISC);
     volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(base + L::OFF_MISC + 4);
     uint32_t* odd_rows = reinterpret_cast<uint32_t*>(base + L::OFF_ODD);
     Sync sy{sbase + (uint32_t)L::OFF_BAR, abort_flag, a.status};
     const uint32_t sK = sbase + L::OFF_K, sV = sbase + L::OFF_V, sQ = sbase + L::OFF_Q;
-    // the next key tile of the share into its ring (the whole warp 0); 1 loaded,
-    // 0 none left, -1 gave up
-    Walk wk = first, wv = first;
-    wk.tiles = wv.tiles = 0;
-    Boxes bk{-1, -1, -1}, bv{-1, -1, -1};
-    int kt = 0, vt = 0;                                  // tiles loaded
-    auto load = [&](bool is_v) -> int {
-        Walk& x = is_v ? wv : wk;
-        Boxes& bo = is_v ? bv : bk;
-        const int per_tile = kTile / k.box;
-        if (x.tiles == 0) {
-            if (!x.next_tiles(k)) return 0;
-            bo.begin(k, x, x.t * per_tile / 32);
-        } else if (x.t * per_tile / 32 != bo.chunk) {
-            bo.advance(k, x);
+    // Nothing but barriers and tensor memory is set up together; every warp then
+    // finds the CTA's share by itself and starts, the producers with the first loads.
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < L::KS; ++s) {
+            ptx::mbar_init(sy.bar(L::B_K_FULL + s), 1);
+            ptx::mbar_init(sy.bar(L::B_K_EMPTY + s), 1);
         }
-        int& cnt = is_v ? vt : kt;
-        const int ns = is_v ? L::VS : L::KS;
-        const int s = cnt % ns, j = cnt / ns;
-        if (!sy.wait((is_v ? L::B_V_EMPTY : L::B_K_EMPTY) + s, (uint32_t)(j & 1) ^ 1u, kSiteKvEmpty)) return -1;
-        const uint32_t fb = sy.bar((is_v ? L::B_V_FULL : L::B_K_FULL) + s);
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive_expect_tx(fb, L::TILE);
-        __syncwarp();
-        // lane i copies 64 columns of box i / KCH of the tile
-        const int i = lane / L::KCH, kc = lane % L::KCH;
-        const int bx = x.t * per_tile + i;
-        const int page = __shfl_sync(0xffffffffu, bo.page, bx & 31);
-        if (i < per_tile) {
-            const int row = page < 0 ? 0 : a.table ? (bx % k.page_boxes) * k.box : bx * k.box;
-            ptx::tma_load_4d((is_v ? sV : sK) + s * L::TILE + kc * L::CHUNK + i * k.box * 128, is_v ? &tm_v : &tm_k,
-                             fb, kc * 64, row, x.h, page);
+        for (int s = 0; s < L::VS; ++s) {
+            ptx::mbar_init(sy.bar(L::B_V_FULL + s), 1);
+            ptx::mbar_init(sy.bar(L::B_V_EMPTY + s), 1);
         }
-        __syncwarp();
-        ++cnt;
-        ++x.t;
-        --x.tiles;
-        return 1;
-    };
-    // a block's rows r = token * G + g of Q, zeros past the last of the
-    // sequence's, into shared memory (warps 2 and 3, asynchronously)
-    auto copy_q = [&](const Walk& x) {
-        constexpr int UPR = D / 8;                       // 16-byte units per row
-        constexpr int STEP = 64 / UPR;                   // rows at a time: 4 or 8
-        const int qt = (int)threadIdx.x - 64, e = qt % UPR, r0 = qt / UPR;
-        const int row_base = x.b * k.block;
-        int j = token_of(k, row_base + r0), g = row_base + r0 - j * k.G;
-        const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(a.q.data) + x.n * a.q.batch_stride +
-                                 (int64_t)(x.h * k.G + g) * a.q.head_stride + (int64_t)j * a.q.token_stride + 8 * e;
-        const int64_t row = STEP * a.q.head_stride, wrap = a.q.token_stride - k.G * a.q.head_stride;
-        const int left = k.G * x.q.count - row_base;
-        const void* some = a.q.data;                     // (nothing is read for the zeros)
-#pragma unroll 4
-        for (int r = r0; r < L::RT * kTile; r += STEP) {
-            ptx::cp_async_16(sQ + (r / kTile) * L::TILE + (e >> 3) * L::CHUNK + (r % kTile) * 128 +
-                                 (((e & 7) ^ (r & 7)) << 4),
-                             r < left ? static_cast<const void*>(p) : some, r < left ? 16u : 0u);
-            p += row;
-            for (g += STEP; g >= k.G; g -= k.G) p += wrap;
+        ptx::mbar_init(sy.bar(L::B_Q_FULL), 1);
+        ptx::mbar_init(sy.bar(L::B_Q_FREE), 1);
+        for (int s = 0; s < 2; ++s) {
+            ptx::mbar_init(sy.bar(L::B_S_FULL + s), 1);
+            ptx::mbar_init(sy.bar(L::B_P_FULL + 2 * s), 4);
+            ptx::mbar_init(sy.bar(L::B_P_FULL + 2 * s + 1), 4);
         }
-    };
-    if (warp == 0) {
-        if (lane == 0) {
-            for (int s = 0; s < L::KS; ++s) {
-                ptx::mbar_init(sy.bar(L::B_K_FULL + s), 1);
-                ptx::mbar_init(sy.bar(L::B_K_EMPTY + s), 1);
-            }
-            for (int s = 0; s < L::VS; ++s) {
-                ptx::mbar_init(sy.bar(L::B_V_FULL + s), 1);
-                ptx::mbar_init(sy.bar(L::B_V_EMPTY + s), 1);
-            }
-            ptx::mbar_init(sy.bar(L::B_Q_FULL), 2);
-            ptx::mbar_init(sy.bar(L::B_Q_FREE), 1);
-            for (int s = 0; s < 2; ++s) {
-                ptx::mbar_init(sy.bar(L::B_S_FULL + s), 1);
-                ptx::mbar_init(sy.bar(L::B_P_FULL + 2 * s), 4);
-                ptx::mbar_init(sy.bar(L::B_P_FULL + 2 * s + 1), 4);
-            }
-            ptx::mbar_init(sy.bar(L::B_O_FULL), 1);
-            ptx::mbar_init(sy.bar(L::B_SYNC), 8);
-            ptx::mbar_init(sy.bar(L::B_DRAIN), 1);
-            *abort_flag = 0u;
-            for (int i = 0; i < 2 * kOddWords; ++i) odd_rows[i] = 0u;
-            ptx::fence_barrier_init();
-        }
-        __syncwarp();
-        // the first tiles are on their way while the rest is set up (the
-        // stages are empty: no wait)
-        static_assert(L::LEAD <= L::KS, "no wait before every barrier is visible");
-        for (int t = 0; t < L::LEAD; ++t) load(false);
-        load(true);
-    }
-    if (warp == 2 || warp == 3) {
-        Walk x = first;
-        if (x.next_tiles(k)) copy_q(x);
+        ptx::mbar_init(sy.bar(L::B_O_FULL), 1);
+        ptx::mbar_init(sy.bar(L::B_SYNC), 8);
+        ptx::mbar_init(sy.bar(L::B_DRAIN), 1);
+        *abort_flag = 0u;
+        for (int i = 0; i < 2 * kOddWords; ++i) odd_rows[i] = 0u;
+        ptx::fence_barrier_init();
     }
     if (warp == 1) {
         ptx::tmem_alloc(ptx::smem_u32(tmem_slot), L::TMEM_COLS);
@@ -493,19 +397,68 @@ paged_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
     // grid to end.  Otherwise the next kernel is not ours to release: it gets
     // the implicit release at this grid's end.
     if (k.merge) ptx::dep_trigger();
+    const int c = (int)blockIdx.x;
+    Walk first{};                            // (no share: nothing left)
+    if (k.whole) {
+        const int per_seq = a.layers * a.kv_heads * k.rb;
+        first.at.s = c / per_seq;
+        const int nh = c / k.rb;
+        first.at.n = nh / a.kv_heads;
+        first.at.h = nh - first.at.n * a.kv_heads;
+        first.at.b = c - nh * k.rb;
+        first.at.q = seq_of(k, first.at.s);
+        first.left = block_tiles(k, first.at.q, first.at.b) + kUnitCost;
+    } else {
+        const Plan plan = make_plan(k);
+        if (c < (int)plan.ctas) {
+            first.at = find(k, plan.start((uint32_t)c));
+            first.left = (int)(plan.start((uint32_t)c + 1) - plan.start((uint32_t)c));
+        }
+    }
     if (warp < 4) {
         ptx::regs_dec<kRegsIssue>();
-        if (warp == 0) {
-            // ------------------------------------------------------ TMA producer
-            for (int got = 1; got >= 0;) {
-                got = load(false);
-                if (got >= 0 && load(true) <= 0) break;
+        if (warp == 0 || warp == 3) {
+            // ------------------------------------- TMA producers: K (0) and V (3)
+            const bool is_v = warp == 3;
+            const CUtensorMap* map = is_v ? &tm_v : &tm_k;
+            const uint32_t dst = (is_v ? sV : sK) + (uint32_t)(lane % L::KCH) * L::CHUNK +
+                                 (uint32_t)(lane / L::KCH * k.box) * 128;
+            const int full = is_v ? L::B_V_FULL : L::B_K_FULL, empty = is_v ? L::B_V_EMPTY : L::B_K_EMPTY;
+            const int stages = is_v ? L::VS : L::KS;
+            const int per_tile = kTile / k.box, column = lane % L::KCH * 64, mine = lane / L::KCH;
+            Walk x = first;
+            Boxes bo{};
+            int s = 0, loaded = 0;
+            uint32_t par = 1;
+            bool ok = true;
+            while (ok && x.next_tiles(k)) {
+                bo.begin(k, x, x.t * per_tile / 32);
+                int bx = x.t * per_tile + mine;                  // this lane's box (lanes past the tile's: none)
+                int in_page = a.table ? bx % k.page_boxes : bx;
+                for (; x.tiles > 0; --x.tiles) {
+                    if ((bx - mine) >> 5 != bo.chunk) bo.advance(k, x);
+                    const int page = __shfl_sync(0xffffffffu, bo.page, bx & 31);
+                    if (!(ok = sy.wait(empty + s, par, kSiteKvEmpty))) break;
+                    if (lane == 0) ptx::mbar_arrive_expect_tx(sy.bar(full + s), L::TILE);
+                    __syncwarp();
+                    if (mine < per_tile)
+                        ptx::tma_load_4d(dst + s * L::TILE, map, sy.bar(full + s), column, page < 0 ? 0 : in_page * k.box,
+                                         x.h, page);
+                    ++loaded;
+                    if (++s == stages) {
+                        s = 0;
+                        par ^= 1u;
+                    }
+                    bx += per_tile;
+                    in_page += per_tile;
+                    if (a.table)
+                        while (in_page >= k.page_boxes) in_page -= k.page_boxes;
+                }
             }
+            __syncwarp();
             // never leave a copy in flight into this CTA's shared memory
-            for (int s = 0; s < L::KS && s < kt; ++s)
-                sy.drain(L::B_K_FULL + s, (uint32_t)(((kt - 1 - s) / L::KS) & 1));
-            for (int s = 0; s < L::VS && s < vt; ++s)
-                sy.drain(L::B_V_FULL + s, (uint32_t)(((vt - 1 - s) / L::VS) & 1));
+            for (int i = 0; i < stages && i < loaded; ++i)
+                sy.drain(full + i, (uint32_t)(((loaded - 1 - i) / stages) & 1));
         } else if (warp == 1) {
             // -------------------------------------------------------- MMA issuer
             constexpr uint32_t idesc_s = ptx::idesc_bf16_f32(128, 128, false, false);
@@ -581,13 +534,26 @@ paged_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
             sy.drain(L::B_DRAIN, 0);
         } else {
             // --------------------------------------------------------- Q copier
-            // (warps 2 and 3) a unit's rows as soon as the unit before needs Q no
-            // more: its last softmax and its output hide the copy
+            // A block's rows r = token * G + g, as soon as the unit before needs Q
+            // no more: its last softmax and its output hide the copy.  Rows past
+            // the sequence's tokens are not filled (a row's score reaches no other).
+            constexpr int UPR = D / 8;                           // 16-byte units per row
+            constexpr int STEP = 32 / UPR;                       // rows at a time: 2 or 4
+            const int e = lane % UPR, r0 = lane / UPR;
+            const int64_t row = STEP * a.q.head_stride, wrap = a.q.token_stride - k.G * a.q.head_stride;
             Walk x = first;
             for (int seg = 0; x.next_tiles(k); ++seg) {
-                if (seg > 0) {
-                    if (!sy.wait(L::B_Q_FREE, (uint32_t)((seg - 1) & 1), kSiteQFull)) break;
-                    copy_q(x);
+                if (seg > 0 && !sy.wait(L::B_Q_FREE, (uint32_t)((seg - 1) & 1), kSiteQFull)) break;
+                const int row_base = x.b * k.block, rows = min(L::RT * kTile, k.G * x.q.count - row_base);
+                int j = token_of(k, row_base + r0), g = row_base + r0 - j * k.G;
+                const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(a.q.data) + x.n * a.q.batch_stride +
+                                         (int64_t)(x.h * k.G + g) * a.q.head_stride + (int64_t)j * a.q.token_stride + 8 * e;
+                uint32_t dst = sQ + (e >> 3) * L::CHUNK;
+#pragma unroll 4
+                for (int r = r0; r < rows; r += STEP) {
+                    ptx::cp_async_16(dst + (r / kTile) * L::TILE + (r % kTile) * 128 + (((e & 7) ^ (r & 7)) << 4), p, 16u);
+                    p += row;
+                    for (g += STEP; g >= k.G; g -= k.G) p += wrap;
                 }
                 ptx::cp_async_wait();
                 ptx::fence_proxy_async_smem();
@@ -716,7 +682,7 @@ paged_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
                         for (int b = 0; b < 2; ++b)
                             mx[b] = ptx::max3(mx[b], __uint_as_float(x[b][e]), __uint_as_float(x[b][e + 1]));
                     const float top = fmaxf(mx[0], mx[1]) * sc;
-                    const bool raise = top > m + kSlack;
+                    const bool raise = sees && top > m + kSlack;   // (other rows' queries are anything)
                     if (__any_sync(0xffffffffu, raise)) {
                         const float f = raise ? ptx::ex2_approx(m - top) : 1.f;
                         if (raise) m = top;
@@ -801,7 +767,7 @@ paged_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
             if (cu.keys > common)
                 for (int i = 0; i < kOddWords; ++i) any_odd |= odd[i] != 0u;
             const int64_t place = 2 * (int64_t)c + cu.part;
-            const float inv = whole ? (l > 0.f || l != l ? 1.f / l : 0.f) : 1.f;
+            const float inv = !whole ? 1.f : sees && (l > 0.f || l != l) ? 1.f / l : 0.f;
             if (!idle) {
 #pragma unroll 1
                 for (int cc = 0; cc < COLS; cc += 32) {
@@ -925,7 +891,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_combine_kernel(const __gr
     const int ca = (int)plan.cta_of(w + kUnitCost), cb = (int)plan.cta_of(w + kUnitCost + (uint32_t)nt - 1);
     const int segs = cb - ca + 1;
     if (segs == 1) return;                   // written by the one CTA
-    const int n = p.s * a.layers + p.nh / a.kv_heads, h = p.nh % a.kv_heads;
+    const int n = p.n, h = p.h;
     const int rows = min(k.block, k.R - p.b * k.block);
     const int outs = rows * (D / 4);
     const int ways = segs > kFew ? kWays : 1;

@@ -60,13 +60,15 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __gr
 // 11 + 11 + 10 of them, -0 = 0, NaN lowest; rows that stay anyway rank above
 // all), ties by row.  One cluster per (batch entry, KV head), each CTA a
 // contiguous run of rows, in shared memory where it fits (it does up to 40960
-// rows a CTA); the histograms are summed through distributed shared memory, and
-// every CTA finds the threshold for itself.  A warp owns a contiguous run of its
-// CTA's rows, so that a row's place among the kept is a sum of the counts
-// before it.
-constexpr int kEvictThreads = 512;
+// rows a CTA).  Of the cluster's histograms each CTA sums a part of the bins
+// through distributed shared memory; the part that holds the threshold names it
+// to all.  (Every CTA summing every bin read 128 KB a pass in a cluster of 16, 4 to 11 us.)
+// A warp owns a contiguous run of its CTA's rows, so that a row's place among
+// the kept is a sum of the counts before it.
+constexpr int kEvictThreads = 1024;
 constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kBins = 2048;
+constexpr int kMaxCluster = 8;
 constexpr int kMaxStaged = 40960;            // rows of a CTA in shared memory
 constexpr int kMaxEvictRows = 1 << 22;
 
@@ -75,6 +77,14 @@ struct EvictKernelArgs {
     int32_t cluster;
     int32_t staged;                          // rows that the shared memory holds
 };
+
+// 16 bytes of another CTA's shared memory
+__device__ __forceinline__ uint4 ld_cluster(uint32_t addr) {
+    uint4 x;
+    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(addr));
+    return x;
+}
 
 // fp32 -> uint32 in the same order, from 1 up; NaN 0
 __device__ __forceinline__ uint32_t weight_key(float x) {
@@ -85,11 +95,11 @@ __device__ __forceinline__ uint32_t weight_key(float x) {
 
 __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __grid_constant__ EvictKernelArgs ka) {
     const statekv_evict_args& a = ka.a;
-    __shared__ uint32_t s_hist[kBins];
-    __shared__ uint32_t s_scan[kEvictWarps + 1];
-    __shared__ uint32_t s_pick[2];
+    __shared__ __align__(16) uint32_t s_hist[kBins], s_part[kBins];
+    __shared__ uint32_t s_rows[kMaxCluster];
+    __shared__ uint32_t s_pick[3];                           // bin, rows of it that stay, its rows
     __shared__ uint32_t s_count[kEvictWarps][2];             // rows above the threshold, rows on it
-    __shared__ uint32_t s_cta[2];
+    __shared__ uint32_t s_cta[kMaxCluster][2];
     extern __shared__ float s_weights[];
     // the move may be launched now; it waits for this grid to end
     ptx::dep_trigger();
@@ -119,65 +129,93 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __gri
     const int per_warp = ((len + C * kEvictWarps - 1) / (C * kEvictWarps) + 31) / 32 * 32;
     const int c0 = min(len, rank * per_warp * kEvictWarps), c1 = min(len, c0 + per_warp * kEvictWarps);
     const int w0 = min(c1, c0 + warp * per_warp), w1 = min(c1, w0 + per_warp);
-    const float* src = w;
-    if (c1 - c0 <= ka.staged) {
-        for (int i = c0 + tid; i < c1; i += kEvictThreads) s_weights[i - c0] = w[i];
-        src = s_weights - c0;
-    }
-    auto key_of = [&](int i) {
-        return i < a.sinks || i >= len - a.recent ? 0xffffffffu : weight_key(src[i]);
+    const bool staged = c1 - c0 <= ka.staged;
+    const float* src = staged ? s_weights - c0 : w;
+    auto key_of = [&](int i, float x) {
+        return i < a.sinks || i >= len - a.recent ? 0xffffffffu : weight_key(x);
     };
     uint32_t need = (uint32_t)keep, prefix = 0, fixed = 0;   // of the rows whose `fixed` bits are `prefix`
     for (int pass = 0; pass < 3; ++pass) {
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
-        for (int i = tid; i < kBins; i += kEvictThreads) s_hist[i] = 0;
+        for (int i = tid; i < kBins; i += kEvictThreads) s_hist[i] = s_part[i] = 0;
         __syncthreads();
-        for (int i = c0 + tid; i < c1; i += kEvictThreads) {
-            const uint32_t key = key_of(i);
-            if ((key & fixed) == prefix) atomicAdd(&s_hist[(key >> shift) & (uint32_t)(bins - 1)], 1u);
+        if (pass == 0) {
+            // the rows come in on the way, eight loads of a thread at a time
+            for (int i0 = c0 + tid; i0 < c1; i0 += 8 * kEvictThreads) {
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = i0 + e * kEvictThreads < c1 ? w[i0 + e * kEvictThreads] : 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int i = i0 + e * kEvictThreads;
+                    if (i >= c1) break;
+                    if (staged) s_weights[i - c0] = x[e];
+                    atomicAdd(&s_hist[key_of(i, x[e]) >> shift], 1u);
+                }
+            }
+        } else {
+#pragma unroll 4
+            for (int i = c0 + tid; i < c1; i += kEvictThreads) {
+                const uint32_t key = key_of(i, src[i]);
+                if ((key & fixed) == prefix) atomicAdd(&s_hist[(key >> shift) & (uint32_t)(bins - 1)], 1u);
+            }
         }
         ptx::cluster_sync();
-        // thread t sums the cluster's bins 4t..4t+3, counted from the top
-        uint32_t bin[4] = {0, 0, 0, 0};
-        const int top = bins - 1 - 4 * tid;
-        if (top >= 0) {
-            for (int r = 0; r < C; ++r) {
+        // CTA r sums the cluster's bins of its part, and tells how many rows they hold
+        const int part = bins / C, groups = part / 4;
+        if (tid < bins / 4) {
+            const int g = tid % groups, r = tid / groups;
+            const uint4 x = ld_cluster(ptx::cluster_map(ptx::smem_u32(&s_hist[rank * part + 4 * g]), (uint32_t)r));
+            if (C == 1) {
+                *reinterpret_cast<uint4*>(&s_part[4 * g]) = x;
+            } else {
+                if (x.x) atomicAdd(&s_part[4 * g], x.x);
+                if (x.y) atomicAdd(&s_part[4 * g + 1], x.y);
+                if (x.z) atomicAdd(&s_part[4 * g + 2], x.z);
+                if (x.w) atomicAdd(&s_part[4 * g + 3], x.w);
+            }
+        }
+        __syncthreads();
+        const int per = part / 32;
+        uint32_t mine = 0, upto;                             // of lane l the bins part - per (l + 1) .. + per
+        if (warp == 0) {
+            for (int b = 0; b < per; ++b) mine += s_part[part - per * (lane + 1) + b];
+            upto = mine;
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    uint32_t x;
-                    asm volatile("ld.shared::cluster.u32 %0, [%1];"
-                                 : "=r"(x) : "r"(ptx::cluster_map(ptx::smem_u32(&s_hist[top - b]), (uint32_t)r)));
-                    bin[b] += x;
+            for (int off = 1; off < 32; off <<= 1) {
+                const uint32_t x = __shfl_up_sync(0xffffffffu, upto, off);
+                if (lane >= off) upto += x;
+            }
+            const uint32_t all = __shfl_sync(0xffffffffu, upto, 31);
+            if (lane < C) ptx::st_cluster_u32(ptx::cluster_map(ptx::smem_u32(&s_rows[rank]), (uint32_t)lane), all);
+        }
+        ptx::cluster_sync();
+        if (warp == 0) {
+            // the part that the threshold is in names it to all
+            uint32_t before = 0;
+            for (int r = C - 1; r > rank; --r) before += s_rows[r];
+            before += upto - mine;
+            if (before < need && need <= before + mine) {
+                int b = part - per * lane - 1;
+                while (before + s_part[b] < need) before += s_part[b--];
+                for (int r = 0; r < C; ++r) {
+                    const uint32_t to = ptx::cluster_map(ptx::smem_u32(&s_pick[0]), (uint32_t)r);
+                    ptx::st_cluster_u32(to, (uint32_t)(rank * part + b));
+                    ptx::st_cluster_u32(to + 4, need - before);
+                    ptx::st_cluster_u32(to + 8, s_part[b]);
                 }
             }
         }
-        const uint32_t mine = bin[0] + bin[1] + bin[2] + bin[3];
-        uint32_t upto = mine;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const uint32_t x = __shfl_up_sync(0xffffffffu, upto, off);
-            if (lane >= off) upto += x;
-        }
-        if (lane == 31) s_scan[warp] = upto;
-        __syncthreads();
-        uint32_t before = upto - mine;
-        for (int i = 0; i < warp; ++i) before += s_scan[i];
-        if (before < need && need <= before + mine) {
-            int b = 0;
-            while (before + bin[b] < need) before += bin[b++];
-            s_pick[0] = (uint32_t)(top - b);
-            s_pick[1] = need - before;
-        }
-        // (also: no CTA clears a histogram that another still reads)
         ptx::cluster_sync();
         prefix |= s_pick[0] << shift;
         fixed |= (uint32_t)(bins - 1) << shift;
         need = s_pick[1];
+        if (need == s_pick[2]) break;                        // the whole bin stays
     }
-    // rows above `prefix` stay, and the first `need` that are equal to it
+    // rows above `prefix` (of the bits that were looked at) stay, and the first `need` that are equal to it
     uint32_t gt = 0, eq = 0;
     for (int i0 = w0; i0 < w1; i0 += 32) {
-        const uint32_t key = i0 + lane < w1 ? key_of(i0 + lane) : 0u;
+        const uint32_t key = i0 + lane < w1 ? key_of(i0 + lane, src[i0 + lane]) & fixed : 0u;
         gt += __popc(__ballot_sync(0xffffffffu, i0 + lane < w1 && key > prefix));
         eq += __popc(__ballot_sync(0xffffffffu, i0 + lane < w1 && key == prefix));
     }
@@ -186,21 +224,22 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __gri
         s_count[warp][1] = eq;
     }
     __syncthreads();
-    if (tid < 2) {
-        uint32_t sum = 0;
-        for (int i = 0; i < kEvictWarps; ++i) sum += s_count[i][tid];
-        s_cta[tid] = sum;
+    if (tid < C) {
+        // this CTA's counts into every CTA's shared memory
+        uint32_t above = 0, on = 0;
+        for (int i = 0; i < kEvictWarps; ++i) {
+            above += s_count[i][0];
+            on += s_count[i][1];
+        }
+        const uint32_t at = ptx::cluster_map(ptx::smem_u32(&s_cta[rank][0]), (uint32_t)tid);
+        ptx::st_cluster_u32(at, above);
+        ptx::st_cluster_u32(at + 4, on);
     }
     ptx::cluster_sync();
     gt = eq = 0;
     for (int r = 0; r < rank; ++r) {
-        uint32_t x, y;
-        asm volatile("ld.shared::cluster.u32 %0, [%1];"
-                     : "=r"(x) : "r"(ptx::cluster_map(ptx::smem_u32(&s_cta[0]), (uint32_t)r)));
-        asm volatile("ld.shared::cluster.u32 %0, [%1];"
-                     : "=r"(y) : "r"(ptx::cluster_map(ptx::smem_u32(&s_cta[1]), (uint32_t)r)));
-        gt += x;
-        eq += y;
+        gt += s_cta[r][0];
+        eq += s_cta[r][1];
     }
     for (int i = 0; i < warp; ++i) {
         gt += s_count[i][0];
@@ -208,7 +247,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __gri
     }
     for (int i0 = w0; i0 < w1; i0 += 32) {
         const int i = i0 + lane;
-        const uint32_t key = i < w1 ? key_of(i) : 0u;
+        const uint32_t key = i < w1 ? key_of(i, src[i]) & fixed : 0u;
         const unsigned above = __ballot_sync(0xffffffffu, i < w1 && key > prefix);
         const unsigned on = __ballot_sync(0xffffffffu, i < w1 && key == prefix);
         const unsigned lower = (1u << lane) - 1u;
@@ -221,8 +260,6 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __gri
         gt += __popc(above);
         eq += __popc(on);
     }
-    // no CTA leaves while another reads its counts
-    ptx::cluster_sync();
 }
 
 // The kept rows move: a CTA takes kMoveRows of one (batch entry, KV head),
@@ -272,20 +309,13 @@ cudaError_t launch_evict(const statekv_evict_args& a, int dev, int sms, cudaStre
     const int64_t cap = paging_of(a).capacity();
     // CTAs of at most 4096 rows, as long as they all run at once
     int c = 1;
-    while (c < 16 && cap > (int64_t)c * 4096 && units * c * 2 <= 2 * sms) c *= 2;
+    while (c < kMaxCluster && cap > (int64_t)c * 4096 && units * c * 2 <= 2 * sms) c *= 2;
     ka.cluster = c;
     const int64_t slice = ((cap + c * kEvictWarps - 1) / (c * kEvictWarps) + 31) / 32 * 32 * kEvictWarps;
     ka.staged = slice <= kMaxStaged ? (int)slice : 0;
-    static std::atomic<uint64_t> done{0}, wide{0};
+    static std::atomic<uint64_t> done{0};
     const void* kernel = reinterpret_cast<const void*>(&evict_select_kernel);
     cudaError_t e = allow_smem(kernel, kMaxStaged * 4, dev, done);
-    if (e == cudaSuccess && c > 8) {
-        const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0ull;
-        if (!(wide.load(std::memory_order_relaxed) & bit)) {
-            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-            if (e == cudaSuccess) wide.fetch_or(bit, std::memory_order_relaxed);
-        }
-    }
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(units * c));

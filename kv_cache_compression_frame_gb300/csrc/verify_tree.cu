@@ -30,11 +30,13 @@ constexpr int kVerifyThreads = 512;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kMaxNodes = 64;
 constexpr int kMaxCluster = 16;
+constexpr int kRoomAlone = 1664, kRoomShared = 768;  // entries of a warp: 213 and 98 KB of p and q a CTA
 
 struct VerifyKernelArgs {
     statekv_verify_args a;
     int32_t cluster;
     int32_t run;                             // entries of a warp, a multiple of 32
+    int32_t room;                            // entries of p, and of q, that a warp has room for, a multiple of 8
 };
 
 // a + b = s + e exactly
@@ -43,6 +45,9 @@ __device__ __forceinline__ void two_sum(float a, float b, float& s, float& e) {
     const float bb = __fsub_rn(s, a);
     e = __fadd_rn(__fsub_rn(a, __fsub_rn(s, bb)), __fsub_rn(b, bb));
 }
+
+// a - b (a fused multiply-add by -1 is exact in the product)
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) { return ptx::fma2(b, make_float2(-1.f, -1.f), a); }
 
 // max(p - c q, 0) as hi + lo
 __device__ __forceinline__ void residual(float p, float q, float ch, float cl, float& hi, float& lo) {
@@ -66,10 +71,14 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const __grid_con
     __shared__ float s_p[kMaxNodes], s_q[kMaxNodes], s_u[kMaxNodes + 1];
     __shared__ long long s_warp[kVerifyWarps];
     __shared__ long long s_sums[2][kMaxCluster];
+    __shared__ __align__(8) uint64_t s_bars[kVerifyWarps][4];
+    extern __shared__ __align__(16) float s_rows[];          // [warps][2][room]: p, q
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int C = ka.cluster, rank = blockIdx.x % C, seq = blockIdx.x / C;
     const float* target = a.target + seq * a.target_stride;
     const float* draft = a.draft ? a.draft + seq * a.draft_stride : nullptr;
+    if (tid < kVerifyWarps * 4) ptx::mbar_init(ptx::smem_u32(&s_bars[0][0]) + 8 * tid, 1);
+    ptx::fence_barrier_init();
     if (tid < a.tokens) {
         const uint64_t mask = a.tree[(int64_t)seq * a.tree_stride + tid] & ((1ull << tid) - 1ull);
         const int parent = mask ? 63 - __clzll((long long)mask) : -1;
@@ -96,44 +105,135 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const __grid_con
     uint64_t refused = 0;                                    // nodes refused here (without a draft)
     const float* p_row = target;
     const float* q_row = draft;
-    // entry v of the residual, without the refused tokens
     auto refused_token = [&](int v) -> bool {
         for (uint64_t b = refused; b; b &= b - 1)
             if (s_token[__ffsll((long long)b) - 1] == v) return true;
         return false;
     };
-    auto entry = [&](int v, float ch, float cl, float& hi, float& lo) {
-        hi = weight(p_row + v);
-        lo = 0.f;
-        if (ch > 0.f) residual(hi, weight(q_row + v), ch, cl, hi, lo);
+    // Entries [from, to) of one of the current rows into this warp's shared
+    // memory at `buf` (16-byte aligned, 4 entries more than that): whole 16-byte
+    // units by bulk copies, on which the warp's barrier `bar` counts, the up to
+    // three entries before and behind them by plain loads, so that nothing
+    // outside of the row is read.  Returns where the first entry lies.
+    auto fetch = [&](const float* row, int from, int to, float* buf, uint32_t bar) -> int {
+        const float* src = row + from;
+        const int off = (int)(reinterpret_cast<uintptr_t>(src) / 4 % 4), n = to - from;
+        const int head = min(n, (4 - off) % 4), body = (n - head) / 4 * 4;
+        if (lane == 0 && body > 0) {
+            ptx::mbar_arrive_expect_tx(bar, (uint32_t)body * 4);
+            ptx::bulk_load(ptx::smem_u32(buf + off + head), src + head, (uint32_t)body * 4, bar);
+        } else if (lane == 0) {
+            ptx::mbar_arrive(bar);
+        }
+        if (lane >= 1 && lane <= head) buf[off + lane - 1] = __ldg(src + lane - 1);
+        const int last = head + body + lane - 4;
+        if (lane >= 4 && last < n) buf[off + last] = __ldg(src + last);
+        return off;
     };
+    // waits for the copies of one phase of a barrier (bounded)
+    auto landed = [&](uint32_t bar, uint32_t parity) {
+        const uint64_t t0 = globaltimer_ns();
+        while (!ptx::mbar_wait_hint(bar, parity, 20000u))
+            if (globaltimer_ns() - t0 > 1000000000ull) {
+                record_error(a.status, (uint32_t)STATEKV_E_TIMEOUT, kSiteKvFull, (uint32_t)warp);
+                break;
+            }
+        __syncwarp();
+    };
+    float* p_buf = s_rows + warp * 2 * ka.room;
+    float* q_buf = p_buf + ka.room;
+    const uint32_t bar = ptx::smem_u32(&s_bars[warp][0]);    // [2 halves][p, q]
+    uint32_t parity = 0;                                     // bit 2 * half + (q)
+    const bool fits = v1 - v0 <= ka.room - 4;
+    int p_off = 0, q_off = 0;                                // where a run's first entries lie
+    int p_node = -2, q_node = -2;                            // whose rows the shared memory holds
     // the residual's sum in units of 2^-52, its parts in s_warp and s_sums
     auto sum_up = [&]() -> long long {
         const float ch = (float)c, cl = (float)(c - (double)ch);
-        float hi = 0.f, lo = 0.f;
-        int v = v0 + lane;
-        constexpr int UNROLL = 8;
-        for (; v + 32 * (UNROLL - 1) < v1; v += 32 * UNROLL) {
-            float p[UNROLL], q[UNROLL];
-#pragma unroll
-            for (int i = 0; i < UNROLL; ++i) {
-                p[i] = weight(p_row + v + 32 * i);
-                q[i] = ch > 0.f ? weight(q_row + v + 32 * i) : 0.f;
+        const bool with_q = ch > 0.f;
+        // two sums side by side, each hi + lo; hi starts above every term, so
+        // that (hi + x) - hi and what it leaves of x are exact
+        float2 hi2 = make_float2(2.f, 2.f), lo2 = make_float2(0.f, 0.f);
+        auto add = [&](float2 p, float2 q) {
+            float2 h = p, l = make_float2(0.f, 0.f);
+            if (with_q) {
+                const float2 t = ptx::fma2(make_float2(-ch, -ch), q, make_float2(0.f, 0.f));   // rounded -ch q
+                h = ptx::add2(p, t);
+                const float2 bb = sub2(h, p);
+                l = ptx::add2(sub2(p, sub2(h, bb)), sub2(t, bb));
+                if (ch != 1.f) {
+                    // what the product lost, and the rest of c
+                    l = ptx::add2(l, ptx::fma2(make_float2(-ch, -ch), q, make_float2(-t.x, -t.y)));
+                    l = ptx::fma2(make_float2(-cl, -cl), q, l);
+                }
+                if (!(h.x + l.x > 0.f)) h.x = l.x = 0.f;
+                if (!(h.y + l.y > 0.f)) h.y = l.y = 0.f;
             }
+            const float2 s = ptx::add2(hi2, h);
+            lo2 = ptx::add2(lo2, ptx::add2(sub2(h, sub2(s, hi2)), l));
+            hi2 = s;
+        };
+        auto add_all = [&](const float* ps, const float* qs, int count) {
+#pragma unroll 4
+            for (int i = lane; i < count; i += 64) {
+                const bool two = i + 32 < count;
+                const float2 p = make_float2(fmaxf(ps[i], 0.f), two ? fmaxf(ps[i + 32], 0.f) : 0.f);
+                float2 q = make_float2(0.f, 0.f);
+                if (with_q) q = make_float2(fmaxf(qs[i], 0.f), two ? fmaxf(qs[i + 32], 0.f) : 0.f);
+                add(p, q);
+            }
+        };
+        if (fits) {
+            // rows that are there already are not read again
+            const bool new_p = p_node != cur, new_q = with_q && q_node != cur;
+            if (new_p || new_q) ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (new_p) p_off = fetch(p_row, v0, v1, p_buf, bar);
+            if (new_q) q_off = fetch(q_row, v0, v1, q_buf, bar + 8);
+            if (new_p) {
+                landed(bar, parity & 1);
+                parity ^= 1;
+                p_node = cur;
+            }
+            if (new_q) {
+                landed(bar + 8, parity >> 1 & 1);
+                parity ^= 2;
+                q_node = cur;
+            }
+            add_all(p_buf + p_off, q_buf + q_off, v1 - v0);
+        } else {
+            // in pieces of half the room, the next one on its way
+            const int half = ka.room / 2, piece = half - 4;
+            int offs[2][2];
+            auto start = [&](int v, int i) {
+                offs[i][0] = fetch(p_row, v, min(v1, v + piece), p_buf + i * half, bar + 16 * i);
+                offs[i][1] = with_q ? fetch(q_row, v, min(v1, v + piece), q_buf + i * half, bar + 16 * i + 8) : 0;
+            };
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            start(v0, 0);
+            int v = v0;
+#pragma unroll 1
+            while (v < v1) {
 #pragma unroll
-            for (int i = 0; i < UNROLL; ++i) {
-                float h = p[i], l = 0.f, e;
-                if (ch > 0.f) residual(p[i], q[i], ch, cl, h, l);
-                two_sum(hi, h, hi, e);
-                lo = __fadd_rn(lo, __fadd_rn(l, e));
+                for (int i = 0; i < 2; ++i, v += piece) {
+                    if (v >= v1) break;
+                    if (v + piece < v1) start(v + piece, i ^ 1);
+                    landed(bar + 16 * i, parity >> (2 * i) & 1);
+                    parity ^= 1u << (2 * i);
+                    if (with_q) {
+                        landed(bar + 16 * i + 8, parity >> (2 * i + 1) & 1);
+                        parity ^= 2u << (2 * i);
+                    }
+                    add_all(p_buf + i * half + offs[i][0], q_buf + i * half + offs[i][1], min(piece, v1 - v));
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                }
             }
         }
-        for (; v < v1; v += 32) {
-            float h, l, e;
-            entry(v, ch, cl, h, l);
-            two_sum(hi, h, hi, e);
-            lo = __fadd_rn(lo, __fadd_rn(l, e));
-        }
+        float hi = hi2.x - 2.f, lo;
+        two_sum(hi, hi2.y - 2.f, hi, lo);
+        lo += lo2.x + lo2.y;
         long long sum = units_of(hi, lo);
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
@@ -227,7 +327,10 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const __grid_con
     for (int i0 = v0; i0 < v1; i0 += 32) {
         const int v = i0 + lane;
         float hi = 0.f, lo = 0.f;
-        if (v < v1 && !refused_token(v)) entry(v, ch, cl, hi, lo);
+        if (v < v1 && !refused_token(v)) {
+            hi = fits ? fmaxf(p_buf[p_off + v - v0], 0.f) : weight(p_row + v);
+            if (ch > 0.f) residual(hi, fits ? fmaxf(q_buf[q_off + v - v0], 0.f) : weight(q_row + v), ch, cl, hi, lo);
+        }
         long long upto = units_of(hi, lo);
         const unsigned some = __ballot_sync(0xffffffffu, upto > 0);
 #pragma unroll
@@ -253,14 +356,24 @@ cudaError_t launch_verify(const statekv_verify_args& a, int dev, int sms, cudaSt
     // as many CTAs per sequence as run at once (clusters of 16 do not fill the
     // device), with four entries a thread at least
     int c = 1;
-    while (c < 16 && (int64_t)a.sequences * c * 2 <= (c < 8 ? sms : sms / 2) && a.vocab > c * 2 * kVerifyThreads * 2) c *= 2;
+    while (c < kMaxCluster && (int64_t)a.sequences * c * 2 <= (c < 8 ? sms : sms / 2) &&
+           a.vocab > c * 2 * kVerifyThreads * 2)
+        c *= 2;
     ka.cluster = c;
     ka.run = (int)(((int64_t)a.vocab + c * kVerifyWarps * 32 - 1) / (c * kVerifyWarps * 32) * 32);
+    // room for the whole run where that leaves the device one CTA per SM, else
+    // for two CTAs on each
+    const int most = (int64_t)a.sequences * c <= sms ? kRoomAlone : kRoomShared;
+    ka.room = std::min(ka.run + 8, most);                    // (a run is a multiple of 32)
+    const int bytes = kVerifyWarps * 2 * ka.room * 4;
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(&verify_kernel), kVerifyWarps * 2 * kRoomAlone * 4, dev, done);
+    if (e != cudaSuccess) return e;
     static std::atomic<uint64_t> wide{0};
     if (c > 8) {
         const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0ull;
         if (!(wide.load(std::memory_order_relaxed) & bit)) {
-            const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&verify_kernel),
+            e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&verify_kernel),
                                                        cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
             if (e != cudaSuccess) return e;
             wide.fetch_or(bit, std::memory_order_relaxed);
@@ -269,6 +382,7 @@ cudaError_t launch_verify(const statekv_verify_args& a, int dev, int sms, cudaSt
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.sequences * c));
     cfg.blockDim = dim3(kVerifyThreads);
+    cfg.dynamicSmemBytes = (size_t)bytes;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
