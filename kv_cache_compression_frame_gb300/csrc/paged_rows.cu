@@ -67,6 +67,7 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __gr
 // the kept is a sum of the counts before it.
 constexpr int kEvictThreads = 1024;
 constexpr int kEvictWarps = kEvictThreads / 32;
+static_assert(kEvictWarps == 32, "one lane per warp in the scans");
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxStaged = 40960;            // rows of a CTA in shared memory
@@ -96,7 +97,7 @@ __device__ __forceinline__ uint32_t weight_key(float x) {
 __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __grid_constant__ EvictKernelArgs ka) {
     const statekv_evict_args& a = ka.a;
     __shared__ __align__(16) uint32_t s_hist[kBins], s_part[kBins];
-    __shared__ uint32_t s_rows[kMaxCluster];
+    __shared__ uint32_t s_rows[kMaxCluster], s_scan[kEvictWarps];
     __shared__ uint32_t s_pick[3];                           // bin, rows of it that stay, its rows
     __shared__ uint32_t s_count[kEvictWarps][2];             // rows above the threshold, rows on it
     __shared__ uint32_t s_cta[kMaxCluster][2];
@@ -176,34 +177,34 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __gri
             }
         }
         __syncthreads();
-        const int per = part / 32;
-        uint32_t mine = 0, upto;                             // of lane l the bins part - per (l + 1) .. + per
-        if (warp == 0) {
-            for (int b = 0; b < per; ++b) mine += s_part[part - per * (lane + 1) + b];
-            upto = mine;
+        // thread t has the t-th bin of the part from the top, or two
+        const int two = part > kEvictThreads, top = part - 1 - (two ? 2 * tid : tid);
+        const uint32_t hi = top >= 0 ? s_part[top] : 0u, lo = two ? s_part[top - 1] : 0u, mine = hi + lo;
+        uint32_t upto = mine;
 #pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const uint32_t x = __shfl_up_sync(0xffffffffu, upto, off);
-                if (lane >= off) upto += x;
-            }
-            const uint32_t all = __shfl_sync(0xffffffffu, upto, 31);
+        for (int off = 1; off < 32; off <<= 1) {
+            const uint32_t x = __shfl_up_sync(0xffffffffu, upto, off);
+            if (lane >= off) upto += x;
+        }
+        if (lane == 31) s_scan[warp] = upto;
+        __syncthreads();
+        const uint32_t of_warp = s_scan[lane];
+        uint32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? of_warp : 0u) + upto - mine;
+        if (warp == 0) {
+            const uint32_t all = __reduce_add_sync(0xffffffffu, of_warp);
             if (lane < C) ptx::st_cluster_u32(ptx::cluster_map(ptx::smem_u32(&s_rows[rank]), (uint32_t)lane), all);
         }
         ptx::cluster_sync();
-        if (warp == 0) {
+        for (int r = C - 1; r > rank; --r) before += s_rows[r];
+        if (before < need && need <= before + mine) {
             // the part that the threshold is in names it to all
-            uint32_t before = 0;
-            for (int r = C - 1; r > rank; --r) before += s_rows[r];
-            before += upto - mine;
-            if (before < need && need <= before + mine) {
-                int b = part - per * lane - 1;
-                while (before + s_part[b] < need) before += s_part[b--];
-                for (int r = 0; r < C; ++r) {
-                    const uint32_t to = ptx::cluster_map(ptx::smem_u32(&s_pick[0]), (uint32_t)r);
-                    ptx::st_cluster_u32(to, (uint32_t)(rank * part + b));
-                    ptx::st_cluster_u32(to + 4, need - before);
-                    ptx::st_cluster_u32(to + 8, s_part[b]);
-                }
+            const bool low = before + hi < need;
+            if (low) before += hi;
+            for (int r = 0; r < C; ++r) {
+                const uint32_t to = ptx::cluster_map(ptx::smem_u32(&s_pick[0]), (uint32_t)r);
+                ptx::st_cluster_u32(to, (uint32_t)(rank * part + top - (low ? 1 : 0)));
+                ptx::st_cluster_u32(to + 4, need - before);
+                ptx::st_cluster_u32(to + 8, low ? lo : hi);
             }
         }
         ptx::cluster_sync();
@@ -214,6 +215,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __gri
     }
     // rows above `prefix` (of the bits that were looked at) stay, and the first `need` that are equal to it
     uint32_t gt = 0, eq = 0;
+#pragma unroll 4
     for (int i0 = w0; i0 < w1; i0 += 32) {
         const uint32_t key = i0 + lane < w1 ? key_of(i0 + lane, src[i0 + lane]) & fixed : 0u;
         gt += __popc(__ballot_sync(0xffffffffu, i0 + lane < w1 && key > prefix));
@@ -245,6 +247,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __gri
         gt += s_count[i][0];
         eq += s_count[i][1];
     }
+#pragma unroll 4
     for (int i0 = w0; i0 < w1; i0 += 32) {
         const int i = i0 + lane;
         const uint32_t key = i < w1 ? key_of(i, src[i]) & fixed : 0u;
