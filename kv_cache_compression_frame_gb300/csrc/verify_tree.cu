@@ -69,6 +69,11 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const __grid_con
     const statekv_verify_args& a = ka.a;
     __shared__ int s_parent[kMaxNodes], s_token[kMaxNodes];  // token -1: out of range
     __shared__ float s_p[kMaxNodes], s_q[kMaxNodes], s_u[kMaxNodes + 1];
+    __shared__ struct {
+        uint64_t refused;
+        float ch, cl;
+        int node, more;
+    } s_pass;
     __shared__ long long s_warp[kVerifyWarps];
     __shared__ long long s_sums[2][kMaxCluster];
     __shared__ __align__(8) uint64_t s_bars[kVerifyWarps][4];
@@ -100,8 +105,9 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const __grid_con
     // this warp's run of the vocabulary
     const int v0 = min((int64_t)a.vocab, (int64_t)(rank * kVerifyWarps + warp) * ka.run);
     const int v1 = min((int64_t)a.vocab, (int64_t)v0 + ka.run);
-    int cur = -1, count = 0, passes = 0;
-    double c = 0.0, R = 1.0;
+    // what the next pass sums, from warp 0's walk
+    int cur = -1, passes = 0;
+    float ch = 0.f, cl = 0.f;                                // c
     uint64_t refused = 0;                                    // nodes refused here (without a draft)
     const float* p_row = target;
     const float* q_row = draft;
@@ -149,7 +155,6 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const __grid_con
     int p_node = -2, q_node = -2;                            // whose rows the shared memory holds
     // the residual's sum in units of 2^-52, its parts in s_warp and s_sums
     auto sum_up = [&]() -> long long {
-        const float ch = (float)c, cl = (float)(c - (double)ch);
         const bool with_q = ch > 0.f;
         // two sums side by side, each hi + lo; hi starts above every term, so
         // that (hi + x) - hi and what it leaves of x are exact
@@ -266,63 +271,92 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const __grid_con
 
     // "every CTA of the cluster has started", before its memory is written
     ptx::cluster_sync();
-    bool summed = false;
+    // The walk, by warp 0 alone (a step takes a dozen fp64 operations, which 512
+    // threads would wait 256 cycles each for).  It goes on until a pass is needed
+    // and leaves what that sums in s_pass; false: no pass, the last one's sum stands.
+    int at = -1, count = 0;                                  // current node, accepted ones
+    double c = 0.0, R = 1.0;
+    uint64_t children = 0, out = 0;                          // of `at` that are left, refused (without a draft)
+    bool summed = false, empty = false;
     long long total = 0;
-    for (int i = 0; i < a.tokens; ++i) {
-        if (s_parent[i] != cur) continue;
-        const double p = s_p[i], q = s_q[i], u = s_u[i];
-        double r;
-        bool stands;
-        if (draft) {
-            r = fmax(p - c * q, 0.0);
-            stands = u * q * R < r;
-        } else {
-            r = s_token[i] >= 0 && refused_token(s_token[i]) ? 0.0 : p;
-            stands = u * R < r;
+    auto children_of = [&](int node) -> uint64_t {
+        const unsigned lo = __ballot_sync(0xffffffffu, lane < a.tokens && s_parent[lane] == node);
+        const unsigned hi = __ballot_sync(0xffffffffu, lane + 32 < a.tokens && s_parent[(lane + 32) % kMaxNodes] == node);
+        return (uint64_t)hi << 32 | lo;
+    };
+    auto walk = [&]() -> bool {
+        while (children) {
+            const int i = __ffsll((long long)children) - 1;
+            children &= children - 1;
+            const double p = s_p[i], q = s_q[i], u = s_u[i];
+            bool again = false;
+            for (uint64_t b = out; b; b &= b - 1) again |= s_token[__ffsll((long long)b) - 1] == s_token[i];
+            const double r = draft ? fmax(p - c * q, 0.0) : again ? 0.0 : p;
+            if (s_token[i] >= 0 && (draft ? u * q * R : u * R) < r) {
+                if (rank == 0 && lane == 0) a.path[(int64_t)seq * a.tokens + count] = i;
+                ++count;
+                at = i;
+                children = children_of(i);
+                c = 0.0;
+                R = 1.0;
+                out = 0;
+                summed = false;
+            } else if (draft) {
+                c += R;
+                summed = true;
+                return true;
+            } else {
+                R = fmax(R - r, 0.0);
+                if (s_token[i] >= 0) out |= 1ull << i;
+            }
         }
-        if (s_token[i] >= 0 && stands) {
-            if (rank == 0 && tid == 0) a.path[(int64_t)seq * a.tokens + count] = i;
-            ++count;
-            cur = i;
+        if (!summed) return summed = true;
+        if (total <= 0 && !empty && (c > 0.0 || out != 0)) {
+            // nothing is left: the target's own row
             c = 0.0;
-            R = 1.0;
-            refused = 0;
-            summed = false;
-            p_row = target + (int64_t)(i + 1) * a.target_row;
-            if (draft) q_row = draft + (int64_t)(i + 1) * a.draft_row;
-        } else if (draft) {
-            c += R;
-            total = sum_up();
-            R = (double)total * 0x1p-52;
-            summed = true;
-        } else {
-            R = fmax(R - r, 0.0);
-            if (s_token[i] >= 0) refused |= 1ull << i;
+            out = 0;
+            return empty = true;
         }
-    }
-    if (!summed) total = sum_up();
-    if (total <= 0 && (c > 0.0 || refused != 0)) {
-        // nothing is left: the target's own row
-        c = 0.0;
-        refused = 0;
+        return false;
+    };
+    if (warp == 0) children = children_of(-1);
+    for (;;) {
+        if (warp == 0) {
+            const bool more = walk();
+            if (lane == 0) {
+                s_pass.more = more;
+                s_pass.node = at;
+                s_pass.ch = (float)c;
+                s_pass.cl = (float)(c - (double)(float)c);
+                s_pass.refused = out;
+            }
+        }
+        __syncthreads();
+        cur = s_pass.node;
+        ch = s_pass.ch;
+        cl = s_pass.cl;
+        refused = s_pass.refused;
+        p_row = target + (int64_t)(cur + 1) * a.target_row;
+        if (draft) q_row = draft + (int64_t)(cur + 1) * a.draft_row;
+        if (!s_pass.more) break;
         total = sum_up();
+        if (warp == 0 && draft) R = (double)total * 0x1p-52;
     }
-    if (rank == 0) {
-        for (int i = count + tid; i < a.tokens; i += kVerifyThreads) a.path[(int64_t)seq * a.tokens + i] = -1;
-        if (tid == 0) {
+    if (rank == 0 && warp == 0) {
+        for (int i = count + lane; i < a.tokens; i += 32) a.path[(int64_t)seq * a.tokens + i] = -1;
+        if (lane == 0) {
             a.counts[seq] = count;
             if (total <= 0) a.next[seq] = 0;
         }
     }
     if (total <= 0) return;
     // the lowest entry whose sum passes `past`
-    const long long past = min((long long)((double)s_u[a.tokens] * (double)total), total - 1);
+    const long long past = min(__double2ll_rd((double)s_u[a.tokens] * (double)total), total - 1);
     const long long* sums = s_sums[(passes - 1) & 1];
     long long before = 0;
     for (int i = 0; i < rank; ++i) before += sums[i];
     for (int i = 0; i < warp; ++i) before += s_warp[i];
     if (past < before || past >= before + s_warp[warp]) return;
-    const float ch = (float)c, cl = (float)(c - (double)ch);
     int last = v0;                                           // the last entry that is not 0
     for (int i0 = v0; i0 < v1; i0 += 32) {
         const int v = i0 + lane;
