@@ -294,6 +294,14 @@ int statekv_accept(statekv_handle* h, int32_t count, const int32_t* path, void* 
 int statekv_decode_sparse(statekv_handle* h, int32_t tokens, int32_t top, const void* q, const void* k,
                           const void* v, void* o, void* cuda_stream);
 
+/*
+ * statekv_decode for a whole text prompt: 1..T tokens at once, d = 64 or 128,
+ * any G <= 64 (the attention is that of statekv_paged_attention below; bf16,
+ * else E_UNSUPPORTED).  The first call allocates the workspace (E_OOM).
+ */
+int statekv_decode_prompt(statekv_handle* h, int32_t tokens, const void* q, const void* k, const void* v,
+                          void* o, void* cuda_stream);
+
 /* Text tokens decoded since the last reset (-1 for a NULL handle). */
 int64_t statekv_text_tokens(const statekv_handle* h);
 
@@ -346,7 +354,7 @@ int statekv_get_scores(statekv_handle* h, int32_t s, int32_t layer,
 
 /* Borrowed DEVICE pointer to the rotated queries Q' of the last frame step
  * ([S][L][Hq][T][d], storage dtype) or, after a text decode (dense, sparse or
- * a tree), of the last such step ([S][L][Hq][tokens][d]).  Valid until the next step. */
+ * a prompt or a tree), of the last such step ([S][L][Hq][tokens][d]).  Valid until the next step. */
 int statekv_get_rotated_query(statekv_handle* h, const void** q_rot);
 
 /* Set the frame index n (teacher forcing / resume); 0 <= n < max_frames. */
@@ -642,7 +650,7 @@ int statekv_sparse_attention(const statekv_sparse_args* args, void* cuda_stream)
  * page), num_pages of them.  table: int32 [batch][table_stride], row i of batch
  * entry n is row i % page_rows of page table[n][i / page_rows]; a table row
  * holds table_pages <= table_stride entries, so a sequence at most table_pages
- * * page_rows < 2^31 rows.  Entries past the last page in use are not looked
+ * * page_rows <= 2^31 - 257 rows.  Entries past the last page in use are not looked
  * at; one in use that is out of [0, num_pages) is recorded (E_DEVICE): its rows
  * read as zeros, and nothing is written there.  Pages may be shared by entries
  * that only read them.  page_rows is a multiple of 16.  table NULL: a plain

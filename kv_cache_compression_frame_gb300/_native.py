@@ -46,7 +46,7 @@ EXPORTS = (
     "statekv_sparse_attention",
     "statekv_set_qk_norm", "statekv_decode_tree", "statekv_accept", "statekv_decode_sparse",
     "statekv_paged_append", "statekv_paged_attention", "statekv_paged_attention_workspace",
-    "statekv_attention_weights", "statekv_evict_rows", "statekv_verify_tree",
+    "statekv_attention_weights", "statekv_evict_rows", "statekv_verify_tree", "statekv_decode_prompt",
 )
 
 BLOCK = 64          # STATEKV_BLOCK
@@ -179,6 +179,7 @@ def load() -> C.CDLL:
         "statekv_set_qk_norm": (C.c_int, [h, _P, _P, C.c_float, _P]),
         "statekv_decode_tree": (C.c_int, [h, C.c_int32, _P, _P, _P, _P, _P, _P, _P]),
         "statekv_accept": (C.c_int, [h, C.c_int32, _P, _P]),
+        "statekv_decode_prompt": (C.c_int, [h, C.c_int32, _P, _P, _P, _P, _P]),
         "statekv_decode_sparse": (C.c_int, [h, C.c_int32, C.c_int32, _P, _P, _P, _P, _P]),
         "statekv_reset": (C.c_int, [h]),
         "statekv_check_device_status": (C.c_int, [h, _P]),

@@ -20,12 +20,18 @@ __host__ __device__ inline Paging paging_of(const Args& a) {
     return {a.table, a.table_stride, a.table_pages, a.num_pages, a.page_rows};
 }
 
+// rows of a sequence: rounded up to tiles they stay in 32 bits
+constexpr int64_t kMaxRows = 0x7fffffffll - 256;
+
 // Sizes of a pool and its table (STATEKV_OK or what to refuse them with).
 inline int paging_ok(const Paging& p, int batch) {
     if (p.num_pages < 0 || p.page_rows < 0 || !ints_ok(p.table)) return STATEKV_E_INVALID_ARG;
-    if (!p.table) return batch > p.num_pages ? STATEKV_E_CAPACITY : STATEKV_OK;
+    if (!p.table) {
+        if (p.capacity() > kMaxRows) return STATEKV_E_UNSUPPORTED;
+        return batch > p.num_pages ? STATEKV_E_CAPACITY : STATEKV_OK;
+    }
     if (p.pages < 0 || p.stride < p.pages || p.page_rows < 16) return STATEKV_E_INVALID_ARG;
-    if (p.page_rows % 16 != 0 || p.capacity() > 0x7fffffffll - 256) return STATEKV_E_UNSUPPORTED;
+    if (p.page_rows % 16 != 0 || p.capacity() > kMaxRows) return STATEKV_E_UNSUPPORTED;
     return STATEKV_OK;
 }
 

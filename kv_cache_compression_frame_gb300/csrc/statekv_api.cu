@@ -72,6 +72,7 @@ struct statekv_handle {
     bool norm = false;
     void* draft_k = nullptr; void* draft_v = nullptr;   // [U][kMaxDraft][d] drafted tokens
     void* tree_ws = nullptr; int64_t tree_ws_bytes = 0;
+    void* prompt_ws = nullptr; int64_t prompt_ws_bytes = 0;      // of decode_prompt
     int32_t draft = 0;                  // tokens of the last tree, 0: nothing to accept
     int8_t* codes = nullptr; float* code_scales = nullptr;   // block summaries of D
     int64_t summarised = 0;             // D rows whose complete blocks have summaries
@@ -806,6 +807,53 @@ int statekv_decode_sparse(statekv_handle* h, int32_t tokens, int32_t top, const 
     pa.batch = batch; pa.layers = c.num_layers; pa.q_heads = c.num_q_heads; pa.kv_heads = c.num_kv_heads;
     pa.tokens = tokens; pa.head_dim = c.head_dim; pa.cache_rows = (int32_t)h->det_pitch;
     if ((r = statekv_sparse_attention(&pa, cuda_stream)) != STATEKV_OK) return r;
+    h->text += tokens;
+    h->draft = 0;
+    return STATEKV_OK;
+}
+
+int statekv_decode_prompt(statekv_handle* h, int32_t tokens, const void* q, const void* k, const void* v, void* o,
+                          void* cuda_stream) {
+    if (!h) return STATEKV_E_INVALID_ARG;
+    int r;
+    if ((r = check_ptr(q)) || (r = check_ptr(k)) || (r = check_ptr(v)) || (r = check_ptr(o))) return r;
+    const statekv_config& c = h->cfg;
+    if (tokens < 1 || tokens > c.frame_tokens) return STATEKV_E_INVALID_ARG;
+    if (c.dtype != STATEKV_BF16 || h->G > 64) return STATEKV_E_UNSUPPORTED;
+    const int64_t visible = h->n * c.frame_tokens + h->text;
+    if (visible + tokens > h->det_pitch) return STATEKV_E_CAPACITY;
+    DeviceGuard g(c.device);
+    if (!g.ok) return cuda_fail();
+    const int batch = c.num_streams * c.num_layers;
+    if (!h->prompt_ws) {
+        const int64_t need = statekv_paged_attention_workspace(batch, c.num_q_heads, c.num_kv_heads, c.frame_tokens,
+                                                               c.head_dim, (int32_t)h->det_pitch);
+        if (need < 0) return STATEKV_E_UNSUPPORTED;
+        if (!dalloc(h, &h->prompt_ws, (size_t)need)) return STATEKV_E_OOM;
+        h->prompt_ws_bytes = need;
+    }
+    RopeArgs ra{};
+    ra.q = q; ra.k = k; ra.v = v;
+    ra.q_rot = h->q_rot; ra.pool_k = nullptr; ra.pool_v = nullptr;
+    ra.det_k = h->det_k; ra.det_v = h->det_v;
+    ra.cs = h->cs + (size_t)visible * (c.head_dim / 2);
+    ra.rows_q = (int64_t)h->U * h->G * tokens;
+    ra.rows_kv = (int64_t)h->U * tokens;
+    ra.T = tokens; ra.d = c.head_dim; ra.slots = h->slots; ra.c = 0;
+    ra.det_pitch = h->det_pitch; ra.det_row0 = visible;
+    h->norm_args(ra);
+    if (launch_rope(ra, c.dtype, reinterpret_cast<cudaStream_t>(cuda_stream), false) != cudaSuccess) return cuda_fail();
+    statekv_paged_attention_args pa{};
+    pa.q = h->view(h->q_rot, c.num_q_heads, tokens); pa.out = h->view(o, c.num_q_heads, tokens);
+    pa.k_pages = h->view(h->det_k, c.num_kv_heads, h->det_pitch);
+    pa.v_pages = h->view(h->det_v, c.num_kv_heads, h->det_pitch);
+    pa.status = h->err; pa.workspace = h->prompt_ws; pa.workspace_bytes = h->prompt_ws_bytes;
+    pa.scale = h->mscale * h->mscale / std::sqrt((double)c.head_dim);
+    pa.length = (int32_t)(visible + tokens);
+    pa.num_pages = batch; pa.page_rows = (int32_t)h->det_pitch;
+    pa.batch = batch; pa.layers = c.num_layers; pa.q_heads = c.num_q_heads; pa.kv_heads = c.num_kv_heads;
+    pa.tokens = tokens; pa.head_dim = c.head_dim;
+    if ((r = statekv_paged_attention(&pa, cuda_stream)) != STATEKV_OK) return r;
     h->text += tokens;
     h->draft = 0;
     return STATEKV_OK;

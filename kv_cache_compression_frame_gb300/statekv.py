@@ -229,6 +229,14 @@ class StateKV:
             _stream_ptr(stream, self.device)), "statekv_decode_sparse")
         return o
 
+    def decode_prompt(self, q, k, v, o=None, stream=None) -> torch.Tensor:
+        """decode() for a whole text prompt: 1 to frame_tokens tokens."""
+        q, k, v, o, tok = self._text_in(q, k, v, o)
+        N.check(self._lib.statekv_decode_prompt(
+            self._h, tok, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+            _stream_ptr(stream, self.device)), "statekv_decode_prompt")
+        return o
+
     def _text_in(self, q, k, v, o):
         tok = q.shape[3] if q.dim() == 5 else -1
         qs = self.q_shape[:3] + (tok, self.q_shape[4])
