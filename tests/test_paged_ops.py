@@ -573,7 +573,7 @@ def verify_case(g, seqs, tok, vocab, seed, spread=2.0):
 @gpu
 @pytest.mark.parametrize("with_draft", [True, False])
 @pytest.mark.parametrize("seqs,tok,vocab", [(1, 1, 2), (3, 7, 100), (40, 5, 33), (2, 64, 4097), (16, 42, 10007), (1, 9, 150001),
-                                            (200, 3, 1)])
+                                            (200, 3, 1), (1, 5, 1_000_003), (160, 4, 40001), (24, 6, 150000)])
 def test_verify(seqs, tok, vocab, with_draft):
     g = gen(seqs + tok)
     p, q, drafted, tree, u = verify_case(g, seqs, tok, vocab, seqs * tok)
@@ -774,6 +774,64 @@ def test_another_stream_and_workspaces():
     with pytest.raises(kv.StateKVError):
         kv.paged_attention(q[0], *c.pools, c.table, lens, scale=0.1,
                            workspace=torch.empty(size - 16, dtype=torch.uint8, device=DEV))
+    kv.check_status()
+
+
+@gpu
+def test_every_operator_captured_and_on_other_streams():
+    """One step of all five, eager on a stream of its own, and as two graphs that
+    are replayed at once: the same bits as eager calls on the default stream."""
+    g = gen(64)
+    c = Cache(g, 3, 2, [700, 90, 333], 32, 64, cap=800)
+    wide = torch.full((3, 40), 1 << 30, dtype=I32, device=DEV)
+    wide[:, :c.table.shape[1]] = c.table
+    table = wide[:, :c.full.shape[1]]                    # rows of a larger table
+    table.copy_(c.full)
+    lens, counts = ints(700, 90, 333), ints(17, 2, 5)
+    q, k, v = randn(g, 3, 8, 17, 64), randn(g, 3, 2, 17, 64), randn(g, 3, 2, 17, 64)
+    p, dr, drafted, tree, u = verify_case(g, 5, 6, 3001, 9)
+    fresh = torch.arange(3 * 4, device=DEV, dtype=I32).view(3, 4)
+
+    def step(pools, out_pools, stream=None):
+        new = kv.paged_append(k, v, *pools, table, lens, counts, stream=stream)
+        out, lse = kv.paged_attention(q, *pools, table, new, counts, scale=0.1, with_lse=True, stream=stream)
+        w = kv.attention_weights(q, lse, pools[0], table, new, counts, scale=0.1, stream=stream)
+        e = kv.evict_rows(*pools, table, new, w, 100, fresh, sinks=3, recent=20, k_out=out_pools[0],
+                          v_out=out_pools[1], stream=stream)
+        return [new, out, lse, w, *e, *out_pools, *kv.verify_tree(p, dr, drafted, tree, u, stream=stream)]
+
+    def state():
+        return [x.clone() for x in c.pools], [torch.zeros(12, 2, 32, 64, dtype=BF16, device=DEV) for _ in range(2)]
+
+    want = step(*state())
+    c.dense = [x.clone() for x in c.dense]
+    for i, (n0, n1) in enumerate(zip((700, 90, 333), (17, 2, 5))):
+        c.dense[0][i, :, n0:n0 + n1], c.dense[1][i, :, n0:n0 + n1] = k[i, :, :n1], v[i, :, :n1]
+    check_attention(q, c, [717, 92, 338], [17, 2, 5], 0.1, want[1], want[2])
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    args = state()
+    torch.cuda.synchronize()
+    got = step(*args, stream=s)
+    s.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    graphs = []
+    for _ in range(2):
+        args = state()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = step(*args)
+        graphs.append((graph, got, torch.cuda.Stream()))
+    for _ in range(10):
+        for graph, _, st in graphs:
+            with torch.cuda.stream(st):
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, got, _ in graphs:
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
     kv.check_status()
 
 
