@@ -663,24 +663,50 @@ paged_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
                     ptx::fence_proxy_async_smem();
                 }
                 if (!idle) {
-                    uint32_t x[2][64];
-                    ptx::tmem_ld_32x32b_x64(t_s, x[0]);
-                    ptx::tmem_ld_32x32b_x64(t_s + 64, x[1]);
-                    ptx::tmem_ld_wait();
-                    if (special) {
-                        const int valid = limit - t * kTile;
+                    // With one row tile HBM is the bound, and what counts is that a
+                    // CTA meets this code cold: 32 columns at a time, read twice,
+                    // it is a quarter as long.  (All 128 at once, fetched while every
+                    // SM asks for its first tiles, the first tile took 4 to 7 us.)
+                    const int valid = limit - t * kTile;
+                    uint32_t x[SPLIT_ROWS ? 2 : 1][64];
+                    auto scores32 = [&](int cc) {
+                        uint32_t (&y)[32] = reinterpret_cast<uint32_t (&)[32]>(x[0]);
+                        ptx::tmem_ld_32x32b_x32(t_s + cc, y);
+                        ptx::tmem_ld_wait();
+                        if (special)
 #pragma unroll
-                        for (int e = 0; e < 64; ++e) {
-                            if (e >= valid) x[0][e] = 0xff800000u;
-                            if (64 + e >= valid) x[1][e] = 0xff800000u;
+                            for (int e = 0; e < 32; ++e)
+                                if (cc + e >= valid) y[e] = 0xff800000u;
+                    };
+                    float mx[2] = {-INFINITY, -INFINITY};
+                    if constexpr (SPLIT_ROWS) {
+                        ptx::tmem_ld_32x32b_x64(t_s, x[0]);
+                        ptx::tmem_ld_32x32b_x64(t_s + 64, x[1]);
+                        ptx::tmem_ld_wait();
+                        if (special) {
+#pragma unroll
+                            for (int e = 0; e < 64; ++e) {
+                                if (e >= valid) x[0][e] = 0xff800000u;
+                                if (64 + e >= valid) x[1][e] = 0xff800000u;
+                            }
+                        }
+#pragma unroll
+                        for (int e = 0; e < 64; e += 2)
+#pragma unroll
+                            for (int b = 0; b < 2; ++b)
+                                mx[b] = ptx::max3(mx[b], __uint_as_float(x[b][e]), __uint_as_float(x[b][e + 1]));
+                    } else {
+#pragma unroll 1
+                        for (int cc = 0; cc < kTile; cc += 32) {
+                            scores32(cc);
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4) {
+                                mx[0] = ptx::max3(mx[0], __uint_as_float(x[0][e]), __uint_as_float(x[0][e + 1]));
+                                mx[1] = ptx::max3(mx[1], __uint_as_float(x[0][e + 2]), __uint_as_float(x[0][e + 3]));
+                            }
+                            __syncwarp();
                         }
                     }
-                    float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-                    for (int e = 0; e < 64; e += 2)
-#pragma unroll
-                        for (int b = 0; b < 2; ++b)
-                            mx[b] = ptx::max3(mx[b], __uint_as_float(x[b][e]), __uint_as_float(x[b][e + 1]));
                     const float top = fmaxf(mx[0], mx[1]) * sc;
                     const bool raise = sees && top > m + kSlack;   // (other rows' queries are anything)
                     if (__any_sync(0xffffffffu, raise)) {
@@ -690,7 +716,7 @@ paged_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
                         __syncwarp();
                         // S full: every product into O so far is done
                         if (i > 0) {
-#pragma unroll
+#pragma unroll (SPLIT_ROWS ? D / 32 : 1)
                             for (int cc = 0; cc < D; cc += 32) {
                                 uint32_t o[32];
                                 ptx::tmem_ld_32x32b_x32(t_o + cc, o);
@@ -704,27 +730,48 @@ paged_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
                     }
                     const float nm = m == -INFINITY ? 0.f : -m;
                     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    // N pairs of columns: exponentials, their sums, P
+                    auto weigh = [&](const uint32_t* from, auto& p) {
+                        constexpr int N = sizeof(p) / 4;
 #pragma unroll
-                    for (int hh = 0; hh < 2; ++hh) {
-                        uint32_t p[32];
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const float2 z = ptx::fma2(make_float2(__uint_as_float(x[hh][2 * e]),
-                                                                   __uint_as_float(x[hh][2 * e + 1])),
+                        for (int e = 0; e < N; ++e) {
+                            const float2 z = ptx::fma2(make_float2(__uint_as_float(from[2 * e]),
+                                                                   __uint_as_float(from[2 * e + 1])),
                                                        make_float2(sc, sc), make_float2(nm, nm));
                             const float2 y = make_float2(ptx::ex2_approx(z.x), ptx::ex2_approx(z.y));
                             sum[e & 1] = ptx::add2(sum[e & 1], y);
                             p[e] = ptx::pack_bf16x2(y.x, y.y);
                         }
-                        ptx::tmem_st_32x32b_x32(t_s + 32 * hh, p);
-                        ptx::tmem_st_wait();
+                    };
+                    // P of a half of 64 keys is stored: itself it is ordered by the
+                    // tensor-memory wait and fence; only cleaned rows of V need a release
+                    auto half_done = [&](int hh) {
                         ptx::tc_fence_before();
                         __syncwarp();
-                        // P itself is ordered by the tensor-memory wait and
-                        // fence; only cleaned rows of V need a release
                         if (lane == 0) {
                             if (special) ptx::mbar_arrive(sy.bar(L::B_P_FULL + 2 * slot + hh));
                             else ptx::mbar_arrive_relaxed(sy.bar(L::B_P_FULL + 2 * slot + hh));
+                        }
+                    };
+                    if constexpr (SPLIT_ROWS) {
+#pragma unroll
+                        for (int hh = 0; hh < 2; ++hh) {
+                            uint32_t p[32];
+                            weigh(x[hh], p);
+                            ptx::tmem_st_32x32b_x32(t_s + 32 * hh, p);
+                            ptx::tmem_st_wait();
+                            half_done(hh);
+                        }
+                    } else {
+#pragma unroll 1
+                        for (int cc = 0; cc < kTile; cc += 32) {
+                            uint32_t p[16];
+                            scores32(cc);
+                            weigh(x[0], p);
+                            __syncwarp();
+                            ptx::tmem_st_32x32b_x16(t_s + cc / 2, p);
+                            ptx::tmem_st_wait();
+                            if (cc & 32) half_done(cc >> 6);
                         }
                     }
                     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
