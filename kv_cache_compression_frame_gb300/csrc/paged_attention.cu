@@ -118,6 +118,14 @@ struct Plan {
     }
 };
 
+__device__ __forceinline__ Plan plan_of(const PagedKernelArgs& k, uint32_t total) {
+    Plan p;
+    p.ctas = min((total + kMinShare - 1) / kMinShare, (uint32_t)k.grid);
+    p.each = total / p.ctas;
+    p.more = total - p.each * p.ctas;
+    return p;
+}
+
 // Cost of one KV head's blocks in sequence s (a whole warp, the same result in
 // every lane).
 __device__ __forceinline__ uint32_t head_cost(const PagedKernelArgs& k, Seq q) {
@@ -139,12 +147,7 @@ __device__ __forceinline__ Plan make_plan(const PagedKernelArgs& k) {
     } else {
         for (int s = 0; s < seqs; ++s) total += head_cost(k, seq_of(k, s));
     }
-    total *= (uint32_t)(k.a.layers * k.a.kv_heads);
-    Plan p;
-    p.ctas = min((total + kMinShare - 1) / kMinShare, (uint32_t)k.grid);
-    p.each = total / p.ctas;
-    p.more = total - p.each * p.ctas;
-    return p;
+    return plan_of(k, total * (uint32_t)(k.a.layers * k.a.kv_heads));
 }
 
 // A place in the schedule: unit (sequence s, batch entry n, KV head h, block b),
@@ -223,6 +226,46 @@ __device__ __forceinline__ Place find(const PagedKernelArgs& k, uint32_t w) {
         w -= base;
     }
     p.v = (int)w;
+    return p;
+}
+
+// The schedule, and the place where CTA c's share starts (a whole warp, the same
+// result in every lane).  The usual case, one block per head and up to 32
+// sequences, takes one look at the lengths.
+__device__ __forceinline__ Place schedule(const PagedKernelArgs& k, int c, Plan& plan) {
+    const int seqs = k.a.batch / k.a.layers, lane = threadIdx.x & 31;
+    Place p{};
+    if (k.rb > 1 || seqs > 32) {
+        plan = make_plan(k);
+        if (c < (int)plan.ctas) p = find(k, plan.start((uint32_t)c));
+        return p;
+    }
+    const uint32_t heads = (uint32_t)(k.a.layers * k.a.kv_heads);
+    Seq q{0, 0};
+    uint32_t cost = 0;
+    if (lane < seqs) {
+        q = seq_of(k, lane);
+        cost = (uint32_t)(block_tiles(k, q, 0) + kUnitCost);
+    }
+    uint32_t upto = cost * heads;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const uint32_t x = __shfl_up_sync(0xffffffffu, upto, off);
+        if (lane >= off) upto += x;
+    }
+    plan = plan_of(k, __shfl_sync(0xffffffffu, upto, 31));
+    if (c >= (int)plan.ctas) return p;
+    uint32_t w = plan.start((uint32_t)c);
+    p.s = __ffs((int)__ballot_sync(0xffffffffu, upto > w)) - 1;
+    w -= __shfl_sync(0xffffffffu, upto - cost * heads, p.s);
+    cost = __shfl_sync(0xffffffffu, cost, p.s);
+    p.q.len = __shfl_sync(0xffffffffu, q.len, p.s);
+    p.q.count = __shfl_sync(0xffffffffu, q.count, p.s);
+    const int nh = (int)(w / cost);
+    p.v = (int)(w - (uint32_t)nh * cost);
+    p.n = nh / k.a.kv_heads;
+    p.h = nh - p.n * k.a.kv_heads;
+    p.n += p.s * k.a.layers;
     return p;
 }
 
@@ -409,11 +452,9 @@ paged_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
         first.at.q = seq_of(k, first.at.s);
         first.left = block_tiles(k, first.at.q, first.at.b) + kUnitCost;
     } else {
-        const Plan plan = make_plan(k);
-        if (c < (int)plan.ctas) {
-            first.at = find(k, plan.start((uint32_t)c));
-            first.left = (int)(plan.start((uint32_t)c + 1) - plan.start((uint32_t)c));
-        }
+        Plan plan;
+        first.at = schedule(k, c, plan);
+        if (c < (int)plan.ctas) first.left = (int)(plan.start((uint32_t)c + 1) - plan.start((uint32_t)c));
     }
     if (warp < 4) {
         ptx::regs_dec<kRegsIssue>();
@@ -921,12 +962,11 @@ __global__ void __launch_bounds__(kMergeThreads) paged_combine_kernel(const __gr
                                                                       int per_cut) {
     const statekv_paged_attention_args& a = k.a;
     const int cut = 1 + blockIdx.x / per_cut, part = blockIdx.x % per_cut;
-    const Plan plan = make_plan(k);
-    Place p{};
+    Plan plan;
+    const Place p = schedule(k, cut, plan);
     uint32_t w = 0;                          // where the unit starts
     bool mine = cut < (int)plan.ctas;
     if (mine) {
-        p = find(k, plan.start((uint32_t)cut));
         w = plan.start((uint32_t)cut) - (uint32_t)p.v;
         mine = p.v > 0 && plan.start((uint32_t)cut - 1) <= w;
     }
