@@ -649,8 +649,9 @@ int statekv_sparse_attention(const statekv_sparse_args* args, void* cuda_stream)
  * [pages][kv_heads][page_rows][head_dim] (batch_stride is the stride of a
  * page), num_pages of them.  table: int32 [batch][table_stride], row i of batch
  * entry n is row i % page_rows of page table[n][i / page_rows]; a table row
- * holds table_pages <= table_stride entries, so a sequence at most table_pages
- * * page_rows <= 2^31 - 257 rows.  Entries past the last page in use are not looked
+ * holds table_pages <= table_stride entries, and with them a sequence at most
+ * table_pages x page_rows rows (2^31 - 257 at most, of a plain cache too).
+ * Entries past the last page in use are not looked
  * at; one in use that is out of [0, num_pages) is recorded (E_DEVICE): its rows
  * read as zeros, and nothing is written there.  Pages may be shared by entries
  * that only read them.  page_rows is a multiple of 16.  table NULL: a plain
@@ -730,7 +731,8 @@ int statekv_paged_attention(const statekv_paged_attention_args* args, void* cuda
  *   out[row] = before[row] + sum over the head group's queries that see the row
  *              of exp(q . k * scale - lse),
  * rows from the length on as before.  q, lengths and counts as for that call;
- * a query whose lse is -infinity adds nothing.  before, out: float
+ * a query whose lse is infinite adds nothing (a key that is not finite gives
+ * its own row what comes of it, and no other).  before, out: float
  * [batch][kv_heads][weight_rows] (before NULL: zeros; out may be before),
  * weight_rows at least the rows a sequence can hold (E_CAPACITY).  Scores and sums in
  * fp32, each row's sum in a fixed order (the same bits on every run).

