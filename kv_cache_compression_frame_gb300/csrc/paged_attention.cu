@@ -276,6 +276,31 @@ __device__ __forceinline__ Place schedule(const PagedKernelArgs& k, int c, Plan&
     return p;
 }
 
+// Where the u-th unit starts in the schedule, and which it is.
+__device__ __forceinline__ uint32_t unit_start(const PagedKernelArgs& k, int u, Place& p) {
+    const int heads = k.a.layers * k.a.kv_heads, lane = threadIdx.x & 31;
+    const int nh = u / k.rb;                 // over all sequences
+    p.n = nh / k.a.kv_heads;
+    p.h = nh - p.n * k.a.kv_heads;
+    p.s = p.n / k.a.layers;
+    p.b = u - nh * k.rb;
+    p.q = seq_of(k, p.s);
+    const uint32_t cost = head_cost(k, p.q);
+    uint32_t w = (uint32_t)(nh - p.s * heads) * cost, before = 0;
+    if (!k.a.lengths && !k.a.counts) {
+        w += (uint32_t)(p.s * heads) * cost;
+    } else if (k.rb == 1) {
+        for (int s = lane; s < p.s; s += 32) before += (uint32_t)(block_tiles(k, seq_of(k, s), 0) + kUnitCost);
+        w += __reduce_add_sync(0xffffffffu, before) * (uint32_t)heads;
+    } else {
+        for (int s = 0; s < p.s; ++s) before += head_cost(k, seq_of(k, s));
+        w += before * (uint32_t)heads;
+    }
+    before = 0;
+    for (int b = lane; b < p.b; b += 32) before += (uint32_t)(block_tiles(k, p.q, b) + kUnitCost);
+    return w + __reduce_add_sync(0xffffffffu, before);
+}
+
 // Walks a share segment by segment.
 struct Walk {
     Place at;                                // the next segment's
@@ -938,12 +963,13 @@ paged_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
 
 // Merges the parts of a unit that several CTAs shared, in CTA order:
 //   O = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i
-// A unit is cut where a CTA's share starts inside of it, so the grid has a few
-// CTAs per share start, and the first start inside a unit merges it.  Thread = 4
-// columns of a row, consecutive threads consecutive rows (how the parts lie).
-// Where a unit has many parts (one layer at 128 k rows: up to 76) kWays threads
-// share an output, each taking every kWays-th part; with up to kFew one thread
-// takes them all and no barrier is needed.
+// Fewer units than shares (one layer at 128 k rows: up to 76 parts each): the
+// grid has many CTAs per unit.  Else a unit is cut where a share starts inside of
+// it, so the grid has a few CTAs per share start, and the first start inside a
+// unit merges it.  Thread = 4 columns of a row, consecutive threads consecutive
+// rows (how the parts lie).  Where a unit has many parts kWays threads share an
+// output, each taking every kWays-th part; with up to kFew one thread takes them
+// all and no barrier is needed.
 constexpr int kMergeThreads = 256;
 constexpr int kWays = 8, kFew = 8;
 
@@ -966,16 +992,19 @@ struct Merge {
 
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) paged_combine_kernel(const __grid_constant__ PagedKernelArgs k,
-                                                                      int per_cut) {
+                                                                      int per, int by_unit) {
     const statekv_paged_attention_args& a = k.a;
-    const int cut = 1 + blockIdx.x / per_cut, part = blockIdx.x % per_cut;
+    const int which = blockIdx.x / per, part = blockIdx.x - which * per;
     Plan plan;
-    const Place p = schedule(k, cut, plan);
+    Place p = schedule(k, by_unit ? 0 : which + 1, plan);
     uint32_t w = 0;                          // where the unit starts
-    bool mine = cut < (int)plan.ctas;
-    if (mine) {
-        w = plan.start((uint32_t)cut) - (uint32_t)p.v;
-        mine = p.v > 0 && plan.start((uint32_t)cut - 1) <= w;
+    bool mine = true;
+    if (by_unit) {
+        w = unit_start(k, which, p);
+    } else if ((mine = which + 1 < (int)plan.ctas)) {
+        const uint32_t cut = plan.start((uint32_t)which + 1);
+        w = cut - (uint32_t)p.v;
+        mine = p.v > 0 && plan.start((uint32_t)which) <= w;
     }
     const int nt = mine ? block_tiles(k, p.q, p.b) : 0;
     // in every CTA, before it may leave: this grid must not end before the one
@@ -993,7 +1022,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_combine_kernel(const __gr
     __shared__ Merge sh[kMergeThreads];
     // part i: the share's first unit's where the share starts in the unit, else its last's
     const int64_t head = 2 * (int64_t)ca + (plan.start((uint32_t)ca) >= w ? 0 : 1);
-    for (int out0 = part * per_step; out0 < outs; out0 += per_cut * per_step) {
+    for (int out0 = part * per_step; out0 < outs; out0 += per * per_step) {
         const int out = out0 + x, c4 = out / rows, r = out - c4 * rows;
         const bool live = out < outs;
         Merge acc;
@@ -1052,13 +1081,15 @@ cudaError_t launch_main(const PagedKernelArgs& k, const CUtensorMap& mk, const C
 }
 
 template <int D>
-cudaError_t launch_combine(const PagedKernelArgs& k, cudaStream_t st) {
-    // up to eight CTAs per cut, but no more than there are steps of the
-    // many-part form
+cudaError_t launch_combine(const PagedKernelArgs& k, int64_t units, int sms, cudaStream_t st) {
+    // about eight CTAs per SM, but no more than there are steps of the many-part
+    // form.  (Eight per cut for two units of 228 rows, 18 MB of parts: 100 us.)
     const int steps = (k.rows * (D / 4) + kMergeThreads / kWays - 1) / (kMergeThreads / kWays);
-    const int per_cut = std::min(steps, 8);
+    const int by_unit = units < k.grid;
+    const int groups = by_unit ? (int)units : k.grid - 1;
+    const int per = std::max(1, std::min(steps, 8 * sms / groups));
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((k.grid - 1) * per_cut));
+    cfg.gridDim = dim3((unsigned)(groups * per));
     cfg.blockDim = dim3(kMergeThreads);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -1066,7 +1097,7 @@ cudaError_t launch_combine(const PagedKernelArgs& k, cudaStream_t st) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, paged_combine_kernel<D>, k, per_cut);
+    return cudaLaunchKernelEx(&cfg, paged_combine_kernel<D>, k, per, by_unit);
 }
 
 // Sizes that follow from the arguments; what to refuse them with.
@@ -1179,6 +1210,6 @@ extern "C" int statekv_paged_attention(const statekv_paged_attention_args* args,
     cudaError_t e = a.head_dim == 128 ? two ? launch_main<128, true>(k, mk, mv, dev, st) : launch_main<128, false>(k, mk, mv, dev, st)
                     : two             ? launch_main<64, true>(k, mk, mv, dev, st)
                                       : launch_main<64, false>(k, mk, mv, dev, st);
-    if (e == cudaSuccess && k.merge) e = a.head_dim == 128 ? launch_combine<128>(k, st) : launch_combine<64>(k, st);
+    if (e == cudaSuccess && k.merge) e = a.head_dim == 128 ? launch_combine<128>(k, z.units, sms, st) : launch_combine<64>(k, z.units, sms, st);
     return e == cudaSuccess ? STATEKV_OK : view_cuda_fail();
 }
