@@ -42,7 +42,7 @@ namespace {
 
 constexpr int kTile = 128;
 constexpr int kItem = 2 * kTile;             // rows of an item
-constexpr int kWeightThreads = 672;          // five warps of their own roles, sixteen (4..19) that add up
+constexpr int kWeightThreads = 704;          // six warps of their own roles, sixteen (4..19) that add up
 constexpr int kRest = 512;                  // rows of a piece of what is copied
 
 struct WeightKernelArgs {
@@ -222,48 +222,49 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         }
         return true;
     };
-    if (warp == 0) {
-        // ------------------------------------------------------------- K tiles
-        // lane i holds the table entry of box i of the item (at most 16), and of
-        // the item after it: read while this one's copies wait for room
-        const int per_tile = kTile / k.box;
+    if (warp == 0 || warp == 21) {
+        // ------------------------------------------- K tiles of a slot (0, 1)
+        // lane i / KCH copies 64 columns of box i / KCH of the tile; it holds the
+        // box's table entry, and that of the next item's: read while this one's
+        // copies wait for room
+        const int slot = warp == 0 ? 0 : 1, per_tile = kTile / k.box, i = lane / L::KCH;
+        const uint32_t dst = sK + (uint32_t)(lane % L::KCH) * L::CHUNK + (uint32_t)(i * k.box) * 128;
         auto entry = [&](const Walk& y) -> int {
-            const int i = lane;
-            if (i >= 2 * per_tile || y.row0 + i * k.box >= y.q.len) return -1;
+            const int row = y.row0 + slot * kTile + i * k.box;
+            if (i >= per_tile || row >= y.q.len) return -1;
             if (!a.table) return y.n;
-            return a.table[(int64_t)y.n * a.table_stride + (y.row0 / k.box + i) / k.page_boxes];
+            return a.table[(int64_t)y.n * a.table_stride + row / k.box / k.page_boxes];
         };
-        int kt = 0;
+        int s = slot, loaded = 0;
+        uint32_t par = 1;
         bool have = x.next(k);
         int e = have ? entry(x) : -1;
-        for (bool ok = true; ok && have;) {
-            const Walk cur = x;
+        while (have) {
+            const int row = x.row0 + slot * kTile + i * k.box, h = x.h;
             int page = e;
-            if (lane < 2 * per_tile && cur.row0 + lane * k.box < cur.q.len && (uint32_t)page >= (uint32_t)a.num_pages) {
+            if (i < per_tile && row < x.q.len && (uint32_t)page >= (uint32_t)a.num_pages) {
                 record_error(a.status, (uint32_t)STATEKV_E_DEVICE, kSitePage, (uint32_t)page);
                 page = -1;
             }
             have = x.next(k);
             if (have) e = entry(x);
-            for (int t = 0; t < 2; ++t, ++kt) {
-                const int s = kt % L::KS;
-                if (!(ok = sy.wait(L::B_K_EMPTY + s, (uint32_t)((kt / L::KS) & 1) ^ 1u, kSiteKvEmpty))) break;
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive_expect_tx(sy.bar(L::B_K_FULL + s), L::TILE);
-                __syncwarp();
-                const int i = lane / L::KCH, kc = lane % L::KCH;
-                const int p = __shfl_sync(0xffffffffu, page, (t * per_tile + i) & 31);
-                if (i < per_tile) {
-                    const int bx = cur.row0 / k.box + t * per_tile + i;
-                    const int row = p < 0 ? 0 : a.table ? (bx % k.page_boxes) * k.box : bx * k.box;
-                    ptx::tma_load_4d(sK + s * L::TILE + kc * L::CHUNK + i * k.box * 128, &tm_k,
-                                     sy.bar(L::B_K_FULL + s), kc * 64, row, cur.h, p);
-                }
-                __syncwarp();
+            if (!sy.wait(L::B_K_EMPTY + s, par, kSiteKvEmpty)) break;
+            if (lane == 0) ptx::mbar_arrive_expect_tx(sy.bar(L::B_K_FULL + s), L::TILE);
+            __syncwarp();
+            if (i < per_tile)
+                ptx::tma_load_4d(dst + s * L::TILE, &tm_k, sy.bar(L::B_K_FULL + s), lane % L::KCH * 64,
+                                 page < 0 ? 0 : a.table ? row / k.box % k.page_boxes * k.box : row, h, page);
+            __syncwarp();
+            ++loaded;
+            if ((s += 2) >= L::KS) {
+                s = slot;
+                par ^= 1u;
             }
         }
-        for (int s = 0; s < L::KS && s < kt; ++s)
-            sy.drain(L::B_K_FULL + s, (uint32_t)(((kt - 1 - s) / L::KS) & 1));
+        // never leave a copy in flight into this CTA's shared memory
+        constexpr int STAGES = L::KS / 2;
+        for (int j = 0; j < STAGES && j < loaded; ++j)
+            sy.drain(L::B_K_FULL + slot + 2 * j, (uint32_t)(((loaded - 1 - j) / STAGES) & 1));
     } else if (warp == 1 || warp == 3) {
         // ---------------------------------------------------------- MMA issuers
         // one per slot: an issuer shares its scheduler with five other warps and
@@ -407,11 +408,32 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         const int c_begin = 64 * half, c_end = split && half == 0 ? 64 : k.n;
         uint32_t s_par = 0, item = 0, buf = 0, qt = 0;
         bool ok = split || half == 0;
-        for (; ok && x.next(k); ++item) {
+        auto weight_at = [&](const Walk& y) -> int64_t {
+            const int row = y.row0 + slot * kTile + lrow;
+            return half == 0 && row < y.q.len ? ((int64_t)y.n * a.kv_heads + y.h) * a.weight_rows + row : -1;
+        };
+        // An item of few queries is a block or two: the next one's weights are on
+        // their way while this one is added up.  (With many queries that costs more
+        // registers than it saves: 225 us for a prompt instead of 211.)
+        Walk ahead = x;
+        bool have = !WIDE && ok && ahead.next(k);
+        int64_t at_next = have ? weight_at(ahead) : -1;
+        float next = at_next >= 0 && a.before ? a.before[at_next] : 0.f;
+        for (; ok && (WIDE ? x.next(k) : have); ++item) {
+            int64_t at;
+            float before;
+            if constexpr (WIDE) {
+                at = weight_at(x);
+                before = at >= 0 && a.before ? a.before[at] : 0.f;
+            } else {
+                x = ahead;
+                at = at_next;
+                before = next;
+                have = ahead.next(k);
+                at_next = have ? weight_at(ahead) : -1;
+                next = at_next >= 0 && a.before ? a.before[at_next] : 0.f;
+            }
             const int row = x.row0 + slot * kTile + lrow;
-            const int64_t at = ((int64_t)x.n * a.kv_heads + x.h) * a.weight_rows + row;
-            const bool live = half == 0 && row < x.q.len;
-            const float before = live && a.before ? a.before[at] : 0.f;
             const int first_new = x.q.len - x.q.count;
             float total = 0.f;
             for (int b = x.b0; b < x.blocks; ++b) {
@@ -426,18 +448,26 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                 float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                 if (x.row0 + kItem > first_new + j0 + 1 || upto < k.tb ||
                     (unseen[0] | unseen[1] | unseen[2] | unseen[3]) != 0u) {
+                    // the columns (from c_begin on) that count for this row
+                    uint64_t seen = 0;
+                    const int j_first = max(from, 0), count = min(upto, k.tb) - j_first;
+                    for (int g = 0; g < k.G && count > 0; ++g) {
+                        const int lo = max(g * k.tb + j_first - c_begin, 0);
+                        const int hi = min(g * k.tb + j_first + count - c_begin, 64);
+                        if (lo < hi) seen |= ~0ull >> (64 - (hi - lo)) << lo;
+                    }
+                    seen &= ~((uint64_t)unseen[2 * half + 1] << 32 | unseen[2 * half]);
 #pragma unroll 1
-                    for (int c = c_begin; c < c_end; c += 16) {
+                    for (int c = c_begin; c < c_end; c += 16, seen >>= 16) {
                         uint32_t v[16];
                         __syncwarp();
                         ptx::tmem_ld_32x32b_x16(t_b + c, v);
                         ptx::tmem_ld_wait();
-                        const uint32_t gone = unseen[c >> 5] >> (c & 31);
+                        const uint32_t now = (uint32_t)seen;
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
-                            const int j = tok[c + e];
                             const float y = ptx::ex2_approx(__uint_as_float(v[e]) * sc);
-                            sum[e & 1].x += c + e < k.cols && j >= from && j < upto && !(gone >> e & 1u) ? y : 0.f;
+                            sum[e & 1].x += now & 1u << e ? y : 0.f;
                         }
                     }
                 } else {
@@ -478,7 +508,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(sy.bar((half == 1 ? L::B_PART : L::B_TAKEN) + slot));
             }
-            if (ok && live) a.out[at] = before + total;
+            if (ok && at >= 0) a.out[at] = before + total;
         }
         while (copy_step()) {}
     }
