@@ -42,7 +42,6 @@ namespace {
 
 constexpr int kTile = 128;
 constexpr int kItem = 2 * kTile;             // rows of an item
-constexpr int kWeightThreads = 704;          // six warps of their own roles, sixteen (4..19) that add up
 constexpr int kRest = 512;                  // rows of a piece of what is copied
 
 struct WeightKernelArgs {
@@ -61,42 +60,71 @@ __device__ __forceinline__ Seq seq_of(const WeightKernelArgs& k, int s) {
     return q;
 }
 
-// Walks the items of a CTA: blockIdx.x, + gridDim.x, ...
+// Walks the items of a CTA: blockIdx.x, + gridDim.x, ...  Within a sequence the
+// step is added as (entries, heads, items of a head), so that only a sequence's
+// first item costs divisions (every role of the kernel takes every step).
 struct Walk {
     int64_t it, end;                         // the next item; items before the next sequence
     int s, per_head;                         // sequence, its items per KV head
+    int dn, dh, di;                          // the step
     Seq q;
-    int n, h, row0;                          // the current item
+    int n, h, i;                             // the current item: entry, head, place in the head
+    int row0;
     int b0, blocks;                          // first query block that sees any row of it; their end
     __device__ void begin() {
         it = blockIdx.x;
         end = 0;
         s = -1;
-        per_head = 0;
     }
     __device__ bool next(const WeightKernelArgs& k) {
-        const int heads = k.a.layers * k.a.kv_heads;
-        while (it >= end) {
-            if (++s >= k.a.batch / k.a.layers) return false;
-            q = seq_of(k, s);
-            per_head = (q.len + kItem - 1) / kItem;
-            end += (int64_t)per_head * heads;
+        if (it < end) {
+            n += dn;
+            h += dh;
+            if ((i += di) >= per_head) {
+                i -= per_head;
+                ++h;
+            }
+            if (h >= k.a.kv_heads) {
+                h -= k.a.kv_heads;
+                ++n;
+            }
+        } else {
+            const int heads = k.a.layers * k.a.kv_heads;
+            do {
+                if (++s >= k.a.batch / k.a.layers) return false;
+                q = seq_of(k, s);
+                per_head = (q.len + kItem - 1) / kItem;
+                end += (int64_t)per_head * heads;
+            } while (it >= end);
+            const int local = (int)(it - (end - (int64_t)per_head * heads)), step = (int)gridDim.x;
+            h = local / per_head;
+            i = local - h * per_head;
+            n = h / k.a.kv_heads;
+            h -= n * k.a.kv_heads;
+            n += s * k.a.layers;
+            dh = step / per_head;
+            di = step - dh * per_head;
+            dn = dh / k.a.kv_heads;
+            dh -= dn * k.a.kv_heads;
+            blocks = (q.count + k.tb - 1) / k.tb;
         }
-        const int local = (int)(it - (end - (int64_t)per_head * heads));
-        const int nh = local / per_head;
-        row0 = (local - nh * per_head) * kItem;
-        n = s * k.a.layers + nh / k.a.kv_heads;
-        h = nh % k.a.kv_heads;
-        blocks = (q.count + k.tb - 1) / k.tb;
-        b0 = max(0, row0 - (q.len - q.count)) / k.tb;
+        row0 = i * kItem;
+        const int past = row0 - (q.len - q.count);
+        b0 = past > 0 ? past / k.tb : 0;
         it += gridDim.x;
         return true;
     }
 };
 
-// WIDE: more than 64 columns, in two halves of eight warps each.
+// WIDE: more than 64 columns, in two halves of eight warps each.  Otherwise two
+// warps copy the rows that no query sees while eight add up.
 template <int D, bool WIDE>
 struct WeightLayout {
+    // warps: K of slot 0, issuer of slot 0, helper, issuer of slot 1; ADDERS that
+    // add up; the copiers; then a second helper and K of slot 1
+    static constexpr int ADDERS = WIDE ? 16 : 8;
+    static constexpr int HELPER = 4 + ADDERS + (WIDE ? 0 : 2), LOADER = HELPER + 1;
+    static constexpr int THREADS = (LOADER + 1) * 32;
     static constexpr int KCH = D / 64;
     static constexpr int CHUNK = 128 * 128;              // [128 rows][64 bf16], 128B-swizzled
     static constexpr int TILE = KCH * CHUNK;
@@ -132,7 +160,7 @@ struct WeightLayout {
 };
 
 template <int D, bool WIDE>
-__global__ void __launch_bounds__(kWeightThreads, 1)
+__global__ void __launch_bounds__((WeightLayout<D, WIDE>::THREADS), 1)
 weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q,
                const __grid_constant__ WeightKernelArgs k) {
     using L = WeightLayout<D, WIDE>;
@@ -180,9 +208,9 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         for (int i = lane; i < 128; i += 32) tok[i] = (uint8_t)(i < k.cols ? i % k.tb : 255);
     // Rows of Q that no query fills are zeros, columns that no query has get a
     // score of -2^127: both once and for all.
-    for (int i = threadIdx.x; i < L::QS * L::QTILE / 16; i += kWeightThreads)
+    for (int i = threadIdx.x; i < L::QS * L::QTILE / 16; i += L::THREADS)
         reinterpret_cast<uint4*>(base + L::OFF_Q)[i] = make_uint4(0u, 0u, 0u, 0u);
-    for (int i = threadIdx.x; i < 128 * 8; i += kWeightThreads) {
+    for (int i = threadIdx.x; i < 128 * 8; i += L::THREADS) {
         const int r = i >> 3, e = i & 7;                         // 16-byte unit e of row r
         uint4 x = make_uint4(0u, 0u, 0u, 0u);
         if (e == 6) x = make_uint4(0x3f803f80u, 0x3f80u, 0u, 0u);            // 1, 1, 1
@@ -197,8 +225,8 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     Walk x;
     x.begin();
     // Rows that no query sees stay as before.  One step copies the next kRest of
-    // the CTA's; false: none left.  The warps that have no columns
-    // take them from the start, the others what is left when they are done.
+    // the CTA's; false: none left.  The copiers take them from the
+    // start, the others what is left when they are done.
     const int pieces = a.out == a.before ? 0 : (a.weight_rows + kRest - 1) / kRest;
     const int64_t all = (int64_t)a.batch * a.kv_heads * pieces;
     auto copy_step = [&]() -> bool {
@@ -222,7 +250,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         }
         return true;
     };
-    if (warp == 0 || warp == 21) {
+    if (warp == 0 || warp == L::LOADER) {
         // ------------------------------------------- K tiles of a slot (0, 1)
         // lane i / KCH copies 64 columns of box i / KCH of the tile; it holds the
         // box's table entry, and that of the next item's: read while this one's
@@ -316,7 +344,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         __syncwarp();
         sy.drain(L::B_DRAIN + slot, 0);
         while (copy_step()) {}
-    } else if (warp == 2 || warp == 20) {
+    } else if (warp == 2 || warp == L::HELPER) {
         // -------------------------------------------- queries and log-sum-exps
         // A block costs a warp 1700 cycles (the splitting, the stores, the latency
         // of the next block's values), so there are two, with a stage each.
@@ -397,17 +425,17 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         // never leave a copy in flight into this CTA's shared memory
         sy.drain(L::B_Q_FULL + mine, q_par);
         while (copy_step()) {}
-    } else {
+    } else if (warp < 4 + L::ADDERS) {
         // --------------------------------------------------------- exponentials
         // slot and half of its columns
-        const int slot = (warp >> 2) - 1 & 1, half = (warp - 4) >> 3, q4 = warp & 3;
+        const int slot = (warp >> 2) - 1 & 1, half = WIDE ? (warp - 4) >> 3 : 0, q4 = warp & 3;
         const int lrow = q4 * 32 + lane;                         // key of the tile = TMEM lane
         const uint32_t t_s = tmem + 256u * slot + ((uint32_t)(q4 * 32) << 16);
         const float sc = k.scale_log2;
         volatile float* part = reinterpret_cast<volatile float*>(base + L::OFF_PART) + slot * 128 + lrow;
         const int c_begin = 64 * half, c_end = split && half == 0 ? 64 : k.n;
         uint32_t s_par = 0, item = 0, buf = 0, qt = 0;
-        bool ok = split || half == 0;
+        bool ok = true;
         auto weight_at = [&](const Walk& y) -> int64_t {
             const int row = y.row0 + slot * kTile + lrow;
             return half == 0 && row < y.q.len ? ((int64_t)y.n * a.kv_heads + y.h) * a.weight_rows + row : -1;
@@ -511,6 +539,8 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             if (ok && at >= 0) a.out[at] = before + total;
         }
         while (copy_step()) {}
+    } else {
+        while (copy_step()) {}
     }
     __syncthreads();
     if (warp == 1) {
@@ -526,7 +556,7 @@ cudaError_t launch_weights(const WeightKernelArgs& k, const CUtensorMap& mk, con
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = allow_smem(reinterpret_cast<const void*>(&weights_kernel<D, WIDE>), L::SMEM, dev, done);
     if (e != cudaSuccess) return e;
-    weights_kernel<D, WIDE><<<(unsigned)grid, kWeightThreads, L::SMEM, st>>>(mk, mq, k);
+    weights_kernel<D, WIDE><<<(unsigned)grid, L::THREADS, L::SMEM, st>>>(mk, mq, k);
     return cudaGetLastError();
 }
 
