@@ -314,9 +314,10 @@ cudaError_t launch_evict(const statekv_evict_args& a, int dev, int sms, cudaStre
     ka.a = a;
     const int64_t units = (int64_t)a.batch * a.kv_heads;
     const int64_t cap = paging_of(a).capacity();
-    // CTAs of at most 4096 rows, as long as they all run at once
+    // CTAs of at most 4096 rows, as long as they all run at once (one per SM: its
+    // 1024 threads take the registers)
     int c = 1;
-    while (c < kMaxCluster && cap > (int64_t)c * 4096 && units * c * 2 <= 2 * sms) c *= 2;
+    while (c < kMaxCluster && cap > (int64_t)c * 4096 && units * c * 2 <= sms) c *= 2;
     ka.cluster = c;
     const int64_t slice = ((cap + c * kEvictWarps - 1) / (c * kEvictWarps) + 31) / 32 * 32 * kEvictWarps;
     ka.staged = slice <= kMaxStaged ? (int)slice : 0;
