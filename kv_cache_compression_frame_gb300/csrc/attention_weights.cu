@@ -18,20 +18,21 @@
 // The log-sum-exp is part of the product: a ninth k-step multiplies a row of ones
 // with -lse / scale in three bf16 terms (24 bits), so S comes out as q . k - lse /
 // scale and a column costs one multiplication, one exponential and one addition.
-// Read from shared memory for each column it took twice the time: the products
-// take all of its bandwidth (8 KB per 64 cycles), and the reads wait for them.
+// (Read from shared memory for each column, 246 us instead of 228 for a prompt:
+// the products take all of its bandwidth, 8 KB per 64 cycles.)
 //
 // Bound: by HBM for a few tokens (K once, 256 bytes a row and 8 of weights), by
 // the exponentials (16384 per tile and block at 32 a cycle) and the tensor cores
 // (576 cycles) for a prompt.
 //
 // Scores and sums in fp32.  In blocks with tokens behind the count, with queries
-// that saw nothing, or over rows that not every token sees, columns are selected.
+// that saw nothing, or over rows that not every token sees, columns are selected,
+// by a mask of bits that each row makes once per block.
 //
 // Measured: one token for each of 16 ragged streams of up to 32768 rows, 8 KV
-// heads, 0.56 GB: 99 us = 5.7 TB/s.  512 tokens over 131072 rows, 12 heads on 2:
-// 211 us; a block takes 1850 cycles, of which the loop over its columns 1540 (the
-// exponentials alone 1024, the products 1152 beside them).
+// heads, 0.56 GB: 95 us = 5.9 TB/s.  512 tokens over 131072 rows, 12 heads on 2:
+// 183 us, 1600 cycles a block (the exponentials alone 1024, the products 1152
+// beside them).
 #include <algorithm>
 
 #include "paged.cuh"
@@ -42,7 +43,7 @@ namespace {
 
 constexpr int kTile = 128;
 constexpr int kItem = 2 * kTile;             // rows of an item
-constexpr int kRest = 512;                  // rows of a piece of what is copied
+constexpr int kRest = 512;                   // rows of a piece of what is copied
 
 struct WeightKernelArgs {
     statekv_attention_weights_args a;

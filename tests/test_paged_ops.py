@@ -122,6 +122,7 @@ def check_attention(q, cache, lengths, counts, scale, out, lse, layers=1, what="
     (1, 1, 257, 257, 0),
     (64, 1, 9, 900, 64),
     (2, 2, 1, 40000, 64),        # one row over many parts
+    (12, 2, 38, 20000, 256),     # 228 rows over many parts
     (12, 2, 130, 3333, 0),
 ])
 def test_attention_sizes(d, hq, hkv, tok, rows, page):
