@@ -733,8 +733,8 @@ int statekv_paged_attention(const statekv_paged_attention_args* args, void* cuda
  * rows from the length on as before.  q, lengths and counts as for that call;
  * a query whose lse is infinite adds nothing (a key that is not finite gives
  * its own row what comes of it, and no other).  before, out: float
- * [batch][kv_heads][weight_rows] (before NULL: zeros; out may be before),
- * weight_rows at least the rows a sequence can hold (E_CAPACITY).  Scores and sums in
+ * [batch][kv_heads][weight_rows] (before NULL: zeros; out may be before, and shares
+ * no memory with it otherwise), weight_rows at least the rows a sequence can hold (E_CAPACITY).  Scores and sums in
  * fp32, each row's sum in a fixed order (the same bits on every run).
  * bf16, head_dim 64 or 128, q_heads / kv_heads <= 64; q and K are read in tiles:
  * their entries do not share memory.  No workspace.

@@ -585,6 +585,8 @@ extern "C" int statekv_attention_weights(const statekv_attention_weights_args* a
     if (!a.lse || !a.out || !view_ok(a.q, 2, a.batch, a.q_heads, a.tokens) ||
         !spread(a.q, a.batch, a.q_heads, a.tokens))
         return STATEKV_E_INVALID_ARG;
+    const int64_t all = (int64_t)a.batch * a.kv_heads * a.weight_rows;
+    if (a.before && a.before != a.out && overlap(a.before, all, a.out, all)) return STATEKV_E_INVALID_ARG;
     const bool cached = !paging_empty(pg);
     if (cached && (!view_ok(a.k_pages, 2, a.num_pages, a.kv_heads, a.page_rows) ||
                    !spread(a.k_pages, a.num_pages, a.kv_heads, a.page_rows)))

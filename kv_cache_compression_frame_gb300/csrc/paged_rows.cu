@@ -427,6 +427,9 @@ extern "C" int statekv_evict_rows(const statekv_evict_args* args, void* cuda_str
                 !apart(*v, a.out_num_pages, a.kv_heads, a.out_page_rows, a.head_dim))
                 return STATEKV_E_INVALID_ARG;
     const int64_t units = (int64_t)a.batch * a.kv_heads;
+    const int64_t w = units * a.weight_rows, o = units * a.out_rows, k = units * a.keep;
+    if (overlap(a.weights, w, a.weights_out, o) || overlap(a.weights, w, a.kept, k) || overlap(a.weights_out, o, a.kept, k))
+        return STATEKV_E_INVALID_ARG;
     if (units * 16 > 0x7fffffffll || units * ((a.keep + kMoveRows - 1) / kMoveRows) > 0x7fffffffll)
         return STATEKV_E_UNSUPPORTED;
     int dev = 0, sms = 0;

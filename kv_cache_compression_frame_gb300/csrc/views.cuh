@@ -39,6 +39,12 @@ inline bool aligned16(const void* p) { return p && reinterpret_cast<uintptr_t>(p
 // An array of 32-bit entries, or none.
 inline bool ints_ok(const void* p) { return reinterpret_cast<uintptr_t>(p) % 4 == 0; }
 
+// Whether two arrays of n and m 32-bit entries share memory.
+inline bool overlap(const void* p, int64_t n, const void* q, int64_t m) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(p), y = reinterpret_cast<uintptr_t>(q);
+    return x < y + 4 * (uint64_t)m && y < x + 4 * (uint64_t)n;
+}
+
 // Rows of `len` entries `stride` apart, or one row (0) for all.
 inline bool rows_ok(int32_t stride, int32_t len) { return stride == 0 || stride >= len; }
 

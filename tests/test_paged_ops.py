@@ -972,6 +972,25 @@ def test_evict_refusals_before_device_work(bad, want):
     assert N.load().statekv_evict_rows(N.EvictArgs(**{**a, **bad}), None) == want
 
 
+@pytest.mark.parametrize("bad", [
+    dict(weights_out=1 << 30), dict(weights_out=(1 << 30) + 2044), dict(weights_out=(1 << 30) - 508),
+    dict(kept=(1 << 30) + 1024), dict(kept=(1 << 31) + 508)])
+def test_evict_arrays_that_share_memory_are_refused(bad):
+    """4 units of 128 weights in, 32 out, 32 rows kept: ranges that share one entry at least."""
+    pool, to = view(b=1 << 20, h=1 << 16), view(1 << 20, b=1 << 20, h=1 << 16)
+    a = dict(PAGED, k_pages=pool, v_pages=pool, k_out=to, v_out=to, out_table=16, out_table_stride=2, out_table_pages=2,
+             out_num_pages=4, out_page_rows=16, out_rows=32, keep=32, sinks=4, recent=8, weights=1 << 30,
+             weights_out=1 << 31, kept=1 << 32, weight_rows=128, length=40, dtype=0)
+    assert N.load().statekv_evict_rows(N.EvictArgs(**{**a, **bad}), None) == N.E_INVALID_ARG
+
+
+@pytest.mark.parametrize("by", [4, 2044, -4, -2044])
+def test_weights_over_a_part_of_what_they_are_added_to_are_refused(by):
+    a = dict(PAGED, q=view(), k_pages=view(b=1 << 20, h=1 << 16), lse=16, before=1 << 30, out=(1 << 30) + by, length=40,
+             tokens=3, q_heads=4, scale=0.1, weight_rows=128)
+    assert N.load().statekv_attention_weights(N.AttentionWeightsArgs(**a), None) == N.E_INVALID_ARG
+
+
 @pytest.mark.parametrize("bad,want", [
     (dict(tokens=0), N.E_INVALID_ARG), (dict(tokens=65), N.E_UNSUPPORTED), (dict(vocab=0), N.E_INVALID_ARG),
     (dict(vocab=1 << 26), N.E_UNSUPPORTED), (dict(tree_stride=4), N.E_INVALID_ARG), (dict(tree=20), N.E_INVALID_ARG),
