@@ -272,6 +272,9 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const __grid_con
         return all;
     };
 
+    // Token 0 until a warp finds its own: where no sum is left, and where rows that
+    // are no probabilities take the sums out of range.
+    if (rank == 0 && tid == 0) a.next[seq] = 0;
     // "every CTA of the cluster has started", before its memory is written
     ptx::cluster_sync();
     // The walk, by warp 0 alone (a step takes a dozen fp64 operations, which 512
@@ -347,10 +350,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const __grid_con
     }
     if (rank == 0 && warp == 0) {
         for (int i = count + lane; i < a.tokens; i += 32) a.path[(int64_t)seq * a.tokens + i] = -1;
-        if (lane == 0) {
-            a.counts[seq] = count;
-            if (total <= 0) a.next[seq] = 0;
-        }
+        if (lane == 0) a.counts[seq] = count;
     }
     if (total <= 0) return;
     // the lowest entry whose sum passes `past`

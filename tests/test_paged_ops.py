@@ -651,6 +651,23 @@ def test_verify_edges():
         kv.check_status()
 
 
+@gpu
+def test_verify_of_rows_that_are_no_probabilities_gives_some_token():
+    """Rows whose sums leave 64 bits in units of 2^-52 (16 warps of 128 entries of
+    14.95 each), infinities, and the largest numbers."""
+    tree, t = kv.tree_masks([-1, 0], DEV)[0], torch.zeros((1, 2), dtype=I32, device=DEV)
+    for vocab, value, u in [(2048, 14.95, 0.999), (2048, 3e38, 0.7), (150001, 1.0, 0.9), (150001, 7.3, 0.6),
+                            (5000, math.inf, 0.5), (150001, math.inf, 0.99)]:
+        p = torch.full((1, 3, vocab), value, device=DEV)
+        for q in (None, p, p.roll(1, -1) / 3):
+            torch.full((4,), -7, dtype=I32, device=DEV)          # what the outputs' memory holds
+            path, counts, after = kv.verify_tree(p, q, t, tree, torch.full((1, 3), u, device=DEV))
+            n = int(counts)
+            assert 0 <= int(after) < vocab and 0 <= n <= 2, (vocab, value)
+            assert path[0].tolist() == list(range(n)) + [-1] * (2 - n), (vocab, value)
+    kv.check_status()
+
+
 # ------------------------------------------------------------------- chains
 @gpu
 def test_a_served_text_eager_and_replayed():
