@@ -54,7 +54,7 @@
 // Measured: one token for each of 16 ragged streams of up to 32768 rows, 8 KV
 // heads, 1.06 GB: 160 us = 6.6 TB/s (HBM).  One token in one layer of 131073
 // rows, 134 MB: 40 us, of which 8.5 pass before the first scores and 4 in the
-// merge.  512 tokens over 131072 rows, 12 heads on 2, 0.41 TFLOP: 286 us = 1.44
+// merge.  512 tokens over 131072 rows, 12 heads on 2, 0.41 TFLOP: 283 us = 1.46
 // PFLOP/s, the tensor pipe 65 % busy.
 #include <algorithm>
 
@@ -70,10 +70,6 @@ constexpr int kUnitCost = 6;                 // a unit's start and end in key ti
 constexpr int kWholeTiles = 8;               // key tiles up to which few units stay whole
 constexpr int kMinShare = 4;                 // least share (in tiles' time) before more CTAs join
 constexpr int kPagedThreads = 384;
-// registers a thread after the split: 128 threads of the first warpgroup and
-// 256 softmax threads, together the 168 x 384 of the launch
-constexpr int kRegsIssue = 56, kRegsSoftmax = 224;
-static_assert(kRegsIssue + 2 * kRegsSoftmax <= 3 * 168, "registers of the launch");
 
 // new rows that not every token of a block sees: less than its tokens
 constexpr int kOddWords = 2 * kTile / 32;
@@ -379,6 +375,11 @@ struct Boxes {
 
 template <int D, bool SPLIT_ROWS>
 struct PagedLayout {
+    // registers a thread after the split: 128 threads of the first warpgroup and
+    // 256 softmax threads, together the 168 x 384 of the launch.  (Two row tiles'
+    // softmax holds 128 scores.  Elsewhere 56 and 224 take 2 to 5 % longer.)
+    static constexpr int REGS_ISSUE = SPLIT_ROWS ? 56 : 88, REGS_SOFTMAX = SPLIT_ROWS ? 224 : 208;
+    static_assert(REGS_ISSUE + 2 * REGS_SOFTMAX <= 3 * 168, "registers of the launch");
     static constexpr int KCH = D / 64;
     static constexpr int CHUNK = 128 * 128;              // [128 rows][64 bf16], 128B-swizzled
     static constexpr int TILE = KCH * CHUNK;
@@ -489,7 +490,7 @@ paged_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
         if (c < (int)plan.ctas) first.left = (int)(plan.start((uint32_t)c + 1) - plan.start((uint32_t)c));
     }
     if (warp < 4) {
-        ptx::regs_dec<kRegsIssue>();
+        ptx::regs_dec<L::REGS_ISSUE>();
         if (warp == 0 || warp == 3) {
             // ------------------------------------- TMA producers: K (0) and V (3)
             const bool is_v = warp == 3;
@@ -542,65 +543,124 @@ paged_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
             const uint32_t qb0 = (uint32_t)ptx::sdesc_sw128(sQ, 16, 1024);
             const uint32_t vb0 = (uint32_t)ptx::sdesc_sw128(sV, L::CHUNK, 1024);
             Walk x = first;
-            int g0 = 0, seg = 0;                             // tiles before this segment, segments done
-            uint32_t p_par[2] = {0, 0};
+            int seg = 0;                                     // segments done
+            uint32_t p_par = 0;                              // bit per slot
             bool ok = true;
-            auto issue_s = [&](int j, bool last) -> bool {
-                const int slot = j & 1, g = g0 + (SPLIT_ROWS ? j >> 1 : j), s = g % L::KS;
-                if (!sy.wait(L::B_K_FULL + s, (uint32_t)((g / L::KS) & 1), kSiteKvFull)) return false;
-                ptx::tc_fence_after();
-                if (ptx::elect_one()) {
-                    const uint32_t kb = kb0 + (uint32_t)s * (L::TILE >> 4);
-                    const uint32_t qb = qb0 + (SPLIT_ROWS ? (uint32_t)slot * (L::TILE >> 4) : 0u);
+            // S of a slot (K stage ks), and the products of 64 keys with V (stage vs)
+            auto mma_s = [&](int slot, int ks) {
+                const uint32_t kb = kb0 + (uint32_t)ks * (L::TILE >> 4);
+                const uint32_t qb = qb0 + (SPLIT_ROWS ? (uint32_t)slot * (L::TILE >> 4) : 0u);
 #pragma unroll
-                    for (int kc = 0; kc < L::KCH; ++kc)
+                for (int kc = 0; kc < L::KCH; ++kc)
 #pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            ptx::umma_ss_lh(tmem + L::TM_S + 128u * slot, qb + kc * (L::CHUNK >> 4) + 2 * ks, kmaj_hi,
-                                            kb + kc * (L::CHUNK >> 4) + 2 * ks, kmaj_hi, idesc_s,
-                                            (kc | ks) ? 1u : 0u);
-                    ptx::umma_commit(sy.bar(L::B_S_FULL + slot));
-                    if (!SPLIT_ROWS || slot == 1) ptx::umma_commit(sy.bar(L::B_K_EMPTY + s));
-                    if (last) ptx::umma_commit(sy.bar(L::B_Q_FREE));
-                }
-                __syncwarp();
-                return true;
+                    for (int e = 0; e < 4; ++e)
+                        ptx::umma_ss_lh(tmem + L::TM_S + 128u * slot, qb + kc * (L::CHUNK >> 4) + 2 * e, kmaj_hi,
+                                        kb + kc * (L::CHUNK >> 4) + 2 * e, kmaj_hi, idesc_s, (kc | e) ? 1u : 0u);
+                ptx::umma_commit(sy.bar(L::B_S_FULL + slot));
             };
-            auto issue_pv = [&](int j) -> bool {
-                const int slot = j & 1, g = g0 + (SPLIT_ROWS ? j >> 1 : j), s = g % L::VS;
-                if (!sy.wait(L::B_V_FULL + s, (uint32_t)((g / L::VS) & 1), kSiteKvFull)) return false;
-                // the first 64 keys' products run while the other 64 are exponentiated
+            auto mma_pv = [&](int slot, int vs, int hf, bool more) {
+                const uint32_t vb = vb0 + (uint32_t)vs * (L::TILE >> 4);
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    if (!sy.wait(L::B_P_FULL + 2 * slot + hf, p_par[slot], kSitePFull)) return false;
-                    ptx::tc_fence_after();
-                    if (ptx::elect_one()) {
-                        const uint32_t vb = vb0 + (uint32_t)s * (L::TILE >> 4);
-#pragma unroll
-                        for (int ks = 4 * hf; ks < 4 * hf + 4; ++ks)     // 16 keys per step
-                            ptx::umma_ts_lh(tmem + L::TM_O + 128u * slot, tmem + L::TM_S + 128u * slot + 8u * ks,
-                                            vb + 128u * ks, v_hi, idesc_o, (j > 1 || ks > 0) ? 1u : 0u);
-                        if (hf == 1 && (!SPLIT_ROWS || slot == 1)) ptx::umma_commit(sy.bar(L::B_V_EMPTY + s));
-                    }
-                    __syncwarp();
-                }
-                p_par[slot] ^= 1u;
-                return true;
+                for (int e = 4 * hf; e < 4 * hf + 4; ++e)        // 16 keys per step
+                    ptx::umma_ts_lh(tmem + L::TM_O + 128u * slot, tmem + L::TM_S + 128u * slot + 8u * e,
+                                    vb + 128u * e, v_hi, idesc_o, (more || e > 0) ? 1u : 0u);
+            };
+            // stages in turn (a division costs more than a product's time here)
+            int ks = 0, vs = 0;
+            uint32_t k_par = 0, v_par = 0;
+            auto next_k = [&] { if (++ks == L::KS) ks = 0, k_par ^= 1u; };
+            auto next_v = [&] { if (++vs == L::VS) vs = 0, v_par ^= 1u; };
+            auto wait_k = [&] { return ok = sy.wait(L::B_K_FULL + ks, k_par, kSiteKvFull); };
+            auto wait_v = [&] { return ok = sy.wait(L::B_V_FULL + vs, v_par, kSiteKvFull); };
+            auto wait_p = [&](int slot, int hf) {
+                return ok = sy.wait(L::B_P_FULL + 2 * slot + hf, p_par >> slot & 1u, kSitePFull);
             };
             for (; ok && x.next_tiles(k); ++seg) {
-                const int jobs = SPLIT_ROWS ? 2 * x.tiles : x.tiles;
                 if (!(ok = sy.wait(L::B_Q_FULL, (uint32_t)(seg & 1), kSiteQFull))) break;
-                ptx::tc_fence_after();
-                ok = issue_s(0, jobs == 1);
-                if (ok && jobs > 1) ok = issue_s(1, jobs == 2);
-                for (int j = 0; ok && j < jobs; ++j) {
-                    ok = issue_pv(j);
-                    if (ok && j + 2 < jobs) ok = issue_s(j + 2, j + 3 == jobs);
+                if constexpr (SPLIT_ROWS) {
+                    // Both slots go through a key tile.  The issuer is what bounds
+                    // this kernel: few MMAs queue up behind the running one, and a wait
+                    // takes it 80 to 110 cycles though nothing is left to wait for.  So
+                    // one wait for K and one for V serve both slots, and what
+                    // belongs together is issued in one piece.
+                    if (!wait_k()) break;
+                    ptx::tc_fence_after();
+                    if (ptx::elect_one()) {
+                        mma_s(0, ks);
+                        mma_s(1, ks);
+                        ptx::umma_commit(sy.bar(L::B_K_EMPTY + ks));
+                        if (x.tiles == 1) ptx::umma_commit(sy.bar(L::B_Q_FREE));
+                    }
+                    __syncwarp();
+                    next_k();
+#pragma unroll 1
+                    for (int t = 0; t < x.tiles; ++t) {
+                        const bool next = t + 1 < x.tiles;
+                        if (!wait_v() || (next && !wait_k())) break;
+#pragma unroll
+                        for (int slot = 0; slot < 2; ++slot) {
+                            // the first 64 keys' products run while the other 64 are exponentiated
+                            if (!wait_p(slot, 0)) break;
+                            ptx::tc_fence_after();
+                            if (ptx::elect_one()) mma_pv(slot, vs, 0, t > 0);
+                            __syncwarp();
+                            if (!wait_p(slot, 1)) break;
+                            ptx::tc_fence_after();
+                            if (ptx::elect_one()) {
+                                mma_pv(slot, vs, 1, true);
+                                if (slot == 1) ptx::umma_commit(sy.bar(L::B_V_EMPTY + vs));
+                                if (next) {
+                                    mma_s(slot, ks);
+                                    if (slot == 1) {
+                                        ptx::umma_commit(sy.bar(L::B_K_EMPTY + ks));
+                                        if (t + 2 == x.tiles) ptx::umma_commit(sy.bar(L::B_Q_FREE));
+                                    }
+                                }
+                            }
+                            __syncwarp();
+                            p_par ^= 1u << slot;
+                        }
+                        if (!ok) break;
+                        next_v();
+                        if (next) next_k();
+                    }
+                } else {
+                    // The slots take key tiles in turn; S runs two ahead of P V.
+                    const int jobs = x.tiles;
+                    for (int j = -2; ok && j < jobs; ++j) {
+                        const int slot = j & 1;
+                        if (j >= 0) {
+                            if (!wait_v()) break;
+#pragma unroll
+                            for (int hf = 0; hf < 2; ++hf) {
+                                if (!wait_p(slot, hf)) break;
+                                ptx::tc_fence_after();
+                                if (ptx::elect_one()) {
+                                    mma_pv(slot, vs, hf, j > 1 || hf > 0);
+                                    if (hf == 1) ptx::umma_commit(sy.bar(L::B_V_EMPTY + vs));
+                                }
+                                __syncwarp();
+                            }
+                            if (!ok) break;
+                            p_par ^= 1u << slot;
+                            next_v();
+                        }
+                        if (j + 2 < jobs) {
+                            if (!wait_k()) break;
+                            ptx::tc_fence_after();
+                            if (ptx::elect_one()) {
+                                mma_s(slot, ks);
+                                ptx::umma_commit(sy.bar(L::B_K_EMPTY + ks));
+                                if (j + 3 == jobs) ptx::umma_commit(sy.bar(L::B_Q_FREE));
+                            }
+                            __syncwarp();
+                            next_k();
+                        }
+                    }
                 }
                 if (!ok) break;
                 if (ptx::elect_one()) ptx::umma_commit(sy.bar(L::B_O_FULL));
                 __syncwarp();
-                g0 += x.tiles;
             }
             if (ptx::elect_one()) ptx::umma_commit(sy.bar(L::B_DRAIN));
             __syncwarp();
@@ -636,7 +696,7 @@ paged_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
         }
     } else {
         // ------------------------------------------------ softmax / epilogue
-        ptx::regs_inc<kRegsSoftmax>();
+        ptx::regs_inc<L::REGS_SOFTMAX>();
         const int tid = (int)threadIdx.x - 128;
         const int slot = tid >> 7, q4 = warp & 3;
         const int st = tid & 127;                                // thread of the slot
