@@ -52,10 +52,13 @@
 // for the rows that see them.
 //
 // Measured: one token for each of 16 ragged streams of up to 32768 rows, 8 KV
-// heads, 1.06 GB: 160 us = 6.6 TB/s (HBM).  One token in one layer of 131073
-// rows, 134 MB: 40 us, of which 8.5 pass before the first scores and 4 in the
-// merge.  512 tokens over 131072 rows, 12 heads on 2, 0.41 TFLOP: 283 us = 1.46
-// PFLOP/s, the tensor pipe 65 % busy.
+// heads, 1.06 GB: 158 us = 6.7 TB/s (HBM).  One token in one layer of 131073
+// rows, 134 MB: 38.5 us, of which 8.5 pass before the first scores and 4 in the
+// merge.  512 tokens over 131072 rows, 12 heads on 2, 0.41 TFLOP: 272 us = 1.52
+// PFLOP/s, the tensor pipe 68 % busy: products alone keep it busy whatever
+// their order, and beside all the copies and tensor-memory accesses of this
+// kernel, but the warp that issues them does not get through its waits in time
+// (each 80 to 110 cycles where nothing is left to wait for).
 #include <algorithm>
 
 #include "paged.cuh"
@@ -546,21 +549,22 @@ paged_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
             int seg = 0;                                     // segments done
             uint32_t p_par = 0;                              // bit per slot
             bool ok = true;
-            // S of a slot (K stage ks), and the products of 64 keys with V (stage vs)
+            // S of a slot (K stage ks), and the products of 64 keys with V (stage vs).
+            // Four steps of a loop: a CTA meets the code cold, and eight take 5 % longer
+            // for 38 tokens over 59208 rows, one 6 % for the prompt.
             auto mma_s = [&](int slot, int ks) {
                 const uint32_t kb = kb0 + (uint32_t)ks * (L::TILE >> 4);
                 const uint32_t qb = qb0 + (SPLIT_ROWS ? (uint32_t)slot * (L::TILE >> 4) : 0u);
-#pragma unroll
-                for (int kc = 0; kc < L::KCH; ++kc)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        ptx::umma_ss_lh(tmem + L::TM_S + 128u * slot, qb + kc * (L::CHUNK >> 4) + 2 * e, kmaj_hi,
-                                        kb + kc * (L::CHUNK >> 4) + 2 * e, kmaj_hi, idesc_s, (kc | e) ? 1u : 0u);
+#pragma unroll 4
+                for (int e = 0; e < 4 * L::KCH; ++e) {
+                    const uint32_t o = (uint32_t)(e >> 2) * (L::CHUNK >> 4) + 2u * (e & 3);
+                    ptx::umma_ss_lh(tmem + L::TM_S + 128u * slot, qb + o, kmaj_hi, kb + o, kmaj_hi, idesc_s, e ? 1u : 0u);
+                }
                 ptx::umma_commit(sy.bar(L::B_S_FULL + slot));
             };
             auto mma_pv = [&](int slot, int vs, int hf, bool more) {
                 const uint32_t vb = vb0 + (uint32_t)vs * (L::TILE >> 4);
-#pragma unroll
+#pragma unroll 4
                 for (int e = 4 * hf; e < 4 * hf + 4; ++e)        // 16 keys per step
                     ptx::umma_ts_lh(tmem + L::TM_O + 128u * slot, tmem + L::TM_S + 128u * slot + 8u * e,
                                     vb + 128u * e, v_hi, idesc_o, (more || e > 0) ? 1u : 0u);
@@ -578,11 +582,11 @@ paged_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
             for (; ok && x.next_tiles(k); ++seg) {
                 if (!(ok = sy.wait(L::B_Q_FULL, (uint32_t)(seg & 1), kSiteQFull))) break;
                 if constexpr (SPLIT_ROWS) {
-                    // Both slots go through a key tile.  The issuer is what bounds
-                    // this kernel: few MMAs queue up behind the running one, and a wait
-                    // takes it 80 to 110 cycles though nothing is left to wait for.  So
-                    // one wait for K and one for V serve both slots, and what
-                    // belongs together is issued in one piece.
+                    // Both slots go through a key tile.  The issuer bounds it, so one
+                    // wait for K and one for V serve both, and what belongs
+                    // together is issued in one piece.  (One wait for all of P
+                    // instead of two gains another 1 % here and costs 8 % over 512
+                    // rows, where the first half's products hide the other's softmax.)
                     if (!wait_k()) break;
                     ptx::tc_fence_after();
                     if (ptx::elect_one()) {
