@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const __grid_con
                 h = ptx::add2(p, t);
                 const float2 bb = sub2(h, p);
                 l = ptx::add2(sub2(p, sub2(h, bb)), sub2(t, bb));
-                if (ch != 1.f) {
+                if (ch != 1.f || cl != 0.f) {
                     // what the product lost, and the rest of c
                     l = ptx::add2(l, ptx::fma2(make_float2(-ch, -ch), q, make_float2(-t.x, -t.y)));
                     l = ptx::fma2(make_float2(-cl, -cl), q, l);

@@ -668,6 +668,33 @@ def test_verify_of_rows_that_are_no_probabilities_gives_some_token():
     kv.check_status()
 
 
+@gpu
+def test_verify_sums_what_a_tiny_residual_leaves():
+    """After a residual R1 <= 2^-24 the whole of c = 1 + R1 counts, not what fp32 holds of it."""
+    f = lambda *x: torch.tensor(x, dtype=F32, device=DEV)  # noqa: E731
+    # residuals 2^-24, 2^-25, 2^-26, all of token 0: it is next whatever the last uniform
+    e = 2.0 ** -24
+    p, q = (f(*x).expand(4, 4, 2).contiguous() for x in ((0.5 + e, 0.5 - e), (0.5, 0.5)))
+    u = f(1 - e).expand(4, 4).contiguous()
+    u[:, 3] = f(0.0, 0.4, 0.75, 1 - e)
+    path, counts, after = kv.verify_tree(p, q, torch.ones((4, 3), dtype=I32, device=DEV),
+                                         kv.tree_masks([-1, -1, -1], DEV)[0], u)
+    assert not counts.any() and not after.any()
+    # one token drafted twice that the target never has, and two others to choose from
+    n, g = 1000, gen(61)
+    q = [5e-8, 0.25, 1e-4, 0.74989995]
+    p = torch.tensor([[0.0, 0.25, 1e-4 + 2e-8, 0.7498]], device=DEV)
+    p[0, 1] = torch.nextafter(p[0, 1], torch.ones_like(p[0, 1]))
+    p, q = p.expand(n, 3, 4).contiguous(), f(*q).expand(n, 3, 4).contiguous()
+    u = torch.rand((n, 3), generator=g, device=DEV)
+    t, tree = torch.zeros((n, 2), dtype=I32, device=DEV), kv.tree_masks([-1, -1], DEV)[0]
+    path, counts, after = kv.verify_tree(p, q, t, tree, u)
+    pc, qc = p[0].cpu(), q[0].cpu()
+    want = [plain_verify(pc, qc, [0, 0], tree[0].tolist(), x)[1] for x in u.cpu().double().tolist()]
+    assert not counts.any() and after.tolist() == want and len(set(want)) == 2
+    kv.check_status()
+
+
 # ------------------------------------------------------------------- chains
 @gpu
 def test_a_served_text_eager_and_replayed():
