@@ -817,9 +817,11 @@ int statekv_evict_rows(const statekv_evict_args* args, void* cuda_stream);
  * When no child is left, the token is the lowest v with
  *   sum over w <= v of r(w) > u * sum of r
  * (where that sum is 0, of p instead of r; where that is 0 too, token 0).
- * Products and sums in 64 bits.  Probabilities are in [0, 1] and sum to 1 up to
- * rounding; NaN and negative ones count as 0, uniforms are clamped to [0, 1).  (Of other
- * rows some nodes and some token come out.)
+ * A child's own test is in 64 bits.  In sums each r(v) is off by at most 2^-47 and
+ * rounded to a whole number of 2^-60, and whole numbers are added: the results do not
+ * depend on the other sequences of the call.  Probabilities are in [0, 1] and sum to 1
+ * up to rounding; NaN and negative ones count as 0, uniforms are clamped to [0, 1).
+ * (Of other rows some nodes and some token come out.)
  *   path     int32 [sequences][tokens]: the accepted nodes, then -1
  *   counts   int32 [sequences], how many
  *   next     int32 [sequences]

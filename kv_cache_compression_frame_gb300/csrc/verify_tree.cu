@@ -15,12 +15,13 @@
 // copies (and kept for the node's next refusal, where the run fits).  Bound by
 // latency: the passes of one sequence follow each other, about 6 us each (rows
 // 1.5 to 1.9, their sum 2.1, the cluster's 1.2, the walk 1).  16 trees of 42
-// nodes over 150001 entries, 4 to 5 passes for the slowest: 35.5 us.
+// nodes over 150001 entries, 4 to 5 passes for the slowest: 35.6 us.
 //
 // Sums decide which token comes out, so they do not depend on how a row is cut:
-// p - c q is formed with its rounding error (two-term products and sums), and
-// terms are added in pairs of fp32 (to about 2^-48) and then in whole numbers of
-// 2^-52.  fp64 adds would do as well at a 64th of the rate.
+// p - c q is formed with its rounding error (two-term products and sums, off by
+// at most 2^-47), each entry is rounded once to a whole number of 2^-60, and whole
+// numbers are added.  The splitting needs fp32 additions only (add_units); fp64
+// ones would run at a 64th of the rate.
 #include <algorithm>
 
 #include "views.cuh"
@@ -34,6 +35,8 @@ constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kMaxNodes = 64;
 constexpr int kMaxCluster = 16;
 constexpr int kRoomAlone = 1664, kRoomShared = 768;  // entries of a warp: 213 and 98 KB of p and q a CTA
+constexpr int kMostAdded = 128;              // entries that a lane adds up in 32 bits (Units)
+static_assert(kRoomAlone / 32 < kMostAdded, "entries of a lane");
 
 struct VerifyKernelArgs {
     statekv_verify_args a;
@@ -42,27 +45,63 @@ struct VerifyKernelArgs {
     int32_t room;                            // entries of p, and of q, that a warp has room for, a multiple of 8
 };
 
-// a + b = s + e exactly
-__device__ __forceinline__ void two_sum(float a, float b, float& s, float& e) {
-    s = __fadd_rn(a, b);
-    const float bb = __fsub_rn(s, a);
-    e = __fadd_rn(__fsub_rn(a, __fsub_rn(s, bb)), __fsub_rn(b, bb));
-}
-
 // a - b (a fused multiply-add by -1 is exact in the product)
 __device__ __forceinline__ float2 sub2(float2 a, float2 b) { return ptx::fma2(b, make_float2(-1.f, -1.f), a); }
 
-// max(p - c q, 0) as hi + lo
-__device__ __forceinline__ void residual(float p, float q, float ch, float cl, float& hi, float& lo) {
-    const float t = __fmul_rn(ch, q), te = __fmaf_rn(ch, q, -t);
-    two_sum(p, -t, hi, lo);
-    lo = __fsub_rn(__fsub_rn(lo, te), __fmul_rn(cl, q));
-    if (!(__fadd_rn(hi, lo) > 0.f)) hi = lo = 0.f;
+// max(p - c q, 0) of two entries as h + l, c = -(mch + mcl)
+__device__ __forceinline__ void residual2(float2 p, float2 q, float2 mch, float2 mcl, float2& h, float2& l) {
+    const float2 t = ptx::fma2(mch, q, make_float2(0.f, 0.f));       // rounded -ch q
+    h = ptx::add2(p, t);
+    const float2 bb = sub2(h, p);
+    l = ptx::add2(sub2(p, sub2(h, bb)), sub2(t, bb));                // what that sum lost, exactly
+    // what the product lost, and the rest of c
+    l = ptx::add2(l, ptx::fma2(mch, q, make_float2(-t.x, -t.y)));
+    l = ptx::fma2(mcl, q, l);
+    if (!(h.x + l.x > 0.f)) h.x = l.x = 0.f;
+    if (!(h.y + l.y > 0.f)) h.y = l.y = 0.f;
 }
 
-// hi + lo in units of 2^-52
-__device__ __forceinline__ long long units_of(float hi, float lo) {
-    return __float2ll_rn(hi * 0x1p52f) + __float2ll_rn(lo * 0x1p52f);
+// A sum in whole numbers of 2^-21, 2^-44 and 2^-60.  x + A for a constant A of
+// 1.5 times a power of two is x rounded to a multiple of A's last place, its bits
+// count them, and x - ((x + A) - A) is the rest, exactly: what an entry adds is a
+// function of the entry alone.  It adds at most 2^23 to the middle one: kMostAdded
+// of them stay in 32 bits.
+constexpr float kTop = 6.f, kMid = 0x1.8p-21f, kLow = 0x1.8p-37f;
+struct Units {
+    uint32_t top = 0u, mid = 0u, low = 0u;
+    __device__ __forceinline__ long long whole() const {
+        return ((long long)(int)top << 39) + ((long long)(int)mid << 16) + (long long)(int)low;
+    }
+};
+
+// Adds two entries h + l, |h| <= 2 and |l| <= 2^-22 (others add some number).
+template <bool WITH_L>
+__device__ __forceinline__ void add_units(Units& u, float2 h, float2 l) {
+    auto both = [](float2 x, float a) {
+        return __float_as_uint(x.x) + __float_as_uint(x.y) - 2u * __float_as_uint(a);
+    };
+    const float2 top = make_float2(kTop, kTop), mid = make_float2(kMid, kMid), low = make_float2(kLow, kLow);
+    float2 x = ptx::add2(h, top);
+    u.top += both(x, kTop);
+    h = sub2(h, sub2(x, top));
+    x = ptx::add2(h, mid);
+    u.mid += both(x, kMid);
+    h = sub2(h, sub2(x, mid));
+    if constexpr (WITH_L) {
+        x = ptx::add2(l, mid);
+        u.mid += both(x, kMid);
+        h = ptx::add2(h, sub2(l, sub2(x, mid)));
+    }
+    u.low += both(ptx::add2(h, low), kLow);
+}
+
+// max(p - c q, 0), or p where `with_q` is not, in units of 2^-60
+__device__ __forceinline__ long long units_of(float p, float q, bool with_q, float ch, float cl) {
+    Units u;
+    float2 h = make_float2(p, 0.f), l = make_float2(0.f, 0.f);
+    if (with_q) residual2(h, make_float2(q, 0.f), make_float2(-ch, -ch), make_float2(-cl, -cl), h, l);
+    add_units<true>(u, h, l);
+    return u.whole();
 }
 
 // NaN and negative values count as 0
@@ -156,40 +195,25 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const __grid_con
     const bool fits = v1 - v0 <= ka.room - 4;
     int p_off = 0, q_off = 0;                                // where a run's first entries lie
     int p_node = -2, q_node = -2;                            // whose rows the shared memory holds
-    // the residual's sum in units of 2^-52, its parts in s_warp and s_sums
+    // the residual's sum in units of 2^-60, its parts in s_warp and s_sums
     auto sum_up = [&]() -> long long {
         const bool with_q = ch > 0.f;
-        // two sums side by side, each hi + lo; hi starts above every term, so
-        // that (hi + x) - hi and what it leaves of x are exact
-        float2 hi2 = make_float2(2.f, 2.f), lo2 = make_float2(0.f, 0.f);
-        auto add = [&](float2 p, float2 q) {
-            float2 h = p, l = make_float2(0.f, 0.f);
-            if (with_q) {
-                const float2 t = ptx::fma2(make_float2(-ch, -ch), q, make_float2(0.f, 0.f));   // rounded -ch q
-                h = ptx::add2(p, t);
-                const float2 bb = sub2(h, p);
-                l = ptx::add2(sub2(p, sub2(h, bb)), sub2(t, bb));
-                if (ch != 1.f || cl != 0.f) {
-                    // what the product lost, and the rest of c
-                    l = ptx::add2(l, ptx::fma2(make_float2(-ch, -ch), q, make_float2(-t.x, -t.y)));
-                    l = ptx::fma2(make_float2(-cl, -cl), q, l);
-                }
-                if (!(h.x + l.x > 0.f)) h.x = l.x = 0.f;
-                if (!(h.y + l.y > 0.f)) h.y = l.y = 0.f;
-            }
-            const float2 s = ptx::add2(hi2, h);
-            lo2 = ptx::add2(lo2, ptx::add2(sub2(h, sub2(s, hi2)), l));
-            hi2 = s;
-        };
+        const float2 mch = make_float2(-ch, -ch), mcl = make_float2(-cl, -cl);
+        long long sum = 0;
         auto add_all = [&](const float* ps, const float* qs, int count) {
+            Units u;
 #pragma unroll 4
             for (int i = lane; i < count; i += 64) {
                 const bool two = i + 32 < count;
-                const float2 p = make_float2(fmaxf(ps[i], 0.f), two ? fmaxf(ps[i + 32], 0.f) : 0.f);
-                float2 q = make_float2(0.f, 0.f);
-                if (with_q) q = make_float2(fmaxf(qs[i], 0.f), two ? fmaxf(qs[i + 32], 0.f) : 0.f);
-                add(p, q);
+                float2 h = make_float2(fmaxf(ps[i], 0.f), two ? fmaxf(ps[i + 32], 0.f) : 0.f), l;
+                if (with_q) {
+                    residual2(h, make_float2(fmaxf(qs[i], 0.f), two ? fmaxf(qs[i + 32], 0.f) : 0.f), mch, mcl, h, l);
+                    add_units<true>(u, h, l);
+                } else {
+                    add_units<false>(u, h, h);
+                }
             }
+            sum += u.whole();
         };
         if (fits) {
             // rows that are there already are not read again
@@ -239,10 +263,6 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const __grid_con
                 }
             }
         }
-        float hi = hi2.x - 2.f, lo;
-        two_sum(hi, hi2.y - 2.f, hi, lo);
-        lo += lo2.x + lo2.y;
-        long long sum = units_of(hi, lo);
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
         if (lane == 0) {
@@ -252,7 +272,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const __grid_con
                 bool again = false;
                 for (uint64_t e = refused & ((1ull << i) - 1ull); e; e &= e - 1)
                     again |= s_token[__ffsll((long long)e) - 1] == x;
-                if (!again && x >= v0 && x < v1) sum -= units_of(s_p[i], 0.f);
+                if (!again && x >= v0 && x < v1) sum -= units_of(s_p[i], 0.f, false, 0.f, 0.f);
             }
             s_warp[warp] = sum > 0 ? sum : 0;
         }
@@ -346,7 +366,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const __grid_con
         if (draft) q_row = draft + (int64_t)(cur + 1) * a.draft_row;
         if (!s_pass.more) break;
         total = sum_up();
-        if (warp == 0 && draft) R = (double)total * 0x1p-52;
+        if (warp == 0 && draft) R = (double)total * 0x1p-60;
     }
     if (rank == 0 && warp == 0) {
         for (int i = count + lane; i < a.tokens; i += 32) a.path[(int64_t)seq * a.tokens + i] = -1;
@@ -363,12 +383,12 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const __grid_con
     int last = v0;                                           // the last entry that is not 0
     for (int i0 = v0; i0 < v1; i0 += 32) {
         const int v = i0 + lane;
-        float hi = 0.f, lo = 0.f;
+        long long upto = 0;
         if (v < v1 && !refused_token(v)) {
-            hi = fits ? fmaxf(p_buf[p_off + v - v0], 0.f) : weight(p_row + v);
-            if (ch > 0.f) residual(hi, fits ? fmaxf(q_buf[q_off + v - v0], 0.f) : weight(q_row + v), ch, cl, hi, lo);
+            const float p = fits ? fmaxf(p_buf[p_off + v - v0], 0.f) : weight(p_row + v);
+            const float q = !(ch > 0.f) ? 0.f : fits ? fmaxf(q_buf[q_off + v - v0], 0.f) : weight(q_row + v);
+            upto = units_of(p, q, ch > 0.f, ch, cl);
         }
-        long long upto = units_of(hi, lo);
         const unsigned some = __ballot_sync(0xffffffffu, upto > 0);
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -383,7 +403,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const __grid_con
         if (some) last = i0 + 31 - __clz((int)some);
         before += __shfl_sync(0xffffffffu, upto, 31);
     }
-    // (where the entries' own sums end below the warp's, by units of 2^-52: the last)
+    // (where the entries are no probabilities and their sums end below the warp's: the last)
     if (lane == 0) a.next[seq] = last;
 }
 

@@ -21,6 +21,7 @@ import ctypes as C
 import math
 import random
 
+import numpy as np
 import pytest
 import torch
 
@@ -692,6 +693,66 @@ def test_verify_sums_what_a_tiny_residual_leaves():
     pc, qc = p[0].cpu(), q[0].cpu()
     want = [plain_verify(pc, qc, [0, 0], tree[0].tolist(), x)[1] for x in u.cpu().double().tolist()]
     assert not counts.any() and after.tolist() == want and len(set(want)) == 2
+    kv.check_status()
+
+
+def near_boundary(seed, vocab, with_draft):
+    """Rows p, q (float32 [vocab]) whose residual after the refused token 5 has
+    sums that pass half of the whole by 2^-48 at entry v, or miss it by that:
+    (p, q, token).  Every entry is 0 or at least 2^-36, a whole number of 2^-60 then,
+    so the sums here are exact."""
+    r = np.random.default_rng(seed)
+    units = lambda x: (x.astype(np.float64) * 2.0 ** 60).astype(np.int64)  # noqa: E731
+    p = np.exp(r.standard_normal(vocab))
+    p[:3] = 1e-2 * p.sum(), 2.0 ** -20, 2.0 ** -30
+    q = np.where(np.arange(vocab) % 7 < 3, 0.9, 1.3) * p
+    p = np.maximum(p / p.sum(), 2.0 ** -36).astype(np.float32)
+    q = np.maximum(q / q.sum(), 2.0 ** -36).astype(np.float32)
+    p[1:3] = 2.0 ** -20, 2.0 ** -30
+    q[:3] = 2.0 ** -36
+    p[5], q[5] = 2.0 ** -34, 2.0 ** -8                       # refused
+
+    def rest():
+        x = units(p) - units(q) if with_draft else units(p)
+        x = np.maximum(x, 0)
+        x[5] = 0
+        return x
+
+    upto = rest().cumsum()
+    v = int(np.searchsorted(2 * upto, upto[-1]))
+    sign = 1 if seed % 2 else -1
+    for i in range(3):
+        # what twice the sum up to v passes the whole by, by the entry i <= v alone
+        x = rest()
+        over = 2 * int(x[:v + 1].sum()) - int(x.sum()) - sign * 2 ** 13
+        p[i] = np.float32(float(p[i]) - over * 2.0 ** -60)
+        assert p[i] > 2.0 ** -35
+    x = rest()
+    over = 2 * int(x[:v + 1].sum()) - int(x.sum())
+    assert v > 100 and abs(over - sign * 2 ** 13) <= 2 ** 8
+    return p, q, v if sign > 0 else v + 1 + int(np.flatnonzero(x[v + 1:])[0])
+
+
+@gpu
+@pytest.mark.parametrize("with_draft", [True, False])
+@pytest.mark.parametrize("vocab", [20011, 40009])
+def test_verify_next_to_a_boundary_in_any_batch(vocab, with_draft):
+    """The token changes where its sum passes u times the whole, however many
+    CTAs the row is cut over: margins of 2^-48 of it, alone and in larger batches.
+    (p - c q with c = 1 is exact as two fp32 numbers, and half the whole is off by 2^-54.)"""
+    n = 128
+    cases = [near_boundary(i, vocab, with_draft) for i in range(n)]
+    p = torch.tensor(np.stack([c[0] for c in cases]), device=DEV)[:, None].expand(n, 2, vocab)
+    q = torch.tensor(np.stack([c[1] for c in cases]), device=DEV)[:, None].expand(n, 2, vocab) if with_draft else None
+    want = [c[2] for c in cases]
+    t = torch.full((n, 1), 5, dtype=I32, device=DEV)
+    u = torch.tensor([[0.999, 0.5]], device=DEV).repeat(n, 1)
+    tree = kv.tree_masks([-1], DEV)[0]
+    for batch in (128, 40, 16, 1):
+        for s in range(0, n, batch):
+            e = min(n, s + batch)
+            _, counts, after = kv.verify_tree(p[s:e], None if q is None else q[s:e], t[s:e], tree, u[s:e])
+            assert not counts.any() and after.tolist() == want[s:e], batch
     kv.check_status()
 
 
