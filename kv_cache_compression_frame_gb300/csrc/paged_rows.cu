@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __gri
     float* w_out = a.weights_out + (int64_t)u * a.out_rows;
     int32_t* kept = a.kept + (int64_t)u * a.keep;
     if (a.new_lengths && h == 0 && n == seq * a.layers && rank == 0 && tid == 0) a.new_lengths[seq] = keep;
-    for (int i = keep + rank * kEvictThreads + tid; i < a.out_rows; i += C * kEvictThreads) {
+    for (int64_t i = (int64_t)keep + rank * kEvictThreads + tid; i < a.out_rows; i += C * kEvictThreads) {
         w_out[i] = 0.f;
         if (i < a.keep) kept[i] = -1;
     }

@@ -525,6 +525,20 @@ def test_evict_long_rows():
     kv.check_status()
 
 
+@gpu
+def test_evict_into_an_array_of_the_most_weights():
+    """Zeros up to the last of 2^31 - 1 entries (counted in steps of a cluster's threads)."""
+    k = torch.arange(40, device=DEV, dtype=F32)[None, None, :, None].expand(1, 1, 40, 8).contiguous()
+    w = torch.rand((1, 1, 40), generator=gen(53), device=DEV)
+    out = [torch.zeros((1, 1, 3, 8), device=DEV) for _ in range(2)]
+    w_out = torch.full((1, 1, 2 ** 31 - 1), 9.0, device=DEV)
+    new, _, kept = kv.evict_rows(k, k.clone(), None, 40, w, 3, None, k_out=out[0], v_out=out[1], weights_out=w_out)
+    want = w[0, 0].topk(3).indices.sort().values
+    assert new == 3 and torch.equal(kept[0, 0].long(), want) and torch.equal(w_out[0, 0, :3], w[0, 0, want])
+    assert int(w_out.count_nonzero()) == 3
+    kv.check_status()
+
+
 # ------------------------------------------------------------- verification
 def plain_verify(target, draft, drafted, masks, uniforms):
     """One sequence, from the definition: the residual after each refusal is a
