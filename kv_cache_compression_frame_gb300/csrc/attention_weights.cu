@@ -229,7 +229,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     // Rows that no query sees stay as before.  One step copies the next kRest of
     // the CTA's; false: none left.  The copiers take them from the
     // start, the others what is left when they are done.
-    const int pieces = a.out == a.before ? 0 : (a.weight_rows + kRest - 1) / kRest;
+    const int pieces = a.out == a.before ? 0 : (int)(((int64_t)a.weight_rows + kRest - 1) / kRest);
     const int64_t all = (int64_t)a.batch * a.kv_heads * pieces;
     auto copy_step = [&]() -> bool {
         int64_t p = 0;
@@ -237,7 +237,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         p = __shfl_sync(0xffffffffu, p, 0);
         if (p >= all) return false;
         const int u = (int)(p / pieces), r0 = (int)(p - (int64_t)u * pieces) * kRest;
-        const int r1 = min(a.weight_rows, r0 + kRest), from = max(r0, seq_of(k, u / a.kv_heads / a.layers).len);
+        const int r1 = a.weight_rows - r0 < kRest ? a.weight_rows : r0 + kRest, from = max(r0, seq_of(k, u / a.kv_heads / a.layers).len);
         const int64_t o = (int64_t)u * a.weight_rows;
         float v[kRest / 32];
 #pragma unroll

@@ -367,6 +367,20 @@ def test_weights_of_rows_that_are_not_finite_stay_their_own():
         kv.check_status()
 
 
+@gpu
+def test_weights_in_an_array_of_the_most_rows():
+    """Rows behind the length are zeros up to the last of 2^31 - 1 (copied in pieces of 512)."""
+    g = gen(54)
+    c = Cache(g, 1, 1, [40], 16, 64)
+    q = randn(g, 1, 1, 3, 64)
+    _, lse = kv.paged_attention(q, *c.pools, c.table, 40, scale=0.1, with_lse=True)
+    out = torch.full((1, 1, 2 ** 31 - 1), 9.0, device=DEV)
+    kv.attention_weights(q, lse, c.pools[0], c.table, 40, scale=0.1, out=out)
+    assert torch.equal(out[:, :, :40], kv.attention_weights(q, lse, c.pools[0], c.table, 40, scale=0.1)[:, :, :40])
+    assert int(out.count_nonzero()) == 40
+    kv.check_status()
+
+
 # ------------------------------------------------------------------- append
 @gpu
 @pytest.mark.parametrize("dtype", [BF16, F32])
