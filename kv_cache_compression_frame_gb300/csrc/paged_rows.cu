@@ -42,8 +42,10 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __gr
         a.new_lengths[seq] = len + count;
     const int es = a.dtype == STATEKV_BF16 ? 2 : 4;
     const int row_units = a.head_dim * es / 16;
-    const int r0 = chunk * kAppendRows, r1 = min(count, r0 + kAppendRows);
-    for (int i = threadIdx.x; i < (r1 - r0) * row_units; i += kAppendThreads) {
+    // (none in most chunks of a batch padded far past its counts: a negative number would
+    // leave 32 bits as a number of units)
+    const int r0 = chunk * kAppendRows, rows = min(max(count - r0, 0), kAppendRows);
+    for (int i = threadIdx.x; i < rows * row_units; i += kAppendThreads) {
         const int r = r0 + i / row_units, x = i % row_units;
         const int row = len + r;
         const int page = page_at(pg, n, a.table ? row / a.page_rows : 0, a.status);
@@ -381,7 +383,7 @@ extern "C" int statekv_paged_append(const statekv_paged_append_args* args, void*
             if (!view_ok(*v, es, a.num_pages, a.kv_heads, a.page_rows) ||
                 !apart(*v, a.num_pages, a.kv_heads, a.page_rows, a.head_dim))
                 return STATEKV_E_INVALID_ARG;
-    const int64_t chunks = std::max(1, (a.tokens + kAppendRows - 1) / kAppendRows);
+    const int64_t chunks = std::max<int64_t>(1, ((int64_t)a.tokens + kAppendRows - 1) / kAppendRows);
     const int64_t grid = (int64_t)a.batch * a.kv_heads * chunks;
     if (grid > 0x7fffffffll) return STATEKV_E_UNSUPPORTED;
     paged_append_kernel<<<(unsigned)grid, kAppendThreads, 0, reinterpret_cast<cudaStream_t>(cuda_stream)>>>(

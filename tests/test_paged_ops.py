@@ -427,6 +427,18 @@ def test_append_that_does_not_fit_is_recorded():
     kv.check_status()
 
 
+@gpu
+def test_append_of_a_tensor_of_the_most_tokens():
+    """Fewer rows than `tokens`, whose blocks of 32 are counted past 2^31 - 1."""
+    k = torch.arange(8, dtype=F32, device=DEV).expand(1, 1, 2 ** 31 - 1, 8)
+    pools = [torch.zeros((1, 1, 100, 8), device=DEV) for _ in range(2)]
+    new = kv.paged_append(k, k, *pools, None, ints(7), ints(80))
+    assert new.tolist() == [87]
+    for p in pools:
+        assert torch.equal(p[0, 0, 7:87], k[0, 0, :80]) and not p[0, 0, :7].any() and not p[0, 0, 87:].any()
+    kv.check_status()
+
+
 # ----------------------------------------------------------------- eviction
 def kept_rows(w, rows, keep, sinks, recent):
     """The rows that stay, by sorting."""
