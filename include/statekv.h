@@ -668,8 +668,8 @@ int statekv_sparse_attention(const statekv_sparse_args* args, void* cuda_stream)
  * if not NULL, receives length + count (memory of its own).  A sequence whose
  * rows do not fit in its table row appends nothing (recorded).  Batch entries
  * that write one page write the same row of it in any order: pages that are
- * appended to are not shared.  k_pages and v_pages do not overlap each other or
- * the new rows.  Any head_dim of whole 16-byte units up to 512; dtype
+ * appended to are not shared.  k_pages and v_pages do not overlap each other
+ * (E_INVALID_ARG; they may lie side by side in one tensor) or the new rows.  Any head_dim of whole 16-byte units up to 512; dtype
  * STATEKV_BF16 or STATEKV_F32.
  */
 typedef struct statekv_paged_append_args {
@@ -772,7 +772,8 @@ int statekv_attention_weights(const statekv_attention_weights_args* args, void* 
  * none of which shares memory with another or an input.  out_rows >= keep; the
  * out table holds out_table_pages * page_rows >= keep rows (E_CAPACITY; both
  * pools have the same page_rows); out_table NULL: batch entry n's
- * rows go to page n of pools that are not the source's.  Any head_dim of whole
+ * rows go to page n.  Where either table is NULL no row of k_out or v_out shares
+ * memory with one of the source's, and never K's with V's (E_INVALID_ARG).  Any head_dim of whole
  * 16-byte units up to 512; dtype STATEKV_BF16 or STATEKV_F32; a sequence holds at
  * most 2^22 rows.
  */

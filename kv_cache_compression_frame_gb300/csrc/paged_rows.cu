@@ -383,6 +383,8 @@ extern "C" int statekv_paged_append(const statekv_paged_append_args* args, void*
             if (!view_ok(*v, es, a.num_pages, a.kv_heads, a.page_rows) ||
                 !apart(*v, a.num_pages, a.kv_heads, a.page_rows, a.head_dim))
                 return STATEKV_E_INVALID_ARG;
+    const Extent pool{a.num_pages, a.kv_heads, a.page_rows};
+    if (!paging_empty(pg) && share(a.k_pages, pool, a.v_pages, pool, a.head_dim, es)) return STATEKV_E_INVALID_ARG;
     const int64_t chunks = std::max<int64_t>(1, ((int64_t)a.tokens + kAppendRows - 1) / kAppendRows);
     const int64_t grid = (int64_t)a.batch * a.kv_heads * chunks;
     if (grid > 0x7fffffffll) return STATEKV_E_UNSUPPORTED;
@@ -432,6 +434,14 @@ extern "C" int statekv_evict_rows(const statekv_evict_args* args, void* cuda_str
     const int64_t w = units * a.weight_rows, o = units * a.out_rows, k = units * a.keep;
     if (overlap(a.weights, w, a.weights_out, o) || overlap(a.weights, w, a.kept, k) || overlap(a.weights_out, o, a.kept, k))
         return STATEKV_E_INVALID_ARG;
+    // K and V go to rows of their own; with both tables the pages that are read and
+    // those that are written are the caller's to keep apart
+    const Extent source{a.num_pages, a.kv_heads, a.page_rows}, target{a.out_num_pages, a.kv_heads, a.out_page_rows};
+    if (!paging_empty(to) && share(a.k_out, target, a.v_out, target, a.head_dim, es)) return STATEKV_E_INVALID_ARG;
+    if ((!a.table || !a.out_table) && !paging_empty(pg) && !paging_empty(to))
+        for (const statekv_view* x : {&a.k_pages, &a.v_pages})
+            for (const statekv_view* y : {&a.k_out, &a.v_out})
+                if (share(*x, source, *y, target, a.head_dim, es)) return STATEKV_E_INVALID_ARG;
     if (units * 16 > 0x7fffffffll || units * ((a.keep + kMoveRows - 1) / kMoveRows) > 0x7fffffffll)
         return STATEKV_E_UNSUPPORTED;
     int dev = 0, sms = 0;

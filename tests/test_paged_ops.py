@@ -1129,6 +1129,73 @@ def test_evict_arrays_that_share_memory_are_refused(bad):
     assert N.load().statekv_evict_rows(N.EvictArgs(**{**a, **bad}), None) == N.E_INVALID_ARG
 
 
+@pytest.mark.parametrize("bad", [
+    dict(v_pages=view(1 << 30, b=1 << 20, h=1 << 16)),                             # the same rows
+    dict(v_pages=view((1 << 30) + 256, b=1 << 20, h=1 << 16)),                     # a row on
+    dict(v_pages=view((1 << 30) + (1 << 17) + 15 * 256, b=1 << 20, h=1 << 16)),    # its head 0's rows 0.. are head 1's 15..
+    dict(v_pages=view((1 << 30) + (19 << 21), b=1 << 20, h=1 << 16)),              # its first page is K's last
+    dict(v_pages=view((1 << 30) - (1 << 21), b=1 << 20, h=1 << 16)),
+    dict(v_pages=view((1 << 30) + (1 << 17) + 256, b=1 << 20, h=1 << 15)),         # other strides within K's range
+    ])
+def test_append_over_shared_memory_is_refused(bad):
+    a = dict(PAGED, k_new=view(), v_new=view(), k_pages=view(1 << 30, b=1 << 20, h=1 << 16),
+             v_pages=view(1 << 31, b=1 << 20, h=1 << 16), tokens=3, dtype=0, lengths=1 << 33, counts=1 << 34)
+    assert N.load().statekv_paged_append(N.PagedAppendArgs(**{**a, **bad}), None) == N.E_INVALID_ARG
+
+
+EVICT = dict(PAGED, k_pages=view(1 << 40, b=1 << 20, h=1 << 16), v_pages=view(1 << 41, b=1 << 20, h=1 << 16),
+             k_out=view(1 << 42, b=1 << 20, h=1 << 16), v_out=view(1 << 43, b=1 << 20, h=1 << 16), table=1 << 28,
+             out_table=1 << 29, out_table_stride=2, out_table_pages=2, out_num_pages=4, out_page_rows=16, out_rows=32, keep=32,
+             sinks=4, recent=8, weights=1 << 30, weights_out=1 << 31, kept=1 << 32, new_lengths=1 << 33, lengths=1 << 34,
+             weight_rows=128, dtype=0)
+PLAIN = dict(table=None, out_table=None, num_pages=2, page_rows=128, out_num_pages=2, out_page_rows=32)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(v_out=view(1 << 42, b=1 << 20, h=1 << 16)),                               # K and V to the same rows
+    dict(v_out=view((1 << 42) + 256, b=1 << 20, h=1 << 16)),
+    dict(PLAIN, k_out=view((1 << 40) + 16 * 256, b=1 << 20, h=1 << 16)),           # rows 16.. of the source
+    dict(PLAIN, k_out=view((1 << 40) + 127 * 256, b=1 << 20, h=1 << 16)),          # its last row
+    dict(PLAIN, v_out=view((1 << 40) + 16 * 256, b=1 << 20, h=1 << 16)),           # V over K's rows
+    dict(PLAIN, v_out=view((1 << 41) - 31 * 256, b=1 << 20, h=1 << 16)),           # the last row out is its first
+    dict(PLAIN, k_out=view((1 << 40) + (1 << 21), b=1 << 21, h=1 << 16)),          # entry 0 goes to the source's entry 1
+    dict(out_table=None, out_num_pages=2, out_page_rows=32, k_out=view((1 << 40) + (5 << 21), b=1 << 20, h=1 << 16)),
+    dict(table=None, page_rows=128, num_pages=2, k_out=view((1 << 40) - (3 << 21), b=1 << 20, h=1 << 16))])
+def test_evict_over_shared_memory_is_refused(bad):
+    assert N.load().statekv_evict_rows(N.EvictArgs(**{**EVICT, **bad}), None) == N.E_INVALID_ARG
+
+
+@gpu
+def test_pools_side_by_side_in_one_tensor_are_apart():
+    """K and V of each page next to each other, and rows evicted to the other part of one plain cache."""
+    g = gen(81)
+    lens, n = [40, 3, 0], 3
+    c = Cache(g, n, 2, [x + 9 for x in lens], 16, 64)
+    for dim in (1, 2, 3):                            # [pages][2][heads][rows][d], ..., [pages][heads][rows][2][d]
+        shape = list(c.pools[0].shape)
+        both = torch.full((*shape[:dim], 2, *shape[dim:]), 9.0, dtype=BF16, device=DEV)
+        pools = both.unbind(dim)
+        k, v = randn(g, n, 2, 9, 64), randn(g, n, 2, 9, 64)
+        assert kv.paged_append(k, v, *pools, c.table, ints(*lens)).tolist() == [x + 9 for x in lens]
+        for pool, x in zip(pools, (k, v)):
+            for i in range(n):
+                assert torch.equal(c.rows(pool, i, lens[i] + 9)[:, lens[i]:], x[i])
+        out = torch.full((*shape[:dim], 2, *shape[dim:]), 9.0, dtype=BF16, device=DEV)
+        to = torch.arange(6, dtype=I32, device=DEV).view(3, 2)
+        w = torch.rand((n, 2, c.table.shape[1] * 16), generator=g, device=DEV)
+        got = kv.evict_rows(*pools, c.table, ints(49, 12, 9), w, 20, to, k_out=out.unbind(dim)[0], v_out=out.unbind(dim)[1])
+        check_evict(c, [49, 12, 9], 1, w, 20, 0, 0, pools, out.unbind(dim), to, got, 16)
+    wide = randn(g, 2, 2, 2, 300, 64)                # [entry][K, V][head][row][d]: rows 0..199 to rows 200..299
+    src, dst = [wide[:, i, :, :200] for i in range(2)], [wide[:, i, :, 200:] for i in range(2)]
+    w = torch.rand((2, 2, 200), generator=g, device=DEV)
+    p = Cache(g, 2, 2, [200, 200], 0, 64)
+    got = kv.evict_rows(*src, None, 200, w, 100, None, k_out=dst[0], v_out=dst[1])
+    check_evict(p, [200, 200], 1, w, 100, 0, 0, src, dst, None, got, 0)
+    with pytest.raises(kv.StateKVError):
+        kv.evict_rows(*src, None, 200, w, 100, None, k_out=wide[:, 0, :, 199:299], v_out=dst[1])
+    kv.check_status()
+
+
 @pytest.mark.parametrize("by", [4, 2044, -4, -2044])
 def test_weights_over_a_part_of_what_they_are_added_to_are_refused(by):
     a = dict(PAGED, q=view(), k_pages=view(b=1 << 20, h=1 << 16), lse=16, before=1 << 30, out=(1 << 30) + by, length=40,
