@@ -385,6 +385,9 @@ extern "C" int statekv_paged_append(const statekv_paged_append_args* args, void*
                 return STATEKV_E_INVALID_ARG;
     const Extent pool{a.num_pages, a.kv_heads, a.page_rows};
     if (!paging_empty(pg) && share(a.k_pages, pool, a.v_pages, pool, a.head_dim, es)) return STATEKV_E_INVALID_ARG;
+    const int64_t seqs = a.batch / a.layers;
+    for (const int32_t* in : {a.lengths, a.counts})
+        if (in && a.new_lengths && overlap(in, seqs, a.new_lengths, seqs)) return STATEKV_E_INVALID_ARG;
     const int64_t chunks = std::max<int64_t>(1, ((int64_t)a.tokens + kAppendRows - 1) / kAppendRows);
     const int64_t grid = (int64_t)a.batch * a.kv_heads * chunks;
     if (grid > 0x7fffffffll) return STATEKV_E_UNSUPPORTED;
@@ -430,10 +433,17 @@ extern "C" int statekv_evict_rows(const statekv_evict_args* args, void* cuda_str
             if (!view_ok(*v, es, a.out_num_pages, a.kv_heads, a.out_page_rows) ||
                 !apart(*v, a.out_num_pages, a.kv_heads, a.out_page_rows, a.head_dim))
                 return STATEKV_E_INVALID_ARG;
-    const int64_t units = (int64_t)a.batch * a.kv_heads;
-    const int64_t w = units * a.weight_rows, o = units * a.out_rows, k = units * a.keep;
-    if (overlap(a.weights, w, a.weights_out, o) || overlap(a.weights, w, a.kept, k) || overlap(a.weights_out, o, a.kept, k))
-        return STATEKV_E_INVALID_ARG;
+    const int64_t units = (int64_t)a.batch * a.kv_heads, seqs = a.batch / a.layers;
+    // (outputs first: an output with each input and with the outputs behind it)
+    struct { const void* p; int64_t n; } arrays[] = {
+        {a.weights_out, units * a.out_rows}, {a.kept, units * a.keep}, {a.new_lengths, seqs},
+        {a.weights, units * a.weight_rows}, {a.lengths, seqs},
+        {a.table, (int64_t)(a.batch - 1) * a.table_stride + a.table_pages},
+        {a.out_table, (int64_t)(a.batch - 1) * a.out_table_stride + a.out_table_pages}};
+    for (int i = 0; i < 3; ++i)
+        for (int j = i + 1; j < 7; ++j)
+            if (arrays[i].p && arrays[j].p && overlap(arrays[i].p, arrays[i].n, arrays[j].p, arrays[j].n))
+                return STATEKV_E_INVALID_ARG;
     // K and V go to rows of their own; with both tables the pages that are read and
     // those that are written are the caller's to keep apart
     const Extent source{a.num_pages, a.kv_heads, a.page_rows}, target{a.out_num_pages, a.kv_heads, a.out_page_rows};

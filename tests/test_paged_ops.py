@@ -1136,7 +1136,7 @@ def test_evict_arrays_that_share_memory_are_refused(bad):
     dict(v_pages=view((1 << 30) + (19 << 21), b=1 << 20, h=1 << 16)),              # its first page is K's last
     dict(v_pages=view((1 << 30) - (1 << 21), b=1 << 20, h=1 << 16)),
     dict(v_pages=view((1 << 30) + (1 << 17) + 256, b=1 << 20, h=1 << 15)),         # other strides within K's range
-    ])
+    dict(new_lengths=(1 << 33) + 4), dict(new_lengths=(1 << 33) - 4), dict(new_lengths=(1 << 34) + 4)])
 def test_append_over_shared_memory_is_refused(bad):
     a = dict(PAGED, k_new=view(), v_new=view(), k_pages=view(1 << 30, b=1 << 20, h=1 << 16),
              v_pages=view(1 << 31, b=1 << 20, h=1 << 16), tokens=3, dtype=0, lengths=1 << 33, counts=1 << 34)
@@ -1160,7 +1160,10 @@ PLAIN = dict(table=None, out_table=None, num_pages=2, page_rows=128, out_num_pag
     dict(PLAIN, v_out=view((1 << 41) - 31 * 256, b=1 << 20, h=1 << 16)),           # the last row out is its first
     dict(PLAIN, k_out=view((1 << 40) + (1 << 21), b=1 << 21, h=1 << 16)),          # entry 0 goes to the source's entry 1
     dict(out_table=None, out_num_pages=2, out_page_rows=32, k_out=view((1 << 40) + (5 << 21), b=1 << 20, h=1 << 16)),
-    dict(table=None, page_rows=128, num_pages=2, k_out=view((1 << 40) - (3 << 21), b=1 << 20, h=1 << 16))])
+    dict(table=None, page_rows=128, num_pages=2, k_out=view((1 << 40) - (3 << 21), b=1 << 20, h=1 << 16)),
+    dict(new_lengths=(1 << 34) + 4), dict(new_lengths=(1 << 31) + 508), dict(new_lengths=(1 << 32) - 4),
+    dict(new_lengths=(1 << 30) + 2044), dict(kept=(1 << 28) - 508), dict(weights_out=(1 << 29) + 12),
+    dict(kept=(1 << 34) - 4)])
 def test_evict_over_shared_memory_is_refused(bad):
     assert N.load().statekv_evict_rows(N.EvictArgs(**{**EVICT, **bad}), None) == N.E_INVALID_ARG
 
