@@ -770,9 +770,9 @@ int statekv_attention_weights(const statekv_attention_weights_args* args, void* 
  *   kept         int32 [batch][kv_heads][keep]: the kept rows, then -1
  *   new_lengths  int32 [sequences]: min(length, keep), if not NULL
  * none of which shares memory with another or an input.  out_rows >= keep; the
- * out table holds out_table_pages * page_rows >= keep rows (E_CAPACITY; both
- * pools have the same page_rows); out_table NULL: batch entry n's
- * rows go to page n.  Where either table is NULL no row of k_out or v_out shares
+ * out table holds out_table_pages * out_page_rows >= keep rows (E_CAPACITY); the pools
+ * may have pages of different sizes, and either table may be NULL.  out_table NULL:
+ * batch entry n's rows go to page n, a plain cache of out_page_rows >= keep rows.  Where either table is NULL no row of k_out or v_out shares
  * memory with one of the source's, and never K's with V's (E_INVALID_ARG).  Any head_dim of whole
  * 16-byte units up to 512; dtype STATEKV_BF16 or STATEKV_F32; a sequence holds at
  * most 2^22 rows.

@@ -185,8 +185,8 @@ def evict_rows(k_pages, v_pages, table, lengths, weights, keep: int, out_table, 
     `sinks`, the last `recent`, and of the others those of the largest weight
     (float32 [n][Hkv][rows], as attention_weights returns them), ties to the
     lower row.  They move, in their order, to the pages of k_out and v_out
-    (default: k_pages and v_pages themselves) that out_table names; those pages
-    are in no entry's table.  Returns (new lengths, weights_out float32
+    (default: k_pages and v_pages themselves; of any page size) that out_table
+    names; those pages are in no entry's table.  Returns (new lengths, weights_out float32
     [n][Hkv][rows of out_table], the kept rows' weights and then zeros, kept
     int32 [n][Hkv][keep], their old rows and then -1)."""
     pages, hkv, rows, d = ps = _shape4(k_pages, "k_pages")

@@ -507,6 +507,27 @@ def test_evict(dtype, layers, page, rows, keep, sinks, recent):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("page,out_page,keep", [(64, 16, 333), (16, 128, 100), (48, 32, 600), (0, 16, 200), (0, 64, 77),
+                                                (32, 0, 150), (16, 0, 500)])
+def test_evict_between_pages_of_two_sizes(page, out_page, keep, dtype):
+    """Pools of their own page sizes, and a plain cache (0) on one side."""
+    g = gen(page + out_page)
+    lens, n = [600, 31, 0, 599], 4
+    c = Cache(g, n, 2, lens, page, 64, dtype)
+    cap = c.cap if c.table is None else c.table.shape[1] * page
+    w = torch.rand((n, 2, cap), generator=g, device=DEV)
+    per = -(-keep // out_page) if out_page else 0
+    order = torch.randperm(n * per, generator=g, device=DEV).view(n, per).to(I32) if out_page else None
+    out = [torch.full((n * per, 2, out_page, 64) if out_page else (n, 2, keep + 3, 64), 9.0, dtype=dtype, device=DEV)
+           for _ in range(2)]
+    got = kv.evict_rows(*c.pools, c.table, ints(*lens), w, keep, order, sinks=3, recent=20, k_out=out[0], v_out=out[1])
+    assert got[1].shape == (n, 2, per * out_page if out_page else keep + 3)
+    check_evict(c, lens, 1, w, keep, 3, 20, c.pools, out, order, got, out_page)
+    kv.check_status()
+
+
+@gpu
 def test_evict_within_one_pool():
     """Source and destination pages of one pool; a page of the source that two
     sequences share stays as it is."""
