@@ -106,8 +106,9 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __gri
     __shared__ uint32_t s_count[kEvictWarps][2];             // rows above the threshold, rows on it
     __shared__ uint32_t s_cta[kMaxCluster][2];
     extern __shared__ float s_weights[];
-    // the move may be launched now; it waits for this grid to end
-    ptx::dep_trigger();
+    // The move, where there is one, may be launched now; it waits for this grid to end.
+    // Otherwise the next kernel is not ours to release.
+    if (a.keep > 0) ptx::dep_trigger();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int C = ka.cluster, rank = blockIdx.x % C, u = blockIdx.x / C;
     const int n = u / a.kv_heads, h = u - n * a.kv_heads, seq = n / a.layers;
