@@ -345,6 +345,28 @@ def test_weights_ragged(layers, page, tok):
 
 
 @gpu
+@pytest.mark.parametrize("seqs,layers,page,hq,tok", [(33, 1, 64, 4, 3), (77, 2, 16, 4, 9), (40, 1, 64, 4, 300),
+                                                     (70, 2, 0, 2, 150)])
+def test_attention_and_weights_of_many_sequences(seqs, layers, page, hq, tok):
+    """More sequences than a warp has lanes, one block of query rows each or
+    several (padded prompts), ragged, some without tokens."""
+    r = random.Random(seqs)
+    lens = [r.choice([0, 1, r.randrange(2, 400), r.randrange(300, 1500)]) for _ in range(seqs - 1)] + [3000]
+    counts = [r.choice([0, 1, min(x, tok), r.randrange(0, min(x, tok) + 1)]) if x else 0 for x in lens[:-1]] + [tok]
+    n = seqs * layers
+    g = gen(seqs)
+    c = Cache(g, n, 2, [x for x in lens for _ in range(layers)], page, 64)
+    q = randn(g, n, hq, tok, 64)
+    out, lse = kv.paged_attention(q, *c.pools, c.table, ints(*lens), ints(*counts), scale=0.125, with_lse=True)
+    check_attention(q, c, lens, counts, 0.125, out, lse, layers)
+    cap = c.cap if c.table is None else c.table.shape[1] * page
+    before = torch.rand((n, 2, cap), generator=g, device=DEV)
+    got = kv.attention_weights(q, lse, c.pools[0], c.table, ints(*lens), ints(*counts), scale=0.125, before=before)
+    check_weights(q, lse, c, lens, counts, 0.125, before, got, layers)
+    kv.check_status()
+
+
+@gpu
 def test_weights_of_rows_that_are_not_finite_stay_their_own():
     g = gen(31)
     c = Cache(g, 1, 1, [400], 16, 64)
