@@ -83,6 +83,35 @@ def test_prompt_captured_and_on_another_stream():
     h.check_device_status()
 
 
+def test_prompt_on_another_stream_is_the_same():
+    """Outputs, queries and appended rows, behind work of that stream that the
+    default stream has not waited for."""
+    g = gen(12)
+    frames = [text(handle(), g, 64) for _ in range(2)]
+    x = text(handle(), g, 30)
+    got = []
+    for s in (None, torch.cuda.Stream()):
+        h = handle()
+        for f in frames:
+            h.prefill_frame(*f)
+        h.decode_prompt(*(y[..., :7, :].contiguous() for y in x))                # allocates
+        rest = [y[..., 7:, :].contiguous() for y in x]
+        late = [torch.zeros_like(y) for y in rest]
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s or torch.cuda.current_stream()):
+            torch.cuda._sleep(20_000_000)
+            for a, b in zip(late, rest):
+                a.copy_(b)
+        o = h.decode_prompt(*late, stream=s)
+        torch.cuda.synchronize()
+        h.check_device_status()
+        got.append((o, h.rotated_query().reshape(-1)[:late[0].numel()].clone(), rows_of(h, "k")[..., :158, :],
+                    rows_of(h, "v")[..., :158, :]))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    assert got[0][0].any()
+
+
 def test_prompt_rules():
     h = handle(max_frames=2)
     g = gen(11)
