@@ -18,7 +18,7 @@
 // The log-sum-exp is part of the product: a ninth k-step multiplies a row of ones
 // with -lse / scale in three bf16 terms (24 bits), so S comes out as q . k - lse /
 // scale and a column costs one multiplication, one exponential and one addition.
-// (Read from shared memory for each column, 246 us instead of 228 for a prompt:
+// (Read from shared memory for each column a prompt took 246 us, and 212 after:
 // the products take all of its bandwidth, 8 KB per 64 cycles.)
 //
 // Bound: by HBM for a few tokens (K once, 256 bytes a row and 8 of weights), by
@@ -30,8 +30,8 @@
 // by a mask of bits that each row makes once per block.
 //
 // Measured: one token for each of 16 ragged streams of up to 32768 rows, 8 KV
-// heads, 0.56 GB: 95 us = 5.9 TB/s.  512 tokens over 131072 rows, 12 heads on 2:
-// 183 us, 2000 cycles a block (the exponentials alone 1024, the products 1152
+// heads, 0.545 GB: 100 us = 5.4 TB/s.  512 tokens over 131072 rows, 12 heads on 2:
+// 185 us, 2000 cycles a block (the exponentials alone 1024, the products 1152
 // beside them): the warps that add up take 1700 of them from scores to sums, and
 // wait 200 for the next.
 #include <algorithm>
@@ -444,7 +444,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         };
         // An item of few queries is a block or two: the next one's weights are on
         // their way while this one is added up.  (With many queries that costs more
-        // registers than it saves: 225 us for a prompt instead of 211.)
+        // registers than it saves: 225 us for a prompt where the kernel took 211 without.)
         Walk ahead = x;
         bool have = !WIDE && ok && ahead.next(k);
         int64_t at_next = have ? weight_at(ahead) : -1;

@@ -52,13 +52,13 @@
 // for the rows that see them.
 //
 // Measured: one token for each of 16 ragged streams of up to 32768 rows, 8 KV
-// heads, 1.06 GB: 158 us = 6.7 TB/s (HBM).  One token in one layer of 131073
-// rows, 134 MB: 38.5 us, of which 8.5 pass before the first scores and 4 in the
-// merge.  512 tokens over 131072 rows, 12 heads on 2, 0.41 TFLOP: 272 us = 1.52
+// heads, 1.06 GB: 169 us = 6.25 TB/s (HBM).  One token in one layer of 131073
+// rows, 134 MB: 38.5 to 40 us, of which 8.5 pass before the first scores and 4 in
+// the merge.  512 tokens over 131072 rows, 12 heads on 2, 0.41 TFLOP: 272 us = 1.52
 // PFLOP/s, the tensor pipe 68 % busy: products alone keep it busy whatever
 // their order, and beside all the copies and tensor-memory accesses of this
 // kernel, but the warp that issues them does not get through its waits in time
-// (each 80 to 110 cycles where nothing is left to wait for).
+// (each 85 to 130 cycles where nothing is left to wait for).
 #include <algorithm>
 
 #include "paged.cuh"

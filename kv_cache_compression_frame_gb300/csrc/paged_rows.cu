@@ -19,7 +19,8 @@ __device__ __forceinline__ char* row_ptr(const statekv_view& v, int page, int h,
 // A CTA takes kAppendRows rows of one (batch entry, KV head); every 16 bytes are
 // read and written once, and a thread's loads are independent of each other.
 // Bound by the launch for a few tokens, by HBM (reads and writes) for a prompt:
-// 512 rows of 56 units, 15 MB in and out, take 7 us.
+// 512 rows of 56 units, 15 MB in and 15 out, take 6.6 us in the kernel and 10.3
+// from launch to launch.
 constexpr int kAppendThreads = 256;
 constexpr int kAppendRows = 32;
 

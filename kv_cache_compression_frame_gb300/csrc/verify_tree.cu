@@ -13,8 +13,8 @@
 // One cluster per sequence; warp 0 of every CTA does the same walk, and a warp
 // sums a contiguous run of the vocabulary, brought to shared memory by bulk
 // copies (and kept for the node's next refusal, where the run fits).  Bound by
-// latency: the passes of one sequence follow each other, about 6 us each (rows
-// 1.5 to 1.9, their sum 2.1, the cluster's 1.2, the walk 1).  16 trees of 42
+// latency: the passes of one sequence follow each other, 5 to 6 us each (rows
+// 1 to 1.6, their sum 2.8, the cluster's 0.9, the walk 1.2).  16 trees of 42
 // nodes over 150001 entries, 4 to 5 passes for the slowest: 35.6 us.
 //
 // Sums decide which token comes out, so they do not depend on how a row is cut:
