@@ -84,47 +84,48 @@ struct Extent {
     int64_t batch, heads, rows;
 };
 
-// Whether rows of two views share memory.  Views of the same strides (K and V next to
-// each other in one tensor, two parts of one cache) do where the distance of their
-// first entries is a sum of differences of indices times the strides; others are
-// taken to where their ranges of addresses do.
+// Whether rows of two views share memory.  They do where the distance of their first
+// entries is a sum of differences of indices times the strides; dimensions of
+// another stride in either are taken as a range.  So K and V next to each other in
+// one tensor, page by page or row by row, and two parts of one cache are told apart.
 inline bool share(const statekv_view& x, const Extent& nx, const statekv_view& y, const Extent& ny, int64_t d, int es) {
-    struct Dim { __int128 stride, before, after; } dims[3];      // steps down, steps up from x's entry to y's
+    struct Dim { __int128 stride, before, after; } dims[3];      // indices of y past x's, of x past y's
     if (nx.batch < 1 || nx.heads < 1 || nx.rows < 1 || ny.batch < 1 || ny.heads < 1 || ny.rows < 1) return false;
-    __int128 reach_x = d, reach_y = d;
-    bool same = true;
+    __int128 up0 = d - 1, down0 = d - 1;
     int count = 0;
     auto take = [&](int64_t n, int64_t s, int64_t m, int64_t t) {
-        reach_x += (__int128)(n - 1) * (n > 1 ? s : 0);
-        reach_y += (__int128)(m - 1) * (m > 1 ? t : 0);
-        if (n > 1 && m > 1 && s != t) same = false;
-        if (n > 1 || m > 1) dims[count++] = {n > 1 ? s : t, m - 1, n - 1};
+        if (n < 2 && m < 2) return;
+        if (n < 2) s = t;                                        // (a stride of one entry leads nowhere)
+        if (m < 2) t = s;
+        if (s == t) {
+            if (s > 0) dims[count++] = {s, m - 1, n - 1};
+        } else {
+            up0 += (__int128)(n - 1) * s;
+            down0 += (__int128)(m - 1) * t;
+        }
     };
     take(nx.batch, x.batch_stride, ny.batch, y.batch_stride);
     take(nx.heads, x.head_stride, ny.heads, y.head_stride);
     take(nx.rows, x.token_stride, ny.rows, y.token_stride);
-    // of y's first entry from x's, in elements (both are on 16-byte boundaries)
-    const __int128 by = ((__int128)reinterpret_cast<uintptr_t>(y.data) - (__int128)reinterpret_cast<uintptr_t>(x.data)) / es;
-    if (by >= reach_x || -by >= reach_y) return false;
-    if (!same) return true;
     std::sort(dims, dims + count, [](const Dim& p, const Dim& q) { return p.stride > q.stride; });
-    // by = sum of k_i stride_i + e, -before_i <= k_i <= after_i, |e| < d: largest stride first, what the
-    // smaller ones reach leaves two steps at most (where they reach further, it is not looked into)
+    // left = sum of k_i stride_i + e, -before_i <= k_i <= after_i, -down0 <= e <= up0: largest stride
+    // first, what the smaller ones reach leaves two steps of it (where they reach further, as in
+    // views that overlap in themselves, it is not looked into)
     auto meet = [&](auto& self, int i, __int128 left) -> bool {
-        if (i == count) return left < d && -left < d;
-        const __int128 s = dims[i].stride;
-        if (s == 0) return self(self, i + 1, left);
-        __int128 up = d - 1, down = d - 1;
+        if (i == count) return left <= up0 && -left <= down0;
+        __int128 up = up0, down = down0;
         for (int j = i + 1; j < count; ++j) up += dims[j].after * dims[j].stride, down += dims[j].before * dims[j].stride;
+        const __int128 s = dims[i].stride;
         auto floor_div = [](__int128 p, __int128 q) { return p / q - (p % q < 0 ? 1 : 0); };
-        const __int128 from = std::max(-dims[i].before, -floor_div(-(left - up), s));
+        const __int128 from = std::max(-dims[i].before, -floor_div(up - left, s));
         const __int128 to = std::min(dims[i].after, floor_div(left + down, s));
         if (to - from > 2) return true;
         for (__int128 k = from; k <= to; ++k)
             if (self(self, i + 1, left - k * s)) return true;
         return false;
     };
-    return meet(meet, 0, by);
+    // y's first entry from x's, in elements (both are on 16-byte boundaries)
+    return meet(meet, 0, ((__int128)reinterpret_cast<uintptr_t>(y.data) - (__int128)reinterpret_cast<uintptr_t>(x.data)) / es);
 }
 
 #ifdef __CUDACC__

@@ -1242,6 +1242,30 @@ def test_pools_side_by_side_in_one_tensor_are_apart():
     kv.check_status()
 
 
+@gpu
+def test_pools_of_other_strides_in_one_tensor_are_apart():
+    """Each page's K by heads, then its V by rows."""
+    g = gen(82)
+    n, lens = 2, [30, 5]
+    c = Cache(g, n, 2, [x + 4 for x in lens], 16, 64)
+
+    def pair():
+        both = torch.full((len(c.pools[0]), 2, 2 * 16 * 64), 9.0, dtype=BF16, device=DEV)
+        return both[:, 0].unflatten(1, (2, 16, 64)), both[:, 1].unflatten(1, (16, 2, 64)).transpose(1, 2)
+
+    pools, out = pair(), pair()
+    k, v = randn(g, n, 2, 4, 64), randn(g, n, 2, 4, 64)
+    assert kv.paged_append(k, v, *pools, c.table, ints(*lens)).tolist() == [34, 9]
+    for pool, x in zip(pools, (k, v)):
+        for i in range(n):
+            assert torch.equal(c.rows(pool, i, lens[i] + 4)[:, lens[i]:], x[i])
+    w = torch.rand((n, 2, c.table.shape[1] * 16), generator=g, device=DEV)
+    to = torch.arange(4, dtype=I32, device=DEV).view(2, 2)
+    got = kv.evict_rows(*pools, c.table, ints(34, 9), w, 20, to, k_out=out[0], v_out=out[1])
+    check_evict(c, [34, 9], 1, w, 20, 0, 0, pools, out, to, got, 16)
+    kv.check_status()
+
+
 @pytest.mark.parametrize("by", [4, 2044, -4, -2044])
 def test_weights_over_a_part_of_what_they_are_added_to_are_refused(by):
     a = dict(PAGED, q=view(), k_pages=view(b=1 << 20, h=1 << 16), lse=16, before=1 << 30, out=(1 << 30) + by, length=40,
