@@ -669,8 +669,8 @@ int statekv_sparse_attention(const statekv_sparse_args* args, void* cuda_stream)
  * rows do not fit in its table row appends nothing (recorded).  Batch entries
  * that write one page write the same row of it in any order: pages that are
  * appended to are not shared.  k_pages and v_pages do not overlap each other
- * (E_INVALID_ARG; they may lie side by side in one tensor) or the new rows.  Any head_dim of whole 16-byte units up to 512; dtype
- * STATEKV_BF16 or STATEKV_F32.
+ * (E_INVALID_ARG; they may lie side by side in one tensor) or the new rows.  Any
+ * head_dim of whole 16-byte units up to 512; dtype STATEKV_BF16 or STATEKV_F32.
  */
 typedef struct statekv_paged_append_args {
     statekv_view k_new, v_new, k_pages, v_pages;
@@ -772,9 +772,10 @@ int statekv_attention_weights(const statekv_attention_weights_args* args, void* 
  * none of which shares memory with another or an input.  out_rows >= keep; the
  * out table holds out_table_pages * out_page_rows >= keep rows (E_CAPACITY); the pools
  * may have pages of different sizes, and either table may be NULL.  out_table NULL:
- * batch entry n's rows go to page n, a plain cache of out_page_rows >= keep rows.  Where either table is NULL no row of k_out or v_out shares
- * memory with one of the source's, and never K's with V's (E_INVALID_ARG).  Any head_dim of whole
- * 16-byte units up to 512; dtype STATEKV_BF16 or STATEKV_F32; a sequence holds at
+ * batch entry n's rows go to page n, a plain cache of out_page_rows >= keep rows.
+ * Where either table is NULL no row of k_out or v_out shares memory with one of the
+ * source's, and never K's with V's (E_INVALID_ARG).  Any head_dim of whole 16-byte
+ * units up to 512; dtype STATEKV_BF16 or STATEKV_F32; a sequence holds at
  * most 2^22 rows.
  */
 typedef struct statekv_evict_args {

@@ -237,7 +237,8 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         p = __shfl_sync(0xffffffffu, p, 0);
         if (p >= all) return false;
         const int u = (int)(p / pieces), r0 = (int)(p - (int64_t)u * pieces) * kRest;
-        const int r1 = a.weight_rows - r0 < kRest ? a.weight_rows : r0 + kRest, from = max(r0, seq_of(k, u / a.kv_heads / a.layers).len);
+        const int r1 = a.weight_rows - r0 < kRest ? a.weight_rows : r0 + kRest;
+        const int from = max(r0, seq_of(k, u / a.kv_heads / a.layers).len);
         const int64_t o = (int64_t)u * a.weight_rows;
         float v[kRest / 32];
 #pragma unroll

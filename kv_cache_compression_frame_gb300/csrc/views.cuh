@@ -125,7 +125,8 @@ inline bool share(const statekv_view& x, const Extent& nx, const statekv_view& y
         return false;
     };
     // y's first entry from x's, in elements (both are on 16-byte boundaries)
-    return meet(meet, 0, ((__int128)reinterpret_cast<uintptr_t>(y.data) - (__int128)reinterpret_cast<uintptr_t>(x.data)) / es);
+    const __int128 x0 = reinterpret_cast<uintptr_t>(x.data), y0 = reinterpret_cast<uintptr_t>(y.data);
+    return meet(meet, 0, (y0 - x0) / es);
 }
 
 #ifdef __CUDACC__
