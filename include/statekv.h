@@ -698,8 +698,8 @@ int statekv_paged_append(const statekv_paged_append_args* args, void* cuda_strea
  * Scores, softmax sums and the output are fp32; the probabilities are rounded
  * to bf16 (2^-8 of each) for the product with V, their sum takes them unrounded.
  * lse, if not NULL: float [batch][q_heads][tokens].
- * bf16, head_dim 64 or 128, q_heads / kv_heads <= 64.  K and V are read in tiles:
- * their entries do not share memory (strides above 0).  workspace: device memory of
+ * bf16, head_dim 64 or 128, q_heads / kv_heads <= 64, that times tokens below 2^26.
+ * K and V are read in tiles: their entries do not share memory (strides above 0).  workspace: device memory of
  * statekv_paged_attention_workspace() bytes, 16-byte aligned, contents
  * irrelevant (NULL where that is 0: a few short caches; cache_rows: the most that
  * a sequence can hold); the size depends on the current device and, with the
@@ -736,8 +736,8 @@ int statekv_paged_attention(const statekv_paged_attention_args* args, void* cuda
  * [batch][kv_heads][weight_rows] (before NULL: zeros; out may be before, and shares
  * no memory with it otherwise), weight_rows at least the rows a sequence can hold (E_CAPACITY).  Scores and sums in
  * fp32, each row's sum in a fixed order (the same bits on every run).
- * bf16, head_dim 64 or 128, q_heads / kv_heads <= 64; q and K are read in tiles:
- * their entries do not share memory.  No workspace.
+ * bf16, head_dim 64 or 128, q_heads / kv_heads <= 64, that times tokens below 2^26;
+ * q and K are read in tiles: their entries do not share memory.  No workspace.
  */
 typedef struct statekv_attention_weights_args {
     statekv_view q, k_pages;

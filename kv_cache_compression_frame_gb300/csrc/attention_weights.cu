@@ -576,6 +576,8 @@ extern "C" int statekv_attention_weights(const statekv_attention_weights_args* a
         return STATEKV_E_INVALID_ARG;
     const int G = a.q_heads / a.kv_heads;
     if ((a.head_dim != 64 && a.head_dim != 128) || G > 64) return STATEKV_E_UNSUPPORTED;
+    // the attention's own limit (a group's log-sum-exps are counted in 32 bits)
+    if ((int64_t)G * a.tokens >= 1 << 26) return STATEKV_E_UNSUPPORTED;
     if (!a.status || !ints_ok(a.status) || !ints_ok(a.lengths) || !ints_ok(a.counts) || !ints_ok(a.lse) ||
         !ints_ok(a.before) || !ints_ok(a.out))
         return STATEKV_E_INVALID_ARG;

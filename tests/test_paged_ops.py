@@ -1266,6 +1266,13 @@ def test_pools_of_other_strides_in_one_tensor_are_apart():
     kv.check_status()
 
 
+@pytest.mark.parametrize("bad", [dict(tokens=1 << 26), dict(tokens=1 << 25), dict(tokens=2 ** 31 - 1)])
+def test_weights_of_more_queries_than_the_attention_takes_are_refused(bad):
+    a = dict(PAGED, q=view(), k_pages=view(b=1 << 20, h=1 << 16), lse=16, out=16, length=40, q_heads=4, scale=0.1,
+             weight_rows=128)
+    assert N.load().statekv_attention_weights(N.AttentionWeightsArgs(**{**a, **bad}), None) == N.E_UNSUPPORTED
+
+
 @pytest.mark.parametrize("by", [4, 2044, -4, -2044])
 def test_weights_over_a_part_of_what_they_are_added_to_are_refused(by):
     a = dict(PAGED, q=view(), k_pages=view(b=1 << 20, h=1 << 16), lse=16, before=1 << 30, out=(1 << 30) + by, length=40,
